@@ -139,7 +139,7 @@ def _quantise(x):
     a = xf.abs().amax(-1)
     m, e = torch.frexp(a)  # a = m 2^e, m in [0.5, 1)
     e = torch.where(m > 0.875, e - 8, e - 9).clamp(E_MIN, E_MAX)  # 448 = 0.875 * 2^9
-    e = torch.where(a > 0, e, torch.zeros_like(e))
+    e = torch.where(a > 0, e, torch.full_like(e, E_MIN))
     y = torch.ldexp(xf, -e[..., None]).clamp(-E4M3_MAX, E4M3_MAX)
     return y.to(torch.float8_e4m3fn), (e + 127).to(torch.uint8)
 
@@ -429,7 +429,7 @@ def _exact_append(s, k, v, start):
     got = {}
     for name, x in (("k", k), ("v", v)):
         a = x.abs().amax(-1)
-        a = torch.where(a > 0, a, E4M3_MAX)
+        a = torch.where(a > 0, a, 2.0 ** E_MIN)
         e = torch.round(torch.log2(a / E4M3_MAX))  # the smallest e with a <= 448 2^e is this one or the next
         e = torch.where(a <= E4M3_MAX * torch.exp2(e), e, e + 1)
         e = torch.where(a <= E4M3_MAX * torch.exp2(e - 1), e - 1, e).clamp(E_MIN, E_MAX)
