@@ -13,13 +13,15 @@ import ctypes
 from ._binding import (  # noqa: F401
     BpkvError, bpkv_alloc_depths, bpkv_cache, bpkv_calibrate_channels, bpkv_clear_status, bpkv_decode_step,
     bpkv_dense_attend, bpkv_encode_append, bpkv_fixed_depths, bpkv_read_status, bpkv_rotate, bpkv_row_cache_stats, bpkv_scan, bpkv_scan_topk, bpkv_scan_topk_noalloc, bpkv_selection_map, bpkv_selftest_wait, bpkv_sparse_attend, bpkv_sparse_attend_vdepth,
-    bpkv_status_string, bpkv_step_args, bpkv_topk, bpkv_union, bpkv_version, bpkv_workspace_size, header_symbols, load)
+    bpkv_qkv_args, bpkv_qkv_rope, bpkv_rows8, bpkv_rows8_append, bpkv_rows8_read, bpkv_shared_attend,
+    bpkv_shared_attend8, bpkv_shared_workspace_size, bpkv_status_string, bpkv_step_args, bpkv_topk, bpkv_union, bpkv_version, bpkv_workspace_size, header_symbols, load)
 
 HEAD_DIM = 128
 WS_SCAN_TOPK, WS_ATTEND, WS_DENSE, WS_STEP = 1, 2, 4, 8
 DEPTH_WATERFILL, DEPTH_FIXED, DEPTH_DENSE, DEPTH_GIVEN = 0, 1, 2, 3
 DEV_OVERFLOW, DEV_SELECT, DEV_TIMEOUT = 1, 2, 4
 STEP_VDEPTH = 1
+QKV_PAIRS, QKV_Q_BF16 = 1, 2
 
 
 class Cache:
@@ -103,6 +105,95 @@ class Cache:
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
 
+class Rows8:
+    """One layer's cache of 8-bit K and V rows (e4m3 codes, one power-of-two
+    scale per row) for N sequences x H KV heads, in device memory."""
+
+    def __init__(self, n_seq: int, n_kv_heads: int, group: int, cap_tokens: int, device="cuda"):
+        import torch
+        if cap_tokens % 512:
+            raise ValueError("cap_tokens must be a multiple of 512")
+        self.device = torch.device(device)
+        rows = (n_seq, n_kv_heads, cap_tokens)
+        self.k8 = torch.empty((*rows, HEAD_DIM), dtype=torch.uint8, device=self.device)
+        self.v8 = torch.empty((*rows, HEAD_DIM), dtype=torch.uint8, device=self.device)
+        self.kexp = torch.empty(rows, dtype=torch.uint8, device=self.device)
+        self.vexp = torch.empty(rows, dtype=torch.uint8, device=self.device)
+        self.seq_len = torch.zeros(n_seq, dtype=torch.int64, device=self.device)
+        self.c = bpkv_rows8(n_seq, n_kv_heads, group, HEAD_DIM, cap_tokens, 0, self.k8.data_ptr(), self.v8.data_ptr(),
+                            self.kexp.data_ptr(), self.vexp.data_ptr(), self.seq_len.data_ptr())
+
+    @property
+    def n_max(self) -> int:
+        return int(self.c.n_max)
+
+    def append(self, k_new, v_new, start=None, status=None, stream=None):
+        """Quantise k_new/v_new [N][H][t][D] bf16 (device) behind every
+        sequence's rows, or at rows start[i] .. (int64 [N], device)."""
+        bpkv_rows8_append(self.c, k_new, v_new, k_new.shape[2], start, status, stream)
+
+    def read(self, t0: int, n: int, stream=None):
+        """(K, V) rows t0 .. t0 + n - 1 of every sequence, bf16 [N][H][n][D]; zeros past its length."""
+        import torch
+        shape = (self.c.n_seq, self.c.n_kv_heads, n, HEAD_DIM)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        bpkv_rows8_read(self.c, t0, n, k, v, stream)
+        return k, v
+
+
+def qkv_args(qkv, q_out, n_kv_heads: int, pos=None, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+             pairs: bool = False, k_out=None, v_out=None, rows8=None, status=None):
+    """bpkv_qkv_args for qkv [N][t][>= (G + 2) H D] bf16 (its last dimension
+    dense) and q_out [N][t][H][G][D] float32 or bf16; inv_freq [rot / 2]
+    float32 says how many channels are rotated; rows8: a Rows8.  The struct
+    keeps the tensors it points to alive."""
+    import torch
+    N, t = qkv.shape[0], qkv.shape[1]
+    H, G = q_out.shape[2], q_out.shape[3]
+
+    def need(ok, what):
+        if not ok:
+            raise ValueError(f"qkv_args: {what}")
+
+    need(qkv.dtype == torch.bfloat16 and qkv.dim() == 3 and qkv.stride(2) == 1, "qkv must be bf16 [N][t][row]")
+    need(N == 1 or t == 1 or qkv.stride(0) == t * qkv.stride(1), "qkv's tokens must lie one stride apart")
+    need(H == n_kv_heads and q_out.shape == (N, t, H, G, HEAD_DIM) and q_out.is_contiguous(), "q_out's shape")
+    need(q_out.dtype in (torch.float32, torch.bfloat16), "q_out must be float32 or bf16")
+    need(qkv.shape[2] >= (G + 2) * H * HEAD_DIM, "qkv's rows hold (G + 2) H heads")
+    for x, dt, shape in ((pos, torch.int64, (N,)), (q_weight, torch.float32, (HEAD_DIM,)),
+                         (k_weight, torch.float32, (HEAD_DIM,)), (k_out, torch.bfloat16, (N, H, t, HEAD_DIM)),
+                         (v_out, torch.bfloat16, (N, H, t, HEAD_DIM))):
+        need(x is None or (x.dtype == dt and tuple(x.shape) == shape and x.is_contiguous()), f"expected {dt} {shape}")
+    need(inv_freq is None or (inv_freq.dtype == torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()),
+         "inv_freq must be float32 [rot / 2]")
+    # one token of one sequence has no stride between tokens; of several sequences it is theirs
+    ld = qkv.stride(1) if t > 1 else qkv.stride(0) if N > 1 else qkv.shape[2] // 8 * 8
+
+    def p(x):
+        return None if x is None else x.data_ptr()
+
+    a = bpkv_qkv_args(N, H, G, HEAD_DIM, t, 0 if inv_freq is None else 2 * inv_freq.numel(),
+                      (QKV_PAIRS if pairs else 0) | (QKV_Q_BF16 if q_out.dtype == torch.bfloat16 else 0), eps, p(qkv),
+                      ld, p(pos), p(inv_freq), p(q_weight), p(k_weight), p(q_out), p(k_out), p(v_out),
+                      ctypes.pointer(rows8.c) if rows8 is not None else None, p(status))
+    a.keep = (qkv, q_out, pos, inv_freq, q_weight, k_weight, k_out, v_out, rows8, status)
+    return a
+
+
+def shared_workspace(cache, prefix=None):
+    """Workspace (uint8, device) of bpkv_shared_attend / bpkv_shared_attend8 for a Cache or Rows8 and its
+    prefixes; its status word is clear."""
+    import torch
+    c = cache.c
+    n = bpkv_shared_workspace_size(c.n_seq, 0 if prefix is None else prefix.c.n_seq, c.n_kv_heads, c.group)
+    if n == 0:
+        raise BpkvError("bpkv_shared_workspace_size", -4)
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    ws[:256].zero_()
+    return ws
+
+
 def cache_array(caches):
     """ctypes array of the bpkv_cache structs of several layers (for bpkv_decode_step)."""
     arr = (bpkv_cache * len(caches))(*[c.c for c in caches])
@@ -115,5 +206,5 @@ def sync_n_max(caches, arr):
         c.c.n_max = s.n_max
 
 
-__all__ = [n for n in dir() if n.startswith("bpkv_")] + ["Cache", "cache_array", "sync_n_max", "BpkvError"]
+__all__ = [n for n in dir() if n.startswith("bpkv_")] + ["Cache", "Rows8", "cache_array", "qkv_args", "shared_workspace", "sync_n_max", "BpkvError"]
 _ = ctypes

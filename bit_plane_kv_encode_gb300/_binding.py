@@ -45,6 +45,22 @@ class bpkv_step_args(ctypes.Structure):
     ]
 
 
+class bpkv_rows8(ctypes.Structure):
+    _fields_ = [
+        ("n_seq", i32), ("n_kv_heads", i32), ("group", i32), ("head_dim", i32), ("cap_tokens", i64), ("n_max", i64),
+        ("k8", P), ("v8", P), ("kexp", P), ("vexp", P), ("seq_len", P),
+    ]
+
+
+class bpkv_qkv_args(ctypes.Structure):
+    _fields_ = [
+        ("n_seq", i32), ("n_kv_heads", i32), ("group", i32), ("head_dim", i32), ("t_new", i32), ("rot_dim", i32),
+        ("flags", i32), ("eps", ctypes.c_float), ("qkv", P), ("ld", i64), ("pos", P), ("inv_freq", P),
+        ("q_weight", P), ("k_weight", P), ("q_out", P), ("k_out", P), ("v_out", P),
+        ("rows8", ctypes.POINTER(bpkv_rows8)), ("status", P),
+    ]
+
+
 _SIGS = {
     "bpkv_version": ([], i32),
     "bpkv_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -68,6 +84,12 @@ _SIGS = {
     "bpkv_dense_attend": ([P, P, P, P, sz, P], ctypes.c_int),
     "bpkv_sparse_attend_vdepth": ([P, P, P, P, P, i32, i32, P, P, P, P], ctypes.c_int),
     "bpkv_decode_step": ([P, i32, P, P, sz, P], ctypes.c_int),
+    "bpkv_rows8_append": ([P, P, P, i32, P, P, P], ctypes.c_int),
+    "bpkv_rows8_read": ([P, i64, i32, P, P, P], ctypes.c_int),
+    "bpkv_qkv_rope": ([P, P], ctypes.c_int),
+    "bpkv_shared_workspace_size": ([i32, i32, i32, i32], sz),
+    "bpkv_shared_attend": ([P, P, P, P, P, P, sz, P], ctypes.c_int),
+    "bpkv_shared_attend8": ([P, P, P, P, P, P, sz, P], ctypes.c_int),
 }
 
 _lib = None
@@ -258,3 +280,36 @@ def bpkv_decode_step(layers_array, n_layers: int, args, ws, ws_bytes: int, strea
     return _check("bpkv_decode_step",
                   load().bpkv_decode_step(layers_array, int(n_layers), ctypes.byref(args), _ptr(ws),
                                           int(ws_bytes), _stream(stream)))
+
+
+def bpkv_rows8_append(c, k_new, v_new, t_new: int, start=None, status=None, stream=None):
+    return _check("bpkv_rows8_append",
+                  load().bpkv_rows8_append(ctypes.byref(c), _ptr(k_new), _ptr(v_new), int(t_new), _ptr(start),
+                                           _ptr(status), _stream(stream)))
+
+
+def bpkv_rows8_read(c, t0: int, n: int, k_out, v_out, stream=None):
+    return _check("bpkv_rows8_read",
+                  load().bpkv_rows8_read(ctypes.byref(c), int(t0), int(n), _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def bpkv_qkv_rope(args, stream=None):
+    return _check("bpkv_qkv_rope", load().bpkv_qkv_rope(ctypes.byref(args), _stream(stream)))
+
+
+def bpkv_shared_workspace_size(n_seq: int, n_prefix: int, n_kv_heads: int, group: int) -> int:
+    return int(load().bpkv_shared_workspace_size(int(n_seq), int(n_prefix), int(n_kv_heads), int(group)))
+
+
+def bpkv_shared_attend(prefix, prefix_of, cache, q, out, ws, ws_bytes: int, stream=None):
+    return _check("bpkv_shared_attend",
+                  load().bpkv_shared_attend(None if prefix is None else ctypes.byref(prefix), _ptr(prefix_of),
+                                            ctypes.byref(cache), _ptr(q), _ptr(out), _ptr(ws), int(ws_bytes),
+                                            _stream(stream)))
+
+
+def bpkv_shared_attend8(prefix, prefix_of, cache, q, out, ws, ws_bytes: int, stream=None):
+    return _check("bpkv_shared_attend8",
+                  load().bpkv_shared_attend8(None if prefix is None else ctypes.byref(prefix), _ptr(prefix_of),
+                                             ctypes.byref(cache), _ptr(q), _ptr(out), _ptr(ws), int(ws_bytes),
+                                             _stream(stream)))

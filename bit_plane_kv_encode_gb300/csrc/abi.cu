@@ -45,6 +45,16 @@ cudaError_t launch_selftest_wait(uint32_t* bar, uint32_t count, uint32_t limit, 
 cudaError_t launch_attend_vdepth(const bpkv_cache& c, const float* q, const int32_t* uidx, const uint8_t* umask,
                                  const int32_t* ucount, int32_t u_cap, int32_t budget_v, float* out,
                                  uint8_t* vdepth, float* weight, cudaStream_t st);
+cudaError_t launch_rows8_append(const bpkv_rows8& c, const uint16_t* k_new, const uint16_t* v_new, int32_t t_new,
+                                const int64_t* start, int32_t* status, cudaStream_t st);
+cudaError_t launch_rows8_read(const bpkv_rows8& c, int64_t t0, int32_t n, uint16_t* k_out, uint16_t* v_out,
+                              cudaStream_t st);
+cudaError_t launch_qkv_rope(const bpkv_qkv_args& a, cudaStream_t st);
+size_t shared_bytes(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group);
+cudaError_t launch_shared(const bpkv_cache* prefix, const int32_t* prefix_of, const bpkv_cache& c, const uint16_t* q,
+                          uint16_t* out, void* ws, cudaStream_t st);
+cudaError_t launch_shared8(const bpkv_rows8* prefix, const int32_t* prefix_of, const bpkv_rows8& c, const uint16_t* q,
+                           uint16_t* out, void* ws, cudaStream_t st);
 
 namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -69,6 +79,26 @@ int check_cache(const bpkv_cache* c) {
   }
   if (c->vplanes && (!aligned(c->vplanes, 16) || !aligned(c->vscales, 16))) return BPKV_EINVAL;
   return BPKV_OK;
+}
+
+int check_rows8(const bpkv_rows8* c) {
+  if (!c) return BPKV_EINVAL;
+  if (c->head_dim != kD) return BPKV_EUNSUPPORTED;
+  if (c->n_seq < 1 || c->n_kv_heads < 1 || c->group < 1 || c->group > BPKV_MAX_GROUP) return BPKV_EINVAL;
+  if (c->n_seq > 65535 || c->n_kv_heads > 65535) return BPKV_EUNSUPPORTED;
+  if (c->cap_tokens < 512 || c->cap_tokens % 512 != 0) return BPKV_EINVAL;
+  if (c->n_max < 0 || c->n_max > c->cap_tokens) return BPKV_EINVAL;
+  if (!c->k8 || !c->v8 || !c->kexp || !c->vexp || !c->seq_len) return BPKV_EINVAL;
+  if (!aligned(c->k8, 16) || !aligned(c->v8, 16) || !aligned(c->kexp, 16) || !aligned(c->vexp, 16) ||
+      !aligned(c->seq_len, 8))
+    return BPKV_EINVAL;
+  return BPKV_OK;
+}
+
+// Rows [n_seq][n_heads][t] that the 8-bit row kernels and the projected-heads
+// kernel handle in one launch.
+bool rows_in_range(int64_t n_seq, int64_t n_heads, int64_t t) {
+  return n_seq * n_heads <= ((int64_t)1 << 34) / t;
 }
 
 int check_k(int32_t k, int32_t n_sink, int32_t n_recent) {
@@ -350,6 +380,99 @@ int bpkv_dense_attend(const bpkv_cache* c, const float* q, float* out, void* ws,
   const Layout L = layout(*c, 1, BPKV_WS_DENSE);
   return cuda_status(launch_attend(*c, q, nullptr, nullptr, nullptr, 1, reinterpret_cast<float*>(at(ws, L.part)),
                                    out, true, as_stream(stream)));
+}
+
+int bpkv_rows8_append(bpkv_rows8* c, const uint16_t* k_new, const uint16_t* v_new, int32_t t_new,
+                      const int64_t* start, int32_t* status, void* stream) {
+  BPKV_TRY(check_rows8(c));
+  if (t_new < 1 || t_new > c->cap_tokens || !k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16))
+    return BPKV_EINVAL;
+  if (!aligned(start, 8) || !aligned(status, 4)) return BPKV_EINVAL;
+  if ((!start || start == c->seq_len) && c->n_max + t_new > c->cap_tokens) return BPKV_EINVAL;
+  if (!rows_in_range(c->n_seq, c->n_kv_heads, t_new)) return BPKV_EUNSUPPORTED;
+  BPKV_TRY(cuda_status(launch_rows8_append(*c, k_new, v_new, t_new, start, status, as_stream(stream))));
+  c->n_max = min64(c->n_max + t_new, c->cap_tokens);
+  return BPKV_OK;
+}
+
+int bpkv_rows8_read(const bpkv_rows8* c, int64_t t0, int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream) {
+  BPKV_TRY(check_rows8(c));
+  if (t0 < 0 || n < 1 || n > c->cap_tokens || t0 > c->cap_tokens - n) return BPKV_EINVAL;
+  if ((!k_out && !v_out) || !aligned(k_out, 16) || !aligned(v_out, 16)) return BPKV_EINVAL;
+  if (!rows_in_range(c->n_seq, c->n_kv_heads, n)) return BPKV_EUNSUPPORTED;
+  return cuda_status(launch_rows8_read(*c, t0, n, k_out, v_out, as_stream(stream)));
+}
+
+int bpkv_qkv_rope(const bpkv_qkv_args* a, void* stream) {
+  if (!a) return BPKV_EINVAL;
+  if (a->head_dim != kD) return BPKV_EUNSUPPORTED;
+  if (a->n_seq < 1 || a->n_kv_heads < 1 || a->group < 1 || a->group > BPKV_MAX_GROUP || a->t_new < 1)
+    return BPKV_EINVAL;
+  if (a->n_seq > 65535 || a->n_kv_heads > 65535) return BPKV_EUNSUPPORTED;
+  if (a->rot_dim < 0 || a->rot_dim > kD || a->rot_dim % 2 != 0 || (a->rot_dim > 0 && !a->inv_freq)) return BPKV_EINVAL;
+  if ((a->flags & ~(BPKV_QKV_PAIRS | BPKV_QKV_Q_BF16)) != 0 || !(a->eps >= 0.f)) return BPKV_EINVAL;
+  if (!a->qkv || !a->q_out || !aligned(a->qkv, 16) || !aligned(a->q_out, 16) || !aligned(a->k_out, 16) ||
+      !aligned(a->v_out, 16) || !aligned(a->inv_freq, 4) || !aligned(a->q_weight, 4) || !aligned(a->k_weight, 4) ||
+      !aligned(a->pos, 8) || !aligned(a->status, 4))
+    return BPKV_EINVAL;
+  if (a->ld % 8 != 0 || a->ld < (int64_t)(a->group + 2) * a->n_kv_heads * kD) return BPKV_EINVAL;
+  if (!a->pos && !a->rows8) return BPKV_EINVAL;
+  if (!rows_in_range(a->n_seq, a->n_kv_heads, a->t_new)) return BPKV_EUNSUPPORTED;
+  bpkv_rows8* c = a->rows8;
+  if (c) {
+    BPKV_TRY(check_rows8(c));
+    if (c->n_seq != a->n_seq || c->n_kv_heads != a->n_kv_heads || a->t_new > c->cap_tokens) return BPKV_EINVAL;
+    if ((!a->pos || a->pos == c->seq_len) && c->n_max + a->t_new > c->cap_tokens) return BPKV_EINVAL;
+  }
+  BPKV_TRY(cuda_status(launch_qkv_rope(*a, as_stream(stream))));
+  if (c) c->n_max = min64(c->n_max + a->t_new, c->cap_tokens);
+  return BPKV_OK;
+}
+
+size_t bpkv_shared_workspace_size(int32_t n_seq, int32_t n_prefix, int32_t n_kv_heads, int32_t group) {
+  if (n_seq < 1 || n_seq > BPKV_SHARED_MAX_SEQ || n_prefix < 0 || n_prefix > BPKV_SHARED_MAX_SEQ || n_kv_heads < 1 ||
+      n_kv_heads > 65535 || group < 1 || group > BPKV_MAX_GROUP)
+    return 0;
+  return shared_bytes(n_seq, n_prefix, n_kv_heads, group);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks that the two row formats share; A is bpkv_cache or bpkv_rows8.
+template <typename A>
+int check_shared(const A* prefix, const int32_t* prefix_of, const A& c, const uint16_t* q, const uint16_t* out,
+                 const void* ws, size_t ws_bytes) {
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(prefix_of, 4)) return BPKV_EINVAL;
+  if (prefix && (prefix->n_kv_heads != c.n_kv_heads || prefix->group != c.group)) return BPKV_EINVAL;
+  const int64_t cap = prefix && prefix->cap_tokens > c.cap_tokens ? prefix->cap_tokens : c.cap_tokens;
+  if (cap >= (int64_t)1 << 31) return BPKV_EUNSUPPORTED;  // a tile's coordinates are 32 bits
+  const size_t need = bpkv_shared_workspace_size(c.n_seq, prefix ? prefix->n_seq : 0, c.n_kv_heads, c.group);
+  if (need == 0) return BPKV_EUNSUPPORTED;
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return BPKV_ENOWORKSPACE;
+  return BPKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bpkv_shared_attend(const bpkv_cache* prefix, const int32_t* prefix_of, const bpkv_cache* c, const uint16_t* q,
+                       uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  BPKV_TRY(check_cache(c));
+  if (prefix) BPKV_TRY(check_cache(prefix));
+  if (c->residency != 0 || (prefix && prefix->residency != 0)) return BPKV_EUNSUPPORTED;
+  BPKV_TRY(check_shared(prefix, prefix_of, *c, q, out, ws, ws_bytes));
+  return cuda_status(launch_shared(prefix, prefix_of, *c, q, out, ws, as_stream(stream)));
+}
+
+int bpkv_shared_attend8(const bpkv_rows8* prefix, const int32_t* prefix_of, const bpkv_rows8* c, const uint16_t* q,
+                        uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  BPKV_TRY(check_rows8(c));
+  if (prefix) BPKV_TRY(check_rows8(prefix));
+  BPKV_TRY(check_shared(prefix, prefix_of, *c, q, out, ws, ws_bytes));
+  return cuda_status(launch_shared8(prefix, prefix_of, *c, q, out, ws, as_stream(stream)));
 }
 
 int bpkv_decode_step(bpkv_cache* layers, int32_t n_layers, const bpkv_step_args* a, void* ws, size_t ws_bytes,

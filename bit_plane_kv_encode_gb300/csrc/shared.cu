@@ -1,0 +1,976 @@
+// Decode attention of a batch that shares prefixes, on the tensor cores
+// (bpkv_shared_attend over bf16 rows, bpkv_shared_attend8 over 8-bit rows).
+//
+// Work.  A unit is a set of query rows that attend over the same KV rows: the
+// query heads of all sequences of one prefix, 256 at a time, for each KV head;
+// and for each sequence and KV head its own rows with its G query heads.  The
+// units' tiles of 128 tokens form one list, cut into equal stretches, one per
+// CTA; a CTA's part of a unit is a segment.  Lengths are read on the device, so
+// the cut fits ragged batches.  Each segment leaves its rows' partial (o, m, l)
+// in the workspace and a second kernel joins them.
+//
+// A segment.  One thread loads K and V tiles by TMA into a ring of shared
+// memory stages, one thread issues the products, and two groups of four warps
+// do the softmax, a thread per query row: S = Q K^T (128 x 128 x 128) into
+// tensor memory, p = exp2(S - m) written back over S as the A operand of
+// O += P V, with O in tensor memory too.  The groups are two streams that take
+// turns at the tensor cores: with more than 128 rows each has its own 128 rows
+// and both take every tile; with fewer both hold the same rows and each takes
+// every other tile.  m only follows the maximum when that has risen by a factor
+// of 2^kLazy, so O is seldom rescaled.
+//
+// 8-bit rows.  The products take the codes as they lie.  q becomes two e4m3
+// pieces of 4 bits under a power-of-two scale of its row, which is all of a
+// bf16 number above 2^-9 of the row's largest.  K's scales multiply S; V's
+// scales join the exponent, a = S 2^ek + ev, so that p' = p 2^ev is what the
+// product needs and p = p' 2^-ev is what the sum needs.  p' becomes two e5m2
+// pieces, together good to 2^-6 (0.25% in the mean square) over the range of a
+// half.
+#include "rows8_core.cuh"
+#include "tc.cuh"
+
+namespace bpkv {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;                       // tokens of a tile, rows of a stream
+constexpr int kPair = 2 * kTile;                 // rows of a prefix unit
+constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
+constexpr int kMaxPre = kMaxSeq + kMaxSeq * BPKV_MAX_GROUP / kPair;  // prefix items: one more per 256 rows
+constexpr int kMaxItems = kMaxPre + kMaxSeq;
+constexpr int kCtas = 152;                       // one per SM
+constexpr int kThreads = 384;
+constexpr int kRing16 = 32 * 1024;               // bytes of a stage: 128 rows of bf16
+constexpr int kRing8 = 16 * 1024;                // 128 rows of codes
+constexpr int kMaxStages = 10;
+constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
+constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
+
+// How far the maximum may pass m before O is rescaled, and where exp2's
+// results sit: bf16 P has float32's range; e5m2 pieces lie in 2^-16 .. 1.75 2^15.
+template <int BITS>
+struct Range {
+  static constexpr float kLazy = BITS == 16 ? 8.f : 4.f;
+  static constexpr float kShift = BITS == 16 ? 0.f : 11.f;
+};
+
+struct SharedArgs {
+  const int32_t* prefix_of;
+  const int64_t* plen;  // NULL: no prefixes
+  const int64_t* len;
+  int64_t pcap, cap;
+  int32_t n_prefix, n_seq, n_heads, group;
+  const uint16_t* q;
+  const uint8_t* exps[2][2];  // [prefix, own][K, V] scale exponents (8-bit rows)
+  int64_t* cum;               // plan for the join: tiles before each item
+  int4* seq_item;             // each sequence's first prefix item (-1: none), its rank among the prefix's, its rows
+  float* pre_o;               // [units + CTAs][2][128][D] partials of prefix units
+  float2* pre_ml;
+  float* own_o;  // [units + CTAs][2][G][D] partials of the sequences' own rows
+  float2* own_ml;
+  int32_t* status;
+  int32_t stages;
+};
+
+struct Maps {
+  CUtensorMap m[2][2];  // [prefix, own][K, V]
+};
+
+// What every CTA works out from the lengths.
+struct Plan {
+  int64_t cum[kMaxItems + 1];  // tiles before each item, for one KV head
+  uint16_t order[kMaxSeq];     // sequences by prefix
+  uint16_t rank[kMaxSeq];      // each sequence's place among its prefix's
+  int16_t pof[kMaxSeq];        // prefix of each sequence, -1: none
+  uint16_t cnt[kMaxSeq];       // sequences of each prefix
+  uint16_t first[kMaxSeq];     // where they begin in order
+  uint16_t item0[kMaxSeq];     // first item of each prefix
+  uint16_t it_p[kMaxPre];      // prefix of each prefix item
+  int32_t n_pre;               // prefix items
+};
+
+template <int BITS>
+struct Scales {};
+
+template <>
+struct Scales<8> {
+  float qf[2][2][kTile];  // scales of the rows of q, by segment parity and stream
+  __align__(16) float tok[2][2][3][kTile];  // by stream, twice: 2^ek log2(e)/sqrt(D), ev, 2^-ev of a tile's tokens
+};
+
+template <int BITS>
+struct Smem {
+  Scales<BITS> sc;
+  Plan plan;
+  uint32_t tmem;
+  uint32_t abort;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full, q_empty, done;
+  uint64_t sc_go[2], sc_full[2][2], sc_empty[2][2];
+};
+
+__device__ __forceinline__ int64_t tiles_of(int64_t n, int64_t cap) {
+  return (max64(0, min64(n, cap)) + kTile - 1) / kTile;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__device__ void make_plan(const SharedArgs& a, Plan& p) {
+  const int tid = threadIdx.x;
+  const int P = a.plen ? a.n_prefix : 0, N = a.n_seq;
+  for (int i = tid; i < N; i += kThreads) {
+    const int x = a.prefix_of ? a.prefix_of[i] : 0;
+    p.pof[i] = (int16_t)(x >= 0 && x < P ? x : -1);
+  }
+  for (int i = tid; i < P; i += kThreads) p.cnt[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < N; i += kThreads) {
+    const int x = p.pof[i];
+    int rank = 0, cnt = 0;
+    for (int j = 0; j < N; ++j) {
+      const bool same = p.pof[j] == x;
+      cnt += same;
+      rank += same && j < i;
+    }
+    if (x >= 0) p.cnt[x] = (uint16_t)cnt;
+    p.rank[i] = (uint16_t)rank;
+  }
+  __syncthreads();
+  const int lane = tid & 31;
+  if (tid < 32) {
+    int at = 0, item = 0;
+    for (int b = 0; b < P; b += 32) {
+      const int x = b + lane;
+      const int c = x < P ? p.cnt[x] : 0;
+      const int it = x < P && c > 0 && a.plen[x] > 0 ? (c * a.group + kPair - 1) / kPair : 0;
+      const int sc = (int)warp_scan(c, lane), si = (int)warp_scan(it, lane);
+      if (x < P) {
+        p.first[x] = (uint16_t)(at + sc - c);
+        p.item0[x] = (uint16_t)(item + si - it);
+        for (int k = 0; k < it; ++k) p.it_p[item + si - it + k] = (uint16_t)x;
+      }
+      at += __shfl_sync(0xffffffffu, sc, 31);
+      item += __shfl_sync(0xffffffffu, si, 31);
+    }
+    __syncwarp();
+    if (lane == 0) p.n_pre = item;
+    int64_t sum = 0;
+    for (int b = 0; b < item + N; b += 32) {
+      const int x = b + lane;
+      int64_t t = 0;
+      if (x < item) t = tiles_of(a.plen[p.it_p[x]], a.pcap);
+      else if (x < item + N) t = tiles_of(a.len[x - item], a.cap);
+      const int64_t c = warp_scan(t, lane);
+      if (x < item + N) p.cum[x] = sum + c - t;
+      sum += __shfl_sync(0xffffffffu, c, 31);
+    }
+    if (lane == 0) p.cum[item + N] = sum;
+  }
+  __syncthreads();
+  for (int i = tid; i < N; i += kThreads) {
+    const int x = p.pof[i];
+    if (x >= 0) p.order[p.first[x] + p.rank[i]] = (uint16_t)i;
+  }
+  if (blockIdx.x == 0) {  // the join reads the plan from the workspace
+    for (int i = tid; i < N; i += kThreads) {
+      const int x = p.pof[i];
+      const bool has = x >= 0 && a.plen[x] > 0;
+      a.seq_item[i] = make_int4(has ? p.item0[x] : -1, p.rank[i], has ? p.cnt[x] * a.group : 0, 0);
+    }
+    for (int i = tid; i <= p.n_pre + N; i += kThreads) a.cum[i + 1] = p.cum[i];
+    if (tid == 0) a.cum[0] = p.n_pre;
+  }
+  __syncthreads();
+}
+
+// CTA c of n takes tiles [c T / n, (c + 1) T / n) of the list of T.
+struct Share {
+  int64_t total;
+  int64_t n;  // CTAs that take part: no more than tiles
+  __device__ Share(int64_t t, int64_t ctas) : total(t), n(min64(t, ctas)) {}
+  __device__ int64_t lo(int64_t c) const { return c * total / n; }
+  __device__ int64_t owner(int64_t tile) const { return ((tile + 1) * n - 1) / total; }
+};
+
+// One CTA's part of a unit.
+struct Segment {
+  bool pre;       // of a prefix
+  int32_t index;  // sequence, or prefix
+  int32_t h;      // KV head
+  int32_t rows;   // query rows of the unit
+  int32_t row0;   // prefix: the unit's first row among the prefix's
+  bool dual;      // both streams take every tile
+  int64_t unit;   // counted within its kind
+  int64_t tile0;  // first tile
+  int32_t tiles;
+  int64_t tokens;  // of the whole unit
+  __device__ int steps() const { return dual ? 2 * tiles : tiles; }
+  __device__ int steps_of(int s) const { return dual ? tiles : (tiles + 1 - s) / 2; }
+  __device__ int tile_of(int s, int j) const { return dual ? j : 2 * j + s; }
+  __device__ int rows_of(int s) const { return dual ? (s ? rows - kTile : kTile) : rows; }
+  // tokens of the segment's tile t that exist
+  __device__ int valid(int t) const { return (int)min64(kTile, tokens - (tile0 + t) * kTile); }
+};
+
+// Walks the segments of one CTA; every role of the CTA walks alike.
+struct Walk {
+  const Plan& p;
+  const SharedArgs& a;
+  int64_t pos, end;
+  int item;
+  __device__ Walk(const Plan& plan, const SharedArgs& args) : p(plan), a(args) {
+    const int items = p.n_pre + a.n_seq;
+    const int64_t total = p.cum[items] * a.n_heads;
+    const Share share(total, gridDim.x);
+    pos = end = 0;
+    item = 0;
+    if ((int64_t)blockIdx.x >= share.n) return;
+    pos = share.lo(blockIdx.x);
+    end = share.lo(blockIdx.x + 1);
+    int lo = 0, hi = items - 1;  // the last item that begins at or before pos
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (p.cum[mid] * a.n_heads <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    item = lo;
+  }
+  __device__ bool next(Segment& s) {
+    if (pos >= end) return false;
+    while (p.cum[item + 1] * a.n_heads <= pos) ++item;
+    const int64_t tiles = p.cum[item + 1] - p.cum[item];
+    const int64_t off = pos - p.cum[item] * a.n_heads;
+    s.h = (int)(off / tiles);
+    s.tile0 = off - s.h * tiles;
+    s.tiles = (int)min64(min64(tiles - s.tile0, end - pos), 1 << 30);
+    s.pre = item < p.n_pre;
+    if (s.pre) {
+      s.index = p.it_p[item];
+      s.row0 = (item - p.item0[s.index]) * kPair;
+      s.rows = min(kPair, p.cnt[s.index] * a.group - s.row0);
+      s.tokens = min64(a.plen[s.index], a.pcap);
+      s.unit = (int64_t)item * a.n_heads + s.h;
+    } else {
+      s.index = item - p.n_pre;
+      s.row0 = 0;
+      s.rows = a.group;
+      s.tokens = min64(a.len[s.index], a.cap);
+      s.unit = (int64_t)s.index * a.n_heads + s.h;
+    }
+    s.dual = s.rows > kTile;
+    pos += s.tiles;
+    return true;
+  }
+};
+
+// ---- shared memory: Smem, then 1024-byte aligned the rows of q, then the ring
+
+template <int BITS>
+struct Shape {
+  static constexpr int kQ = kTile * kD * 2;                       // one stream's rows of q (16 bits, or two 8-bit pieces)
+  static constexpr int kStage = BITS == 16 ? kRing16 : kRing8;    // K or V tile
+  static constexpr int kExps = BITS == 16 ? 0 : 2 * kTile;        // exponent bytes that come with V
+  static constexpr int kSmemMax = 227 * 1024;
+  static constexpr int kBase = (sizeof(Smem<BITS>) + 1023) / 1024 * 1024 + 1024;
+  static constexpr int stages(bool dual) {
+    const int n = (kSmemMax - kBase - (dual ? 2 : 1) * kQ) / (kStage + kExps);
+    return n < kMaxStages ? n : kMaxStages;
+  }
+  static int bytes(bool dual) { return kBase + (dual ? 2 : 1) * kQ + stages(dual) * (kStage + kExps); }
+};
+
+static_assert(Shape<16>::stages(true) >= 4 && Shape<8>::stages(true) >= 8, "two tiles of K and V at least");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes of row r, chunk c of a 128-byte-row tile in the 128-byte swizzle
+__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// The rows of q of one stream into shared memory, by its 128 threads.
+template <int BITS>
+__device__ __forceinline__ void load_q(const SharedArgs& a, const Plan& p, const Segment& g, int s, unsigned char* dst,
+                                       float* qf) {
+  const int t = threadIdx.x & 127, l16 = t & 15;
+  const int rows = g.rows_of(s), base = g.row0 + (g.dual ? s * kTile : 0);
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    const int r = r0 + t / 16;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const int x = base + r;
+      const int seq = g.pre ? p.order[p.first[g.index] + x / a.group] : g.index;
+      const int head = g.pre ? x % a.group : x;
+      w = *reinterpret_cast<const uint4*>(a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
+    }
+    if constexpr (BITS == 16) {
+      if (r < rows) *reinterpret_cast<uint4*>(dst + (l16 / 8) * (kTile * 128) + swz(r, l16 & 7)) = w;
+    } else {
+      // x 2^-e with the row's largest magnitude in 128 .. 256: hi to 4 bits, lo the 4 (with its sign) below
+      uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = max(m & 0xffffu, m >> 16);
+      const int e = max(-100, (int)(m >> 7) - 127 - 7);
+      const float f = exp2i(-e);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t h2[2], l2[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float x0 = __uint_as_float(ww[2 * i + j] << 16) * f;
+          const float x1 = __uint_as_float(ww[2 * i + j] & 0xffff0000u) * f;
+          h2[j] = e4m3x2(x0, x1);
+          const float2 y = __half22float2(half2_of_e4m3x2((uint16_t)h2[j]));
+          l2[j] = e4m3x2(x0 - y.x, x1 - y.y);
+        }
+        hi[i] = h2[0] | (h2[1] << 16);
+        lo[i] = l2[0] | (l2[1] << 16);
+      }
+      if (r < rows) {
+        const uint32_t at = swz(r, l16 >> 1) + (l16 & 1) * 8;
+        *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + kTile * 128 + at) = make_uint2(lo[0], lo[1]);
+        if (l16 == 0) qf[r] = exp2i(e);
+      }
+    }
+  }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_constant__ SharedArgs a,
+                                                               const __grid_constant__ Maps maps) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  Smem<BITS>& sm = *reinterpret_cast<Smem<BITS>*>(raw);
+  unsigned char* q_smem = raw + ((smem_u32(raw) + sizeof(Smem<BITS>) + 1023) / 1024 * 1024 - smem_u32(raw));
+  using S = Shape<BITS>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_stage = a.stages;
+  const bool any_dual = a.plen && a.n_seq * a.group > kTile;
+  unsigned char* ring = q_smem + (any_dual ? 2 : 1) * S::kQ;
+  unsigned char* ring_exps = ring + n_stage * S::kStage;  // [stage][K bytes, V bytes]
+  volatile uint32_t* abort = &sm.abort;
+
+  if (tid == 0) {
+    sm.abort = 0;
+    for (int i = 0; i < n_stage; ++i) {
+      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm.s_full[s]), 1);
+      mbar_init(smem_u32(&sm.p_ready[s]), 4);
+      mbar_init(smem_u32(&sm.o_done[s]), 1);
+      mbar_init(smem_u32(&sm.sc_go[s]), 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&sm.sc_full[s][b]), 1);
+        mbar_init(smem_u32(&sm.sc_empty[s][b]), 4);
+      }
+    }
+    mbar_init(smem_u32(&sm.q_full), 8);
+    mbar_init(smem_u32(&sm.q_empty), 1);
+    mbar_init(smem_u32(&sm.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_shared();
+  }
+  if (warp == 2) tmem_alloc(smem_u32(&sm.tmem), kTmemCols);
+  if (warp == 3 && lane < 4) prefetch_map(&maps.m[lane >> 1][lane & 1]);
+  fence_before();
+  pdl_enter();
+  make_plan(a, sm.plan);  // ends with a barrier of the CTA
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  Walk walk(sm.plan, a);
+  Segment g;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- loads: K then V of every tile
+      uint32_t stage = 0, phase = 0, issued = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        const CUtensorMap* km = &maps.m[g.pre ? 0 : 1][0];
+        const int64_t base = (int64_t)g.index * a.n_heads + g.h;
+        const int64_t cap = g.pre ? a.pcap : a.cap;
+        for (int t = 0; ok && t < g.tiles; ++t) {
+          const int64_t tok = (g.tile0 + t) * kTile;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && mbar_wait(smem_u32(&sm.empty[stage]), phase ^ 1, abort);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&sm.full[stage]);
+            const uint32_t dst = smem_u32(ring + stage * S::kStage);
+            mbar_expect_tx(bar, S::kStage + (kv ? S::kExps : 0));
+            if constexpr (BITS == 16) {
+              tma_load_4d(dst, km + kv, bar, 0, (int)tok, 0, (int)base);
+            } else {
+              tma_load_3d(dst, km + kv, bar, 0, (int)tok, (int)base);
+              if (kv) {
+                const uint32_t e = smem_u32(ring_exps + stage * S::kExps);
+                bulk_load(e, a.exps[g.pre ? 0 : 1][0] + base * cap + tok, kTile, bar);
+                bulk_load(e + kTile, a.exps[g.pre ? 0 : 1][1] + base * cap + tok, kTile, bar);
+              }
+            }
+            ++issued;
+            if (++stage == (uint32_t)n_stage) stage = 0, phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {  // the copies in flight must land before the CTA's shared memory is given up
+        uint32_t never = 0;
+        for (uint32_t k = issued > (uint32_t)n_stage ? issued - n_stage : 0; k < issued; ++k)
+          mbar_wait(smem_u32(&sm.full[k % n_stage]), (k / n_stage) & 1, &never);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- products.  Step i of a segment is stream i & 1; S of step i is
+      // issued before O of step i - 1, so the tensor cores work while the
+      // other stream's softmax runs.  Products run in the order issued: S(i)
+      // overwrites P(i - 2) only after O(i - 2) has read it.
+      constexpr uint32_t kDescS = BITS == 16 ? mma_desc(1, 1, 0, kTile, kTile) : mma_desc(0, 0, 0, kTile, kTile);
+      constexpr uint32_t kDescO = BITS == 16 ? mma_desc(1, 1, 1, kTile, kD) : mma_desc(1, 0, 1, kTile, kD);
+      uint32_t tile_no = 0;  // tiles before this segment
+      uint32_t seg = 0, p_phase = 0;
+      bool ok = true;
+      auto stage_of = [&](uint32_t use, uint32_t& ph) {
+        ph = (use / n_stage) & 1;
+        return use % n_stage;
+      };
+      while (ok && walk.next(g)) {
+        ok = mbar_wait(smem_u32(&sm.q_full), seg & 1, abort);
+        if (!ok) break;
+        const int steps = g.steps();
+        for (int i = 0; ok && i <= steps; ++i) {
+          if (i < steps) {
+            const int s = i & 1;
+            uint32_t ph;
+            const uint32_t st = stage_of(2 * (tile_no + (g.dual ? i >> 1 : i)), ph);
+            ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort);
+            if (!ok) break;
+            fence_after();
+            const uint32_t kb = smem_u32(ring + st * S::kStage);
+            const uint32_t qb = smem_u32(q_smem + (g.dual ? s : 0) * S::kQ);
+            const uint32_t d = tmem + s * kTile;
+            if constexpr (BITS == 16) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t o = (k / 4) * (kTile * 128) + (k % 4) * 32;
+                mma16_ss(d, smem_desc(qb + o, 16, 1024), smem_desc(kb + o, 16, 1024), kDescS, k > 0);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // both pieces of q against the same codes
+                mma8_ss(d, smem_desc(qb + (k / 4) * (kTile * 128) + (k % 4) * 32, 16, 1024),
+                        smem_desc(kb + (k % 4) * 32, 16, 1024), kDescS, k > 0);
+            }
+            mma_commit(smem_u32(&sm.s_full[s]));
+            if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
+            if (i == steps - 1) mma_commit(smem_u32(&sm.q_empty));
+          }
+          if (i > 0) {
+            const int j = i - 1, s = j & 1;
+            uint32_t ph;
+            const uint32_t st = stage_of(2 * (tile_no + (g.dual ? j >> 1 : j)) + 1, ph);
+            ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort) &&
+                 mbar_wait(smem_u32(&sm.p_ready[s]), (p_phase >> s) & 1, abort);
+            if (!ok) break;
+            p_phase ^= 1u << s;
+            fence_after();
+            const uint32_t vb = smem_u32(ring + st * S::kStage);
+            const uint32_t p = tmem + s * kTile, d = tmem + 2 * kTile + s * kD;
+            const uint32_t acc = j >= 2;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (BITS == 16)
+                mma16_ts(d, p + k * 8, smem_desc(vb + k * 16 * 128, kTile * 128, 1024), kDescO, acc | (k > 0));
+              else  // four products of the high pieces, four of the low
+                mma8_ts(d, p + k * 8, smem_desc(vb + (k % 4) * 32 * 128, 16, 1024), kDescO, acc | (k > 0));
+            }
+            if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
+            if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
+          }
+        }
+        tile_no += g.tiles;
+        ++seg;
+      }
+      // every product is complete before tensor memory is given up
+      uint32_t never = 0;
+      mma_commit(smem_u32(&sm.done));
+      mbar_wait(smem_u32(&sm.done), 0, &never);
+    }
+  } else if (warp < 4) {
+    if constexpr (BITS == 8) {
+      // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
+      // segment when the stream does: further ahead, a stage's phase bit would
+      // be that of an earlier fill.
+      const int s = warp - 2;
+      uint32_t tile_no = 0, n = 0, go = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        const int steps = g.steps_of(s);
+        if (steps > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_go[s]), go, abort));
+          if (!ok) break;
+          go ^= 1;
+        }
+        for (int j = 0; j < steps; ++j, ++n) {
+          const int t = g.tile_of(s, j), b = n & 1;
+          const uint32_t use = 2 * (tile_no + t) + 1, st = use % n_stage;
+          ok = mbar_wait(smem_u32(&sm.sc_empty[s][b]), ((n >> 1) & 1) ^ 1, abort) &&
+               mbar_wait(smem_u32(&sm.full[st]), (use / n_stage) & 1, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t* e = reinterpret_cast<const uint32_t*>(ring_exps + st * S::kExps);
+          const uint32_t ke = e[lane], ve = e[kTile / 4 + lane];
+          const int valid = g.valid(t) - lane * 4;
+          float kf[4], ev[4], iv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = min(max((int)((ke >> (8 * i)) & 0xff) - kExpBias, kExpMin), kExpMax);
+            const int v = min(max((int)((ve >> (8 * i)) & 0xff) - kExpBias, kExpMin), kExpMax);
+            kf[i] = i < valid ? exp2i(k) * kLogScale : 0.f;
+            ev[i] = i < valid ? (float)v : 0.f;
+            iv[i] = i < valid ? exp2i(-v) : 0.f;
+          }
+          *reinterpret_cast<float4*>(&sm.sc.tok[s][b][0][lane * 4]) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+          *reinterpret_cast<float4*>(&sm.sc.tok[s][b][1][lane * 4]) = make_float4(ev[0], ev[1], ev[2], ev[3]);
+          *reinterpret_cast<float4*>(&sm.sc.tok[s][b][2][lane * 4]) = make_float4(iv[0], iv[1], iv[2], iv[3]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[s][b]));
+        }
+        tile_no += g.tiles;
+      }
+    }
+  } else {
+    // ---- softmax of stream s, a thread per row
+    const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
+    uint32_t tile_no = 0, seg = 0, s_phase = 0, o_phase = 0, n = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      if (seg > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_empty), (seg - 1) & 1, abort));
+        if (!ok) break;
+      }
+      if (g.dual || s == 0) {
+        float* qf = nullptr;
+        if constexpr (BITS == 8) qf = sm.sc.qf[seg & 1][g.dual ? s : 0];
+        load_q<BITS>(a, sm.plan, g, s, q_smem + (g.dual ? s : 0) * S::kQ, qf);
+        fence_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+      // also keeps a stream without a tile here from arriving for the next segment early
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_full), seg & 1, abort));
+      if (!ok) break;
+      float qf = 1.f;
+      if constexpr (BITS == 8) qf = sm.sc.qf[seg & 1][g.dual ? s : 0][row];
+      const int rows = g.rows_of(s), steps = g.steps_of(s);
+      if (BITS == 8 && steps > 0 && lane == 0) mbar_arrive(smem_u32(&sm.sc_go[s]));
+      const bool active = w4 * 32 < rows;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < steps; ++j, ++n) {
+        const int t = g.tile_of(s, j), valid = g.valid(t), b = n & 1;
+        ok = mbar_wait(smem_u32(&sm.s_full[s]), s_phase, abort);
+        if (BITS == 8) ok = ok && mbar_wait(smem_u32(&sm.sc_full[s][b]), (n >> 1) & 1, abort);
+        if (valid < kTile && (!g.dual || s == 0)) {
+          // rows of V past the last token may hold anything: zeros, so that 0 x does not become NaN
+          const uint32_t use = 2 * (tile_no + t) + 1, st = use % n_stage;
+          ok = ok && mbar_wait(smem_u32(&sm.full[st]), (use / n_stage) & 1, abort);
+          if (ok) {
+            constexpr int kChunks = BITS == 16 ? 16 : 8;  // 16-byte pieces of a row
+            for (int x = row; x < (kTile - valid) * kChunks; x += kTile) {
+              const int r = valid + x / kChunks, c = x % kChunks;
+              *reinterpret_cast<uint4*>(ring + st * S::kStage + (c / 8) * (kTile * 128) + r * 128 + (c % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_phase ^= 1;
+        if (active) {
+          fence_after();
+          uint32_t x[kTile];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld32(ts + k * 32, x + k * 32);
+          wait_ld();
+          if constexpr (BITS == 8) {
+#pragma unroll
+            for (int k = 0; k < kTile; k += 4) {
+              const float4 kf = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][0][k]);
+              const float4 ev = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][1][k]);
+              x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]) * kf.x, qf, ev.x));
+              x[k + 1] = __float_as_uint(fmaf(__uint_as_float(x[k + 1]) * kf.y, qf, ev.y));
+              x[k + 2] = __float_as_uint(fmaf(__uint_as_float(x[k + 2]) * kf.z, qf, ev.z));
+              x[k + 3] = __float_as_uint(fmaf(__uint_as_float(x[k + 3]) * kf.w, qf, ev.w));
+            }
+          }
+          if (valid < kTile) {
+#pragma unroll
+            for (int k = 0; k < kTile; ++k)
+              if (k >= valid) x[k] = 0xff800000u;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
+          constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
+          if (j == 0) {
+            m = mx;
+          } else {
+            const bool up = mx > m + Range<BITS>::kLazy / kUnit;
+            if (__any_sync(0xffffffffu, up)) {
+              // S of this step is complete, so O of the step before it is too
+              const float f = up ? ex2((m - mx) * kUnit) : 1.f;
+              l *= f;
+              if (up) m = mx;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t o[32];
+                tmem_ld32(to + k * 32, o);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(to + k * 32, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
+          if constexpr (BITS == 16) {
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float p0 = ex2(fmaf(__uint_as_float(x[k * 32 + 2 * i]), kUnit, -base));
+                const float p1 = ex2(fmaf(__uint_as_float(x[k * 32 + 2 * i + 1]), kUnit, -base));
+                ls[(2 * i) & 3] += p0;
+                ls[(2 * i + 1) & 3] += p1;
+                const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                p[i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              tmem_st16(ts + k * 16, p);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          } else {
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t hi[8], lo[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 iv = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][2][k * 32 + i * 4]);
+                float p[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) p[c] = ex2(__uint_as_float(x[k * 32 + i * 4 + c]) - base);
+                ls[0] = fmaf(p[0], iv.x, ls[0]);
+                ls[1] = fmaf(p[1], iv.y, ls[1]);
+                ls[2] = fmaf(p[2], iv.z, ls[2]);
+                ls[3] = fmaf(p[3], iv.w, ls[3]);
+                // the upper byte of a half is the e5m2 number below it: adding
+                // half a step first rounds (p is positive, the rest has a sign)
+                uint32_t h[2], r[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const __half2 v = __floats2half2_rn(p[2 * c], p[2 * c + 1]);
+                  h[c] = (*reinterpret_cast<const uint32_t*>(&v) + 0x00800080u) & 0xff00ff00u;
+                  const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&h[c]));
+                  r[c] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
+                }
+                hi[i] = __byte_perm(h[0], h[1], 0x7531);
+                lo[i] = __byte_perm(r[0], r[1], 0x7531);
+              }
+              tmem_st8(ts + k * 8, hi);
+              tmem_st8(ts + 32 + k * 8, lo);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          }
+          wait_st();
+          fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.p_ready[s]));
+          if (BITS == 8) mbar_arrive(smem_u32(&sm.sc_empty[s][b]));
+        }
+      }
+      if (!ok) break;
+      if (steps > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.o_done[s]), o_phase, abort));
+        if (!ok) break;
+        o_phase ^= 1;
+      }
+      if (active) {
+        fence_after();
+        const int64_t slot = (g.unit + blockIdx.x) * 2 + s;
+        float* po = g.pre ? a.pre_o + (slot * kTile + row) * kD : a.own_o + (slot * a.group + row) * kD;
+        if (steps > 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tmem_ld32(to + k * 32, o);
+            wait_ld();
+            if (row < rows) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(po + k * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+          }
+        }
+        if (row < rows) {
+          float2* pm = g.pre ? a.pre_ml + slot * kTile + row : a.own_ml + slot * a.group + row;
+          *pm = make_float2(m * (BITS == 16 ? kLogScale : 1.f), l);
+        }
+        fence_before();
+      }
+      tile_no += g.tiles;
+      ++seg;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (tid == 0 && sm.abort) set_status(a.status, BPKV_DEV_TIMEOUT);
+  if (warp == 2) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l, a CTA per query row
+
+constexpr int kMaxParts = 4 * (kCtas + 1);
+
+__global__ void __launch_bounds__(kD) k_shared_join(const __grid_constant__ SharedArgs a, int32_t ctas, uint16_t* out) {
+  pdl_enter();
+  __shared__ float s_w[kMaxParts], s_l[kMaxParts], s_red[kD / 32];
+  const int64_t r = blockIdx.x;
+  const int g = (int)(r % a.group);
+  const int64_t u = r / a.group;  // sequence and KV head
+  const int h = (int)(u % a.n_heads), i = (int)(u / a.n_heads);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t* cum = a.cum + 1;
+  const int n_pre = (int)a.cum[0];
+  const Share share(cum[n_pre + a.n_seq] * a.n_heads, ctas);
+  // the row's parts: of its prefix (one stream's, or both), then of its own rows
+  int64_t pre0 = 0, own0 = 0;  // first slot times 2, plus the stream
+  int pre_n = 0, own_n = 0, pre_step = 1, pre_row = 0;
+  const int4 si = a.seq_item[i];
+  if (si.x >= 0) {
+    const int64_t row = (int64_t)si.y * a.group + g;
+    const int item = si.x + (int)(row / kPair);
+    const int64_t tiles = cum[item + 1] - cum[item], at = cum[item] * a.n_heads + h * tiles;
+    const int64_t c0 = share.owner(at), c1 = share.owner(at + tiles - 1);
+    const int in = (int)(row % kPair);
+    const bool dual = si.z - (item - si.x) * kPair > kTile;  // each stream has its own rows
+    pre0 = ((int64_t)item * a.n_heads + h + c0) * 2 + (dual ? in / kTile : 0);
+    pre_step = dual ? 2 : 1;
+    pre_n = (int)(c1 - c0 + 1) * (dual ? 1 : 2);
+    pre_row = in % kTile;
+  }
+  {
+    const int item = n_pre + i;
+    const int64_t tiles = cum[item + 1] - cum[item], at = cum[item] * a.n_heads + h * tiles;
+    if (tiles > 0) {
+      const int64_t c0 = share.owner(at), c1 = share.owner(at + tiles - 1);
+      own0 = (u + c0) * 2;
+      own_n = (int)(c1 - c0 + 1) * 2;
+    }
+  }
+  const int n = pre_n + own_n;
+  float M = -INFINITY;
+  for (int k = tid; k < n; k += kD) {
+    const float2 ml = k < pre_n ? a.pre_ml[(pre0 + (int64_t)k * pre_step) * kTile + pre_row]
+                                : a.own_ml[(own0 + k - pre_n) * a.group + g];
+    s_w[k] = ml.y == 0.f ? -INFINITY : fmaxf(ml.x, -3e38f);  // no tokens; a sum that is NaN stays one
+    s_l[k] = ml.y;
+    M = fmaxf(M, s_w[k]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kD / 32; ++w) M = fmaxf(M, s_red[w]);
+  float L = 0.f, O = 0.f;
+  for (int k = 0; k < n; ++k) {
+    if (s_w[k] == -INFINITY) continue;  // a part without tokens: its o is not written
+    const float w = ex2(s_w[k] - M);
+    const float* o = k < pre_n ? a.pre_o + ((pre0 + (int64_t)k * pre_step) * kTile + pre_row) * kD
+                               : a.own_o + ((own0 + k - pre_n) * a.group + g) * kD;
+    L = fmaf(w, s_l[k], L);
+    O = fmaf(w, o[tid], O);
+  }
+  out[r * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(L == 0.f ? 0.f : O / L));
+}
+
+// ---- host side
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Space {
+  size_t cum, seq_item, pre_o, pre_ml, own_o, own_ml, total;
+};
+
+Space space(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
+  Space s;
+  size_t off = 256;  // status word
+  s.cum = off;
+  off = up256(off + (kMaxItems + 2) * sizeof(int64_t));
+  s.seq_item = off;
+  off = up256(off + n_seq * sizeof(int4));
+  // a segment is unit u's part in CTA c, slot u + c of its kind
+  const size_t pre = n_prefix ? (min64(n_prefix, n_seq) + n_seq * group / kPair) * n_heads + kCtas : 0;
+  const size_t own = n_seq * n_heads + kCtas;
+  s.pre_o = off;
+  off = up256(off + pre * kPair * kD * sizeof(float));
+  s.pre_ml = off;
+  off = up256(off + pre * kPair * sizeof(float2));
+  s.own_o = off;
+  off = up256(off + own * 2 * group * kD * sizeof(float));
+  s.own_ml = off;
+  off = up256(off + own * 2 * group * sizeof(float2));
+  s.total = off;
+  return s;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return f;
+}
+
+// Rows [units][cap][D] as tiles of 128 rows in 128-byte swizzled rows.
+template <int BITS>
+bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  if constexpr (BITS == 16) {  // two halves of 64 channels
+    const cuuint64_t dim[4] = {64, (cuuint64_t)cap, 2, (cuuint64_t)units};
+    const cuuint64_t stride[3] = {kD * 2, 128, (cuuint64_t)cap * kD * 2};
+    const cuuint32_t box[4] = {64, kTile, 2, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), dim, stride, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dim[3] = {kD, (cuuint64_t)cap, (cuuint64_t)units};
+  const cuuint64_t stride[2] = {kD, (cuuint64_t)cap * kD};
+  const cuuint32_t box[3] = {kD, kTile, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(rows), dim, stride, box, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One side's rows: K and V (with their exponents for 8-bit rows).
+struct Side {
+  const void* rows[2];
+  const uint8_t* exps[2];
+  const int64_t* len;
+  int64_t cap, n_max;
+  int32_t n;
+};
+
+template <int BITS>
+cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of, int32_t n_heads, int32_t group,
+                   const uint16_t* q, uint16_t* out, void* ws, cudaStream_t st) {
+  const Space sp = space(own.n, prefix ? prefix->n : 0, n_heads, group);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  Maps maps;
+  const Side* sides[2] = {prefix ? prefix : &own, &own};
+  SharedArgs a = {};
+  for (int i = 0; i < 2; ++i)
+    for (int kv = 0; kv < 2; ++kv) {
+      if (!make_map<BITS>(&maps.m[i][kv], sides[i]->rows[kv], (int64_t)sides[i]->n * n_heads, sides[i]->cap))
+        return cudaErrorInvalidValue;
+      a.exps[i][kv] = sides[i]->exps[kv];
+    }
+  a.prefix_of = prefix_of;
+  a.plen = prefix ? prefix->len : nullptr;
+  a.len = own.len;
+  a.pcap = prefix ? prefix->cap : 0;
+  a.cap = own.cap;
+  a.n_prefix = prefix ? prefix->n : 0;
+  a.n_seq = own.n;
+  a.n_heads = n_heads;
+  a.group = group;
+  a.q = q;
+  a.cum = reinterpret_cast<int64_t*>(w + sp.cum);
+  a.seq_item = reinterpret_cast<int4*>(w + sp.seq_item);
+  a.pre_o = reinterpret_cast<float*>(w + sp.pre_o);
+  a.pre_ml = reinterpret_cast<float2*>(w + sp.pre_ml);
+  a.own_o = reinterpret_cast<float*>(w + sp.own_o);
+  a.own_ml = reinterpret_cast<float2*>(w + sp.own_ml);
+  a.status = static_cast<int32_t*>(ws);
+  const bool dual = prefix && own.n * group > kTile;
+  a.stages = Shape<BITS>::stages(dual);
+  const int smem = Shape<BITS>::bytes(dual);
+  cudaError_t e = cudaFuncSetAttribute(k_shared_attend<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Shape<BITS>::kSmemMax);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than tiles, as far as the host knows
+  const int64_t most = n_heads * ((own.n_max + kTile - 1) / kTile * own.n +
+                                  (prefix ? (prefix->n_max + kTile - 1) / kTile *
+                                                (min64(prefix->n, own.n) + (int64_t)own.n * group / kPair)
+                                          : 0));
+  const int ctas = (int)max64(1, min64(kCtas, most));
+  e = launch_pdl(k_shared_attend<BITS>, dim3(ctas), dim3(kThreads), (size_t)smem, st, a, maps);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_shared_join, dim3((unsigned)((int64_t)own.n * n_heads * group)), dim3(kD), 0, st, a,
+                    (int32_t)ctas, out);
+}
+
+}  // namespace
+
+size_t shared_bytes(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
+  return space(n_seq, n_prefix, n_heads, group).total;
+}
+
+cudaError_t launch_shared(const bpkv_cache* p, const int32_t* prefix_of, const bpkv_cache& c, const uint16_t* q,
+                          uint16_t* out, void* ws, cudaStream_t st) {
+  Side side[2];
+  const bpkv_cache* cs[2] = {p, &c};
+  for (int i = 0; i < 2; ++i)
+    if (cs[i])
+      side[i] = {{cs[i]->k_rows, cs[i]->v_rows}, {nullptr, nullptr}, cs[i]->seq_len, cs[i]->cap_tokens, cs[i]->n_max,
+                 cs[i]->n_seq};
+  return launch<16>(p ? &side[0] : nullptr, side[1], prefix_of, c.n_kv_heads, c.group, q, out, ws, st);
+}
+
+cudaError_t launch_shared8(const bpkv_rows8* p, const int32_t* prefix_of, const bpkv_rows8& c, const uint16_t* q,
+                           uint16_t* out, void* ws, cudaStream_t st) {
+  Side side[2];
+  const bpkv_rows8* cs[2] = {p, &c};
+  for (int i = 0; i < 2; ++i)
+    if (cs[i])
+      side[i] = {{cs[i]->k8, cs[i]->v8}, {cs[i]->kexp, cs[i]->vexp}, cs[i]->seq_len, cs[i]->cap_tokens, cs[i]->n_max,
+                 cs[i]->n_seq};
+  return launch<8>(p ? &side[0] : nullptr, side[1], prefix_of, c.n_kv_heads, c.group, q, out, ws, st);
+}
+
+}  // namespace bpkv

@@ -360,6 +360,137 @@ int bpkv_sparse_attend_vdepth(const bpkv_cache *c, const float *q, const int32_t
 int bpkv_dense_attend(const bpkv_cache *c, const float *q, float *out, void *ws, size_t ws_bytes,
                       void *stream);
 
+/* ------------------------------------------------------------- 8-bit rows */
+/*
+ * A cache of 8-bit K and V rows: 258 bytes per token and KV head instead of
+ * the 512 of the bf16 rows.  Layouts (row-major, last index fastest):
+ *   k8, v8      uint8 [N][H][cap][D]  e4m3 codes (4 exponent, 3 mantissa bits)
+ *   kexp, vexp  uint8 [N][H][cap]     the row's scale 2^(byte - 127)
+ *   seq_len     int64 [N]             device memory: tokens stored per sequence
+ * A row's scale is the smallest power of two 2^e with max_j |x_j| <= 448 2^e
+ * (448: the largest e4m3 value), e held to -48..32 (-48 for a row of zeros); its
+ * codes are x_j 2^-e rounded to nearest even, saturated at 448 (reached only
+ * above 448 2^32).  Scaling by a power of two is exact, so the code's rounding
+ * (relative 2^-4 at most, absolute 2^(e-10) below 2^(e-6)) is the only one,
+ * and a code times its scale is exactly a bf16 number.  Exponent bytes outside
+ * 79..159 are never written and are read as the nearest of these.  A row with
+ * an infinity or NaN keeps NaN where it had NaN; its other codes say nothing.
+ * All arrays are device memory; k8, v8, kexp and vexp start on 16-byte
+ * boundaries; cap_tokens is a multiple of 512; group is used by the attention.
+ * n_max is host state, an upper bound of every seq_len[i]; the appending calls
+ * raise it.
+ */
+typedef struct bpkv_rows8 {
+  int32_t n_seq;
+  int32_t n_kv_heads;
+  int32_t group;
+  int32_t head_dim;
+  int64_t cap_tokens;
+  int64_t n_max;
+  uint8_t *k8;
+  uint8_t *v8;
+  uint8_t *kexp;
+  uint8_t *vexp;
+  int64_t *seq_len;
+} bpkv_rows8;
+
+/*
+ * Quantise t_new tokens per sequence, k_new/v_new [N][H][t_new][D] bf16
+ * (device, 16-byte aligned), into rows p .. p + t_new - 1 of sequence i and
+ * set seq_len[i] = p + t_new, with p = seq_len[i] (start NULL) or p = start[i]
+ * (int64 [N], device: rows written before are overwritten, e.g. after drafted
+ * tokens were rejected).  A sequence whose rows would leave 0 .. cap_tokens
+ * keeps its rows and its length, and BPKV_DEV_OVERFLOW is set in *status
+ * (device, NULL to skip).  n_max becomes min(n_max + t_new, cap_tokens).
+ * With start given its values bound nothing on the host: raise n_max yourself
+ * when one is above n_max.
+ * BPKV_EINVAL when t_new < 1, t_new > cap_tokens, or (start NULL) n_max + t_new
+ * > cap_tokens.
+ */
+int bpkv_rows8_append(bpkv_rows8 *c, const uint16_t *k_new, const uint16_t *v_new, int32_t t_new,
+                      const int64_t *start, int32_t *status, void *stream);
+
+/*
+ * Read rows t0 .. t0 + n - 1 of every sequence back as bf16, k_out/v_out
+ * [N][H][n][D] (device, 16-byte aligned; either may be NULL): code times scale,
+ * which bf16 holds exactly.  Rows at or past seq_len[i] read as zeros.
+ * BPKV_EINVAL when t0 < 0, n < 1 or t0 + n > cap_tokens.
+ */
+int bpkv_rows8_read(const bpkv_rows8 *c, int64_t t0, int32_t n, uint16_t *k_out, uint16_t *v_out, void *stream);
+
+/* ------------------------------------------------------------- projected heads */
+#define BPKV_QKV_PAIRS 1   /* rotate neighbouring channels (2 i, 2 i + 1) instead of (i, i + rot_dim / 2) */
+#define BPKV_QKV_Q_BF16 2  /* q_out is bf16 (for bpkv_shared_attend), else float32 (for the scans) */
+
+typedef struct bpkv_qkv_args {
+  int32_t n_seq, n_kv_heads, group, head_dim;
+  int32_t t_new;            /* tokens per sequence */
+  int32_t rot_dim;          /* rotated channels: even, 0 .. D */
+  int32_t flags;            /* BPKV_QKV_* */
+  float eps;                /* of the norms, >= 0 */
+  const uint16_t *qkv;      /* bf16 [N][t_new][ld]: H G query heads, H key heads, H value heads of D */
+  int64_t ld;               /* elements from one token to the next: a multiple of 8, >= (G + 2) H D */
+  const int64_t *pos;       /* [N] device: position of each sequence's first token (NULL: rows8->seq_len) */
+  const float *inv_freq;    /* [rot_dim / 2] device: radians per position */
+  const float *q_weight;    /* [D] device, NULL: the query heads are not normed */
+  const float *k_weight;    /* [D] device, NULL: the key heads are not normed */
+  void *q_out;              /* [N][t_new][H][G][D] float32 or bf16 */
+  uint16_t *k_out;          /* [N][H][t_new][D] bf16, as bpkv_encode_append takes it (NULL to skip) */
+  uint16_t *v_out;          /* [N][H][t_new][D] bf16 (NULL to skip) */
+  bpkv_rows8 *rows8;        /* NULL, or the cache the keys and values are appended to at pos[i] */
+  int32_t *status;          /* device, NULL to skip: BPKV_DEV_OVERFLOW as bpkv_rows8_append sets it */
+} bpkv_qkv_args;
+
+/*
+ * From a layer's projections to what the caches and the attention take, in one
+ * pass over the heads: every query and key head is normed, y = x / sqrt(mean_j
+ * x_j^2 + eps) w_j (weight given; float32), its first rot_dim channels are
+ * rotated by the angle of the token's position p = pos[i] + t,
+ *   (y_a, y_b) -> (y_a cos u - y_b sin u, y_b cos u + y_a sin u), u = p inv_freq[i],
+ * with the product p inv_freq[i] taken exactly and reduced to a turn in 64-bit
+ * fixed point, and rounded once to its output type.  Values are copied.
+ * With rows8 the keys (as rounded to bf16) and values are quantised into rows
+ * pos[i] .. of that cache, exactly as bpkv_rows8_append does with start = pos;
+ * pos NULL or rows8->seq_len appends behind the stored tokens.  rows8 must have
+ * the same n_seq, n_kv_heads and head_dim.
+ * q_out, k_out, v_out and qkv are device memory on 16-byte boundaries and do
+ * not overlap.  BPKV_EINVAL for t_new < 1, an odd rot_dim or one outside
+ * 0 .. D, unknown flags, eps < 0, ld too small or not a multiple of 8, pos and
+ * rows8 both NULL, no inv_freq with rot_dim > 0, or as bpkv_rows8_append.
+ */
+int bpkv_qkv_rope(const bpkv_qkv_args *a, void *stream);
+
+/* ------------------------------------------------------------- shared prefixes */
+/*
+ * Decode attention of N sequences of which many share a long prefix: query
+ * head g of sequence i attends over rows 0 .. seq_len[p] - 1 of prefix p =
+ * prefix_of[i] and over its own rows 0 .. seq_len[i] - 1,
+ *   o = sum_x softmax_x(q . k_x / sqrt(D)) v_x over both sets together,
+ * zeros when both are empty.  A prefix is stored once, as one sequence of the
+ * cache `prefix`, and its rows are read once for all the query heads of all
+ * the sequences that share it (up to 256 at a time), on the tensor cores.
+ *   prefix     the P prefixes (NULL: none); same n_kv_heads and group as c
+ *   prefix_of  int32 [N] device; values outside 0 .. P - 1 mean no prefix.
+ *              NULL: every sequence has prefix 0
+ *   q          bf16 [N][H][G][D], out bf16 [N][H][G][D] (16-byte aligned)
+ * Logits, softmax statistics and sums are float32; the softmax weights enter
+ * the products as bf16 (bpkv_shared_attend) or as two 3-bit pieces
+ * (bpkv_shared_attend8, where q enters as two e4m3 pieces of 4 bits).  Rows past
+ * the lengths may hold anything.  Stored rows, q and logits must be finite.
+ * Device memory only: BPKV_EUNSUPPORTED for residency 1, and for more than
+ * BPKV_SHARED_MAX_SEQ sequences or prefixes.  Workspace:
+ * bpkv_shared_workspace_size bytes, 256-byte aligned, with nothing kept in it
+ * from call to call; its first 256 bytes hold the status word
+ * (BPKV_DEV_TIMEOUT when a wait inside the kernel gave up; clear it first).
+ */
+#define BPKV_SHARED_MAX_SEQ 512
+
+size_t bpkv_shared_workspace_size(int32_t n_seq, int32_t n_prefix, int32_t n_kv_heads, int32_t group);
+int bpkv_shared_attend(const bpkv_cache *prefix, const int32_t *prefix_of, const bpkv_cache *c, const uint16_t *q,
+                       uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, const bpkv_rows8 *c, const uint16_t *q,
+                        uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------- decode step */
 #define BPKV_DEPTH_WATERFILL 0  /* bpkv_alloc_depths with sigma2 and budget_q */
 #define BPKV_DEPTH_FIXED 1      /* bpkv_fixed_depths(fixed_channels, fixed_depth) */
