@@ -397,8 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
   Walk walk(sm.plan, a);
   Segment g;
 
+  if (warp < 4) {
+    // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
+    regs_fewer<80>();
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---- loads: K then V of every tile
       uint32_t stage = 0, phase = 0, issued = 0;
       bool ok = true;
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---- products.  Step i of a segment is stream i & 1; S of step i is
       // issued before O of step i - 1, so the tensor cores work while the
       // other stream's softmax runs.  Products run in the order issued: S(i)
@@ -463,20 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
             ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort);
             if (!ok) break;
             fence_after();
-            const uint32_t kb = smem_u32(ring + st * S::kStage);
-            const uint32_t qb = smem_u32(q_smem + (g.dual ? s : 0) * S::kQ);
+            const uint32_t kb = smem_desc(smem_u32(ring + st * S::kStage), 16);
+            const uint32_t qb = smem_desc(smem_u32(q_smem + (g.dual ? s : 0) * S::kQ), 16);
             const uint32_t d = tmem + s * kTile;
             if constexpr (BITS == 16) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const uint32_t o = (k / 4) * (kTile * 128) + (k % 4) * 32;
-                mma16_ss(d, smem_desc(qb + o, 16, 1024), smem_desc(kb + o, 16, 1024), kDescS, k > 0);
+                const uint32_t o = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+                mma16_ss(d, qb + o, kb + o, kDescS, k > 0);
               }
             } else {
 #pragma unroll
               for (int k = 0; k < 8; ++k)  // both pieces of q against the same codes
-                mma8_ss(d, smem_desc(qb + (k / 4) * (kTile * 128) + (k % 4) * 32, 16, 1024),
-                        smem_desc(kb + (k % 4) * 32, 16, 1024), kDescS, k > 0);
+                mma8_ss(d, qb + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4), kb + ((k % 4) * 32 >> 4), kDescS, k > 0);
             }
             mma_commit(smem_u32(&sm.s_full[s]));
             if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
@@ -491,15 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
             if (!ok) break;
             p_phase ^= 1u << s;
             fence_after();
-            const uint32_t vb = smem_u32(ring + st * S::kStage);
+            const uint32_t vb = smem_desc(smem_u32(ring + st * S::kStage), BITS == 16 ? kTile * 128 : 16);
             const uint32_t p = tmem + s * kTile, d = tmem + 2 * kTile + s * kD;
             const uint32_t acc = j >= 2;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               if (BITS == 16)
-                mma16_ts(d, p + k * 8, smem_desc(vb + k * 16 * 128, kTile * 128, 1024), kDescO, acc | (k > 0));
+                mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, acc | (k > 0));
               else  // four products of the high pieces, four of the low
-                mma8_ts(d, p + k * 8, smem_desc(vb + (k % 4) * 32 * 128, 16, 1024), kDescO, acc | (k > 0));
+                mma8_ts(d, p + k * 8, vb + ((k % 4) * 32 * 128 >> 4), kDescO, acc | (k > 0));
             }
             if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
             if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       mma_commit(smem_u32(&sm.done));
       mbar_wait(smem_u32(&sm.done), 0, &never);
     }
-  } else if (warp < 4) {
+  } else {
     if constexpr (BITS == 8) {
       // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
       // segment when the stream does: further ahead, a stage's phase bit would
@@ -556,8 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
         tile_no += g.tiles;
       }
     }
+  }
   } else {
     // ---- softmax of stream s, a thread per row
+    regs_more<208>();
     const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
@@ -608,83 +612,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
         s_phase ^= 1;
         if (active) {
           fence_after();
-          uint32_t x[kTile];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(ts + k * 32, x + k * 32);
+          float x[kTile];
+          uint32_t* xu = reinterpret_cast<uint32_t*>(x);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld32(ts, xu);
+          tmem_ld32(ts + 32, xu + 32);
           wait_ld();
-          if constexpr (BITS == 8) {
+          tmem_ld32(ts + 64, xu + 64);
+          tmem_ld32(ts + 96, xu + 96);
 #pragma unroll
-            for (int k = 0; k < kTile; k += 4) {
-              const float4 kf = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][0][k]);
-              const float4 ev = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][1][k]);
-              x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]) * kf.x, qf, ev.x));
-              x[k + 1] = __float_as_uint(fmaf(__uint_as_float(x[k + 1]) * kf.y, qf, ev.y));
-              x[k + 2] = __float_as_uint(fmaf(__uint_as_float(x[k + 2]) * kf.z, qf, ev.z));
-              x[k + 3] = __float_as_uint(fmaf(__uint_as_float(x[k + 3]) * kf.w, qf, ev.w));
+          for (int half = 0; half < 2; ++half) {
+            if (half) wait_ld();
+            if constexpr (BITS == 8) {
+#pragma unroll
+              for (int k = half * 64; k < half * 64 + 64; k += 4) {
+                const float4 kf = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][0][k]);
+                const float4 ev = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][1][k]);
+                const F2 q2(qf, qf);
+                fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
+                fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
+              }
             }
-          }
-          if (valid < kTile) {
+            if (valid < kTile) {
 #pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              if (k >= valid) x[k] = 0xff800000u;
-          }
-          float mx = -INFINITY;
+              for (int k = half * 64; k < half * 64 + 64; ++k)
+                if (k >= valid) x[k] = -INFINITY;
+            }
 #pragma unroll
-          for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
+            for (int k = half * 64; k < half * 64 + 64; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
+          }
+          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
           constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
           if (j == 0) {
-            m = mx;
+            m = top;
           } else {
-            const bool up = mx > m + Range<BITS>::kLazy / kUnit;
+            const bool up = top > m + Range<BITS>::kLazy / kUnit;
             if (__any_sync(0xffffffffu, up)) {
-              // S of this step is complete, so O of the step before it is too
-              const float f = up ? ex2((m - mx) * kUnit) : 1.f;
+              // S of this step is complete, so O of the stream's step before it is too
+              const float f = up ? ex2((m - top) * kUnit) : 1.f;
               l *= f;
-              if (up) m = mx;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t o[32];
-                tmem_ld32(to + k * 32, o);
+              if (up) m = top;
+#pragma unroll 1
+              for (int k = 0; k < kD; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + k, o);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(to + k * 32, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(to + k, o);
               }
             }
           }
           const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
-          if constexpr (BITS == 16) {
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const F2 base2(-base, -base), unit2(kUnit, kUnit);
+          F2 ls[4] = {F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kTile; k += 32) {
+            if constexpr (BITS == 16) {
               uint32_t p[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float p0 = ex2(fmaf(__uint_as_float(x[k * 32 + 2 * i]), kUnit, -base));
-                const float p1 = ex2(fmaf(__uint_as_float(x[k * 32 + 2 * i + 1]), kUnit, -base));
-                ls[(2 * i) & 3] += p0;
-                ls[(2 * i + 1) & 3] += p1;
+                float p0, p1;
+                fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                ls[i & 3] = add2(ls[i & 3], F2(p0, p1));
                 const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
                 p[i] = *reinterpret_cast<const uint32_t*>(&h);
               }
-              tmem_st16(ts + k * 16, p);
-            }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          } else {
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+              tmem_st16(ts + k / 2, p);
+            } else {
               uint32_t hi[8], lo[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 iv = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][2][k * 32 + i * 4]);
+                const float4 iv = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][2][k + i * 4]);
                 float p[4];
+                add2(F2(x[k + 4 * i], x[k + 4 * i + 1]), base2).get(p[0], p[1]);
+                add2(F2(x[k + 4 * i + 2], x[k + 4 * i + 3]), base2).get(p[2], p[3]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) p[c] = ex2(__uint_as_float(x[k * 32 + i * 4 + c]) - base);
-                ls[0] = fmaf(p[0], iv.x, ls[0]);
-                ls[1] = fmaf(p[1], iv.y, ls[1]);
-                ls[2] = fmaf(p[2], iv.z, ls[2]);
-                ls[3] = fmaf(p[3], iv.w, ls[3]);
+                for (int c = 0; c < 4; ++c) p[c] = ex2(p[c]);
+                ls[(2 * i) & 3] = fma2(F2(p[0], p[1]), F2(iv.x, iv.y), ls[(2 * i) & 3]);
+                ls[(2 * i + 1) & 3] = fma2(F2(p[2], p[3]), F2(iv.z, iv.w), ls[(2 * i + 1) & 3]);
                 // the upper byte of a half is the e5m2 number below it: adding
                 // half a step first rounds (p is positive, the rest has a sign)
                 uint32_t h[2], r[2];
@@ -698,11 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
                 hi[i] = __byte_perm(h[0], h[1], 0x7531);
                 lo[i] = __byte_perm(r[0], r[1], 0x7531);
               }
-              tmem_st8(ts + k * 8, hi);
-              tmem_st8(ts + 32 + k * 8, lo);
+              tmem_st8(ts + k / 4, hi);
+              tmem_st8(ts + 32 + k / 4, lo);
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           }
+          float l0, l1;
+          add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])).get(l0, l1);
+          l += l0 + l1;
           wait_st();
           fence_before();
         }
