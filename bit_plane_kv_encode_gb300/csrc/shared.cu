@@ -64,14 +64,22 @@ struct SharedArgs {
   int32_t n_prefix, n_seq, n_heads, group;
   const uint16_t* q;
   const uint8_t* exps[2][2];  // [prefix, own][K, V] scale exponents (8-bit rows)
-  int64_t* cum;               // plan for the join: tiles before each item
-  int4* seq_item;             // each sequence's first prefix item (-1: none), its rank among the prefix's, its rows
+  struct Parts* parts;        // [N][H][G] where each query row's partials are
   float* pre_o;               // [units + CTAs][2][128][D] partials of prefix units
   float2* pre_ml;
-  float* own_o;  // [units + CTAs][2][G][D] partials of the sequences' own rows
+  float* own_o;  // [units + CTAs][2][4][G][D] partials of the sequences' own rows
   float2* own_ml;
   int32_t* status;
   int32_t stages;
+};
+
+// A query row's partials (m, l and o), counted in rows of the two kinds: of each
+// of pre_n segments pre_sub, then of each of own_n segments 2 x 4.
+struct Parts {
+  int64_t pre, own;  // first
+  int32_t pre_n, own_n;
+  int32_t pre_sub;   // 1, or both streams' copies
+  int32_t pre_span;  // rows from one copy to the next
 };
 
 struct Maps {
@@ -181,15 +189,6 @@ __device__ void make_plan(const SharedArgs& a, Plan& p) {
     const int x = p.pof[i];
     if (x >= 0) p.order[p.first[x] + p.rank[i]] = (uint16_t)i;
   }
-  if (blockIdx.x == 0) {  // the join reads the plan from the workspace
-    for (int i = tid; i < N; i += kThreads) {
-      const int x = p.pof[i];
-      const bool has = x >= 0 && a.plen[x] > 0;
-      a.seq_item[i] = make_int4(has ? p.item0[x] : -1, p.rank[i], has ? p.cnt[x] * a.group : 0, 0);
-    }
-    for (int i = tid; i <= p.n_pre + N; i += kThreads) a.cum[i + 1] = p.cum[i];
-    if (tid == 0) a.cum[0] = p.n_pre;
-  }
   __syncthreads();
 }
 
@@ -201,6 +200,39 @@ struct Share {
   __device__ int64_t lo(int64_t c) const { return c * total / n; }
   __device__ int64_t owner(int64_t tile) const { return ((tile + 1) * n - 1) / total; }
 };
+
+// Copies of a unit's rows among the 128 of a stream.  With 64 rows or fewer
+// the copies' softmax threads share the tile's tokens, so that all four warps
+// work; each copy has its own m, l and o.
+__device__ __forceinline__ int copies_of(int rows) { return rows <= kTile / 4 ? 4 : rows <= kTile / 2 ? 2 : 1; }
+
+// Where the partials of query row r = (sequence, KV head, head of the group) will be.
+__device__ Parts parts_of(const SharedArgs& a, const Plan& p, const Share& share, int64_t r) {
+  const int g = (int)(r % a.group);
+  const int64_t u = r / a.group;
+  const int h = (int)(u % a.n_heads), i = (int)(u / a.n_heads);
+  Parts q = {};
+  const int x = p.pof[i];
+  if (x >= 0 && a.plen[x] > 0) {
+    const int row = p.rank[i] * a.group + g, item = p.item0[x] + row / kPair;
+    const int in = row % kPair, rows = min(kPair, p.cnt[x] * a.group - row + in);
+    const int64_t tiles = p.cum[item + 1] - p.cum[item], at = p.cum[item] * a.n_heads + h * tiles;
+    const int64_t c0 = share.owner(at);
+    const bool dual = rows > kTile;
+    q.pre_n = (int)(share.owner(at + tiles - 1) - c0) + 1;
+    q.pre = ((int64_t)item * a.n_heads + h + c0) * kPair + in;
+    q.pre_sub = dual ? 1 : 2 * copies_of(rows);
+    q.pre_span = kTile / copies_of(rows);
+  }
+  const int item = p.n_pre + i;
+  const int64_t tiles = p.cum[item + 1] - p.cum[item], at = p.cum[item] * a.n_heads + h * tiles;
+  if (tiles > 0) {
+    const int64_t c0 = share.owner(at);
+    q.own_n = (int)(share.owner(at + tiles - 1) - c0) + 1;
+    q.own = (u + c0) * 8 * a.group + g;
+  }
+  return q;
+}
 
 // One CTA's part of a unit.
 struct Segment {
@@ -218,6 +250,7 @@ struct Segment {
   __device__ int steps_of(int s) const { return dual ? tiles : (tiles + 1 - s) / 2; }
   __device__ int tile_of(int s, int j) const { return dual ? j : 2 * j + s; }
   __device__ int rows_of(int s) const { return dual ? (s ? rows - kTile : kTile) : rows; }
+  __device__ int copies() const { return dual ? 1 : copies_of(rows); }
   // tokens of the segment's tile t that exist
   __device__ int valid(int t) const { return (int)min64(kTile, tokens - (tile0 + t) * kTile); }
 };
@@ -306,17 +339,19 @@ __device__ __forceinline__ void load_q(const SharedArgs& a, const Plan& p, const
                                        float* qf) {
   const int t = threadIdx.x & 127, l16 = t & 15;
   const int rows = g.rows_of(s), base = g.row0 + (g.dual ? s * kTile : 0);
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    const int r = r0 + t / 16;
+  const int span = kTile / g.copies();
+  const int blocks = (rows + 7) / 8;  // of each copy
+  for (int b = 0; b < blocks * g.copies(); ++b) {
+    const int of = (b % blocks) * 8 + t / 16, r = b / blocks * span + of;
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const int x = base + r;
+    if (of < rows) {
+      const int x = base + of;
       const int seq = g.pre ? p.order[p.first[g.index] + x / a.group] : g.index;
       const int head = g.pre ? x % a.group : x;
       w = *reinterpret_cast<const uint4*>(a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
     }
     if constexpr (BITS == 16) {
-      if (r < rows) *reinterpret_cast<uint4*>(dst + (l16 / 8) * (kTile * 128) + swz(r, l16 & 7)) = w;
+      if (of < rows) *reinterpret_cast<uint4*>(dst + (l16 / 8) * (kTile * 128) + swz(r, l16 & 7)) = w;
     } else {
       // x 2^-e with the row's largest magnitude in 128 .. 256: hi to 4 bits, lo the 4 (with its sign) below
       uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
@@ -341,7 +376,7 @@ __device__ __forceinline__ void load_q(const SharedArgs& a, const Plan& p, const
         hi[i] = h2[0] | (h2[1] << 16);
         lo[i] = l2[0] | (l2[1] << 16);
       }
-      if (r < rows) {
+      if (of < rows) {
         const uint32_t at = swz(r, l16 >> 1) + (l16 & 1) * 8;
         *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(dst + kTile * 128 + at) = make_uint2(lo[0], lo[1]);
@@ -349,6 +384,131 @@ __device__ __forceinline__ void load_q(const SharedArgs& a, const Plan& p, const
       }
     }
   }
+}
+
+// One tile of one query row: S from tensor memory, this thread's columns
+// (32 NCH of them, the part-th) to weights over it, zeros to the others; m and
+// l of the row's columns so far, and O when m moves.
+template <int BITS, int NCH>
+__device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int part, int valid, bool first, float qf,
+                                             const float* scales, float& m, float& l) {
+  constexpr int kCols = 32 * NCH, kHalves = NCH == 4 ? 2 : 1;
+  const int c0 = part * kCols;
+            float x[kCols];
+            uint32_t* xu = reinterpret_cast<uint32_t*>(x);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < kCols; k += 32) {
+    tmem_ld32(ts + c0 + k, xu + k);
+    if (NCH == 4 && k == 32) wait_ld();  // the first half is looked at while the second comes
+  }
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) {
+    if (half || NCH < 4) wait_ld();
+    constexpr int kPer = kCols / kHalves;
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int k = half * kPer; k < (half + 1) * kPer; k += 4) {
+        const float4 kf = *reinterpret_cast<const float4*>(scales + c0 + k);
+        const float4 ev = *reinterpret_cast<const float4*>(scales + kTile + c0 + k);
+        const F2 q2(qf, qf);
+        fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
+        fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
+      }
+    }
+    if (valid < c0 + kCols) {
+#pragma unroll
+      for (int k = half * kPer; k < (half + 1) * kPer; ++k)
+        if (c0 + k >= valid) x[k] = -INFINITY;
+    }
+#pragma unroll
+    for (int k = half * kPer; k < (half + 1) * kPer; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
+  }
+  const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+            constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
+            if (first) {
+              m = top;
+            } else {
+              const bool up = top > m + Range<BITS>::kLazy / kUnit;
+              if (__any_sync(0xffffffffu, up)) {
+                // S of this step is complete, so O of the stream's step before it is too
+                const float f = up ? ex2((m - top) * kUnit) : 1.f;
+                l *= f;
+                if (up) m = top;
+#pragma unroll 1
+                for (int k = 0; k < kD; k += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(to + k, o);
+                  wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st16(to + k, o);
+                }
+              }
+            }
+            const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
+            const F2 base2(-base, -base), unit2(kUnit, kUnit);
+            F2 ls[4] = {F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < kCols; k += 32) {
+              if constexpr (BITS == 16) {
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float p0, p1;
+                  fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
+                  p0 = ex2(p0);
+                  p1 = ex2(p1);
+                  ls[i & 3] = add2(ls[i & 3], F2(p0, p1));
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                  p[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                tmem_st16(ts + (c0 + k) / 2, p);
+              } else {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 iv = *reinterpret_cast<const float4*>(scales + 2 * kTile + c0 + k + i * 4);
+                  float p[4];
+                  add2(F2(x[k + 4 * i], x[k + 4 * i + 1]), base2).get(p[0], p[1]);
+                  add2(F2(x[k + 4 * i + 2], x[k + 4 * i + 3]), base2).get(p[2], p[3]);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) p[c] = ex2(p[c]);
+                  ls[(2 * i) & 3] = fma2(F2(p[0], p[1]), F2(iv.x, iv.y), ls[(2 * i) & 3]);
+                  ls[(2 * i + 1) & 3] = fma2(F2(p[2], p[3]), F2(iv.z, iv.w), ls[(2 * i + 1) & 3]);
+                  // the upper byte of a half is the e5m2 number below it: adding
+                  // half a step first rounds (p is positive, the rest has a sign)
+                  uint32_t h[2], r[2];
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const __half2 v = __floats2half2_rn(p[2 * c], p[2 * c + 1]);
+                    h[c] = (*reinterpret_cast<const uint32_t*>(&v) + 0x00800080u) & 0xff00ff00u;
+                    const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&h[c]));
+                    r[c] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
+                  }
+                  hi[i] = __byte_perm(h[0], h[1], 0x7531);
+                  lo[i] = __byte_perm(r[0], r[1], 0x7531);
+                }
+                tmem_st8(ts + (c0 + k) / 4, hi);
+                tmem_st8(ts + 32 + (c0 + k) / 4, lo);
+              }
+            }
+            if constexpr (NCH < 4) {
+    const uint32_t zero[16] = {};
+#pragma unroll
+    for (int k = 0; k < kTile; k += 32)
+      if (k / kCols != part) {
+        if constexpr (BITS == 16) {
+          tmem_st16(ts + k / 2, zero);
+        } else {
+          tmem_st8(ts + k / 4, zero);
+          tmem_st8(ts + 32 + k / 4, zero);
+        }
+      }
+  }
+  float l0, l1;
+            add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])).get(l0, l1);
+            l += l0 + l1;
 }
 
 template <int BITS>
@@ -516,6 +676,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       mbar_wait(smem_u32(&sm.done), 0, &never);
     }
   } else {
+    // ---- this CTA's share of the join's table
+    {
+      const Share share(sm.plan.cum[sm.plan.n_pre + a.n_seq] * a.n_heads, gridDim.x);
+      const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
+      for (int64_t r = blockIdx.x + (int64_t)gridDim.x * (tid - 64); r < n; r += (int64_t)gridDim.x * 64)
+        a.parts[r] = parts_of(a, sm.plan, share, r);
+    }
     if constexpr (BITS == 8) {
       // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
       // segment when the stream does: further ahead, a stage's phase bit would
@@ -585,9 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       if (!ok) break;
       float qf = 1.f;
       if constexpr (BITS == 8) qf = sm.sc.qf[seg & 1][g.dual ? s : 0][row];
-      const int rows = g.rows_of(s), steps = g.steps_of(s);
+      const int rows = g.rows_of(s), steps = g.steps_of(s), copies = g.copies();
+      const int span = kTile / copies, r = row % span;  // this thread's row of the unit
       if (BITS == 8 && steps > 0 && lane == 0) mbar_arrive(smem_u32(&sm.sc_go[s]));
-      const bool active = w4 * 32 < rows;
+      const bool active = r - lane < rows;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++n) {
         const int t = g.tile_of(s, j), valid = g.valid(t), b = n & 1;
@@ -612,107 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
         s_phase ^= 1;
         if (active) {
           fence_after();
-          float x[kTile];
-          uint32_t* xu = reinterpret_cast<uint32_t*>(x);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld32(ts, xu);
-          tmem_ld32(ts + 32, xu + 32);
-          wait_ld();
-          tmem_ld32(ts + 64, xu + 64);
-          tmem_ld32(ts + 96, xu + 96);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (half) wait_ld();
-            if constexpr (BITS == 8) {
-#pragma unroll
-              for (int k = half * 64; k < half * 64 + 64; k += 4) {
-                const float4 kf = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][0][k]);
-                const float4 ev = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][1][k]);
-                const F2 q2(qf, qf);
-                fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
-                fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
-              }
-            }
-            if (valid < kTile) {
-#pragma unroll
-              for (int k = half * 64; k < half * 64 + 64; ++k)
-                if (k >= valid) x[k] = -INFINITY;
-            }
-#pragma unroll
-            for (int k = half * 64; k < half * 64 + 64; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
-          }
-          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-          constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
-          if (j == 0) {
-            m = top;
-          } else {
-            const bool up = top > m + Range<BITS>::kLazy / kUnit;
-            if (__any_sync(0xffffffffu, up)) {
-              // S of this step is complete, so O of the stream's step before it is too
-              const float f = up ? ex2((m - top) * kUnit) : 1.f;
-              l *= f;
-              if (up) m = top;
-#pragma unroll 1
-              for (int k = 0; k < kD; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(to + k, o);
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16(to + k, o);
-              }
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
-          const F2 base2(-base, -base), unit2(kUnit, kUnit);
-          F2 ls[4] = {F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f)};
-#pragma unroll
-          for (int k = 0; k < kTile; k += 32) {
-            if constexpr (BITS == 16) {
-              uint32_t p[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float p0, p1;
-                fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                ls[i & 3] = add2(ls[i & 3], F2(p0, p1));
-                const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                p[i] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              tmem_st16(ts + k / 2, p);
-            } else {
-              uint32_t hi[8], lo[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 iv = *reinterpret_cast<const float4*>(&sm.sc.tok[s][b][2][k + i * 4]);
-                float p[4];
-                add2(F2(x[k + 4 * i], x[k + 4 * i + 1]), base2).get(p[0], p[1]);
-                add2(F2(x[k + 4 * i + 2], x[k + 4 * i + 3]), base2).get(p[2], p[3]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) p[c] = ex2(p[c]);
-                ls[(2 * i) & 3] = fma2(F2(p[0], p[1]), F2(iv.x, iv.y), ls[(2 * i) & 3]);
-                ls[(2 * i + 1) & 3] = fma2(F2(p[2], p[3]), F2(iv.z, iv.w), ls[(2 * i + 1) & 3]);
-                // the upper byte of a half is the e5m2 number below it: adding
-                // half a step first rounds (p is positive, the rest has a sign)
-                uint32_t h[2], r[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const __half2 v = __floats2half2_rn(p[2 * c], p[2 * c + 1]);
-                  h[c] = (*reinterpret_cast<const uint32_t*>(&v) + 0x00800080u) & 0xff00ff00u;
-                  const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&h[c]));
-                  r[c] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
-                }
-                hi[i] = __byte_perm(h[0], h[1], 0x7531);
-                lo[i] = __byte_perm(r[0], r[1], 0x7531);
-              }
-              tmem_st8(ts + k / 4, hi);
-              tmem_st8(ts + 32 + k / 4, lo);
-            }
-          }
-          float l0, l1;
-          add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])).get(l0, l1);
-          l += l0 + l1;
+          const float* scales = nullptr;
+          if constexpr (BITS == 8) scales = sm.sc.tok[s][b][0];
+          if (copies == 1) softmax_step<BITS, 4>(ts, to, 0, valid, j == 0, qf, scales, m, l);
+          else if (copies == 2) softmax_step<BITS, 2>(ts, to, w4 >> 1, valid, j == 0, qf, scales, m, l);
+          else softmax_step<BITS, 1>(ts, to, w4, valid, j == 0, qf, scales, m, l);
           wait_st();
           fence_before();
         }
@@ -731,24 +803,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       if (active) {
         fence_after();
         const int64_t slot = (g.unit + blockIdx.x) * 2 + s;
-        float* po = g.pre ? a.pre_o + (slot * kTile + row) * kD : a.own_o + (slot * a.group + row) * kD;
+        const int64_t at = g.pre ? slot * kTile + row : (slot * 4 + row / span) * a.group + r;
+        float* po = (g.pre ? a.pre_o : a.own_o) + at * kD;
         if (steps > 0) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t o[32];
             tmem_ld32(to + k * 32, o);
             wait_ld();
-            if (row < rows) {
+            if (r < rows) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<uint4*>(po + k * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
         }
-        if (row < rows) {
-          float2* pm = g.pre ? a.pre_ml + slot * kTile + row : a.own_ml + slot * a.group + row;
-          *pm = make_float2(m * (BITS == 16 ? kLogScale : 1.f), l);
-        }
+        if (r < rows) (g.pre ? a.pre_ml : a.own_ml)[at] = make_float2(m * (BITS == 16 ? kLogScale : 1.f), l);
         fence_before();
       }
       tile_no += g.tiles;
@@ -764,69 +834,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
 
 // ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l, a CTA per query row
 
-constexpr int kMaxParts = 4 * (kCtas + 1);
+constexpr int kJoinWarps = 8;
+constexpr int kMaxParts = 2 * 8 * (kCtas + 1);
 
-__global__ void __launch_bounds__(kD) k_shared_join(const __grid_constant__ SharedArgs a, int32_t ctas, uint16_t* out) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_constant__ SharedArgs a, uint16_t* out) {
   pdl_enter();
-  __shared__ float s_w[kMaxParts], s_l[kMaxParts], s_red[kD / 32];
+  __shared__ float s_w[kMaxParts];
+  __shared__ float s_red[2][kJoinWarps];
+  __shared__ float4 s_o[kJoinWarps][kD / 4];
   const int64_t r = blockIdx.x;
-  const int g = (int)(r % a.group);
-  const int64_t u = r / a.group;  // sequence and KV head
-  const int h = (int)(u % a.n_heads), i = (int)(u / a.n_heads);
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t* cum = a.cum + 1;
-  const int n_pre = (int)a.cum[0];
-  const Share share(cum[n_pre + a.n_seq] * a.n_heads, ctas);
-  // the row's parts: of its prefix (one stream's, or both), then of its own rows
-  int64_t pre0 = 0, own0 = 0;  // first slot times 2, plus the stream
-  int pre_n = 0, own_n = 0, pre_step = 1, pre_row = 0;
-  const int4 si = a.seq_item[i];
-  if (si.x >= 0) {
-    const int64_t row = (int64_t)si.y * a.group + g;
-    const int item = si.x + (int)(row / kPair);
-    const int64_t tiles = cum[item + 1] - cum[item], at = cum[item] * a.n_heads + h * tiles;
-    const int64_t c0 = share.owner(at), c1 = share.owner(at + tiles - 1);
-    const int in = (int)(row % kPair);
-    const bool dual = si.z - (item - si.x) * kPair > kTile;  // each stream has its own rows
-    pre0 = ((int64_t)item * a.n_heads + h + c0) * 2 + (dual ? in / kTile : 0);
-    pre_step = dual ? 2 : 1;
-    pre_n = (int)(c1 - c0 + 1) * (dual ? 1 : 2);
-    pre_row = in % kTile;
-  }
-  {
-    const int item = n_pre + i;
-    const int64_t tiles = cum[item + 1] - cum[item], at = cum[item] * a.n_heads + h * tiles;
-    if (tiles > 0) {
-      const int64_t c0 = share.owner(at), c1 = share.owner(at + tiles - 1);
-      own0 = (u + c0) * 2;
-      own_n = (int)(c1 - c0 + 1) * 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Parts q = a.parts[r];
+  const int n_pre = q.pre_n * q.pre_sub, n = n_pre + 8 * q.own_n;
+  // row of part k among its kind's
+  auto row_of = [&](int k) -> int64_t {
+    if (k < n_pre) return q.pre + (int64_t)(k / q.pre_sub) * kPair + (k % q.pre_sub) * q.pre_span;
+    return q.own + (int64_t)(k - n_pre) * a.group;
+  };
+  constexpr int kPer = (kMaxParts + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+  float ms[kPer], lv[kPer], M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = tid + i * kJoinWarps * 32;
+    ms[i] = -INFINITY;
+    lv[i] = 0.f;
+    if (k < n) {
+      const float2 ml = (k < n_pre ? a.pre_ml : a.own_ml)[row_of(k)];
+      lv[i] = ml.y;
+      ms[i] = ml.y == 0.f ? -INFINITY : fmaxf(ml.x, -3e38f);  // no tokens; a sum that is NaN stays one
+      M = fmaxf(M, ms[i]);
     }
-  }
-  const int n = pre_n + own_n;
-  float M = -INFINITY;
-  for (int k = tid; k < n; k += kD) {
-    const float2 ml = k < pre_n ? a.pre_ml[(pre0 + (int64_t)k * pre_step) * kTile + pre_row]
-                                : a.own_ml[(own0 + k - pre_n) * a.group + g];
-    s_w[k] = ml.y == 0.f ? -INFINITY : fmaxf(ml.x, -3e38f);  // no tokens; a sum that is NaN stays one
-    s_l[k] = ml.y;
-    M = fmaxf(M, s_w[k]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[tid >> 5] = M;
+  if (lane == 0) s_red[0][warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kD / 32; ++w) M = fmaxf(M, s_red[w]);
-  float L = 0.f, O = 0.f;
-  for (int k = 0; k < n; ++k) {
-    if (s_w[k] == -INFINITY) continue;  // a part without tokens: its o is not written
-    const float w = ex2(s_w[k] - M);
-    const float* o = k < pre_n ? a.pre_o + ((pre0 + (int64_t)k * pre_step) * kTile + pre_row) * kD
-                               : a.own_o + ((own0 + k - pre_n) * a.group + g) * kD;
-    L = fmaf(w, s_l[k], L);
-    O = fmaf(w, o[tid], O);
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_red[0][w]);
+  float L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = tid + i * kJoinWarps * 32;
+    if (k < n) {
+      const float w = ms[i] == -INFINITY ? 0.f : ex2(ms[i] - M);
+      s_w[k] = ms[i] == -INFINITY ? -1.f : w;  // negative: o was not written
+      L = fmaf(w, lv[i], L);
+    }
   }
-  out[r * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(L == 0.f ? 0.f : O / L));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) s_red[1][warp] = L;
+  __syncthreads();
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = warp; k0 < n; k0 += 4 * kJoinWarps) {
+    float4 v[4];
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * kJoinWarps;
+      w[i] = k < n ? s_w[k] : -1.f;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (w[i] >= 0.f || w[i] != w[i])
+        v[i] = reinterpret_cast<const float4*>((k < n_pre ? a.pre_o : a.own_o) + row_of(k) * kD)[lane];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      O.x = fmaf(w[i], v[i].x, O.x);
+      O.y = fmaf(w[i], v[i].y, O.y);
+      O.z = fmaf(w[i], v[i].z, O.z);
+      O.w = fmaf(w[i], v[i].w, O.w);
+    }
+  }
+  s_o[warp][lane] = O;
+  __syncthreads();
+  if (tid < kD) {
+    float o = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      o += reinterpret_cast<const float*>(s_o[w])[tid];
+      l += s_red[1][w];
+    }
+    out[r * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o / l));
+  }
 }
 
 // ---- host side
@@ -834,16 +923,14 @@ __global__ void __launch_bounds__(kD) k_shared_join(const __grid_constant__ Shar
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Space {
-  size_t cum, seq_item, pre_o, pre_ml, own_o, own_ml, total;
+  size_t parts, pre_o, pre_ml, own_o, own_ml, total;
 };
 
 Space space(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
   Space s;
   size_t off = 256;  // status word
-  s.cum = off;
-  off = up256(off + (kMaxItems + 2) * sizeof(int64_t));
-  s.seq_item = off;
-  off = up256(off + n_seq * sizeof(int4));
+  s.parts = off;
+  off = up256(off + n_seq * n_heads * group * sizeof(Parts));
   // a segment is unit u's part in CTA c, slot u + c of its kind
   const size_t pre = n_prefix ? (min64(n_prefix, n_seq) + n_seq * group / kPair) * n_heads + kCtas : 0;
   const size_t own = n_seq * n_heads + kCtas;
@@ -852,9 +939,9 @@ Space space(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
   s.pre_ml = off;
   off = up256(off + pre * kPair * sizeof(float2));
   s.own_o = off;
-  off = up256(off + own * 2 * group * kD * sizeof(float));
+  off = up256(off + own * 8 * group * kD * sizeof(float));
   s.own_ml = off;
-  off = up256(off + own * 2 * group * sizeof(float2));
+  off = up256(off + own * 8 * group * sizeof(float2));
   s.total = off;
   return s;
 }
@@ -930,8 +1017,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   a.n_heads = n_heads;
   a.group = group;
   a.q = q;
-  a.cum = reinterpret_cast<int64_t*>(w + sp.cum);
-  a.seq_item = reinterpret_cast<int4*>(w + sp.seq_item);
+  a.parts = reinterpret_cast<Parts*>(w + sp.parts);
   a.pre_o = reinterpret_cast<float*>(w + sp.pre_o);
   a.pre_ml = reinterpret_cast<float2*>(w + sp.pre_ml);
   a.own_o = reinterpret_cast<float*>(w + sp.own_o);
@@ -951,8 +1037,8 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   const int ctas = (int)max64(1, min64(kCtas, most));
   e = launch_pdl(k_shared_attend<BITS>, dim3(ctas), dim3(kThreads), (size_t)smem, st, a, maps);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_shared_join, dim3((unsigned)((int64_t)own.n * n_heads * group)), dim3(kD), 0, st, a,
-                    (int32_t)ctas, out);
+  return launch_pdl(k_shared_join, dim3((unsigned)((int64_t)own.n * n_heads * group)), dim3(kJoinWarps * 32), 0, st, a,
+                    out);
 }
 
 }  // namespace
