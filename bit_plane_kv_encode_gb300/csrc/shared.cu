@@ -1,13 +1,6 @@
-// Decode attention of a batch that shares prefixes, on the tensor cores
-// (bpkv_shared_attend over bf16 rows, bpkv_shared_attend8 over 8-bit rows).
-//
-// Work.  A unit is a set of query rows that attend over the same KV rows: the
-// query heads of all sequences of one prefix, 256 at a time, for each KV head;
-// and for each sequence and KV head its own rows with its G query heads.  The
-// units' tiles of 128 tokens form one list, cut into equal stretches, one per
-// CTA; a CTA's part of a unit is a segment.  Lengths are read on the device, so
-// the cut fits ragged batches.  Each segment leaves its rows' partial (o, m, l)
-// in the workspace and a second kernel joins them.
+// Attention of many query rows over a shared prefix, on the 5th-generation
+// tensor cores (the wide half of bpkv_shared_attend over bf16 rows and
+// bpkv_shared_attend8 over 8-bit rows; the plan is in shared_plan.cuh).
 //
 // A segment.  One thread loads K and V tiles by TMA into a ring of shared
 // memory stages, one thread issues the products, and two groups of four warps
@@ -27,20 +20,21 @@
 // pieces, together good to 2^-6 (0.25% in the mean square) over the range of a
 // half.
 #include "rows8_core.cuh"
+#include "shared_plan.cuh"
 #include "tc.cuh"
 
 namespace bpkv {
+namespace shared {
+
+template <int BITS>
+cudaError_t launch_few(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);
+int few_tile(int bits);
 
 namespace {
 
 using namespace tc;
 
-constexpr int kTile = 128;                       // tokens of a tile, rows of a stream
-constexpr int kPair = 2 * kTile;                 // rows of a prefix unit
-constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
-constexpr int kMaxPre = kMaxSeq + kMaxSeq * BPKV_MAX_GROUP / kPair;  // prefix items: one more per 256 rows
-constexpr int kMaxItems = kMaxPre + kMaxSeq;
-constexpr int kCtas = 152;                       // one per SM
+constexpr int kTile = kWideTile;
 constexpr int kThreads = 384;
 constexpr int kRing16 = 32 * 1024;               // bytes of a stage: 128 rows of bf16
 constexpr int kRing8 = 16 * 1024;                // 128 rows of codes
@@ -56,47 +50,8 @@ struct Range {
   static constexpr float kShift = BITS == 16 ? 0.f : 11.f;
 };
 
-struct SharedArgs {
-  const int32_t* prefix_of;
-  const int64_t* plen;  // NULL: no prefixes
-  const int64_t* len;
-  int64_t pcap, cap;
-  int32_t n_prefix, n_seq, n_heads, group;
-  const uint16_t* q;
-  const uint8_t* exps[2][2];  // [prefix, own][K, V] scale exponents (8-bit rows)
-  struct Parts* parts;        // [N][H][G] where each query row's partials are
-  float* pre_o;               // [units + CTAs][2][128][D] partials of prefix units
-  float2* pre_ml;
-  float* own_o;  // [units + CTAs][2][4][G][D] partials of the sequences' own rows
-  float2* own_ml;
-  int32_t* status;
-  int32_t stages;
-};
-
-// A query row's partials (m, l and o), counted in rows of the two kinds: of each
-// of pre_n segments pre_sub, then of each of own_n segments 2 x 4.
-struct Parts {
-  int64_t pre, own;  // first
-  int32_t pre_n, own_n;
-  int32_t pre_sub;   // 1, or both streams' copies
-  int32_t pre_span;  // rows from one copy to the next
-};
-
 struct Maps {
-  CUtensorMap m[2][2];  // [prefix, own][K, V]
-};
-
-// What every CTA works out from the lengths.
-struct Plan {
-  int64_t cum[kMaxItems + 1];  // tiles before each item, for one KV head
-  uint16_t order[kMaxSeq];     // sequences by prefix
-  uint16_t rank[kMaxSeq];      // each sequence's place among its prefix's
-  int16_t pof[kMaxSeq];        // prefix of each sequence, -1: none
-  uint16_t cnt[kMaxSeq];       // sequences of each prefix
-  uint16_t first[kMaxSeq];     // where they begin in order
-  uint16_t item0[kMaxSeq];     // first item of each prefix
-  uint16_t it_p[kMaxPre];      // prefix of each prefix item
-  int32_t n_pre;               // prefix items
+  CUtensorMap m[2];  // K, V
 };
 
 template <int BITS>
@@ -120,129 +75,14 @@ struct Smem {
   uint64_t sc_go[2], sc_full[2][2], sc_empty[2][2];
 };
 
-__device__ __forceinline__ int64_t tiles_of(int64_t n, int64_t cap) {
-  return (max64(0, min64(n, cap)) + kTile - 1) / kTile;
-}
-
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
-__device__ void make_plan(const SharedArgs& a, Plan& p) {
-  const int tid = threadIdx.x;
-  const int P = a.plen ? a.n_prefix : 0, N = a.n_seq;
-  for (int i = tid; i < N; i += kThreads) {
-    const int x = a.prefix_of ? a.prefix_of[i] : 0;
-    p.pof[i] = (int16_t)(x >= 0 && x < P ? x : -1);
-  }
-  for (int i = tid; i < P; i += kThreads) p.cnt[i] = 0;
-  __syncthreads();
-  for (int i = tid; i < N; i += kThreads) {
-    const int x = p.pof[i];
-    int rank = 0, cnt = 0;
-    for (int j = 0; j < N; ++j) {
-      const bool same = p.pof[j] == x;
-      cnt += same;
-      rank += same && j < i;
-    }
-    if (x >= 0) p.cnt[x] = (uint16_t)cnt;
-    p.rank[i] = (uint16_t)rank;
-  }
-  __syncthreads();
-  const int lane = tid & 31;
-  if (tid < 32) {
-    int at = 0, item = 0;
-    for (int b = 0; b < P; b += 32) {
-      const int x = b + lane;
-      const int c = x < P ? p.cnt[x] : 0;
-      const int it = x < P && c > 0 && a.plen[x] > 0 ? (c * a.group + kPair - 1) / kPair : 0;
-      const int sc = (int)warp_scan(c, lane), si = (int)warp_scan(it, lane);
-      if (x < P) {
-        p.first[x] = (uint16_t)(at + sc - c);
-        p.item0[x] = (uint16_t)(item + si - it);
-        for (int k = 0; k < it; ++k) p.it_p[item + si - it + k] = (uint16_t)x;
-      }
-      at += __shfl_sync(0xffffffffu, sc, 31);
-      item += __shfl_sync(0xffffffffu, si, 31);
-    }
-    __syncwarp();
-    if (lane == 0) p.n_pre = item;
-    int64_t sum = 0;
-    for (int b = 0; b < item + N; b += 32) {
-      const int x = b + lane;
-      int64_t t = 0;
-      if (x < item) t = tiles_of(a.plen[p.it_p[x]], a.pcap);
-      else if (x < item + N) t = tiles_of(a.len[x - item], a.cap);
-      const int64_t c = warp_scan(t, lane);
-      if (x < item + N) p.cum[x] = sum + c - t;
-      sum += __shfl_sync(0xffffffffu, c, 31);
-    }
-    if (lane == 0) p.cum[item + N] = sum;
-  }
-  __syncthreads();
-  for (int i = tid; i < N; i += kThreads) {
-    const int x = p.pof[i];
-    if (x >= 0) p.order[p.first[x] + p.rank[i]] = (uint16_t)i;
-  }
-  __syncthreads();
-}
-
-// CTA c of n takes tiles [c T / n, (c + 1) T / n) of the list of T.
-struct Share {
-  int64_t total;
-  int64_t n;  // CTAs that take part: no more than tiles
-  __device__ Share(int64_t t, int64_t ctas) : total(t), n(min64(t, ctas)) {}
-  __device__ int64_t lo(int64_t c) const { return c * total / n; }
-  __device__ int64_t owner(int64_t tile) const { return ((tile + 1) * n - 1) / total; }
-};
-
-// Copies of a unit's rows among the 128 of a stream.  With 64 rows or fewer
-// the copies' softmax threads share the tile's tokens, so that all four warps
-// work; each copy has its own m, l and o.
-__device__ __forceinline__ int copies_of(int rows) { return rows <= kTile / 4 ? 4 : rows <= kTile / 2 ? 2 : 1; }
-
-// Where the partials of query row r = (sequence, KV head, head of the group) will be.
-__device__ Parts parts_of(const SharedArgs& a, const Plan& p, const Share& share, int64_t r) {
-  const int g = (int)(r % a.group);
-  const int64_t u = r / a.group;
-  const int h = (int)(u % a.n_heads), i = (int)(u / a.n_heads);
-  Parts q = {};
-  const int x = p.pof[i];
-  if (x >= 0 && a.plen[x] > 0) {
-    const int row = p.rank[i] * a.group + g, item = p.item0[x] + row / kPair;
-    const int in = row % kPair, rows = min(kPair, p.cnt[x] * a.group - row + in);
-    const int64_t tiles = p.cum[item + 1] - p.cum[item], at = p.cum[item] * a.n_heads + h * tiles;
-    const int64_t c0 = share.owner(at);
-    const bool dual = rows > kTile;
-    q.pre_n = (int)(share.owner(at + tiles - 1) - c0) + 1;
-    q.pre = ((int64_t)item * a.n_heads + h + c0) * kPair + in;
-    q.pre_sub = dual ? 1 : 2 * copies_of(rows);
-    q.pre_span = kTile / copies_of(rows);
-  }
-  const int item = p.n_pre + i;
-  const int64_t tiles = p.cum[item + 1] - p.cum[item], at = p.cum[item] * a.n_heads + h * tiles;
-  if (tiles > 0) {
-    const int64_t c0 = share.owner(at);
-    q.own_n = (int)(share.owner(at + tiles - 1) - c0) + 1;
-    q.own = (u + c0) * 8 * a.group + g;
-  }
-  return q;
-}
-
 // One CTA's part of a unit.
 struct Segment {
-  bool pre;       // of a prefix
-  int32_t index;  // sequence, or prefix
+  int32_t index;  // prefix
   int32_t h;      // KV head
   int32_t rows;   // query rows of the unit
-  int32_t row0;   // prefix: the unit's first row among the prefix's
+  int32_t row0;   // its first among the prefix's
   bool dual;      // both streams take every tile
-  int64_t unit;   // counted within its kind
+  int64_t unit;
   int64_t tile0;  // first tile
   int32_t tiles;
   int64_t tokens;  // of the whole unit
@@ -258,48 +98,37 @@ struct Segment {
 // Walks the segments of one CTA; every role of the CTA walks alike.
 struct Walk {
   const Plan& p;
-  const SharedArgs& a;
+  const Args& a;
   int64_t pos, end;
   int item;
-  __device__ Walk(const Plan& plan, const SharedArgs& args) : p(plan), a(args) {
-    const int items = p.n_pre + a.n_seq;
-    const int64_t total = p.cum[items] * a.n_heads;
-    const Share share(total, gridDim.x);
+  __device__ Walk(const Plan& plan, const Args& args) : p(plan), a(args) {
+    const Share share(p.wide[p.n_pre] * a.n_heads, a.wide_ctas);
     pos = end = 0;
     item = 0;
     if ((int64_t)blockIdx.x >= share.n) return;
     pos = share.lo(blockIdx.x);
     end = share.lo(blockIdx.x + 1);
-    int lo = 0, hi = items - 1;  // the last item that begins at or before pos
+    int lo = 0, hi = p.n_pre - 1;  // the last item that begins at or before pos
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (p.cum[mid] * a.n_heads <= pos) lo = mid;
+      if (p.wide[mid] * a.n_heads <= pos) lo = mid;
       else hi = mid - 1;
     }
     item = lo;
   }
   __device__ bool next(Segment& s) {
     if (pos >= end) return false;
-    while (p.cum[item + 1] * a.n_heads <= pos) ++item;
-    const int64_t tiles = p.cum[item + 1] - p.cum[item];
-    const int64_t off = pos - p.cum[item] * a.n_heads;
+    while (p.wide[item + 1] * a.n_heads <= pos) ++item;
+    const int64_t tiles = p.wide[item + 1] - p.wide[item];
+    const int64_t off = pos - p.wide[item] * a.n_heads;
     s.h = (int)(off / tiles);
     s.tile0 = off - s.h * tiles;
-    s.tiles = (int)min64(min64(tiles - s.tile0, end - pos), 1 << 30);
-    s.pre = item < p.n_pre;
-    if (s.pre) {
-      s.index = p.it_p[item];
-      s.row0 = (item - p.item0[s.index]) * kPair;
-      s.rows = min(kPair, p.cnt[s.index] * a.group - s.row0);
-      s.tokens = min64(a.plen[s.index], a.pcap);
-      s.unit = (int64_t)item * a.n_heads + s.h;
-    } else {
-      s.index = item - p.n_pre;
-      s.row0 = 0;
-      s.rows = a.group;
-      s.tokens = min64(a.len[s.index], a.cap);
-      s.unit = (int64_t)s.index * a.n_heads + s.h;
-    }
+    s.tiles = (int)min64(tiles - s.tile0, end - pos);
+    s.index = p.it_p[item];
+    s.row0 = (item - p.item0[s.index]) * kPair;
+    s.rows = pre_rows(a, p, item);
+    s.tokens = tokens_of(a.plen[s.index], a.pcap);
+    s.unit = (int64_t)item * a.n_heads + s.h;
     s.dual = s.rows > kTile;
     pos += s.tiles;
     return true;
@@ -335,7 +164,7 @@ __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 12
 
 // The rows of q of one stream into shared memory, by its 128 threads.
 template <int BITS>
-__device__ __forceinline__ void load_q(const SharedArgs& a, const Plan& p, const Segment& g, int s, unsigned char* dst,
+__device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segment& g, int s, unsigned char* dst,
                                        float* qf) {
   const int t = threadIdx.x & 127, l16 = t & 15;
   const int rows = g.rows_of(s), base = g.row0 + (g.dual ? s * kTile : 0);
@@ -346,8 +175,7 @@ __device__ __forceinline__ void load_q(const SharedArgs& a, const Plan& p, const
     uint4 w = make_uint4(0, 0, 0, 0);
     if (of < rows) {
       const int x = base + of;
-      const int seq = g.pre ? p.order[p.first[g.index] + x / a.group] : g.index;
-      const int head = g.pre ? x % a.group : x;
+      const int seq = p.order[p.first[g.index] + x / a.group], head = x % a.group;
       w = *reinterpret_cast<const uint4*>(a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
     }
     if constexpr (BITS == 16) {
@@ -512,15 +340,15 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int part,
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_constant__ SharedArgs a,
-                                                               const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_constant__ Args a,
+                                                             const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char raw[];
   Smem<BITS>& sm = *reinterpret_cast<Smem<BITS>*>(raw);
   unsigned char* q_smem = raw + ((smem_u32(raw) + sizeof(Smem<BITS>) + 1023) / 1024 * 1024 - smem_u32(raw));
   using S = Shape<BITS>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_stage = a.stages;
-  const bool any_dual = a.plen && a.n_seq * a.group > kTile;
+  const bool any_dual = a.n_seq * a.group > kTile;
   unsigned char* ring = q_smem + (any_dual ? 2 : 1) * S::kQ;
   unsigned char* ring_exps = ring + n_stage * S::kStage;  // [stage][K bytes, V bytes]
   volatile uint32_t* abort = &sm.abort;
@@ -548,10 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
     fence_async_shared();
   }
   if (warp == 2) tmem_alloc(smem_u32(&sm.tmem), kTmemCols);
-  if (warp == 3 && lane < 4) prefetch_map(&maps.m[lane >> 1][lane & 1]);
+  if (warp == 3 && lane < 2) prefetch_map(&maps.m[lane]);
   fence_before();
-  pdl_enter();
-  make_plan(a, sm.plan);  // ends with a barrier of the CTA
+  // the streaming kernel may start once this one has seen all earlier work complete
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  make_plan(a, sm.plan, kTile);  // ends with a barrier of the CTA
   fence_after();
   const uint32_t tmem = sm.tmem;
   Walk walk(sm.plan, a);
@@ -566,9 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       uint32_t stage = 0, phase = 0, issued = 0;
       bool ok = true;
       while (ok && walk.next(g)) {
-        const CUtensorMap* km = &maps.m[g.pre ? 0 : 1][0];
         const int64_t base = (int64_t)g.index * a.n_heads + g.h;
-        const int64_t cap = g.pre ? a.pcap : a.cap;
         for (int t = 0; ok && t < g.tiles; ++t) {
           const int64_t tok = (g.tile0 + t) * kTile;
 #pragma unroll
@@ -579,13 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
             const uint32_t dst = smem_u32(ring + stage * S::kStage);
             mbar_expect_tx(bar, S::kStage + (kv ? S::kExps : 0));
             if constexpr (BITS == 16) {
-              tma_load_4d(dst, km + kv, bar, 0, (int)tok, 0, (int)base);
+              tma_load_4d(dst, &maps.m[kv], bar, 0, (int)tok, 0, (int)base);
             } else {
-              tma_load_3d(dst, km + kv, bar, 0, (int)tok, (int)base);
+              tma_load_3d(dst, &maps.m[kv], bar, 0, (int)tok, (int)base);
               if (kv) {
                 const uint32_t e = smem_u32(ring_exps + stage * S::kExps);
-                bulk_load(e, a.exps[g.pre ? 0 : 1][0] + base * cap + tok, kTile, bar);
-                bulk_load(e + kTile, a.exps[g.pre ? 0 : 1][1] + base * cap + tok, kTile, bar);
+                bulk_load(e, a.exps[0][0] + base * a.pcap + tok, kTile, bar);
+                bulk_load(e + kTile, a.exps[0][1] + base * a.pcap + tok, kTile, bar);
               }
             }
             ++issued;
@@ -676,13 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       mbar_wait(smem_u32(&sm.done), 0, &never);
     }
   } else {
-    // ---- this CTA's share of the join's table
-    {
-      const Share share(sm.plan.cum[sm.plan.n_pre + a.n_seq] * a.n_heads, gridDim.x);
-      const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
-      for (int64_t r = blockIdx.x + (int64_t)gridDim.x * (tid - 64); r < n; r += (int64_t)gridDim.x * 64)
-        a.parts[r] = parts_of(a, sm.plan, share, r);
-    }
     if constexpr (BITS == 8) {
       // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
       // segment when the stream does: further ahead, a stage's phase bit would
@@ -802,9 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
       }
       if (active) {
         fence_after();
-        const int64_t slot = (g.unit + blockIdx.x) * 2 + s;
-        const int64_t at = g.pre ? slot * kTile + row : (slot * 4 + row / span) * a.group + r;
-        float* po = (g.pre ? a.pre_o : a.own_o) + at * kD;
+        const int64_t at = wide_row(a, g.unit, blockIdx.x) + s * kTile + row;
+        float* po = a.part_o + at * kD;
         if (steps > 0) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -818,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
             }
           }
         }
-        if (r < rows) (g.pre ? a.pre_ml : a.own_ml)[at] = make_float2(m * (BITS == 16 ? kLogScale : 1.f), l);
+        if (r < rows) a.part_ml[at] = make_float2(m * (BITS == 16 ? kLogScale : 1.f), l);
         fence_before();
       }
       tile_no += g.tiles;
@@ -832,116 +652,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_attend(const __grid_cons
   if (warp == 2) tmem_dealloc(tmem, kTmemCols);
 }
 
-// ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l, a CTA per query row
-
-constexpr int kJoinWarps = 8;
-constexpr int kMaxParts = 2 * 8 * (kCtas + 1);
-
-__global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_constant__ SharedArgs a, uint16_t* out) {
-  pdl_enter();
-  __shared__ float s_w[kMaxParts];
-  __shared__ float s_red[2][kJoinWarps];
-  __shared__ float4 s_o[kJoinWarps][kD / 4];
-  const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Parts q = a.parts[r];
-  const int n_pre = q.pre_n * q.pre_sub, n = n_pre + 8 * q.own_n;
-  // row of part k among its kind's
-  auto row_of = [&](int k) -> int64_t {
-    if (k < n_pre) return q.pre + (int64_t)(k / q.pre_sub) * kPair + (k % q.pre_sub) * q.pre_span;
-    return q.own + (int64_t)(k - n_pre) * a.group;
-  };
-  constexpr int kPer = (kMaxParts + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
-  float ms[kPer], lv[kPer], M = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = tid + i * kJoinWarps * 32;
-    ms[i] = -INFINITY;
-    lv[i] = 0.f;
-    if (k < n) {
-      const float2 ml = (k < n_pre ? a.pre_ml : a.own_ml)[row_of(k)];
-      lv[i] = ml.y;
-      ms[i] = ml.y == 0.f ? -INFINITY : fmaxf(ml.x, -3e38f);  // no tokens; a sum that is NaN stays one
-      M = fmaxf(M, ms[i]);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[0][warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_red[0][w]);
-  float L = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = tid + i * kJoinWarps * 32;
-    if (k < n) {
-      const float w = ms[i] == -INFINITY ? 0.f : ex2(ms[i] - M);
-      s_w[k] = ms[i] == -INFINITY ? -1.f : w;  // negative: o was not written
-      L = fmaf(w, lv[i], L);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) s_red[1][warp] = L;
-  __syncthreads();
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = warp; k0 < n; k0 += 4 * kJoinWarps) {
-    float4 v[4];
-    float w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = k0 + i * kJoinWarps;
-      w[i] = k < n ? s_w[k] : -1.f;
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (w[i] >= 0.f || w[i] != w[i])
-        v[i] = reinterpret_cast<const float4*>((k < n_pre ? a.pre_o : a.own_o) + row_of(k) * kD)[lane];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      O.x = fmaf(w[i], v[i].x, O.x);
-      O.y = fmaf(w[i], v[i].y, O.y);
-      O.z = fmaf(w[i], v[i].z, O.z);
-      O.w = fmaf(w[i], v[i].w, O.w);
-    }
-  }
-  s_o[warp][lane] = O;
-  __syncthreads();
-  if (tid < kD) {
-    float o = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      o += reinterpret_cast<const float*>(s_o[w])[tid];
-      l += s_red[1][w];
-    }
-    out[r * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o / l));
-  }
-}
-
 // ---- host side
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Space {
-  size_t parts, pre_o, pre_ml, own_o, own_ml, total;
+  size_t parts, ml, o, total;
+  int64_t few0, own0;  // first partial rows of the kinds
 };
 
 Space space(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
   Space s;
+  // a segment is unit u's part in worker w, slot u + w of its kind
+  const int64_t pre = n_prefix ? (min64(n_prefix, n_seq) + n_seq * group / kPair) * n_heads : 0;
+  const int64_t wide = n_prefix && n_seq * group > kFew ? (pre + kSms) * kPair : 0;
+  const int64_t few = n_prefix ? (pre + kSms * kFewWarps) * kFew : 0;
+  const int64_t own = (n_seq * n_heads + kSms * kFewWarps) * group;
+  s.few0 = wide;
+  s.own0 = wide + few;
   size_t off = 256;  // status word
   s.parts = off;
   off = up256(off + n_seq * n_heads * group * sizeof(Parts));
-  // a segment is unit u's part in CTA c, slot u + c of its kind
-  const size_t pre = n_prefix ? (min64(n_prefix, n_seq) + n_seq * group / kPair) * n_heads + kCtas : 0;
-  const size_t own = n_seq * n_heads + kCtas;
-  s.pre_o = off;
-  off = up256(off + pre * kPair * kD * sizeof(float));
-  s.pre_ml = off;
-  off = up256(off + pre * kPair * sizeof(float2));
-  s.own_o = off;
-  off = up256(off + own * 8 * group * kD * sizeof(float));
-  s.own_ml = off;
-  off = up256(off + own * 8 * group * sizeof(float2));
+  s.ml = off;
+  off = up256(off + (wide + few + own) * sizeof(float2));
+  s.o = off;
+  off = up256(off + (wide + few + own) * kD * sizeof(float));
   s.total = off;
   return s;
 }
@@ -998,13 +733,11 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
                    const uint16_t* q, uint16_t* out, void* ws, cudaStream_t st) {
   const Space sp = space(own.n, prefix ? prefix->n : 0, n_heads, group);
   unsigned char* w = static_cast<unsigned char*>(ws);
-  Maps maps;
   const Side* sides[2] = {prefix ? prefix : &own, &own};
-  SharedArgs a = {};
+  Args a = {};
   for (int i = 0; i < 2; ++i)
     for (int kv = 0; kv < 2; ++kv) {
-      if (!make_map<BITS>(&maps.m[i][kv], sides[i]->rows[kv], (int64_t)sides[i]->n * n_heads, sides[i]->cap))
-        return cudaErrorInvalidValue;
+      a.rows[i][kv] = sides[i]->rows[kv];
       a.exps[i][kv] = sides[i]->exps[kv];
     }
   a.prefix_of = prefix_of;
@@ -1018,30 +751,41 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   a.group = group;
   a.q = q;
   a.parts = reinterpret_cast<Parts*>(w + sp.parts);
-  a.pre_o = reinterpret_cast<float*>(w + sp.pre_o);
-  a.pre_ml = reinterpret_cast<float2*>(w + sp.pre_ml);
-  a.own_o = reinterpret_cast<float*>(w + sp.own_o);
-  a.own_ml = reinterpret_cast<float2*>(w + sp.own_ml);
+  a.part_ml = reinterpret_cast<float2*>(w + sp.ml);
+  a.part_o = reinterpret_cast<float*>(w + sp.o);
+  a.few0 = sp.few0;
+  a.own0 = sp.own0;
   a.status = static_cast<int32_t*>(ws);
-  const bool dual = prefix && own.n * group > kTile;
-  a.stages = Shape<BITS>::stages(dual);
-  const int smem = Shape<BITS>::bytes(dual);
-  cudaError_t e = cudaFuncSetAttribute(k_shared_attend<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Shape<BITS>::kSmemMax);
-  if (e != cudaSuccess) return e;
-  // no more CTAs than tiles, as far as the host knows
-  const int64_t most = n_heads * ((own.n_max + kTile - 1) / kTile * own.n +
-                                  (prefix ? (prefix->n_max + kTile - 1) / kTile *
-                                                (min64(prefix->n, own.n) + (int64_t)own.n * group / kPair)
-                                          : 0));
-  const int ctas = (int)max64(1, min64(kCtas, most));
-  e = launch_pdl(k_shared_attend<BITS>, dim3(ctas), dim3(kThreads), (size_t)smem, st, a, maps);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_shared_join, dim3((unsigned)((int64_t)own.n * n_heads * group)), dim3(kJoinWarps * 32), 0, st, a,
-                    out);
+  // no more CTAs than tiles, as far as the host knows (longer sequences than
+  // it knows of only find fewer CTAs)
+  const int64_t units = prefix ? min64(prefix->n, own.n) + (int64_t)own.n * group / kPair : 0;
+  const int64_t wide = prefix && own.n * group > kFew ? n_heads * units * ((prefix->n_max + kTile - 1) / kTile) : 0;
+  const int64_t tok = few_tile(BITS);
+  const int64_t few = n_heads * ((own.n_max + tok - 1) / tok * own.n + (prefix ? (prefix->n_max + tok - 1) / tok * units : 0));
+  a.wide_ctas = (int32_t)max64(1, min64(kSms, wide));
+  a.few_workers = (int32_t)max64(1, min64(kSms, few)) * kFewWarps;
+  const bool has_wide = prefix && own.n * group > kFew;
+  if (has_wide) {
+    Maps maps;
+    for (int kv = 0; kv < 2; ++kv)
+      if (!make_map<BITS>(&maps.m[kv], prefix->rows[kv], (int64_t)prefix->n * n_heads, prefix->cap))
+        return cudaErrorInvalidValue;
+    const bool dual = own.n * group > kTile;
+    a.stages = Shape<BITS>::stages(dual);
+    cudaError_t e = cudaFuncSetAttribute(k_shared_wide<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Shape<BITS>::kSmemMax);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(k_shared_wide<BITS>, dim3(a.wide_ctas), dim3(kThreads), (size_t)Shape<BITS>::bytes(dual), st, a, maps);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_few<BITS>(a, !has_wide, out, st);
 }
 
 }  // namespace
+
+}  // namespace shared
+
+using namespace shared;
 
 size_t shared_bytes(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
   return space(n_seq, n_prefix, n_heads, group).total;

@@ -1,0 +1,559 @@
+// Attention of few query rows over long rows of KV: each sequence's G heads
+// over its own rows, and prefixes of at most 16 query rows (the streaming half
+// of bpkv_shared_attend / bpkv_shared_attend8; the plan is in shared_plan.cuh).
+//
+// Bound by the bytes of K and V, so every warp is a worker with its own ring of
+// asynchronous copies (three stages of 8 KB: 16 tokens of bf16, 32 of codes)
+// that runs ahead across the borders of units, and nothing in the CTA waits for
+// anything else.  Products are S^T = K Q^T and O^T = V^T P^T, so that the 16
+// side of the warp-level matrix instruction holds tokens or channels and the 8
+// side the query rows: no part of a product is padding for G = 8, and P^T is
+// S^T's own registers through one 8 x 8 transpose.  The 5th-generation tensor
+// instructions take 128 rows at least, and the units here change every few
+// tiles: there a switch of unit cost 2.5 us, more than the tiles between two.
+//
+// 8-bit rows: a code is exactly a half, so codes become halves in registers;
+// channels are taken in the order the bytes come in (the same for K and q).
+// K's scales multiply S, V's join the exponent as in the wide kernel: p' = p
+// 2^ev is the weight in the product, p = p' 2^-ev the term of the sum.
+#include "rows8_core.cuh"
+#include "shared_plan.cuh"
+
+namespace bpkv {
+namespace shared {
+
+namespace {
+
+constexpr int kThreads = kFewWarps * 32;
+constexpr int kStages = 3;
+constexpr int kStage = 8192;  // K rows then V rows
+constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
+
+template <int BITS>
+struct Shape {
+  static constexpr int kTok = BITS == 16 ? 16 : 32;       // tokens of a stage
+  static constexpr int kSub = kTok / 16;                  // 16-token blocks of a stage
+  static constexpr int kRow = kD * BITS / 8;              // bytes of a row
+  static constexpr int kExps = BITS == 16 ? 0 : 2 * kTok; // exponent bytes
+  static constexpr int kRing = kFewWarps * kStages * (kStage + kExps);
+  static constexpr int kSmem = kRing + (int)sizeof(Plan);
+  static constexpr float kLazy = BITS == 16 ? 8.f : 4.f;  // rise of the maximum before O is rescaled
+  static constexpr float kShift = BITS == 16 ? 0.f : 11.f;  // p' below 2^15: a half
+};
+
+// One worker's way through its tiles.
+struct Walk {
+  const Plan& p;
+  const Args& a;
+  int tok;
+  int64_t pos, end;
+  int item, h;
+  int64_t t, tiles, n, row0, unit;
+  int side;  // 0: a prefix, 1: own rows
+  int index;
+  __device__ __forceinline__ Walk(const Plan& plan, const Args& args, int worker, int tile) : p(plan), a(args), tok(tile) {
+    const int items = p.n_pre + a.n_seq;
+    const Share share(p.few[items] * a.n_heads, a.few_workers);
+    pos = end = 0;
+    if (worker >= share.n) return;
+    pos = share.lo(worker);
+    end = share.lo(worker + 1);
+    int lo = 0, hi = items - 1;  // the last item that begins at or before pos
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (p.few[mid] * a.n_heads <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    item = lo;
+    const int64_t off = pos - p.few[item] * a.n_heads;
+    tiles = p.few[item + 1] - p.few[item];
+    h = (int)(off / tiles);
+    t = off - h * tiles;
+    set();
+  }
+  __device__ __forceinline__ void set() {
+    side = item < p.n_pre ? 0 : 1;
+    index = side ? item - p.n_pre : p.it_p[item];
+    const int64_t u = (int64_t)index * a.n_heads + h;
+    unit = side ? u : (int64_t)item * a.n_heads + h;
+    row0 = u * (side ? a.cap : a.pcap);
+    n = side ? tokens_of(a.len[index], a.cap) : tokens_of(a.plen[index], a.pcap);
+  }
+  __device__ __forceinline__ bool more() const { return pos < end; }
+  // one tile on; true when that is another unit's
+  __device__ __forceinline__ bool next() {
+    ++pos;
+    if (++t < tiles) return false;
+    t = 0;
+    if (++h == a.n_heads) {
+      h = 0;
+      if (pos < end) {
+        do ++item;
+        while (p.few[item + 1] == p.few[item]);
+        tiles = p.few[item + 1] - p.few[item];
+      }
+    }
+    if (pos < end) set();
+    return true;
+  }
+  __device__ __forceinline__ int valid() const { return (int)min64(tok, n - t * tok); }
+};
+
+__device__ __forceinline__ void cp16_zero(uint32_t dst, const void* src, bool there) {
+  const int n = there ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <int BITS>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t* b) {
+  if constexpr (BITS == 16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if constexpr (BITS == 16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+__device__ __forceinline__ uint32_t halves(uint32_t codes) {
+  const __half2 h = half2_of_e4m3x2((uint16_t)codes);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Issue the copies of the walk's tile into a stage.
+template <int BITS>
+__device__ __forceinline__ void load_tile(const Walk& w, uint32_t stage, uint32_t exps) {
+  using S = Shape<BITS>;
+  const int lane = threadIdx.x & 31, valid = w.valid();
+  const int64_t row = w.row0 + w.t * S::kTok;
+  constexpr int kChunks = S::kRow / 16;  // 16-byte pieces of a row
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const unsigned char* src = static_cast<const unsigned char*>(w.a.rows[w.side][kv]) + row * S::kRow;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = i * 32 + lane, tok = x / kChunks, c = x % kChunks;
+      cp16_zero(stage + kv * (kStage / 2) + tok * S::kRow + ((c ^ (tok & 7)) << 4), src + x * 16, tok < valid);
+    }
+    if (BITS == 8 && lane < 2) cp16_zero(exps + kv * S::kTok + lane * 16, w.a.exps[w.side][kv] + row + lane * 16, true);
+  }
+}
+
+// q of the unit as the 8-side operand of S^T, rows lane / 4 (+ 8), for 8-bit
+// rows as halves under a power-of-two scale of the row.
+template <int BITS, int NB>
+__device__ __forceinline__ void load_q(const Walk& w, int rows, uint32_t (*qb)[8][2], float (*qf)[2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const Args& a = w.a;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = nb * 8 + g;
+    const uint16_t* q = nullptr;
+    if (r < rows) {
+      int seq = w.index, head = r;
+      if (w.side == 0) {
+        const int x = (w.item - w.p.item0[w.index]) * kPair + r;
+        seq = w.p.order[w.p.first[w.index] + x / a.group];
+        head = x % a.group;
+      }
+      q = a.q + (((int64_t)seq * a.n_heads + w.h) * a.group + head) * kD;
+    }
+    if constexpr (BITS == 16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        qb[nb][k][0] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c) : 0u;
+        qb[nb][k][1] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * c) : 0u;
+      }
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint2 v = q ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c) : make_uint2(0u, 0u);
+        qb[nb][k][0] = v.x;
+        qb[nb][k][1] = v.y;
+        m = __vmaxu2(m, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+      }
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      m = max(m & 0xffffu, m >> 16);
+      const int e = max(-100, (int)(m >> 7) - 127 - 7);  // the largest within 128 .. 256
+      const float f = exp2i(-e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          qb[nb][k][i] = pack<8>(__uint_as_float(qb[nb][k][i] << 16) * f, __uint_as_float(qb[nb][k][i] & 0xffff0000u) * f);
+      const float s = exp2i(e);  // of row g; this thread's sums are of rows 2 c, 2 c + 1
+      qf[nb][0] = __shfl_sync(0xffffffffu, s, 8 * c);
+      qf[nb][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
+    }
+  }
+}
+
+template <int BITS, int NB>
+__global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constant__ Args a, int32_t wait_first) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  using S = Shape<BITS>;
+  Plan& plan = *reinterpret_cast<Plan*>(smem + S::kRing);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  // Behind the wide kernel of the same call, which starts this one only after
+  // its own wait, what that wait covered is complete: only the end waits, so
+  // that the two overlap.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+  make_plan(a, plan, S::kTok);
+  {
+    const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
+    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * tid; r < n; r += (int64_t)gridDim.x * kThreads)
+      a.parts[r] = parts_of(a, plan, r);
+  }
+  const int worker = warp * gridDim.x + blockIdx.x;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  unsigned char* exps = smem + kFewWarps * kStages * kStage + warp * kStages * S::kExps;
+  Walk ahead(plan, a, worker, S::kTok), cur(plan, a, worker, S::kTok);
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (ahead.more()) {
+      load_tile<BITS>(ahead, ring + i * kStage, smem_u32(exps) + i * S::kExps);
+      ahead.next();
+    }
+    cp_async_commit();
+  }
+  uint32_t qb[NB][8][2];
+  float qf[NB][2], o[NB][8][4], m[NB][2], l[NB][2];
+  int rows = 0;
+  bool fresh = true;
+  int st = 0;
+  while (cur.more()) {
+    if (fresh) {
+      rows = cur.side ? a.group : pre_rows(a, plan, cur.item);
+      load_q<BITS, NB>(cur, rows, qb, qf);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nb][j][i] = 0.f;
+      }
+    }
+    cp_wait<kStages - 2>();
+    __syncwarp();  // everyone's copies of this stage have landed, and the stage before is read
+    {
+      const int into = st == 0 ? kStages - 1 : st - 1;
+      if (ahead.more()) {
+        load_tile<BITS>(ahead, ring + into * kStage, smem_u32(exps) + into * S::kExps);
+        ahead.next();
+      }
+      cp_async_commit();
+    }
+    const uint32_t ks = ring + st * kStage, vs = ks + kStage / 2;
+    const bool two = NB > 1 && rows > 8;
+    const int valid = cur.valid();
+    float x[S::kSub][NB][4];
+    float iv[S::kSub][2];
+    // ---- S^T of the stage's tokens: this thread has tokens g, g + 8 of each block, rows 2 c, 2 c + 1
+#pragma unroll
+    for (int b = 0; b < S::kSub; ++b) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[b][nb][i] = 0.f;
+      const int tok = b * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; k += BITS == 16 ? 1 : 2) {
+        uint32_t r[4];
+        if constexpr (BITS == 16) {
+          ldm4(r, ks + tok * S::kRow + (((2 * k + (lane >> 4)) ^ (tok & 7)) << 4));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            if (nb == 0 || two) mma<16>(x[b][nb], r, qb[nb][k]);
+        } else {
+          ldm4(r, ks + tok * S::kRow + (((k + (lane >> 4)) ^ (tok & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t f[4] = {halves(r[2 * i]), halves(r[2 * i + 1]), halves(r[2 * i] >> 16),
+                                   halves(r[2 * i + 1] >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb == 0 || two) mma<8>(x[b][nb], f, qb[nb][k + i]);
+          }
+        }
+      }
+      if constexpr (BITS == 8) {
+        const unsigned char* e = exps + st * S::kExps + b * 16 + g;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ke = min(max((int)e[8 * i] - kExpBias, kExpMin), kExpMax);
+          const int ve = min(max((int)e[S::kTok + 8 * i] - kExpBias, kExpMin), kExpMax);
+          const float kf = exp2i(ke) * kLogScale, ev = (float)ve;
+          iv[b][i] = exp2i(-ve);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            x[b][nb][2 * i] = fmaf(x[b][nb][2 * i] * kf, qf[nb][0], ev);
+            x[b][nb][2 * i + 1] = fmaf(x[b][nb][2 * i + 1] * kf, qf[nb][1], ev);
+          }
+        }
+      }
+      if (valid < S::kTok) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (b * 16 + g + 8 * i >= valid) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) x[b][nb][2 * i] = x[b][nb][2 * i + 1] = -INFINITY;
+          }
+      }
+    }
+    // ---- m follows the maximum when that has risen far enough
+    constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
+    float top[NB][2];
+    bool up = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        top[nb][i] = fmaxf(x[0][nb][i], x[0][nb][2 + i]);
+#pragma unroll
+        for (int b = 1; b < S::kSub; ++b) top[nb][i] = fmaxf(top[nb][i], fmaxf(x[b][nb][i], x[b][nb][2 + i]));
+        up |= top[nb][i] > m[nb][i] + S::kLazy / kUnit;
+      }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float t = top[nb][i];
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+          if (t > m[nb][i]) {
+            const float f = ex2((m[nb][i] - t) * kUnit);
+            m[nb][i] = t;
+            l[nb][i] *= f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              o[nb][j][i] *= f;
+              o[nb][j][2 + i] *= f;
+            }
+          }
+        }
+    }
+    float base[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        base[nb][i] = m[nb][i] == -INFINITY ? 0.f : fmaf(m[nb][i], kUnit, -S::kShift);
+    // ---- P^T, and O^T += V^T P^T
+#pragma unroll
+    for (int b = 0; b < S::kSub; ++b) {
+      uint32_t pb[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = ex2(fmaf(x[b][nb][i], kUnit, -base[nb][i & 1]));
+          l[nb][i & 1] = BITS == 16 ? l[nb][i & 1] + p[i] : fmaf(p[i], iv[b][i >> 1], l[nb][i & 1]);
+        }
+        pb[nb][0] = transpose8(pack<BITS>(p[0], p[1]));
+        pb[nb][1] = transpose8(pack<BITS>(p[2], p[3]));
+      }
+      if constexpr (BITS == 16) {
+        const int tok = b * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t r[4];
+          ldm4t(r, vs + tok * S::kRow + (((2 * j + ((lane >> 3) & 1)) ^ (tok & 7)) << 4));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            if (nb == 0 || two) mma<16>(o[nb][j], r, pb[nb]);
+        }
+      } else {
+        const int tok = b * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          uint32_t r[4];
+          ldm4t(r, vs + tok * S::kRow + (((j + (lane >> 4)) ^ (tok & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // of two neighbouring channels: the even ones are rows 0 .. 7 of the product, the odd ones 8 .. 15
+            const uint32_t f[4] = {halves(__byte_perm(r[2 * i], 0, 0x4420)), halves(__byte_perm(r[2 * i], 0, 0x4431)),
+                                   halves(__byte_perm(r[2 * i + 1], 0, 0x4420)),
+                                   halves(__byte_perm(r[2 * i + 1], 0, 0x4431))};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb == 0 || two) mma<8>(o[nb][j + i], f, pb[nb]);
+          }
+        }
+      }
+    }
+    st = st == kStages - 1 ? 0 : st + 1;
+    // ---- the end of a segment: its partial rows
+    const int64_t at = cur.side ? own_row(a, cur.unit, worker) : few_row(a, cur.unit, worker);
+    fresh = cur.next();
+    if (fresh || !cur.more()) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = nb * 8 + 2 * c + i;
+          float s = l[nb][i];
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+          if (r < rows) {
+            float* po = a.part_o + (at + r) * kD;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (BITS == 16) {
+                po[16 * j + g] = o[nb][j][i];
+                po[16 * j + 8 + g] = o[nb][j][2 + i];
+              } else {
+                *reinterpret_cast<float2*>(po + 16 * j + 2 * g) = make_float2(o[nb][j][i], o[nb][j][2 + i]);
+              }
+            }
+            if (g == 0) a.part_ml[at + r] = make_float2(m[nb][i] * kUnit, s);
+          }
+        }
+    }
+  }
+  cp_wait<0>();
+  // the join follows this kernel: it must find the wide kernel complete too
+  if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l, a CTA per query row
+
+constexpr int kJoinWarps = 8;
+constexpr int kMaxParts = 8 * (kSms + 1) + kSms * kFewWarps + kSms * kFewWarps;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_constant__ Args a, uint16_t* out) {
+  pdl_enter();
+  __shared__ float s_w[kMaxParts];
+  __shared__ float s_red[2][kJoinWarps];
+  __shared__ float4 s_o[kJoinWarps][kD / 4];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Parts q = a.parts[r];
+  const int n_pre = q.pre_n * q.pre_sub, n = n_pre + q.own_n;
+  auto row_of = [&](int k) -> int64_t {
+    if (k >= n_pre) return q.own + (int64_t)(k - n_pre) * a.group;
+    return q.pre + (int64_t)(k / q.pre_sub) * q.pre_step + (k % q.pre_sub) * q.pre_span;
+  };
+  float M = -INFINITY;
+  for (int k = tid; k < n; k += kJoinWarps * 32) {
+    const float2 ml = a.part_ml[row_of(k)];
+    s_w[k] = ml.y == 0.f ? -INFINITY : fmaxf(ml.x, -3e38f);  // no tokens; a sum that is NaN stays one
+    M = fmaxf(M, s_w[k]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_red[0][w]);
+  // each warp takes every eighth part; its lanes the channels, its lane 0 the sum
+  float L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = warp; k0 < n; k0 += 4 * kJoinWarps) {
+    float4 v[4];
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * kJoinWarps;
+      const float mk = k < n ? s_w[k] : -INFINITY;
+      w[i] = 0.f;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mk != -INFINITY) {  // else o was not written
+        const int64_t row = row_of(k);
+        w[i] = ex2(mk - M);
+        v[i] = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
+        L = fmaf(w[i], a.part_ml[row].y, L);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      O.x = fmaf(w[i], v[i].x, O.x);
+      O.y = fmaf(w[i], v[i].y, O.y);
+      O.z = fmaf(w[i], v[i].z, O.z);
+      O.w = fmaf(w[i], v[i].w, O.w);
+    }
+  }
+  s_o[warp][lane] = O;
+  if (lane == 0) s_red[1][warp] = L;
+  __syncthreads();
+  if (tid < kD) {
+    float o = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      o += reinterpret_cast<const float*>(s_o[w])[tid];
+      sum += s_red[1][w];
+    }
+    out[r * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o / sum));
+  }
+}
+
+template <int BITS, int NB>
+cudaError_t go(const Args& a, int ctas, bool wait_first, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(k_shared_few<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Shape<BITS>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_shared_few<BITS, NB>, dim3(ctas), dim3(kThreads), (size_t)Shape<BITS>::kSmem, st, a,
+                    (int32_t)wait_first);
+}
+
+}  // namespace
+
+// The streaming kernel, then the join.  wait_first: no wide kernel came before.
+template <int BITS>
+cudaError_t launch_few(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st) {
+  const int ctas = a.few_workers / kFewWarps;
+  const cudaError_t e = a.plen ? go<BITS, 2>(a, ctas, wait_first, st) : go<BITS, 1>(a, ctas, wait_first, st);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_shared_join, dim3((unsigned)((int64_t)a.n_seq * a.n_heads * a.group)), dim3(kJoinWarps * 32), 0,
+                    st, a, out);
+}
+
+template cudaError_t launch_few<16>(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<8>(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);
+
+int few_tile(int bits) { return bits == 16 ? Shape<16>::kTok : Shape<8>::kTok; }
+
+}  // namespace shared
+}  // namespace bpkv

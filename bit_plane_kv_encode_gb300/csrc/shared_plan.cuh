@@ -1,0 +1,240 @@
+// How the shared-prefix attention's work is laid out: units, tiles, the cut of
+// the tiles over workers, and where the partial results go.
+//
+// A unit is a set of query rows that attend over the same KV rows: the query
+// heads of all sequences of one prefix, 256 at a time, for each KV head; and
+// for each sequence and KV head its own rows with its G query heads.  Units of
+// more than kFew rows belong to the tensor-core kernel (k_shared_wide, tiles of
+// kWideTile tokens, a CTA per worker), the others to the streaming kernel
+// (k_shared_few, a warp per worker).  Each kernel's tiles form one list, cut
+// into equal stretches, one per worker; a worker's part of a unit is a segment
+// and leaves its rows' (m, l, o).  Lengths are read on the device, so the cut
+// fits ragged batches; every CTA works the same plan out for itself.
+#pragma once
+
+#include "common.cuh"
+
+namespace bpkv {
+namespace shared {
+
+constexpr int kWideTile = 128;       // tokens of a wide tile, rows of a stream
+constexpr int kPair = 2 * kWideTile; // rows of a prefix unit
+constexpr int kFew = 16;             // rows a streaming unit has at most
+constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
+constexpr int kMaxPre = kMaxSeq + kMaxSeq * BPKV_MAX_GROUP / kPair;  // prefix items: one more per 256 rows
+constexpr int kMaxItems = kMaxPre + kMaxSeq;
+constexpr int kSms = 152;
+constexpr int kFewWarps = 8;         // per CTA of the streaming kernel
+
+// A query row's partials, as rows of the partial buffers: of each of pre_n
+// segments pre_sub copies, then of each of own_n segments one.
+struct Parts {
+  int64_t pre, own;   // first
+  int32_t pre_n, own_n;
+  int32_t pre_sub;    // 1, or the copies of both streams
+  int32_t pre_span;   // rows from one copy to the next
+  int32_t pre_step;   // rows from one segment to the next
+  int32_t pad;
+};
+
+struct Args {
+  const int32_t* prefix_of;
+  const int64_t* plen;  // NULL: no prefixes
+  const int64_t* len;
+  int64_t pcap, cap;
+  int32_t n_prefix, n_seq, n_heads, group;
+  const uint16_t* q;
+  const void* rows[2][2];     // [prefix, own][K, V]
+  const uint8_t* exps[2][2];  // scale exponents of 8-bit rows
+  Parts* parts;               // [N][H][G]
+  float* part_o;              // [rows][D]
+  float2* part_ml;            // [rows] maximum (log2 domain) and sum
+  int64_t few0, own0;         // first rows of the streaming kernel's prefix units and own units
+  int32_t* status;
+  int32_t wide_ctas, few_workers;
+  int32_t stages;             // of the wide kernel's ring
+};
+
+struct Plan {
+  int64_t wide[kMaxPre + 1];   // wide tiles before each prefix item, for one KV head
+  int64_t few[kMaxItems + 1];  // streaming tiles before each prefix item, then before each sequence
+  uint16_t order[kMaxSeq];     // sequences by prefix
+  uint16_t rank[kMaxSeq];      // each sequence's place among its prefix's
+  int16_t pof[kMaxSeq];        // prefix of each sequence, -1: none
+  uint16_t cnt[kMaxSeq];       // sequences of each prefix
+  uint16_t first[kMaxSeq];     // where they begin in order
+  uint16_t item0[kMaxSeq];     // first item of each prefix
+  uint16_t it_p[kMaxPre];      // prefix of each prefix item
+  int32_t n_pre;               // prefix items
+};
+
+__device__ __forceinline__ int64_t tokens_of(int64_t n, int64_t cap) { return max64(0, min64(n, cap)); }
+
+// Exclusive sums of n values in place, the total behind them; one warp.
+__device__ __forceinline__ void warp_sums(int64_t* v, int n) {
+  const int lane = threadIdx.x & 31;
+  int64_t sum = 0;
+  for (int b = 0; b < n; b += 32) {
+    const int64_t t = b + lane < n ? v[b + lane] : 0;
+    int64_t c = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += u;
+    }
+    if (b + lane < n) v[b + lane] = sum + c - t;
+    sum += __shfl_sync(0xffffffffu, c, 31);
+  }
+  if (lane == 0) v[n] = sum;
+}
+
+__device__ __forceinline__ int pre_rows(const Args& a, const Plan& p, int item) {
+  const int x = p.it_p[item];
+  return min(kPair, p.cnt[x] * a.group - (item - p.item0[x]) * kPair);
+}
+
+// All threads of the CTA; ends with a barrier.
+__device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+  const int P = a.plen ? a.n_prefix : 0, N = a.n_seq;
+  if (P > 0) {
+    for (int i = tid; i < N; i += nt) {
+      const int x = a.prefix_of ? a.prefix_of[i] : 0;
+      p.pof[i] = (int16_t)(x >= 0 && x < P ? x : -1);
+    }
+    for (int x = tid; x < P; x += nt) {
+      p.cnt[x] = 0;
+      p.wide[x] = tokens_of(a.plen[x], a.pcap);  // until the items are known
+    }
+    __syncthreads();
+    if (a.prefix_of) {
+      for (int i = tid; i < N; i += nt) {
+        const int x = p.pof[i];
+        int rank = 0, cnt = 0;
+        for (int j = 0; j < N; ++j) {
+          const bool same = p.pof[j] == x;
+          cnt += same;
+          rank += same && j < i;
+        }
+        if (x >= 0) p.cnt[x] = (uint16_t)cnt;
+        p.rank[i] = (uint16_t)rank;
+      }
+    } else {
+      for (int i = tid; i < N; i += nt) p.rank[i] = (uint16_t)i;
+      if (tid == 0) p.cnt[0] = (uint16_t)N;
+    }
+    __syncthreads();
+    if (tid < 32) {
+      int at = 0, item = 0;
+      for (int b = 0; b < P; b += 32) {
+        const int x = b + lane;
+        const int c = x < P ? p.cnt[x] : 0;
+        const int it = x < P && p.wide[x] > 0 ? (c * a.group + kPair - 1) / kPair : 0;
+        int sc = c, si = it;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, sc, o), w = __shfl_up_sync(0xffffffffu, si, o);
+          if (lane >= o) {
+            sc += u;
+            si += w;
+          }
+        }
+        if (x < P) {
+          p.first[x] = (uint16_t)(at + sc - c);
+          p.item0[x] = (uint16_t)(item + si - it);
+          for (int k = 0; k < it; ++k) p.it_p[item + si - it + k] = (uint16_t)x;
+        }
+        at += __shfl_sync(0xffffffffu, sc, 31);
+        item += __shfl_sync(0xffffffffu, si, 31);
+      }
+      if (lane == 0) p.n_pre = item;
+    }
+  } else {
+    for (int i = tid; i < N; i += nt) p.pof[i] = -1;
+    if (tid == 0) p.n_pre = 0;
+  }
+  __syncthreads();
+  const int n_pre = p.n_pre;
+  for (int i = tid; i < n_pre + N; i += nt) {
+    if (i < n_pre) {
+      const int64_t n = tokens_of(a.plen[p.it_p[i]], a.pcap);
+      const bool wide = pre_rows(a, p, i) > kFew;
+      p.wide[i] = wide ? (n + kWideTile - 1) / kWideTile : 0;
+      p.few[i] = wide ? 0 : (n + few_tile - 1) / few_tile;
+    } else {
+      const int s = i - n_pre, x = p.pof[s];
+      p.few[i] = (tokens_of(a.len[s], a.cap) + few_tile - 1) / few_tile;
+      if (x >= 0) p.order[p.first[x] + p.rank[s]] = (uint16_t)s;
+    }
+  }
+  __syncthreads();
+  if (tid < 32) warp_sums(p.few, n_pre + N);
+  else if (tid < 64) warp_sums(p.wide, n_pre);
+  __syncthreads();
+}
+
+// Worker w of n takes tiles [w T / n, (w + 1) T / n) of a list of T.
+struct Share {
+  int64_t total;
+  int64_t n;  // workers that take part: no more than tiles
+  __device__ Share(int64_t t, int64_t workers) : total(t), n(min64(t, workers)) {}
+  __device__ int64_t lo(int64_t w) const { return w * total / n; }
+  __device__ int64_t owner(int64_t tile) const { return ((tile + 1) * n - 1) / total; }
+};
+
+// Copies of a wide unit's rows among the 128 of a stream.  With 64 rows or
+// fewer the copies' softmax threads share the tile's tokens, so that all four
+// warps work; each copy has its own m, l and o.
+__device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 4 ? 4 : rows <= kWideTile / 2 ? 2 : 1; }
+
+// Partial rows of segment (unit, worker): the segments in order have ascending
+// unit + worker, each its own.
+__device__ __forceinline__ int64_t wide_row(const Args& a, int64_t unit, int64_t cta) { return (unit + cta) * kPair; }
+__device__ __forceinline__ int64_t few_row(const Args& a, int64_t unit, int64_t worker) {
+  return a.few0 + (unit + worker) * kFew;
+}
+__device__ __forceinline__ int64_t own_row(const Args& a, int64_t unit, int64_t worker) {
+  return a.own0 + (unit + worker) * a.group;
+}
+
+// Where the partials of query row r = (sequence, KV head, head of the group) will be.
+__device__ __forceinline__ Parts parts_of(const Args& a, const Plan& p, int64_t r) {
+  const Share wide(p.wide[p.n_pre] * a.n_heads, a.wide_ctas);
+  const Share few(p.few[p.n_pre + a.n_seq] * a.n_heads, a.few_workers);
+  const int g = (int)(r % a.group);
+  const int64_t u = r / a.group;
+  const int h = (int)(u % a.n_heads), i = (int)(u / a.n_heads);
+  Parts q = {};
+  const int x = p.pof[i];
+  const int row = x >= 0 ? p.rank[i] * a.group + g : 0, item = x >= 0 ? p.item0[x] + row / kPair : 0;
+  if (x >= 0 && item < p.n_pre && p.it_p[item] == x) {  // a prefix of length 0 has no items
+    const int in = row % kPair, rows = pre_rows(a, p, item);
+    const bool is_wide = rows > kFew;
+    const Share& share = is_wide ? wide : few;
+    const int64_t* sums = is_wide ? p.wide : p.few;
+    const int64_t tiles = sums[item + 1] - sums[item], at = sums[item] * a.n_heads + h * tiles;
+    const int64_t w0 = share.owner(at), unit = (int64_t)item * a.n_heads + h;
+    q.pre_n = (int)(share.owner(at + tiles - 1) - w0) + 1;
+    if (is_wide) {
+      q.pre = wide_row(a, unit, w0) + in;
+      q.pre_sub = rows > kWideTile ? 1 : 2 * copies_of(rows);
+      q.pre_span = kWideTile / copies_of(rows);
+      q.pre_step = kPair;
+    } else {
+      q.pre = few_row(a, unit, w0) + in;
+      q.pre_sub = 1;
+      q.pre_step = kFew;
+    }
+  }
+  const int own = p.n_pre + i;
+  const int64_t tiles = p.few[own + 1] - p.few[own], at = p.few[own] * a.n_heads + h * tiles;
+  if (tiles > 0) {
+    const int64_t w0 = few.owner(at);
+    q.own_n = (int)(few.owner(at + tiles - 1) - w0) + 1;
+    q.own = own_row(a, u, w0) + g;
+  }
+  return q;
+}
+
+}  // namespace shared
+}  // namespace bpkv
