@@ -35,7 +35,8 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = kWideTile;
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 16;                // eight a stream: two for each 32 rows
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
 constexpr int kRing16 = 32 * 1024;               // bytes of a stage: 128 rows of bf16
 constexpr int kRing8 = 16 * 1024;                // 128 rows of codes
 constexpr int kMaxStages = 10;
@@ -73,6 +74,9 @@ struct Smem {
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t q_full, q_empty, done;
   uint64_t sc_go[2], sc_full[2][2], sc_empty[2][2];
+  uint64_t pair[2][4];       // the two warps of 32 rows
+  float mx[2][2][kTile];     // by stream and half: the maximum of each row
+  float lx[2][kTile];        // the second halves' sums
 };
 
 // One CTA's part of a unit.
@@ -162,181 +166,245 @@ __device__ __forceinline__ float ex2(float x) {
 // 16 bytes of row r, chunk c of a 128-byte-row tile in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// The rows of q of one stream into shared memory, by its 128 threads.
+// One row's eight channels w of q as the products take them, r the row.
 template <int BITS>
-__device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segment& g, int s, unsigned char* dst,
-                                       float* qf) {
-  const int t = threadIdx.x & 127, l16 = t & 15;
-  const int rows = g.rows_of(s), base = g.row0 + (g.dual ? s * kTile : 0);
-  const int span = kTile / g.copies();
-  const int blocks = (rows + 7) / 8;  // of each copy
-  for (int b = 0; b < blocks * g.copies(); ++b) {
-    const int of = (b % blocks) * 8 + t / 16, r = b / blocks * span + of;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (of < rows) {
-      const int x = base + of;
-      const int seq = p.order[p.first[g.index] + x / a.group], head = x % a.group;
-      w = *reinterpret_cast<const uint4*>(a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
+__device__ __forceinline__ void put_q(const uint4& w, int r, int l16, bool there, unsigned char* dst, float* qf) {
+  if constexpr (BITS == 16) {
+    if (there) *reinterpret_cast<uint4*>(dst + (l16 / 8) * (kTile * 128) + swz(r, l16 & 7)) = w;
+  } else {
+    // x 2^-e with the row's largest magnitude in 128 .. 256: hi to 4 bits, lo the 4 (with its sign) below
+    uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = max(m & 0xffffu, m >> 16);
+    const int e = max(-100, (int)(m >> 7) - 127 - 7);
+    const float f = exp2i(-e);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h2[2], l2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x0 = __uint_as_float(ww[2 * i + j] << 16) * f;
+        const float x1 = __uint_as_float(ww[2 * i + j] & 0xffff0000u) * f;
+        h2[j] = e4m3x2(x0, x1);
+        const float2 y = __half22float2(half2_of_e4m3x2((uint16_t)h2[j]));
+        l2[j] = e4m3x2(x0 - y.x, x1 - y.y);
+      }
+      hi[i] = h2[0] | (h2[1] << 16);
+      lo[i] = l2[0] | (l2[1] << 16);
     }
-    if constexpr (BITS == 16) {
-      if (of < rows) *reinterpret_cast<uint4*>(dst + (l16 / 8) * (kTile * 128) + swz(r, l16 & 7)) = w;
-    } else {
-      // x 2^-e with the row's largest magnitude in 128 .. 256: hi to 4 bits, lo the 4 (with its sign) below
-      uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = max(m & 0xffffu, m >> 16);
-      const int e = max(-100, (int)(m >> 7) - 127 - 7);
-      const float f = exp2i(-e);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t h2[2], l2[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float x0 = __uint_as_float(ww[2 * i + j] << 16) * f;
-          const float x1 = __uint_as_float(ww[2 * i + j] & 0xffff0000u) * f;
-          h2[j] = e4m3x2(x0, x1);
-          const float2 y = __half22float2(half2_of_e4m3x2((uint16_t)h2[j]));
-          l2[j] = e4m3x2(x0 - y.x, x1 - y.y);
-        }
-        hi[i] = h2[0] | (h2[1] << 16);
-        lo[i] = l2[0] | (l2[1] << 16);
-      }
-      if (of < rows) {
-        const uint32_t at = swz(r, l16 >> 1) + (l16 & 1) * 8;
-        *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + kTile * 128 + at) = make_uint2(lo[0], lo[1]);
-        if (l16 == 0) qf[r] = exp2i(e);
-      }
+    if (there) {
+      const uint32_t at = swz(r, l16 >> 1) + (l16 & 1) * 8;
+      *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + kTile * 128 + at) = make_uint2(lo[0], lo[1]);
+      if (l16 == 0) qf[r] = exp2i(e);
     }
   }
 }
 
-// One tile of one query row: S from tensor memory, this thread's columns
-// (32 NCH of them, the part-th) to weights over it, zeros to the others; m and
-// l of the row's columns so far, and O when m moves.
-template <int BITS, int NCH>
-__device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int part, int valid, bool first, float qf,
-                                             const float* scales, float& m, float& l) {
-  constexpr int kCols = 32 * NCH, kHalves = NCH == 4 ? 2 : 1;
-  const int c0 = part * kCols;
-            float x[kCols];
-            uint32_t* xu = reinterpret_cast<uint32_t*>(x);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// The rows of q of one stream into shared memory, by its 256 threads (t), four
+// loads of each in flight.
+template <int BITS>
+__device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segment& g, int s, int t, unsigned char* dst,
+                                       float* qf) {
+  const int l16 = t & 15, rows = g.rows_of(s), span = kTile / g.copies();
+  const int base = g.row0 + (g.dual ? s * kTile : 0), first = p.first[g.index];
+#pragma unroll 1
+  for (int b = 0; b < kTile; b += 64) {
+    uint4 w[4];
 #pragma unroll
-  for (int k = 0; k < kCols; k += 32) {
-    tmem_ld32(ts + c0 + k, xu + k);
-    if (NCH == 4 && k == 32) wait_ld();  // the first half is looked at while the second comes
-  }
-#pragma unroll
-  for (int half = 0; half < kHalves; ++half) {
-    if (half || NCH < 4) wait_ld();
-    constexpr int kPer = kCols / kHalves;
-    if constexpr (BITS == 8) {
-#pragma unroll
-      for (int k = half * kPer; k < (half + 1) * kPer; k += 4) {
-        const float4 kf = *reinterpret_cast<const float4*>(scales + c0 + k);
-        const float4 ev = *reinterpret_cast<const float4*>(scales + kTile + c0 + k);
-        const F2 q2(qf, qf);
-        fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
-        fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
+    for (int i = 0; i < 4; ++i) {
+      const int of = (b + i * 16 + t / 16) & (span - 1);
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (of < rows) {
+        const uint32_t x = base + of, seq = p.order[first + x / (uint32_t)a.group], head = x % (uint32_t)a.group;
+        w[i] = *reinterpret_cast<const uint4*>(a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
       }
     }
-    if (valid < c0 + kCols) {
 #pragma unroll
-      for (int k = half * kPer; k < (half + 1) * kPer; ++k)
-        if (c0 + k >= valid) x[k] = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      const int r = b + i * 16 + t / 16;
+      put_q<BITS>(w[i], r, l16, (r & (span - 1)) < rows, dst, qf);
     }
-#pragma unroll
-    for (int k = half * kPer; k < (half + 1) * kPer; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
   }
-  const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-            constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
-            if (first) {
-              m = top;
-            } else {
-              const bool up = top > m + Range<BITS>::kLazy / kUnit;
-              if (__any_sync(0xffffffffu, up)) {
-                // S of this step is complete, so O of the stream's step before it is too
-                const float f = up ? ex2((m - top) * kUnit) : 1.f;
-                l *= f;
-                if (up) m = top;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  if constexpr (N >= 32) {
+#pragma unroll
+    for (int k = 0; k < N; k += 32) tmem_ld32(addr + k, r + k);
+  } else {
+    tmem_ld16(addr, r);
+  }
+}
+
+// What a softmax thread keeps of its row, in the two warps that share it.
+struct RowState {
+  float m, l;         // reference of the weights, and the sum of this thread's
+  float qf;           // scale of the row of q (8-bit rows)
+  float* mine;        // where this thread's maximum goes, and the other's is
+  const float* other;
+  uint32_t bar, phase;  // of the two warps
+  volatile uint32_t* abort;
+  // Both warps have arrived (false: gave up).
+  __device__ __forceinline__ bool meet() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort));
+    phase ^= 1;
+    return ok;
+  }
+};
+
+// One tile of one query row: S from tensor memory, this thread's COLS columns
+// (of the row's copy, the half-th) to weights over it, and zeros to columns of
+// other copies.  Both threads of a row read S before either writes over it, and
+// agree on the maximum; m follows it, and O, half by half, follows m.
+template <int BITS, int COLS>
+__device__ __forceinline__ bool softmax_step(RowState& st, uint32_t ts, uint32_t to, int copy, int half, int valid,
+                                             bool first, const float* scales) {
+  const int c0 = (copy * 2 + half) * COLS;
+  float x[COLS];
+  tmem_ld<COLS>(ts + c0, x);
+  wait_ld();
+  if constexpr (BITS == 8) {
+    const F2 q2(st.qf, st.qf);
+#pragma unroll
+    for (int k = 0; k < COLS; k += 4) {
+      const float4 kf = *reinterpret_cast<const float4*>(scales + c0 + k);
+      const float4 ev = *reinterpret_cast<const float4*>(scales + kTile + c0 + k);
+      fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
+      fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
+    }
+  }
+  if (valid < c0 + COLS) {
+#pragma unroll
+    for (int k = 0; k < COLS; ++k)
+      if (c0 + k >= valid) x[k] = -INFINITY;
+  }
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < COLS; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
+  float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+  *st.mine = top;
+  if (!st.meet()) return false;
+  top = fmaxf(top, *st.other);
+  constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
+  if (first) {
+    st.m = top;
+  } else {
+    const bool up = top > st.m + Range<BITS>::kLazy / kUnit;
+    if (__any_sync(0xffffffffu, up)) {
+      // S of this step is complete, so O of the stream's step before it is too
+      const float f = up ? ex2((st.m - top) * kUnit) : 1.f;
+      st.l *= f;
+      if (up) st.m = top;
 #pragma unroll 1
-                for (int k = 0; k < kD; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(to + k, o);
-                  wait_ld();
+      for (int k = half * 64; k < half * 64 + 64; k += 16) {
+        uint32_t o[16];
+        tmem_ld16(to + k, o);
+        wait_ld();
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  tmem_st16(to + k, o);
-                }
-              }
-            }
-            const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
-            const F2 base2(-base, -base), unit2(kUnit, kUnit);
-            F2 ls[4] = {F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f)};
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st16(to + k, o);
+      }
+    }
+  }
+  const float base = st.m == -INFINITY ? 0.f : fmaf(st.m, kUnit, -Range<BITS>::kShift);
+  const F2 base2(-base, -base), unit2(kUnit, kUnit);
+  F2 ls[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+  constexpr int kChunk = COLS < 32 ? COLS : 32;
 #pragma unroll
-            for (int k = 0; k < kCols; k += 32) {
-              if constexpr (BITS == 16) {
-                uint32_t p[16];
+  for (int k = 0; k < COLS; k += kChunk) {
+    if constexpr (BITS == 16) {
+      uint32_t p[kChunk / 2];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float p0, p1;
-                  fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
-                  p0 = ex2(p0);
-                  p1 = ex2(p1);
-                  ls[i & 3] = add2(ls[i & 3], F2(p0, p1));
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                  p[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                tmem_st16(ts + (c0 + k) / 2, p);
-              } else {
-                uint32_t hi[8], lo[8];
+      for (int i = 0; i < kChunk / 2; ++i) {
+        float p0, p1;
+        fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        ls[i & 1] = add2(ls[i & 1], F2(p0, p1));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+        p[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if constexpr (kChunk == 32) tmem_st16(ts + (c0 + k) / 2, p);
+      else tmem_st8(ts + (c0 + k) / 2, p);
+    } else {
+      uint32_t hi[kChunk / 4], lo[kChunk / 4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 iv = *reinterpret_cast<const float4*>(scales + 2 * kTile + c0 + k + i * 4);
-                  float p[4];
-                  add2(F2(x[k + 4 * i], x[k + 4 * i + 1]), base2).get(p[0], p[1]);
-                  add2(F2(x[k + 4 * i + 2], x[k + 4 * i + 3]), base2).get(p[2], p[3]);
+      for (int i = 0; i < kChunk / 4; ++i) {
+        const float4 iv = *reinterpret_cast<const float4*>(scales + 2 * kTile + c0 + k + i * 4);
+        float p[4];
+        add2(F2(x[k + 4 * i], x[k + 4 * i + 1]), base2).get(p[0], p[1]);
+        add2(F2(x[k + 4 * i + 2], x[k + 4 * i + 3]), base2).get(p[2], p[3]);
 #pragma unroll
-                  for (int c = 0; c < 4; ++c) p[c] = ex2(p[c]);
-                  ls[(2 * i) & 3] = fma2(F2(p[0], p[1]), F2(iv.x, iv.y), ls[(2 * i) & 3]);
-                  ls[(2 * i + 1) & 3] = fma2(F2(p[2], p[3]), F2(iv.z, iv.w), ls[(2 * i + 1) & 3]);
-                  // the upper byte of a half is the e5m2 number below it: adding
-                  // half a step first rounds (p is positive, the rest has a sign)
-                  uint32_t h[2], r[2];
+        for (int c = 0; c < 4; ++c) p[c] = ex2(p[c]);
+        ls[0] = fma2(F2(p[0], p[1]), F2(iv.x, iv.y), ls[0]);
+        ls[1] = fma2(F2(p[2], p[3]), F2(iv.z, iv.w), ls[1]);
+        // the upper byte of a half is the e5m2 number below it: adding half a
+        // step first rounds (p is positive, the rest has a sign)
+        uint32_t h[2], r[2];
 #pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    const __half2 v = __floats2half2_rn(p[2 * c], p[2 * c + 1]);
-                    h[c] = (*reinterpret_cast<const uint32_t*>(&v) + 0x00800080u) & 0xff00ff00u;
-                    const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&h[c]));
-                    r[c] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
-                  }
-                  hi[i] = __byte_perm(h[0], h[1], 0x7531);
-                  lo[i] = __byte_perm(r[0], r[1], 0x7531);
-                }
-                tmem_st8(ts + (c0 + k) / 4, hi);
-                tmem_st8(ts + 32 + (c0 + k) / 4, lo);
-              }
-            }
-            if constexpr (NCH < 4) {
+        for (int c = 0; c < 2; ++c) {
+          const __half2 v = __floats2half2_rn(p[2 * c], p[2 * c + 1]);
+          h[c] = (*reinterpret_cast<const uint32_t*>(&v) + 0x00800080u) & 0xff00ff00u;
+          const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&h[c]));
+          r[c] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
+        }
+        hi[i] = __byte_perm(h[0], h[1], 0x7531);
+        lo[i] = __byte_perm(r[0], r[1], 0x7531);
+      }
+      if constexpr (kChunk == 32) {
+        tmem_st8(ts + (c0 + k) / 4, hi);
+        tmem_st8(ts + 32 + (c0 + k) / 4, lo);
+      } else {
+        tmem_st4(ts + (c0 + k) / 4, hi);
+        tmem_st4(ts + 32 + (c0 + k) / 4, lo);
+      }
+    }
+  }
+  if constexpr (COLS < 64) {
     const uint32_t zero[16] = {};
 #pragma unroll
-    for (int k = 0; k < kTile; k += 32)
-      if (k / kCols != part) {
+    for (int k = 0; k < 4; ++k)  // 32 columns each
+      if (k * 32 / (2 * COLS) != copy && (k & 1) == half) {
         if constexpr (BITS == 16) {
-          tmem_st16(ts + k / 2, zero);
+          tmem_st16(ts + k * 16, zero);
         } else {
-          tmem_st8(ts + k / 4, zero);
-          tmem_st8(ts + 32 + k / 4, zero);
+          tmem_st8(ts + k * 8, zero);
+          tmem_st8(ts + 32 + k * 8, zero);
         }
       }
   }
   float l0, l1;
-            add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])).get(l0, l1);
-            l += l0 + l1;
+  add2(ls[0], ls[1]).get(l0, l1);
+  st.l += l0 + l1;
+  return true;
+}
+
+// Sixteen columns of this warp's rows, a row a lane, to sixteen bytes of four
+// neighbouring rows a lane: lane q of four ends with the rows' q-th four columns.
+__device__ __forceinline__ void quads(uint32_t (&r)[16]) {
+  const int q = threadIdx.x & 3;
+#pragma unroll
+  for (int u = 0; u < 4; u += 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 1 ? r[4 * u + i] : r[4 * u + 4 + i], 1);
+      if (q & 1) r[4 * u + i] = y;
+      else r[4 * u + 4 + i] = y;
+    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 2 ? r[i] : r[8 + i], 2);
+    if (q & 2) r[i] = y;
+    else r[8 + i] = y;
+  }
 }
 
 template <int BITS>
@@ -361,15 +429,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sm.s_full[s]), 1);
-      mbar_init(smem_u32(&sm.p_ready[s]), 4);
+      mbar_init(smem_u32(&sm.p_ready[s]), 8);
       mbar_init(smem_u32(&sm.o_done[s]), 1);
-      mbar_init(smem_u32(&sm.sc_go[s]), 4);
+      mbar_init(smem_u32(&sm.sc_go[s]), 8);
+      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.pair[s][w]), 2);
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&sm.sc_full[s][b]), 1);
-        mbar_init(smem_u32(&sm.sc_empty[s][b]), 4);
+        mbar_init(smem_u32(&sm.sc_empty[s][b]), 8);
       }
     }
-    mbar_init(smem_u32(&sm.q_full), 8);
+    mbar_init(smem_u32(&sm.q_full), kSoftmaxWarps);
     mbar_init(smem_u32(&sm.q_empty), 1);
     mbar_init(smem_u32(&sm.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -388,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
   Segment g;
 
   if (warp < 4) {
-    // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
-    regs_fewer<80>();
+    // registers: 128 x 64 + 512 x 104 of the launch's 640 x 96
+    regs_fewer<64>();
   if (warp == 0) {
     if (elect_one()) {
       // ---- loads: K then V of every tile
@@ -548,12 +617,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
     }
   }
   } else {
-    // ---- softmax of stream s, a thread per row
-    regs_more<208>();
-    const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
+    // ---- softmax of stream s: two threads a row, each half of its columns
+    regs_more<104>();
+    const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
     uint32_t tile_no = 0, seg = 0, s_phase = 0, o_phase = 0, n = 0;
+    RowState st = {};
+    st.mine = &sm.mx[s][half][row];
+    st.other = &sm.mx[s][half ^ 1][row];
+    st.bar = smem_u32(&sm.pair[s][w4]);
+    st.abort = abort;
     bool ok = true;
     while (ok && walk.next(g)) {
       if (seg > 0) {
@@ -563,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
       if (g.dual || s == 0) {
         float* qf = nullptr;
         if constexpr (BITS == 8) qf = sm.sc.qf[seg & 1][g.dual ? s : 0];
-        load_q<BITS>(a, sm.plan, g, s, q_smem + (g.dual ? s : 0) * S::kQ, qf);
+        load_q<BITS>(a, sm.plan, g, s, half * 128 + row, q_smem + (g.dual ? s : 0) * S::kQ, qf);
         fence_async_shared();
       }
       __syncwarp();
@@ -571,26 +645,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
       // also keeps a stream without a tile here from arriving for the next segment early
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_full), seg & 1, abort));
       if (!ok) break;
-      float qf = 1.f;
-      if constexpr (BITS == 8) qf = sm.sc.qf[seg & 1][g.dual ? s : 0][row];
+      if constexpr (BITS == 8) st.qf = sm.sc.qf[seg & 1][g.dual ? s : 0][row];
       const int rows = g.rows_of(s), steps = g.steps_of(s), copies = g.copies();
-      const int span = kTile / copies, r = row % span;  // this thread's row of the unit
+      const int r = row & (kTile / copies - 1), copy = row / (kTile / copies);  // this thread's row of the unit
       if (BITS == 8 && steps > 0 && lane == 0) mbar_arrive(smem_u32(&sm.sc_go[s]));
       const bool active = r - lane < rows;
-      float m = -INFINITY, l = 0.f;
+      st.m = -INFINITY;
+      st.l = 0.f;
       for (int j = 0; j < steps; ++j, ++n) {
         const int t = g.tile_of(s, j), valid = g.valid(t), b = n & 1;
         ok = mbar_wait(smem_u32(&sm.s_full[s]), s_phase, abort);
         if (BITS == 8) ok = ok && mbar_wait(smem_u32(&sm.sc_full[s][b]), (n >> 1) & 1, abort);
         if (valid < kTile && (!g.dual || s == 0)) {
           // rows of V past the last token may hold anything: zeros, so that 0 x does not become NaN
-          const uint32_t use = 2 * (tile_no + t) + 1, st = use % n_stage;
-          ok = ok && mbar_wait(smem_u32(&sm.full[st]), (use / n_stage) & 1, abort);
+          const uint32_t use = 2 * (tile_no + t) + 1, stage = use % n_stage;
+          ok = ok && mbar_wait(smem_u32(&sm.full[stage]), (use / n_stage) & 1, abort);
           if (ok) {
             constexpr int kChunks = BITS == 16 ? 16 : 8;  // 16-byte pieces of a row
-            for (int x = row; x < (kTile - valid) * kChunks; x += kTile) {
-              const int r = valid + x / kChunks, c = x % kChunks;
-              *reinterpret_cast<uint4*>(ring + st * S::kStage + (c / 8) * (kTile * 128) + r * 128 + (c % 8) * 16) =
+            for (int x = half * 128 + row; x < (kTile - valid) * kChunks; x += 2 * kTile) {
+              const int v = valid + x / kChunks, c = x % kChunks;
+              *reinterpret_cast<uint4*>(ring + stage * S::kStage + (c / 8) * (kTile * 128) + v * 128 + (c % 8) * 16) =
                   make_uint4(0, 0, 0, 0);
             }
             fence_async_shared();
@@ -603,9 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
           fence_after();
           const float* scales = nullptr;
           if constexpr (BITS == 8) scales = sm.sc.tok[s][b][0];
-          if (copies == 1) softmax_step<BITS, 4>(ts, to, 0, valid, j == 0, qf, scales, m, l);
-          else if (copies == 2) softmax_step<BITS, 2>(ts, to, w4 >> 1, valid, j == 0, qf, scales, m, l);
-          else softmax_step<BITS, 1>(ts, to, w4, valid, j == 0, qf, scales, m, l);
+          if (copies == 1) ok = softmax_step<BITS, 64>(st, ts, to, 0, half, valid, j == 0, scales);
+          else if (copies == 2) ok = softmax_step<BITS, 32>(st, ts, to, copy, half, valid, j == 0, scales);
+          else ok = softmax_step<BITS, 16>(st, ts, to, copy, half, valid, j == 0, scales);
+          if (!ok) break;
           wait_st();
           fence_before();
         }
@@ -624,21 +699,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
       if (active) {
         fence_after();
         const int64_t at = wide_row(a, g.unit, blockIdx.x) + s * kTile + row;
-        float* po = a.part_o + at * kD;
         if (steps > 0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t o[32];
-            tmem_ld32(to + k * 32, o);
+          if (half) sm.lx[s][row] = st.l;
+          if (!(ok = st.meet())) break;
+          const int q = lane & 3;
+          float* po = a.part_o + (at - q) * kD + half * 64 + q * 4;
+#pragma unroll 1
+          for (int k = 0; k < 64; k += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + half * 64 + k, o);
             wait_ld();
-            if (r < rows) {
+            quads(o);
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(po + k * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            }
+            for (int i = 0; i < 4; ++i)
+              if (r - q + i < rows)
+                *reinterpret_cast<uint4*>(po + i * kD + k) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-        if (r < rows) a.part_ml[at] = make_float2(m * (BITS == 16 ? kLogScale : 1.f), l);
+        if (!half && r < rows)
+          a.part_ml[at] = make_float2(st.m * (BITS == 16 ? kLogScale : 1.f), st.l + (steps > 0 ? sm.lx[s][row] : 0.f));
         fence_before();
       }
       tile_no += g.tiles;
