@@ -1,10 +1,26 @@
 // Rows of a KV cache quantised to 8 bits as they are written, and read back.
+//
+// Bound by bytes.  Sixteen lanes take a row of K and the same row of V, eight
+// channels each (16 bytes of bf16, 8 of codes); with many rows each group
+// takes four, its loads issued together, so that enough bytes are in flight.
+// The rows' exponent bytes of a CTA meet in shared memory and leave as runs of
+// neighbouring bytes.
 #include "rows8_core.cuh"
 
 namespace bpkv {
 
 constexpr int kR8Threads = 256;
-constexpr int kR8Rows = kR8Threads / 16;  // rows a CTA holds at once
+constexpr int kR8Groups = kR8Threads / 16;
+constexpr int kR8Many = 4;  // rows of a group when there are many
+
+// Rows per group: four once that still leaves every SM some CTAs.
+bool many_rows(int64_t rows) { return rows >= (int64_t)152 * 4 * kR8Groups * kR8Many; }
+
+// r = u n + t, in 32 bits where that is enough.
+__device__ __forceinline__ void split(int64_t r, int32_t n, int64_t& u, int64_t& t) {
+  u = r < (1ll << 32) ? (int64_t)((uint32_t)r / (uint32_t)n) : r / n;
+  t = r - u * n;
+}
 
 struct AppendArgs {
   Rows8Out c;
@@ -15,34 +31,60 @@ struct AppendArgs {
   int32_t n_seq, n_heads, t_new, bump;
 };
 
-__global__ void __launch_bounds__(kR8Threads) k_rows8_append(AppendArgs a) {
+template <int R>
+__global__ void __launch_bounds__(kR8Threads) k_rows8_append(const __grid_constant__ AppendArgs a) {
   pdl_enter();
-  const int l16 = threadIdx.x & 15;
-  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.t_new;
-  const int64_t r = (int64_t)blockIdx.x * kR8Rows + threadIdx.x / 16;
-  const bool there = r < rows;
-  uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-  int64_t dst = 0;
-  bool store = false;
-  if (there) {
-    const int64_t unit = r / a.t_new, t = r % a.t_new;
-    const int64_t s = unit / a.n_heads;
-    const int64_t p = a.start[s];
-    store = rows8_fits(p, a.t_new, a.c.cap);
-    dst = unit * a.c.cap + p + t;
-    if (store) {
-      kw = *reinterpret_cast<const uint4*>(a.k_new + r * kD + l16 * 8);
-      vw = *reinterpret_cast<const uint4*>(a.v_new + r * kD + l16 * 8);
-    }
-    if (t == 0 && unit % a.n_heads == 0 && l16 == 0) {
-      if (!store)
-        set_status(a.status, BPKV_DEV_OVERFLOW);
-      else if (!a.bump)
-        a.c.seq_len[s] = p + a.t_new;
+  __shared__ uint8_t s_exp[2][kR8Groups * R];
+  __shared__ int64_t s_dst[kR8Groups * R];  // -1: not written
+  const int tid = threadIdx.x, l16 = tid & 15, grp = tid >> 4;
+  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.t_new, r0 = (int64_t)blockIdx.x * (kR8Groups * R);
+  uint4 w[R][2];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + i * kR8Groups + grp;
+    w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      w[i][0] = *reinterpret_cast<const uint4*>(a.k_new + r * kD + l16 * 8);
+      w[i][1] = *reinterpret_cast<const uint4*>(a.v_new + r * kD + l16 * 8);
     }
   }
-  store_row8(kw, a.c.k8, a.c.kexp, dst, l16, store);
-  store_row8(vw, a.c.v8, a.c.vexp, dst, l16, store);
+  if (tid < kR8Groups * R) {
+    const int64_t r = r0 + tid;
+    int64_t dst = -1;
+    if (r < rows) {
+      int64_t unit, t, s, h;
+      split(r, a.t_new, unit, t);
+      split(unit, a.n_heads, s, h);
+      const int64_t p = a.start[s];
+      if (rows8_fits(p, a.t_new, a.c.cap)) dst = unit * a.c.cap + p + t;
+      if (t == 0 && h == 0) {
+        if (dst < 0)
+          set_status(a.status, BPKV_DEV_OVERFLOW);
+        else if (!a.bump)
+          a.c.seq_len[s] = p + a.t_new;
+      }
+    }
+    s_dst[tid] = dst;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t dst = s_dst[i * kR8Groups + grp];
+    const int ke = row_exponent(w[i][0]), ve = row_exponent(w[i][1]);
+    if (l16 == 0) {
+      s_exp[0][i * kR8Groups + grp] = (uint8_t)(ke + kExpBias);
+      s_exp[1][i * kR8Groups + grp] = (uint8_t)(ve + kExpBias);
+    }
+    if (dst >= 0) {
+      *reinterpret_cast<uint2*>(a.c.k8 + dst * kD + l16 * 8) = row_codes(w[i][0], ke);
+      *reinterpret_cast<uint2*>(a.c.v8 + dst * kD + l16 * 8) = row_codes(w[i][1], ve);
+    }
+  }
+  __syncthreads();
+  if (tid < 2 * kR8Groups * R) {
+    const int kv = tid / (kR8Groups * R), x = tid % (kR8Groups * R);
+    if (s_dst[x] >= 0) (kv ? a.c.vexp : a.c.kexp)[s_dst[x]] = s_exp[kv][x];
+  }
 }
 
 // Lengths after an append at the lengths themselves, once every CTA has read them.
@@ -63,8 +105,9 @@ cudaError_t launch_rows8_append(const bpkv_rows8& c, const uint16_t* k_new, cons
   AppendArgs a{{c.k8, c.v8, c.kexp, c.vexp, c.seq_len, c.cap_tokens}, k_new, v_new, bump ? c.seq_len : start, status,
                c.n_seq, c.n_kv_heads, t_new, bump ? 1 : 0};
   const int64_t rows = (int64_t)c.n_seq * c.n_kv_heads * t_new;
-  const cudaError_t e =
-      launch_pdl(k_rows8_append, dim3((unsigned)((rows + kR8Rows - 1) / kR8Rows)), dim3(kR8Threads), 0, st, a);
+  const int per = kR8Groups * (many_rows(rows) ? kR8Many : 1);
+  const cudaError_t e = launch_pdl(many_rows(rows) ? k_rows8_append<kR8Many> : k_rows8_append<1>,
+                                   dim3((unsigned)((rows + per - 1) / per)), dim3(kR8Threads), 0, st, a);
   if (e != cudaSuccess || !bump) return e;
   return launch_rows8_bump(c, t_new, st);
 }
@@ -84,27 +127,45 @@ __device__ __forceinline__ uint32_t bf16x2_of(uint16_t codes, float s) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__global__ void __launch_bounds__(kR8Threads) k_rows8_read(ReadArgs a) {
+template <int R>
+__global__ void __launch_bounds__(kR8Threads) k_rows8_read(const __grid_constant__ ReadArgs a) {
   pdl_enter();
   const int l16 = threadIdx.x & 15;
   const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.n;
-  const int64_t r = (int64_t)blockIdx.x * kR8Rows + threadIdx.x / 16;
-  if (r >= rows) return;
-  const int64_t unit = r / a.n, x = a.t0 + r % a.n;
-  const bool there = x < min64(a.seq_len[unit / a.n_heads], a.cap);
+  const int64_t r0 = (int64_t)blockIdx.x * (kR8Groups * R) + threadIdx.x / 16;
+  uint2 c[R][2];
+  int e[R][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!a.out[i]) continue;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (there) {
-      const int64_t row = unit * a.cap + x;
-      const uint2 c = *reinterpret_cast<const uint2*>(a.codes[i] + row * kD + l16 * 8);
-      const int e = min(max((int)a.exps[i][row] - kExpBias, kExpMin), kExpMax);
-      const float s = exp2i(e);
-      w = make_uint4(bf16x2_of(c.x & 0xffffu, s), bf16x2_of(c.x >> 16, s), bf16x2_of(c.y & 0xffffu, s),
-                     bf16x2_of(c.y >> 16, s));
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + i * kR8Groups;
+    c[i][0] = c[i][1] = make_uint2(0, 0);
+    e[i][0] = e[i][1] = 0;
+    if (r < rows) {
+      int64_t unit, t, s, h;
+      split(r, a.n, unit, t);
+      split(unit, a.n_heads, s, h);
+      if (a.t0 + t < min64(a.seq_len[s], a.cap)) {
+        const int64_t row = unit * a.cap + a.t0 + t;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+          if (a.out[kv]) {
+            c[i][kv] = *reinterpret_cast<const uint2*>(a.codes[kv] + row * kD + l16 * 8);
+            e[i][kv] = a.exps[kv][row];
+          }
+      }
     }
-    *reinterpret_cast<uint4*>(a.out[i] + r * kD + l16 * 8) = w;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + i * kR8Groups;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      if (r < rows && a.out[kv]) {
+        const float f = exp2i(min(max(e[i][kv] - kExpBias, kExpMin), kExpMax));
+        const uint2 x = c[i][kv];
+        *reinterpret_cast<uint4*>(a.out[kv] + r * kD + l16 * 8) = make_uint4(
+            bf16x2_of(x.x & 0xffffu, f), bf16x2_of(x.x >> 16, f), bf16x2_of(x.y & 0xffffu, f), bf16x2_of(x.y >> 16, f));
+      }
   }
 }
 
@@ -112,7 +173,9 @@ cudaError_t launch_rows8_read(const bpkv_rows8& c, int64_t t0, int32_t n, uint16
                               cudaStream_t st) {
   ReadArgs a{{c.k8, c.v8}, {c.kexp, c.vexp}, {k_out, v_out}, c.seq_len, c.cap_tokens, t0, c.n_seq, c.n_kv_heads, n};
   const int64_t rows = (int64_t)c.n_seq * c.n_kv_heads * n;
-  return launch_pdl(k_rows8_read, dim3((unsigned)((rows + kR8Rows - 1) / kR8Rows)), dim3(kR8Threads), 0, st, a);
+  const int per = kR8Groups * (many_rows(rows) ? kR8Many : 1);
+  return launch_pdl(many_rows(rows) ? k_rows8_read<kR8Many> : k_rows8_read<1>, dim3((unsigned)((rows + per - 1) / per)),
+                    dim3(kR8Threads), 0, st, a);
 }
 
 }  // namespace bpkv
