@@ -34,9 +34,14 @@ __device__ __forceinline__ __half2 half2_of_e4m3x2(uint16_t c) {
   return *reinterpret_cast<__half2*>(&r);
 }
 
+// Magnitude bits of eight bf16 channels: the largest of each half of the words.
+__device__ __forceinline__ uint32_t abs_max(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+}
+
 // Scale exponent of a row from the 8 bf16 channels w of each of its 16 lanes.
 __device__ __forceinline__ int row_exponent(const uint4& w) {
-  uint32_t a = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  uint32_t a = abs_max(w);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, o));
   return rows8_exponent(max(a & 0xffffu, a >> 16));
@@ -64,16 +69,6 @@ struct Rows8Out {
 
 __host__ __device__ __forceinline__ bool rows8_fits(int64_t start, int64_t t_new, int64_t cap) {
   return start >= 0 && start <= cap - t_new;
-}
-
-// Sixteen lanes store the codes of a row they hold (lane l16 of the row; all
-// 32 lanes of the warp take part in the shuffles, `store` says which write).
-__device__ __forceinline__ void store_row8(const uint4& w, uint8_t* codes, uint8_t* exps, int64_t row, int l16,
-                                           bool store) {
-  const int e = row_exponent(w);
-  if (!store) return;
-  *reinterpret_cast<uint2*>(codes + row * kD + l16 * 8) = row_codes(w, e);
-  if (l16 == 0) exps[row] = (uint8_t)(e + kExpBias);
 }
 
 }  // namespace bpkv
