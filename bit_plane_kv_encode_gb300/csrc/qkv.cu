@@ -86,7 +86,7 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* y) {
 }
 
 template <int ROT>
-__global__ void __launch_bounds__(kQkvThreads) k_qkv_rope(const __grid_constant__ QkvArgs a) {
+__global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_constant__ QkvArgs a) {
   pdl_enter();
   __shared__ __align__(16) float4 s_tab[2][kQkvTokens][32];
   __shared__ __align__(16) float4 s_w[2][2][16];  // [query, key][first, second four][eight channels]

@@ -125,7 +125,7 @@ struct Walk {
     while (p.wide[item + 1] * a.n_heads <= pos) ++item;
     const int64_t tiles = p.wide[item + 1] - p.wide[item];
     const int64_t off = pos - p.wide[item] * a.n_heads;
-    s.h = (int)(off / tiles);
+    s.h = (int)quot(off, tiles);
     s.tile0 = off - s.h * tiles;
     s.tiles = (int)min64(tiles - s.tile0, end - pos);
     s.index = p.it_p[item];

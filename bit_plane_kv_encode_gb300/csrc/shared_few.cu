@@ -67,7 +67,7 @@ struct Walk {
     item = lo;
     const int64_t off = pos - p.few[item] * a.n_heads;
     tiles = p.few[item + 1] - p.few[item];
-    h = (int)(off / tiles);
+    h = (int)quot(off, tiles);
     t = off - h * tiles;
     set();
   }
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
   const int worker = warp * gridDim.x + blockIdx.x;
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   unsigned char* exps = smem + kFewWarps * kStages * kStage + warp * kStages * S::kExps;
-  Walk ahead(plan, a, worker, S::kTok), cur(plan, a, worker, S::kTok);
+  Walk ahead(plan, a, worker, S::kTok), cur = ahead;
   for (int i = 0; i < kStages - 1; ++i) {
     if (ahead.more()) {
       load_tile<BITS>(ahead, ring + i * kStage, smem_u32(exps) + i * S::kExps);
@@ -458,74 +458,98 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
   if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l, a CTA per query row
+// ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l
+//
+// W warps a row; each takes every W-th part, with its own running maximum, so
+// that a part's (m, l) and o are loaded together: two round trips in all, the
+// table's and the parts'.  Many rows have few parts each and take one warp,
+// few rows have many and take eight.
 
 constexpr int kJoinWarps = 8;
-constexpr int kMaxParts = 8 * (kSms + 1) + kSms * kFewWarps + kSms * kFewWarps;
+constexpr int kJoinDeep = 8;  // parts in flight
 
+template <int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_constant__ Args a, uint16_t* out) {
   pdl_enter();
-  __shared__ float s_w[kMaxParts];
-  __shared__ float s_red[2][kJoinWarps];
   __shared__ float4 s_o[kJoinWarps][kD / 4];
-  const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Parts q = a.parts[r];
-  const int n_pre = q.pre_n * q.pre_sub, n = n_pre + q.own_n;
-  auto row_of = [&](int k) -> int64_t {
-    if (k >= n_pre) return q.own + (int64_t)(k - n_pre) * a.group;
-    return q.pre + (int64_t)(k / q.pre_sub) * q.pre_step + (k % q.pre_sub) * q.pre_span;
-  };
-  float M = -INFINITY;
-  for (int k = tid; k < n; k += kJoinWarps * 32) {
-    const float2 ml = a.part_ml[row_of(k)];
-    s_w[k] = ml.y == 0.f ? -INFINITY : fmaxf(ml.x, -3e38f);  // no tokens; a sum that is NaN stays one
-    M = fmaxf(M, s_w[k]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[0][warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_red[0][w]);
-  // each warp takes every eighth part; its lanes the channels, its lane 0 the sum
-  float L = 0.f;
+  __shared__ float2 s_ml[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part0 = warp % W;
+  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.group;
+  const int64_t r = (int64_t)blockIdx.x * (kJoinWarps / W) + warp / W;
+  float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = warp; k0 < n; k0 += 4 * kJoinWarps) {
-    float4 v[4];
-    float w[4];
+  if (r < rows) {
+    const Parts q = a.parts[r];
+    const int n_pre = q.pre_n * q.pre_sub, n = n_pre + q.own_n;
+    for (int k0 = part0; k0 < n; k0 += W * kJoinDeep) {
+      float2 ml[kJoinDeep];
+      float4 o[kJoinDeep];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = k0 + i * kJoinWarps;
-      const float mk = k < n ? s_w[k] : -INFINITY;
-      w[i] = 0.f;
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mk != -INFINITY) {  // else o was not written
-        const int64_t row = row_of(k);
-        w[i] = ex2(mk - M);
-        v[i] = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
-        L = fmaf(w[i], a.part_ml[row].y, L);
+      for (int i = 0; i < kJoinDeep; ++i) {
+        const int k = k0 + i * W;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (k < n) {
+          const uint32_t seg = q.pre_sub > 1 ? (uint32_t)k / (uint32_t)q.pre_sub : k;
+          const int64_t row = k < n_pre
+                                  ? q.pre + (int64_t)seg * q.pre_step + (k - (int)seg * q.pre_sub) * q.pre_span
+                                  : q.own + (int64_t)(k - n_pre) * a.group;
+          ml[i] = a.part_ml[row];
+          o[i] = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kJoinDeep; ++i) {
+        if (ml[i].y != 0.f) ml[i].x = fmaxf(ml[i].x, -3e38f);  // a sum that is NaN stays one
+        top = fmaxf(top, ml[i].y != 0.f ? ml[i].x : -INFINITY);
+      }
+      if (top == -INFINITY) continue;
+      const float f = ex2(M - top);
+      M = top;
+      L *= f;
+      O.x *= f;
+      O.y *= f;
+      O.z *= f;
+      O.w *= f;
+#pragma unroll
+      for (int i = 0; i < kJoinDeep; ++i) {
+        if (ml[i].y == 0.f) continue;  // no tokens: o was not written
+        const float w = ex2(ml[i].x - M);
+        L = fmaf(w, ml[i].y, L);
+        O.x = fmaf(w, o[i].x, O.x);
+        O.y = fmaf(w, o[i].y, O.y);
+        O.z = fmaf(w, o[i].z, O.z);
+        O.w = fmaf(w, o[i].w, O.w);
       }
     }
+  }
+  if constexpr (W > 1) {
+    s_o[warp][lane] = O;
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (part0 != 0) return;
+    float top = M;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      O.x = fmaf(w[i], v[i].x, O.x);
-      O.y = fmaf(w[i], v[i].y, O.y);
-      O.z = fmaf(w[i], v[i].z, O.z);
-      O.w = fmaf(w[i], v[i].w, O.w);
+    for (int w = 1; w < W; ++w) top = fmaxf(top, s_ml[warp + w].x);
+    const float f = top == -INFINITY ? 0.f : ex2(M - top);
+    L *= f;
+    O = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float2 ml = s_ml[warp + w];
+      const float g = ml.y == 0.f ? 0.f : ex2(ml.x - top);
+      const float4 v = s_o[warp + w][lane];
+      L = fmaf(g, ml.y, L);
+      O.x = fmaf(g, v.x, O.x);
+      O.y = fmaf(g, v.y, O.y);
+      O.z = fmaf(g, v.z, O.z);
+      O.w = fmaf(g, v.w, O.w);
     }
   }
-  s_o[warp][lane] = O;
-  if (lane == 0) s_red[1][warp] = L;
-  __syncthreads();
-  if (tid < kD) {
-    float o = 0.f, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      o += reinterpret_cast<const float*>(s_o[w])[tid];
-      sum += s_red[1][w];
-    }
-    out[r * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o / sum));
+  if (r < rows) {
+    const float s = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2*>(out + r * kD + lane * 4) =
+        make_uint2(pack<16>(O.x * s, O.y * s), pack<16>(O.z * s, O.w * s));
   }
 }
 
@@ -546,8 +570,11 @@ cudaError_t launch_few(const Args& a, bool wait_first, uint16_t* out, cudaStream
   const int ctas = a.few_workers / kFewWarps;
   const cudaError_t e = a.plen ? go<BITS, 2>(a, ctas, wait_first, st) : go<BITS, 1>(a, ctas, wait_first, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_shared_join, dim3((unsigned)((int64_t)a.n_seq * a.n_heads * a.group)), dim3(kJoinWarps * 32), 0,
-                    st, a, out);
+  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.group;
+  const int warps = rows <= 152 * 4 ? 8 : rows <= 152 * 16 ? 2 : 1;
+  const auto join = warps == 8 ? k_shared_join<8> : warps == 2 ? k_shared_join<2> : k_shared_join<1>;
+  return launch_pdl(join, dim3((unsigned)((rows * warps + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, st, a,
+                    out);
 }
 
 template cudaError_t launch_few<16>(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);

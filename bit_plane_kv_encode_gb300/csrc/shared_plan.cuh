@@ -68,6 +68,13 @@ struct Plan {
   int32_t n_pre;               // prefix items
 };
 
+// a / b of numbers that are not negative; in 32 bits where they fit, which they
+// nearly always do: a 64-bit division is some 100 dependent instructions.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 __device__ __forceinline__ int64_t tokens_of(int64_t n, int64_t cap) { return max64(0, min64(n, cap)); }
 
 // Exclusive sums of n values in place, the total behind them; one warp.
@@ -178,8 +185,8 @@ struct Share {
   int64_t total;
   int64_t n;  // workers that take part: no more than tiles
   __device__ Share(int64_t t, int64_t workers) : total(t), n(min64(t, workers)) {}
-  __device__ int64_t lo(int64_t w) const { return w * total / n; }
-  __device__ int64_t owner(int64_t tile) const { return ((tile + 1) * n - 1) / total; }
+  __device__ int64_t lo(int64_t w) const { return quot(w * total, n); }
+  __device__ int64_t owner(int64_t tile) const { return quot((tile + 1) * n - 1, total); }
 };
 
 // Copies of a wide unit's rows among the 128 of a stream.  With 64 rows or
@@ -201,9 +208,8 @@ __device__ __forceinline__ int64_t own_row(const Args& a, int64_t unit, int64_t 
 __device__ __forceinline__ Parts parts_of(const Args& a, const Plan& p, int64_t r) {
   const Share wide(p.wide[p.n_pre] * a.n_heads, a.wide_ctas);
   const Share few(p.few[p.n_pre + a.n_seq] * a.n_heads, a.few_workers);
-  const int g = (int)(r % a.group);
-  const int64_t u = r / a.group;
-  const int h = (int)(u % a.n_heads), i = (int)(u / a.n_heads);
+  const int64_t u = quot(r, a.group);
+  const int g = (int)(r - u * a.group), i = (int)quot(u, a.n_heads), h = (int)(u - (int64_t)i * a.n_heads);
   Parts q = {};
   const int x = p.pof[i];
   const int row = x >= 0 ? p.rank[i] * a.group + g : 0, item = x >= 0 ? p.item0[x] + row / kPair : 0;
