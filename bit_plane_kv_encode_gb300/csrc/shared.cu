@@ -35,12 +35,13 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = kWideTile;
-constexpr int kSoftmaxWarps = 16;                // eight a stream: two for each 32 rows
+constexpr int kSoftmaxWarps = 8;                 // four a stream, a thread per row
 constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
 constexpr int kRing16 = 32 * 1024;               // bytes of a stage: 128 rows of bf16
 constexpr int kRing8 = 16 * 1024;                // 128 rows of codes
 constexpr int kMaxStages = 10;
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
+constexpr int kSfu = 4;  // of eight weights, those by the special function unit (two at a time)
 constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
 
 // How far the maximum may pass m before O is rescaled, and where exp2's
@@ -74,9 +75,8 @@ struct Smem {
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t q_full, q_empty, done;
   uint64_t sc_go[2], sc_full[2][2], sc_empty[2][2];
-  uint64_t pair[2][4];       // the two warps of 32 rows
-  float mx[2][2][kTile];     // by stream and half: the maximum of each row
-  float lx[2][kTile];        // the second halves' sums
+  uint64_t p_half[2], fin;
+  float2 ml[2][kTile];  // each row's maximum and sum, where both streams hold the rows
 };
 
 // One CTA's part of a unit.
@@ -166,145 +166,134 @@ __device__ __forceinline__ float ex2(float x) {
 // 16 bytes of row r, chunk c of a 128-byte-row tile in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// One row's eight channels w of q as the products take them, r the row.
+// The rows of q of one stream into shared memory, by n threads (t): all rows'
+// copies are issued, then awaited.  For 8-bit products a row's sixteen lanes
+// turn what they copied, in place, into two e4m3 pieces under a power of two:
+// x 2^-e with the row's largest magnitude in 128 .. 256, hi to 4 bits, lo the 4
+// (with its sign) below.
 template <int BITS>
-__device__ __forceinline__ void put_q(const uint4& w, int r, int l16, bool there, unsigned char* dst, float* qf) {
-  if constexpr (BITS == 16) {
-    if (there) *reinterpret_cast<uint4*>(dst + (l16 / 8) * (kTile * 128) + swz(r, l16 & 7)) = w;
-  } else {
-    // x 2^-e with the row's largest magnitude in 128 .. 256: hi to 4 bits, lo the 4 (with its sign) below
-    uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = max(m & 0xffffu, m >> 16);
-    const int e = max(-100, (int)(m >> 7) - 127 - 7);
-    const float f = exp2i(-e);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t h2[2], l2[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x0 = __uint_as_float(ww[2 * i + j] << 16) * f;
-        const float x1 = __uint_as_float(ww[2 * i + j] & 0xffff0000u) * f;
-        h2[j] = e4m3x2(x0, x1);
-        const float2 y = __half22float2(half2_of_e4m3x2((uint16_t)h2[j]));
-        l2[j] = e4m3x2(x0 - y.x, x1 - y.y);
-      }
-      hi[i] = h2[0] | (h2[1] << 16);
-      lo[i] = l2[0] | (l2[1] << 16);
-    }
-    if (there) {
-      const uint32_t at = swz(r, l16 >> 1) + (l16 & 1) * 8;
-      *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(dst + kTile * 128 + at) = make_uint2(lo[0], lo[1]);
-      if (l16 == 0) qf[r] = exp2i(e);
+__device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segment& g, int s, int t, int n,
+                                       unsigned char* dst, float* qf) {
+  const int l16 = t & 15, rows = g.rows_of(s), span = kTile / g.copies();
+  const uint32_t base = g.row0 + (g.dual ? s * kTile : 0), first = p.first[g.index], group = a.group;
+  unsigned char* half = dst + (l16 / 8) * (kTile * 128);
+#pragma unroll 1
+  for (int r = t / 16; r < kTile; r += n / 16) {
+    const uint32_t of = r & (span - 1);
+    if ((int)of < rows) {
+      const uint32_t x = base + of, seq = p.order[first + x / group], head = x % group;
+      cp_async16(half + (BITS == 16 ? swz(r, l16 & 7) : (uint32_t)(r * 128 + (l16 & 7) * 16)),
+                 a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
     }
   }
-}
-
-// The rows of q of one stream into shared memory, by its 256 threads (t), four
-// loads of each in flight.
-template <int BITS>
-__device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segment& g, int s, int t, unsigned char* dst,
-                                       float* qf) {
-  const int l16 = t & 15, rows = g.rows_of(s), span = kTile / g.copies();
-  const int base = g.row0 + (g.dual ? s * kTile : 0), first = p.first[g.index];
+  cp_async_commit();
+  cp_async_wait_all();
+  if constexpr (BITS == 8) {
 #pragma unroll 1
-  for (int b = 0; b < kTile; b += 64) {
-    uint4 w[4];
+    for (int r = t / 16; r < kTile; r += n / 16) {
+      const uint4 w = *reinterpret_cast<const uint4*>(half + r * 128 + (l16 & 7) * 16);
+      uint32_t m = abs_max(w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int of = (b + i * 16 + t / 16) & (span - 1);
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (of < rows) {
-        const uint32_t x = base + of, seq = p.order[first + x / (uint32_t)a.group], head = x % (uint32_t)a.group;
-        w[i] = *reinterpret_cast<const uint4*>(a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
+      for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = max(m & 0xffffu, m >> 16);
+      const int e = max(-100, (int)(m >> 7) - 127 - 7);
+      const float f = exp2i(-e);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = __uint_as_float(ww[i] << 16) * f, x1 = __uint_as_float(ww[i] & 0xffff0000u) * f;
+        hi[i] = e4m3x2(x0, x1);
+        const float2 y = __half22float2(half2_of_e4m3x2((uint16_t)hi[i]));
+        lo[i] = e4m3x2(x0 - y.x, x1 - y.y);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = b + i * 16 + t / 16;
-      put_q<BITS>(w[i], r, l16, (r & (span - 1)) < rows, dst, qf);
+      __syncwarp();  // the row's lanes have read it
+      if ((r & (span - 1)) < rows) {
+        const uint32_t at = swz(r, l16 >> 1) + (l16 & 1) * 8;
+        *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(dst + kTile * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if (l16 == 0) qf[r] = exp2i(e);
+      }
     }
   }
 }
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float* x) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  if constexpr (N >= 32) {
 #pragma unroll
-    for (int k = 0; k < N; k += 32) tmem_ld32(addr + k, r + k);
-  } else {
-    tmem_ld16(addr, r);
-  }
+  for (int k = 0; k < N; k += 32) tmem_ld32(addr + k, reinterpret_cast<uint32_t*>(x) + k);
 }
 
-// What a softmax thread keeps of its row, in the two warps that share it.
-struct RowState {
-  float m, l;         // reference of the weights, and the sum of this thread's
-  float qf;           // scale of the row of q (8-bit rows)
-  float* mine;        // where this thread's maximum goes, and the other's is
-  const float* other;
-  uint32_t bar, phase;  // of the two warps
-  volatile uint32_t* abort;
-  // Both warps have arrived (false: gave up).
-  __device__ __forceinline__ bool meet() {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort));
-    phase ^= 1;
-    return ok;
-  }
-};
+// 2^x of a pair without the special function unit, which does 16 a cycle and SM
+// and would be the bound: x = n + f with n the nearest integer (taken by adding
+// 1.5 2^23), 2^f by the cubic with the smallest largest relative error on [-1/2,
+// 1/2] (found by Remez exchange: 7.5e-5, a thirtieth of what the rounding of
+// the weight to bf16 may lose), n added to the exponent.  x below -126 counts as that.
+__device__ __forceinline__ void ex2_pair(F2 x, float& p0, float& p1) {
+  constexpr float kRound = 12582912.f;
+  float x0, x1;
+  x.get(x0, x1);
+  x = F2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const F2 r = add2(x, F2(kRound, kRound));
+  const F2 f = add2(x, mul2(add2(r, F2(-kRound, -kRound)), F2(-1.f, -1.f)));
+  F2 p = fma2(f, F2(0.055171669f, 0.055171669f), F2(0.24261112f, 0.24261112f));
+  p = fma2(p, f, F2(0.69326099f, 0.69326099f));
+  p = fma2(p, f, F2(0.99992807f, 0.99992807f));
+  float r0, r1;
+  r.get(r0, r1);
+  p.get(p0, p1);
+  p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23));
+  p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23));
+}
 
 // One tile of one query row: S from tensor memory, this thread's COLS columns
-// (of the row's copy, the half-th) to weights over it, and zeros to columns of
-// other copies.  Both threads of a row read S before either writes over it, and
-// agree on the maximum; m follows it, and O, half by half, follows m.
+// (the copy-th) to weights over it, zeros to the other copies'; m and l of the
+// row's columns so far, and O when m moves.  With one copy the first 64 tokens'
+// weights are announced on `half` as soon as they are there.
 template <int BITS, int COLS>
-__device__ __forceinline__ bool softmax_step(RowState& st, uint32_t ts, uint32_t to, int copy, int half, int valid,
-                                             bool first, const float* scales) {
-  const int c0 = (copy * 2 + half) * COLS;
+__device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int copy, int valid, bool first, float qf,
+                                             const float* scales, uint32_t half, float& m, float& l) {
+  const int c0 = copy * COLS;
   float x[COLS];
-  tmem_ld<COLS>(ts + c0, x);
-  wait_ld();
-  if constexpr (BITS == 8) {
-    const F2 q2(st.qf, st.qf);
-#pragma unroll
-    for (int k = 0; k < COLS; k += 4) {
-      const float4 kf = *reinterpret_cast<const float4*>(scales + c0 + k);
-      const float4 ev = *reinterpret_cast<const float4*>(scales + kTile + c0 + k);
-      fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
-      fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
-    }
-  }
-  if (valid < c0 + COLS) {
-#pragma unroll
-    for (int k = 0; k < COLS; ++k)
-      if (c0 + k >= valid) x[k] = -INFINITY;
-  }
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  constexpr int kParts = COLS > 64 ? 2 : 1, kPer = COLS / kParts;
+  tmem_ld<kPer>(ts + c0, x);
+  wait_ld();
+  if constexpr (kParts == 2) tmem_ld<kPer>(ts + kPer, x + kPer);  // comes while the first part is looked at
 #pragma unroll
-  for (int k = 0; k < COLS; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
-  float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-  *st.mine = top;
-  if (!st.meet()) return false;
-  top = fmaxf(top, *st.other);
+  for (int part = 0; part < kParts; ++part) {
+    if (part) wait_ld();
+    if constexpr (BITS == 8) {
+      const F2 q2(qf, qf);
+#pragma unroll
+      for (int k = part * kPer; k < (part + 1) * kPer; k += 4) {
+        const float4 kf = *reinterpret_cast<const float4*>(scales + c0 + k);
+        const float4 ev = *reinterpret_cast<const float4*>(scales + kTile + c0 + k);
+        fma2(mul2(F2(x[k], x[k + 1]), F2(kf.x, kf.y)), q2, F2(ev.x, ev.y)).get(x[k], x[k + 1]);
+        fma2(mul2(F2(x[k + 2], x[k + 3]), F2(kf.z, kf.w)), q2, F2(ev.z, ev.w)).get(x[k + 2], x[k + 3]);
+      }
+    }
+    if (valid < c0 + COLS) {
+#pragma unroll
+      for (int k = part * kPer; k < (part + 1) * kPer; ++k)
+        if (c0 + k >= valid) x[k] = -INFINITY;
+    }
+#pragma unroll
+    for (int k = part * kPer; k < (part + 1) * kPer; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
+  }
+  const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
   constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
   if (first) {
-    st.m = top;
+    m = top;
   } else {
-    const bool up = top > st.m + Range<BITS>::kLazy / kUnit;
+    const bool up = top > m + Range<BITS>::kLazy / kUnit;
     if (__any_sync(0xffffffffu, up)) {
       // S of this step is complete, so O of the stream's step before it is too
-      const float f = up ? ex2((st.m - top) * kUnit) : 1.f;
-      st.l *= f;
-      if (up) st.m = top;
+      const float f = up ? ex2((m - top) * kUnit) : 1.f;
+      l *= f;
+      if (up) m = top;
 #pragma unroll 1
-      for (int k = half * 64; k < half * 64 + 64; k += 16) {
+      for (int k = 0; k < kD; k += 16) {
         uint32_t o[16];
         tmem_ld16(to + k, o);
         wait_ld();
@@ -314,44 +303,46 @@ __device__ __forceinline__ bool softmax_step(RowState& st, uint32_t ts, uint32_t
       }
     }
   }
-  const float base = st.m == -INFINITY ? 0.f : fmaf(st.m, kUnit, -Range<BITS>::kShift);
+  const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
   const F2 base2(-base, -base), unit2(kUnit, kUnit);
   F2 ls[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-  constexpr int kChunk = COLS < 32 ? COLS : 32;
 #pragma unroll
-  for (int k = 0; k < COLS; k += kChunk) {
-    if constexpr (BITS == 16) {
-      uint32_t p[kChunk / 2];
+  for (int k = 0; k < COLS; k += 32) {
+    float p[32];
 #pragma unroll
-      for (int i = 0; i < kChunk / 2; ++i) {
-        float p0, p1;
-        fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        ls[i & 1] = add2(ls[i & 1], F2(p0, p1));
-        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-        p[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < 32; i += 2) {
+      const F2 v(x[k + i], x[k + i + 1]);
+      const F2 e = BITS == 16 ? fma2(v, unit2, base2) : add2(v, base2);
+      if (COLS > 64 && i % 8 >= kSfu) {
+        ex2_pair(e, p[i], p[i + 1]);
+      } else {
+        e.get(p[i], p[i + 1]);
+        p[i] = ex2(p[i]);
+        p[i + 1] = ex2(p[i + 1]);
       }
-      if constexpr (kChunk == 32) tmem_st16(ts + (c0 + k) / 2, p);
-      else tmem_st8(ts + (c0 + k) / 2, p);
+    }
+    if constexpr (BITS == 16) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        ls[i & 1] = add2(ls[i & 1], F2(p[2 * i], p[2 * i + 1]));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * i], p[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      tmem_st16(ts + (c0 + k) / 2, w);
     } else {
-      uint32_t hi[kChunk / 4], lo[kChunk / 4];
+      uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int i = 0; i < kChunk / 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float4 iv = *reinterpret_cast<const float4*>(scales + 2 * kTile + c0 + k + i * 4);
-        float p[4];
-        add2(F2(x[k + 4 * i], x[k + 4 * i + 1]), base2).get(p[0], p[1]);
-        add2(F2(x[k + 4 * i + 2], x[k + 4 * i + 3]), base2).get(p[2], p[3]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) p[c] = ex2(p[c]);
-        ls[0] = fma2(F2(p[0], p[1]), F2(iv.x, iv.y), ls[0]);
-        ls[1] = fma2(F2(p[2], p[3]), F2(iv.z, iv.w), ls[1]);
+        ls[0] = fma2(F2(p[4 * i], p[4 * i + 1]), F2(iv.x, iv.y), ls[0]);
+        ls[1] = fma2(F2(p[4 * i + 2], p[4 * i + 3]), F2(iv.z, iv.w), ls[1]);
         // the upper byte of a half is the e5m2 number below it: adding half a
         // step first rounds (p is positive, the rest has a sign)
         uint32_t h[2], r[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const __half2 v = __floats2half2_rn(p[2 * c], p[2 * c + 1]);
+          const __half2 v = __floats2half2_rn(p[4 * i + 2 * c], p[4 * i + 2 * c + 1]);
           h[c] = (*reinterpret_cast<const uint32_t*>(&v) + 0x00800080u) & 0xff00ff00u;
           const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&h[c]));
           r[c] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
@@ -359,20 +350,21 @@ __device__ __forceinline__ bool softmax_step(RowState& st, uint32_t ts, uint32_t
         hi[i] = __byte_perm(h[0], h[1], 0x7531);
         lo[i] = __byte_perm(r[0], r[1], 0x7531);
       }
-      if constexpr (kChunk == 32) {
-        tmem_st8(ts + (c0 + k) / 4, hi);
-        tmem_st8(ts + 32 + (c0 + k) / 4, lo);
-      } else {
-        tmem_st4(ts + (c0 + k) / 4, hi);
-        tmem_st4(ts + 32 + (c0 + k) / 4, lo);
-      }
+      tmem_st8(ts + (c0 + k) / 4, hi);
+      tmem_st8(ts + 32 + (c0 + k) / 4, lo);
+    }
+    if (COLS > 64 && k == 32) {
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(half);
     }
   }
-  if constexpr (COLS < 64) {
+  if constexpr (COLS < kTile) {
     const uint32_t zero[16] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k)  // 32 columns each
-      if (k * 32 / (2 * COLS) != copy && (k & 1) == half) {
+      if (k * 32 / COLS != copy) {
         if constexpr (BITS == 16) {
           tmem_st16(ts + k * 16, zero);
         } else {
@@ -383,8 +375,7 @@ __device__ __forceinline__ bool softmax_step(RowState& st, uint32_t ts, uint32_t
   }
   float l0, l1;
   add2(ls[0], ls[1]).get(l0, l1);
-  st.l += l0 + l1;
-  return true;
+  l += l0 + l1;
 }
 
 // Sixteen columns of this warp's rows, a row a lane, to sixteen bytes of four
@@ -429,17 +420,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sm.s_full[s]), 1);
-      mbar_init(smem_u32(&sm.p_ready[s]), 8);
+      mbar_init(smem_u32(&sm.p_half[s]), 4);
+      mbar_init(smem_u32(&sm.p_ready[s]), 4);
       mbar_init(smem_u32(&sm.o_done[s]), 1);
-      mbar_init(smem_u32(&sm.sc_go[s]), 8);
-      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.pair[s][w]), 2);
+      mbar_init(smem_u32(&sm.sc_go[s]), 4);
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&sm.sc_full[s][b]), 1);
-        mbar_init(smem_u32(&sm.sc_empty[s][b]), 8);
+        mbar_init(smem_u32(&sm.sc_empty[s][b]), 4);
       }
     }
     mbar_init(smem_u32(&sm.q_full), kSoftmaxWarps);
     mbar_init(smem_u32(&sm.q_empty), 1);
+    mbar_init(smem_u32(&sm.fin), kSoftmaxWarps);
     mbar_init(smem_u32(&sm.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_shared();
@@ -457,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
   Segment g;
 
   if (warp < 4) {
-    // registers: 128 x 64 + 512 x 104 of the launch's 640 x 96
-    regs_fewer<64>();
+    // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
+    regs_fewer<80>();
   if (warp == 0) {
     if (elect_one()) {
       // ---- loads: K then V of every tile
@@ -545,21 +537,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
             const int j = i - 1, s = j & 1;
             uint32_t ph;
             const uint32_t st = stage_of(2 * (tile_no + (g.dual ? j >> 1 : j)) + 1, ph);
-            ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort) &&
-                 mbar_wait(smem_u32(&sm.p_ready[s]), (p_phase >> s) & 1, abort);
-            if (!ok) break;
+            const uint32_t pp = (p_phase >> s) & 1;
             p_phase ^= 1u << s;
+            ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort) && mbar_wait(smem_u32(&sm.p_half[s]), pp, abort);
+            if (!ok) break;
             fence_after();
             const uint32_t vb = smem_desc(smem_u32(ring + st * S::kStage), BITS == 16 ? kTile * 128 : 16);
             const uint32_t p = tmem + s * kTile, d = tmem + 2 * kTile + s * kD;
             const uint32_t acc = j >= 2;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (BITS == 16)
-                mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, acc | (k > 0));
-              else  // four products of the high pieces, four of the low
-                mma8_ts(d, p + k * 8, vb + ((k % 4) * 32 * 128 >> 4), kDescO, acc | (k > 0));
+            for (int h = 0; h < 2; ++h) {  // 64 tokens each
+              if (h) {
+                ok = mbar_wait(smem_u32(&sm.p_ready[s]), pp, abort);
+                if (!ok) break;
+                fence_after();
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (BITS == 16) {
+                  const int k = h * 4 + i;
+                  mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, acc | (h | i));
+                } else {  // two products of the high pieces, two of the low
+                  const int k = h * 2 + (i & 1);
+                  mma8_ts(d, p + (i >> 1) * 32 + k * 8, vb + (k * 32 * 128 >> 4), kDescO, acc | (h | i));
+                }
+              }
             }
+            if (!ok) break;
             if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
             if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
           }
@@ -617,41 +621,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
     }
   }
   } else {
-    // ---- softmax of stream s: two threads a row, each half of its columns
-    regs_more<104>();
-    const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, w4 = warp & 3, row = w4 * 32 + lane;
+    // ---- softmax of stream s, a thread per row
+    regs_more<208>();
+    const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
-    uint32_t tile_no = 0, seg = 0, s_phase = 0, o_phase = 0, n = 0;
-    RowState st = {};
-    st.mine = &sm.mx[s][half][row];
-    st.other = &sm.mx[s][half ^ 1][row];
-    st.bar = smem_u32(&sm.pair[s][w4]);
-    st.abort = abort;
+    uint32_t tile_no = 0, seg = 0, s_phase = 0, o_phase = 0, fin_phase = 0, n = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
       if (seg > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_empty), (seg - 1) & 1, abort));
         if (!ok) break;
       }
-      if (g.dual || s == 0) {
-        float* qf = nullptr;
-        if constexpr (BITS == 8) qf = sm.sc.qf[seg & 1][g.dual ? s : 0];
-        load_q<BITS>(a, sm.plan, g, s, half * 128 + row, q_smem + (g.dual ? s : 0) * S::kQ, qf);
-        fence_async_shared();
-      }
+      float* qfs = nullptr;
+      if constexpr (BITS == 8) qfs = sm.sc.qf[seg & 1][g.dual ? s : 0];
+      load_q<BITS>(a, sm.plan, g, s, g.dual ? row : tid - 128, g.dual ? 128 : 256, q_smem + (g.dual ? s : 0) * S::kQ, qfs);
+      fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       // also keeps a stream without a tile here from arriving for the next segment early
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_full), seg & 1, abort));
       if (!ok) break;
-      if constexpr (BITS == 8) st.qf = sm.sc.qf[seg & 1][g.dual ? s : 0][row];
+      const float qf = BITS == 8 ? qfs[row] : 1.f;
       const int rows = g.rows_of(s), steps = g.steps_of(s), copies = g.copies();
       const int r = row & (kTile / copies - 1), copy = row / (kTile / copies);  // this thread's row of the unit
       if (BITS == 8 && steps > 0 && lane == 0) mbar_arrive(smem_u32(&sm.sc_go[s]));
       const bool active = r - lane < rows;
-      st.m = -INFINITY;
-      st.l = 0.f;
+      float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++n) {
         const int t = g.tile_of(s, j), valid = g.valid(t), b = n & 1;
         ok = mbar_wait(smem_u32(&sm.s_full[s]), s_phase, abort);
@@ -662,30 +658,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
           ok = ok && mbar_wait(smem_u32(&sm.full[stage]), (use / n_stage) & 1, abort);
           if (ok) {
             constexpr int kChunks = BITS == 16 ? 16 : 8;  // 16-byte pieces of a row
-            for (int x = half * 128 + row; x < (kTile - valid) * kChunks; x += 2 * kTile) {
+            for (int x = row; x < (kTile - valid) * kChunks; x += kTile) {
               const int v = valid + x / kChunks, c = x % kChunks;
               *reinterpret_cast<uint4*>(ring + stage * S::kStage + (c / 8) * (kTile * 128) + v * 128 + (c % 8) * 16) =
                   make_uint4(0, 0, 0, 0);
             }
             fence_async_shared();
+            __syncwarp();  // the first half's announcement is for these too
           }
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         s_phase ^= 1;
+        const bool whole = copies == 1 && active;
         if (active) {
           fence_after();
           const float* scales = nullptr;
           if constexpr (BITS == 8) scales = sm.sc.tok[s][b][0];
-          if (copies == 1) ok = softmax_step<BITS, 64>(st, ts, to, 0, half, valid, j == 0, scales);
-          else if (copies == 2) ok = softmax_step<BITS, 32>(st, ts, to, copy, half, valid, j == 0, scales);
-          else ok = softmax_step<BITS, 16>(st, ts, to, copy, half, valid, j == 0, scales);
-          if (!ok) break;
+          const uint32_t half = smem_u32(&sm.p_half[s]);
+          if (copies == 1) softmax_step<BITS, 128>(ts, to, 0, valid, j == 0, qf, scales, half, m, l);
+          else if (copies == 2) softmax_step<BITS, 64>(ts, to, copy, valid, j == 0, qf, scales, half, m, l);
+          else softmax_step<BITS, 32>(ts, to, copy, valid, j == 0, qf, scales, half, m, l);
           wait_st();
           fence_before();
         }
         __syncwarp();
         if (lane == 0) {
+          if (!whole) mbar_arrive(smem_u32(&sm.p_half[s]));
           mbar_arrive(smem_u32(&sm.p_ready[s]));
           if (BITS == 8) mbar_arrive(smem_u32(&sm.sc_empty[s][b]));
         }
@@ -696,28 +695,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
         if (!ok) break;
         o_phase ^= 1;
       }
-      if (active) {
+      m *= BITS == 16 ? kLogScale : 1.f;
+      // streams that hold the same rows join them: each writes half of the channels
+      float f0 = 1.f, f1 = 0.f;
+      if (!g.dual) {
+        sm.ml[s][row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.fin));
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.fin), fin_phase, abort));
+        if (!ok) break;
+        fin_phase ^= 1;
+        const float2 a0 = sm.ml[0][row], a1 = sm.ml[1][row];
+        m = fmaxf(a0.x, a1.x);
+        f0 = a0.y == 0.f ? 0.f : ex2(a0.x - m);
+        f1 = a1.y == 0.f ? 0.f : ex2(a1.x - m);
+        l = f0 * a0.y + f1 * a1.y;
+      }
+      if (active && g.steps_of(0) > 0) {
         fence_after();
-        const int64_t at = wide_row(a, g.unit, blockIdx.x) + s * kTile + row;
-        if (steps > 0) {
-          if (half) sm.lx[s][row] = st.l;
-          if (!(ok = st.meet())) break;
-          const int q = lane & 3;
-          float* po = a.part_o + (at - q) * kD + half * 64 + q * 4;
+        const int64_t at = wide_row(a, g.unit, blockIdx.x) + (g.dual ? s * kTile : 0) + row;
+        const int q = lane & 3, c0 = g.dual ? 0 : s * 64, c1 = g.dual ? kD : c0 + 64;
+        const uint32_t o0 = g.dual ? to : tmem + lanes + 2 * kTile;
+        const bool both = !g.dual && g.steps_of(1) > 0;
+        float* po = a.part_o + (at - q) * kD + q * 4;
 #pragma unroll 1
-          for (int k = 0; k < 64; k += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + half * 64 + k, o);
+        for (int k = c0; k < c1; k += 16) {
+          uint32_t o[16];
+          tmem_ld16(o0 + k, o);
+          if (both) {
+            uint32_t v[16];
+            tmem_ld16(o0 + kD + k, v);
             wait_ld();
-            quads(o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (r - q + i < rows)
-                *reinterpret_cast<uint4*>(po + i * kD + k) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(v[i]) * f1));
+          } else {
+            wait_ld();
           }
+          quads(o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r - q + i < rows)
+              *reinterpret_cast<uint4*>(po + i * kD + k) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
-        if (!half && r < rows)
-          a.part_ml[at] = make_float2(st.m * (BITS == 16 ? kLogScale : 1.f), st.l + (steps > 0 ? sm.lx[s][row] : 0.f));
+        if ((g.dual || s == 0) && r < rows) a.part_ml[at] = make_float2(m, l);
         fence_before();
       }
       tile_no += g.tiles;

@@ -31,7 +31,7 @@ constexpr int kFewWarps = 8;         // per CTA of the streaming kernel
 struct Parts {
   int64_t pre, own;   // first
   int32_t pre_n, own_n;
-  int32_t pre_sub;    // 1, or the copies of both streams
+  int32_t pre_sub;    // copies of the row
   int32_t pre_span;   // rows from one copy to the next
   int32_t pre_step;   // rows from one segment to the next
   int32_t pad;
@@ -223,7 +223,7 @@ __device__ __forceinline__ Parts parts_of(const Args& a, const Plan& p, int64_t 
     q.pre_n = (int)(share.owner(at + tiles - 1) - w0) + 1;
     if (is_wide) {
       q.pre = wide_row(a, unit, w0) + in;
-      q.pre_sub = rows > kWideTile ? 1 : 2 * copies_of(rows);
+      q.pre_sub = copies_of(rows);
       q.pre_span = kWideTile / copies_of(rows);
       q.pre_step = kPair;
     } else {
