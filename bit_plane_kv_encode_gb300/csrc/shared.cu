@@ -41,7 +41,6 @@ constexpr int kRing16 = 32 * 1024;               // bytes of a stage: 128 rows o
 constexpr int kRing8 = 16 * 1024;                // 128 rows of codes
 constexpr int kMaxStages = 10;
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
-constexpr int kSfu = 4;  // of eight weights, those by the special function unit (two at a time)
 constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
 
 // How far the maximum may pass m before O is rescaled, and where exp2's
@@ -224,28 +223,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float* x) {
   for (int k = 0; k < N; k += 32) tmem_ld32(addr + k, reinterpret_cast<uint32_t*>(x) + k);
 }
 
-// 2^x of a pair without the special function unit, which does 16 a cycle and SM
-// and would be the bound: x = n + f with n the nearest integer (taken by adding
-// 1.5 2^23), 2^f by the cubic with the smallest largest relative error on [-1/2,
-// 1/2] (found by Remez exchange: 7.5e-5, a thirtieth of what the rounding of
-// the weight to bf16 may lose), n added to the exponent.  x below -126 counts as that.
-__device__ __forceinline__ void ex2_pair(F2 x, float& p0, float& p1) {
-  constexpr float kRound = 12582912.f;
-  float x0, x1;
-  x.get(x0, x1);
-  x = F2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const F2 r = add2(x, F2(kRound, kRound));
-  const F2 f = add2(x, mul2(add2(r, F2(-kRound, -kRound)), F2(-1.f, -1.f)));
-  F2 p = fma2(f, F2(0.055171669f, 0.055171669f), F2(0.24261112f, 0.24261112f));
-  p = fma2(p, f, F2(0.69326099f, 0.69326099f));
-  p = fma2(p, f, F2(0.99992807f, 0.99992807f));
-  float r0, r1;
-  r.get(r0, r1);
-  p.get(p0, p1);
-  p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23));
-  p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23));
-}
-
 // One tile of one query row: S from tensor memory, this thread's COLS columns
 // (the copy-th) to weights over it, zeros to the other copies'; m and l of the
 // row's columns so far, and O when m moves.  With one copy the first 64 tokens'
@@ -313,13 +290,9 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int copy,
     for (int i = 0; i < 32; i += 2) {
       const F2 v(x[k + i], x[k + i + 1]);
       const F2 e = BITS == 16 ? fma2(v, unit2, base2) : add2(v, base2);
-      if (COLS > 64 && i % 8 >= kSfu) {
-        ex2_pair(e, p[i], p[i + 1]);
-      } else {
-        e.get(p[i], p[i + 1]);
-        p[i] = ex2(p[i]);
-        p[i + 1] = ex2(p[i + 1]);
-      }
+      e.get(p[i], p[i + 1]);
+      p[i] = ex2(p[i]);
+      p[i + 1] = ex2(p[i + 1]);
     }
     if constexpr (BITS == 16) {
       uint32_t w[16];
@@ -499,9 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
       uint32_t tile_no = 0;  // tiles before this segment
       uint32_t seg = 0, p_phase = 0;
       bool ok = true;
-      auto stage_of = [&](uint32_t use, uint32_t& ph) {
-        ph = (use / n_stage) & 1;
-        return use % n_stage;
+      uint32_t k_st = 0, k_ph = 0, v_st = 1, v_ph = 0;
+      auto skip = [&](uint32_t& st, uint32_t& ph) {  // two stages on
+        st += 2;
+        if (st >= (uint32_t)n_stage) st -= n_stage, ph ^= 1;
       };
       while (ok && walk.next(g)) {
         ok = mbar_wait(smem_u32(&sm.q_full), seg & 1, abort);
@@ -510,10 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
         for (int i = 0; ok && i <= steps; ++i) {
           if (i < steps) {
             const int s = i & 1;
-            uint32_t ph;
-            const uint32_t st = stage_of(2 * (tile_no + (g.dual ? i >> 1 : i)), ph);
-            ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort);
-            if (!ok) break;
+            const uint32_t st = k_st;
+            if (!g.dual || s == 0) {
+              ok = mbar_wait(smem_u32(&sm.full[st]), k_ph, abort);
+              if (!ok) break;
+            }
             fence_after();
             const uint32_t kb = smem_desc(smem_u32(ring + st * S::kStage), 16);
             const uint32_t qb = smem_desc(smem_u32(q_smem + (g.dual ? s : 0) * S::kQ), 16);
@@ -530,16 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
                 mma8_ss(d, qb + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4), kb + ((k % 4) * 32 >> 4), kDescS, k > 0);
             }
             mma_commit(smem_u32(&sm.s_full[s]));
-            if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
+            if (!g.dual || s) {
+              mma_commit(smem_u32(&sm.empty[st]));
+              skip(k_st, k_ph);
+            }
             if (i == steps - 1) mma_commit(smem_u32(&sm.q_empty));
           }
           if (i > 0) {
             const int j = i - 1, s = j & 1;
-            uint32_t ph;
-            const uint32_t st = stage_of(2 * (tile_no + (g.dual ? j >> 1 : j)) + 1, ph);
+            const uint32_t st = v_st;
             const uint32_t pp = (p_phase >> s) & 1;
             p_phase ^= 1u << s;
-            ok = mbar_wait(smem_u32(&sm.full[st]), ph, abort) && mbar_wait(smem_u32(&sm.p_half[s]), pp, abort);
+            ok = (g.dual && s) || mbar_wait(smem_u32(&sm.full[st]), v_ph, abort);
+            ok = ok && mbar_wait(smem_u32(&sm.p_half[s]), pp, abort);
             if (!ok) break;
             fence_after();
             const uint32_t vb = smem_desc(smem_u32(ring + st * S::kStage), BITS == 16 ? kTile * 128 : 16);
@@ -564,7 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
               }
             }
             if (!ok) break;
-            if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
+            if (!g.dual || s) {
+              mma_commit(smem_u32(&sm.empty[st]));
+              skip(v_st, v_ph);
+            }
             if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
           }
         }
