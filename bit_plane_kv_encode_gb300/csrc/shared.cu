@@ -176,7 +176,7 @@ __device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segme
   const int l16 = t & 15, rows = g.rows_of(s), span = kTile / g.copies();
   const uint32_t base = g.row0 + (g.dual ? s * kTile : 0), first = p.first[g.index], group = a.group;
   unsigned char* half = dst + (l16 / 8) * (kTile * 128);
-#pragma unroll 1
+#pragma unroll 4
   for (int r = t / 16; r < kTile; r += n / 16) {
     const uint32_t of = r & (span - 1);
     if ((int)of < rows) {
@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
     if (elect_one()) {
       // ---- loads: K then V of every tile
       uint32_t stage = 0, phase = 0, issued = 0;
+      const uint64_t policy = evict_first_policy();
       bool ok = true;
       while (ok && walk.next(g)) {
         const int64_t base = (int64_t)g.index * a.n_heads + g.h;
@@ -441,9 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
             const uint32_t dst = smem_u32(ring + stage * S::kStage);
             mbar_expect_tx(bar, S::kStage + (kv ? S::kExps : 0));
             if constexpr (BITS == 16) {
-              tma_load_4d(dst, &maps.m[kv], bar, 0, (int)tok, 0, (int)base);
+              tma_load_4d(dst, &maps.m[kv], bar, 0, (int)tok, 0, (int)base, policy);
             } else {
-              tma_load_3d(dst, &maps.m[kv], bar, 0, (int)tok, (int)base);
+              tma_load_3d(dst, &maps.m[kv], bar, 0, (int)tok, (int)base, policy);
               if (kv) {
                 const uint32_t e = smem_u32(ring_exps + stage * S::kExps);
                 bulk_load(e, a.exps[0][0] + base * a.pcap + tok, kTile, bar);

@@ -99,9 +99,11 @@ struct Walk {
   __device__ __forceinline__ int valid() const { return (int)min64(tok, n - t * tok); }
 };
 
-__device__ __forceinline__ void cp16_zero(uint32_t dst, const void* src, bool there) {
+__device__ __forceinline__ void cp16_zero(uint32_t dst, const void* src, bool there, uint64_t policy) {
   const int n = there ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(n),
+               "l"(policy)
+               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -159,7 +161,7 @@ __device__ __forceinline__ uint32_t halves(uint32_t codes) {
 
 // Issue the copies of the walk's tile into a stage.
 template <int BITS>
-__device__ __forceinline__ void load_tile(const Walk& w, uint32_t stage, uint32_t exps) {
+__device__ __forceinline__ void load_tile(const Walk& w, uint32_t stage, uint32_t exps, uint64_t policy) {
   using S = Shape<BITS>;
   const int lane = threadIdx.x & 31, valid = w.valid();
   const int64_t row = w.row0 + w.t * S::kTok;
@@ -170,9 +172,9 @@ __device__ __forceinline__ void load_tile(const Walk& w, uint32_t stage, uint32_
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int x = i * 32 + lane, tok = x / kChunks, c = x % kChunks;
-      cp16_zero(stage + kv * (kStage / 2) + tok * S::kRow + ((c ^ (tok & 7)) << 4), src + x * 16, tok < valid);
+      cp16_zero(stage + kv * (kStage / 2) + tok * S::kRow + ((c ^ (tok & 7)) << 4), src + x * 16, tok < valid, policy);
     }
-    if (BITS == 8 && lane < 2) cp16_zero(exps + kv * S::kTok + lane * 16, w.a.exps[w.side][kv] + row + lane * 16, true);
+    if (BITS == 8 && lane < 2) cp16_zero(exps + kv * S::kTok + lane * 16, w.a.exps[w.side][kv] + row + lane * 16, true, policy);
   }
 }
 
@@ -239,21 +241,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
   make_plan(a, plan, S::kTok);
-  {
-    const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
-    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * tid; r < n; r += (int64_t)gridDim.x * kThreads)
-      a.parts[r] = parts_of(a, plan, r);
-  }
   const int worker = warp * gridDim.x + blockIdx.x;
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   unsigned char* exps = smem + kFewWarps * kStages * kStage + warp * kStages * S::kExps;
   Walk ahead(plan, a, worker, S::kTok), cur = ahead;
+  const uint64_t policy = evict_first_policy();
   for (int i = 0; i < kStages - 1; ++i) {
     if (ahead.more()) {
-      load_tile<BITS>(ahead, ring + i * kStage, smem_u32(exps) + i * S::kExps);
+      load_tile<BITS>(ahead, ring + i * kStage, smem_u32(exps) + i * S::kExps, policy);
       ahead.next();
     }
     cp_async_commit();
+  }
+  // the join's table, while the first copies come
+  {
+    const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
+    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * tid; r < n; r += (int64_t)gridDim.x * kThreads)
+      a.parts[r] = parts_of(a, plan, r);
   }
   uint32_t qb[NB][8][2];
   float qf[NB][2], o[NB][8][4], m[NB][2], l[NB][2];
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
     {
       const int into = st == 0 ? kStages - 1 : st - 1;
       if (ahead.more()) {
-        load_tile<BITS>(ahead, ring + into * kStage, smem_u32(exps) + into * S::kExps);
+        load_tile<BITS>(ahead, ring + into * kStage, smem_u32(exps) + into * S::kExps, policy);
         ahead.next();
       }
       cp_async_commit();

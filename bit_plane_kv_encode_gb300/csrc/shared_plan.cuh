@@ -100,18 +100,31 @@ __device__ __forceinline__ int pre_rows(const Args& a, const Plan& p, int item) 
   return min(kPair, p.cnt[x] * a.group - (item - p.item0[x]) * kPair);
 }
 
-// All threads of the CTA; ends with a barrier.
+// All threads of the CTA (at least 256); ends with a barrier.  The lengths are
+// loaded at once; a single prefix, the usual case, needs no search for who has
+// which.
 __device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   const int P = a.plen ? a.n_prefix : 0, N = a.n_seq;
-  if (P > 0) {
-    for (int i = tid; i < N; i += nt) {
-      const int x = a.prefix_of ? a.prefix_of[i] : 0;
-      p.pof[i] = (int16_t)(x >= 0 && x < P ? x : -1);
-    }
+  constexpr int kPer = kMaxSeq / 256;
+  int64_t own[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid + k * nt;
+    own[k] = i < N ? tokens_of(a.len[i], a.cap) : 0;
+  }
+  if (P == 0) {
+    for (int i = tid; i < N; i += nt) p.pof[i] = -1;
+    if (tid == 0) p.n_pre = 0;
+  } else {
     for (int x = tid; x < P; x += nt) {
       p.cnt[x] = 0;
       p.wide[x] = tokens_of(a.plen[x], a.pcap);  // until the items are known
+    }
+    for (int i = tid; i < N; i += nt) {
+      const int x = a.prefix_of ? a.prefix_of[i] : 0;
+      p.pof[i] = (int16_t)(x >= 0 && x < P ? x : -1);
+      if (!a.prefix_of) p.rank[i] = (uint16_t)i;
     }
     __syncthreads();
     if (a.prefix_of) {
@@ -126,52 +139,53 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) 
         if (x >= 0) p.cnt[x] = (uint16_t)cnt;
         p.rank[i] = (uint16_t)rank;
       }
-    } else {
-      for (int i = tid; i < N; i += nt) p.rank[i] = (uint16_t)i;
-      if (tid == 0) p.cnt[0] = (uint16_t)N;
+      __syncthreads();
     }
-    __syncthreads();
     if (tid < 32) {
       int at = 0, item = 0;
       for (int b = 0; b < P; b += 32) {
         const int x = b + lane;
-        const int c = x < P ? p.cnt[x] : 0;
+        const int c = x >= P ? 0 : a.prefix_of ? p.cnt[x] : x == 0 ? N : 0;
         const int it = x < P && p.wide[x] > 0 ? (c * a.group + kPair - 1) / kPair : 0;
         int sc = c, si = it;
+        if (P > 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, sc, o), w = __shfl_up_sync(0xffffffffu, si, o);
-          if (lane >= o) {
-            sc += u;
-            si += w;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sc, o), w = __shfl_up_sync(0xffffffffu, si, o);
+            if (lane >= o) {
+              sc += u;
+              si += w;
+            }
           }
         }
         if (x < P) {
+          p.cnt[x] = (uint16_t)c;
           p.first[x] = (uint16_t)(at + sc - c);
           p.item0[x] = (uint16_t)(item + si - it);
           for (int k = 0; k < it; ++k) p.it_p[item + si - it + k] = (uint16_t)x;
         }
-        at += __shfl_sync(0xffffffffu, sc, 31);
-        item += __shfl_sync(0xffffffffu, si, 31);
+        const int last = P > 1 ? 31 : 0;
+        at += __shfl_sync(0xffffffffu, sc, last);
+        item += __shfl_sync(0xffffffffu, si, last);
       }
       if (lane == 0) p.n_pre = item;
     }
-  } else {
-    for (int i = tid; i < N; i += nt) p.pof[i] = -1;
-    if (tid == 0) p.n_pre = 0;
   }
   __syncthreads();
   const int n_pre = p.n_pre;
-  for (int i = tid; i < n_pre + N; i += nt) {
-    if (i < n_pre) {
-      const int64_t n = tokens_of(a.plen[p.it_p[i]], a.pcap);
-      const bool wide = pre_rows(a, p, i) > kFew;
-      p.wide[i] = wide ? (n + kWideTile - 1) / kWideTile : 0;
-      p.few[i] = wide ? 0 : (n + few_tile - 1) / few_tile;
-    } else {
-      const int s = i - n_pre, x = p.pof[s];
-      p.few[i] = (tokens_of(a.len[s], a.cap) + few_tile - 1) / few_tile;
-      if (x >= 0) p.order[p.first[x] + p.rank[s]] = (uint16_t)s;
+  for (int i = tid; i < n_pre; i += nt) {
+    const int64_t n = tokens_of(a.plen[p.it_p[i]], a.pcap);
+    const bool wide = pre_rows(a, p, i) > kFew;
+    p.wide[i] = wide ? (n + kWideTile - 1) / kWideTile : 0;
+    p.few[i] = wide ? 0 : (n + few_tile - 1) / few_tile;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid + k * nt;
+    if (i < N) {
+      p.few[n_pre + i] = (own[k] + few_tile - 1) / few_tile;
+      const int x = p.pof[i];
+      if (x >= 0) p.order[p.first[x] + p.rank[i]] = (uint16_t)i;
     }
   }
   __syncthreads();
