@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_consta
     auto load = [&](int j, int h, uint4& wa, uint4& wb) {
       if (j < n_tok) {
         const uint16_t* x = a.qkv + (tok0 + j) * a.ld + (head0 + h) * kD;
-        wa = *reinterpret_cast<const uint4*>(x + ca * 8);
-        wb = *reinterpret_cast<const uint4*>(x + cb * 8);
+        wa = __ldcs(reinterpret_cast<const uint4*>(x + ca * 8));
+        wb = __ldcs(reinterpret_cast<const uint4*>(x + cb * 8));
       }
     };
     int j = j0, h = h0;

@@ -44,8 +44,8 @@ __global__ void __launch_bounds__(kR8Threads) k_rows8_append(const __grid_consta
     const int64_t r = r0 + i * kR8Groups + grp;
     w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
     if (r < rows) {
-      w[i][0] = *reinterpret_cast<const uint4*>(a.k_new + r * kD + l16 * 8);
-      w[i][1] = *reinterpret_cast<const uint4*>(a.v_new + r * kD + l16 * 8);
+      w[i][0] = __ldcs(reinterpret_cast<const uint4*>(a.k_new + r * kD + l16 * 8));
+      w[i][1] = __ldcs(reinterpret_cast<const uint4*>(a.v_new + r * kD + l16 * 8));
     }
   }
   if (tid < kR8Groups * R) {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kR8Threads) k_rows8_read(const __grid_constant
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv)
           if (a.out[kv]) {
-            c[i][kv] = *reinterpret_cast<const uint2*>(a.codes[kv] + row * kD + l16 * 8);
+            c[i][kv] = __ldcs(reinterpret_cast<const uint2*>(a.codes[kv] + row * kD + l16 * 8));
             e[i][kv] = a.exps[kv][row];
           }
       }
