@@ -854,8 +854,8 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
         return cudaErrorInvalidValue;
     const bool dual = own.n * group > kTile;
     a.stages = Shape<BITS>::stages(dual);
-    cudaError_t e = cudaFuncSetAttribute(k_shared_wide<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Shape<BITS>::kSmemMax);
+    static std::atomic<uint64_t> done;
+    cudaError_t e = allow_smem(k_shared_wide<BITS>, Shape<BITS>::kSmemMax, done);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_shared_wide<BITS>, dim3(a.wide_ctas), dim3(kThreads), (size_t)Shape<BITS>::bytes(dual), st, a, maps);
     if (e != cudaSuccess) return e;

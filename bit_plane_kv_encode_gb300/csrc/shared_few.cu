@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_co
 
 template <int BITS, int NB>
 cudaError_t go(const Args& a, int ctas, bool wait_first, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(k_shared_few<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Shape<BITS>::kSmem);
+  static std::atomic<uint64_t> done;
+  const cudaError_t e = allow_smem(k_shared_few<BITS, NB>, Shape<BITS>::kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_shared_few<BITS, NB>, dim3(ctas), dim3(kThreads), (size_t)Shape<BITS>::kSmem, st, a,
                     (int32_t)wait_first);

@@ -12,10 +12,26 @@
 // fits ragged batches; every CTA works the same plan out for itself.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace bpkv {
 namespace shared {
+
+// Lets a kernel use `bytes` of shared memory, once for each device; `done` is
+// the kernel's own.
+template <typename K>
+inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 constexpr int kWideTile = 128;       // tokens of a wide tile, rows of a stream
 constexpr int kPair = 2 * kWideTile; // rows of a prefix unit
