@@ -67,7 +67,7 @@ struct Scales<8> {
 template <int BITS>
 struct Smem {
   Scales<BITS> sc;
-  Plan plan;
+  WidePlan plan;
   uint32_t tmem;
   uint32_t abort;
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -100,11 +100,11 @@ struct Segment {
 
 // Walks the segments of one CTA; every role of the CTA walks alike.
 struct Walk {
-  const Plan& p;
+  const WidePlan& p;
   const Args& a;
   int64_t pos, end;
   int item;
-  __device__ Walk(const Plan& plan, const Args& args) : p(plan), a(args) {
+  __device__ Walk(const WidePlan& plan, const Args& args) : p(plan), a(args) {
     const Share share(p.wide[p.n_pre] * a.n_heads, a.wide_ctas);
     pos = end = 0;
     item = 0;
@@ -171,7 +171,7 @@ __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 12
 // x 2^-e with the row's largest magnitude in 128 .. 256, hi to 4 bits, lo the 4
 // (with its sign) below.
 template <int BITS>
-__device__ __forceinline__ void load_q(const Args& a, const Plan& p, const Segment& g, int s, int t, int n,
+__device__ __forceinline__ void load_q(const Args& a, const WidePlan& p, const Segment& g, int s, int t, int n,
                                        unsigned char* dst, float* qf) {
   const int l16 = t & 15, rows = g.rows_of(s), span = kTile / g.copies();
   const uint32_t base = g.row0 + (g.dual ? s * kTile : 0), first = p.first[g.index], group = a.group;
@@ -738,6 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Most prefix units that n_seq sequences can make.
+int64_t units(int64_t n_seq, int64_t n_prefix, int64_t group, int log) {
+  return n_prefix ? min64(n_prefix, n_seq) + (n_seq * group >> log) : 0;
+}
+
 struct Space {
   size_t parts, ml, o, total;
   int64_t few0, own0;  // first partial rows of the kinds
@@ -746,9 +751,8 @@ struct Space {
 Space space(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
   Space s;
   // a segment is unit u's part in worker w, slot u + w of its kind
-  const int64_t pre = n_prefix ? (min64(n_prefix, n_seq) + n_seq * group / kPair) * n_heads : 0;
-  const int64_t wide = n_prefix && n_seq * group > kFew ? (pre + kSms) * kPair : 0;
-  const int64_t few = n_prefix ? (pre + kSms * kFewWarps) * kFew : 0;
+  const int64_t wide = n_prefix && n_seq * group > kFew ? (units(n_seq, n_prefix, group, kPairLog) * n_heads + kSms) * kPair : 0;
+  const int64_t few = n_prefix ? (units(n_seq, n_prefix, group, kFewLog) * n_heads + kSms * kFewWarps) * kFew : 0;
   const int64_t own = (n_seq * n_heads + kSms * kFewWarps) * group;
   s.few0 = wide;
   s.own0 = wide + few;
@@ -801,6 +805,13 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Short prefixes are streamed by units of 16 rows, from L2 again for each, and
+// the wide kernel is left out, while that reads at most this many bytes.  With
+// 32 sequences of 8 x 4 heads, streamed / wide, in us: 300 tokens 15.2 / 21.6,
+// 1000 tokens 19.3 / 22.0, 2000 tokens (66 MB) 27.7 / 24.2, 4000 tokens 40.2 /
+// 25.0; 8-bit rows: 2000 tokens (33 MB) 22.4 / 29.4, 4000 tokens 31.4 / 30.0.
+constexpr int64_t kStreamBytes = 60000000;
+
 // One side's rows: K and V (with their exponents for 8-bit rows).
 struct Side {
   const void* rows[2];
@@ -838,15 +849,18 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   a.few0 = sp.few0;
   a.own0 = sp.own0;
   a.status = static_cast<int32_t*>(ws);
+  const int64_t pn = prefix ? prefix->n : 0, pmax = prefix ? prefix->n_max : 0;
+  const int64_t again =
+      max64(min64(pn, own.n), (own.n * group + kFew - 1) / kFew) * n_heads * pmax * (BITS == 16 ? 4 * kD : 2 * kD);
+  const bool has_wide = prefix && own.n * group > kFew && again > kStreamBytes;
+  a.unit_log = has_wide ? kPairLog : kFewLog;
   // no more CTAs than tiles, as far as the host knows (longer sequences than
   // it knows of only find fewer CTAs)
-  const int64_t units = prefix ? min64(prefix->n, own.n) + (int64_t)own.n * group / kPair : 0;
-  const int64_t wide = prefix && own.n * group > kFew ? n_heads * units * ((prefix->n_max + kTile - 1) / kTile) : 0;
-  const int64_t tok = few_tile(BITS);
-  const int64_t few = n_heads * ((own.n_max + tok - 1) / tok * own.n + (prefix ? (prefix->n_max + tok - 1) / tok * units : 0));
+  const int64_t n_units = units(own.n, pn, group, a.unit_log), tok = few_tile(BITS);
+  const int64_t wide = has_wide ? n_heads * n_units * ((pmax + kTile - 1) / kTile) : 0;
+  const int64_t few = n_heads * ((own.n_max + tok - 1) / tok * own.n + n_units * ((pmax + tok - 1) / tok));
   a.wide_ctas = (int32_t)max64(1, min64(kSms, wide));
   a.few_workers = (int32_t)max64(1, min64(kSms, few)) * kFewWarps;
-  const bool has_wide = prefix && own.n * group > kFew;
   if (has_wide) {
     Maps maps;
     for (int kv = 0; kv < 2; ++kv)

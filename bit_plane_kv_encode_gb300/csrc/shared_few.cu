@@ -36,14 +36,14 @@ struct Shape {
   static constexpr int kRow = kD * BITS / 8;              // bytes of a row
   static constexpr int kExps = BITS == 16 ? 0 : 2 * kTok; // exponent bytes
   static constexpr int kRing = kFewWarps * kStages * (kStage + kExps);
-  static constexpr int kSmem = kRing + (int)sizeof(Plan);
+  static constexpr int kSmem = kRing + (int)sizeof(FewPlan);
   static constexpr float kLazy = BITS == 16 ? 8.f : 4.f;  // rise of the maximum before O is rescaled
   static constexpr float kShift = BITS == 16 ? 0.f : 11.f;  // p' below 2^15: a half
 };
 
 // One worker's way through its tiles.
 struct Walk {
-  const Plan& p;
+  const FewPlan& p;
   const Args& a;
   int tok;
   int64_t pos, end;
@@ -51,7 +51,7 @@ struct Walk {
   int64_t t, tiles, n, row0, unit;
   int side;  // 0: a prefix, 1: own rows
   int index;
-  __device__ __forceinline__ Walk(const Plan& plan, const Args& args, int worker, int tile) : p(plan), a(args), tok(tile) {
+  __device__ __forceinline__ Walk(const FewPlan& plan, const Args& args, int worker, int tile) : p(plan), a(args), tok(tile) {
     const int items = p.n_pre + a.n_seq;
     const Share share(p.few[items] * a.n_heads, a.few_workers);
     pos = end = 0;
@@ -191,7 +191,7 @@ __device__ __forceinline__ void load_q(const Walk& w, int rows, uint32_t (*qb)[8
     if (r < rows) {
       int seq = w.index, head = r;
       if (w.side == 0) {
-        const int x = (w.item - w.p.item0[w.index]) * kPair + r;
+        const int x = ((w.item - w.p.item0[w.index]) << a.unit_log) + r;
         seq = w.p.order[w.p.first[w.index] + x / a.group];
         head = x % a.group;
       }
@@ -233,7 +233,7 @@ template <int BITS, int NB>
 __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constant__ Args a, int32_t wait_first) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = Shape<BITS>;
-  Plan& plan = *reinterpret_cast<Plan*>(smem + S::kRing);
+  FewPlan& plan = *reinterpret_cast<FewPlan*>(smem + S::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   // Behind the wide kernel of the same call, which starts this one only after
   // its own wait, what that wait covered is complete: only the end waits, so

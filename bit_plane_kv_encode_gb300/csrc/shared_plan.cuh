@@ -2,9 +2,9 @@
 // the tiles over workers, and where the partial results go.
 //
 // A unit is a set of query rows that attend over the same KV rows: the query
-// heads of all sequences of one prefix, 256 at a time, for each KV head; and
-// for each sequence and KV head its own rows with its G query heads.  Units of
-// more than kFew rows belong to the tensor-core kernel (k_shared_wide, tiles of
+// heads of all sequences of one prefix, 256 at a time (16 where the prefixes are
+// short), for each KV head; and for each sequence and KV head its own rows with
+// its G query heads.  Units of more than kFew rows belong to the tensor-core kernel (k_shared_wide, tiles of
 // kWideTile tokens, a CTA per worker), the others to the streaming kernel
 // (k_shared_few, a warp per worker).  Each kernel's tiles form one list, cut
 // into equal stretches, one per worker; a worker's part of a unit is a segment
@@ -34,11 +34,11 @@ inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
 }
 
 constexpr int kWideTile = 128;       // tokens of a wide tile, rows of a stream
-constexpr int kPair = 2 * kWideTile; // rows of a prefix unit
+constexpr int kPair = 2 * kWideTile; // rows of a wide unit at most
+constexpr int kPairLog = 8;
 constexpr int kFew = 16;             // rows a streaming unit has at most
+constexpr int kFewLog = 4;
 constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
-constexpr int kMaxPre = kMaxSeq + kMaxSeq * BPKV_MAX_GROUP / kPair;  // prefix items: one more per 256 rows
-constexpr int kMaxItems = kMaxPre + kMaxSeq;
 constexpr int kSms = 152;
 constexpr int kFewWarps = 8;         // per CTA of the streaming kernel
 
@@ -68,21 +68,33 @@ struct Args {
   int64_t few0, own0;         // first rows of the streaming kernel's prefix units and own units
   int32_t* status;
   int32_t wide_ctas, few_workers;
+  int32_t unit_log;           // rows of a prefix unit: kPairLog, or kFewLog without the wide kernel
   int32_t stages;             // of the wide kernel's ring
 };
 
+// Prefix items there can be with units of 2^log rows: one more for every full unit.
+constexpr int max_pre(int log) { return kMaxSeq + (kMaxSeq * BPKV_MAX_GROUP >> log); }
+
+// What every CTA works out; the wide kernel needs no streaming tiles.
+template <int MAX_PRE, bool STREAM>
 struct Plan {
-  int64_t wide[kMaxPre + 1];   // wide tiles before each prefix item, for one KV head
-  int64_t few[kMaxItems + 1];  // streaming tiles before each prefix item, then before each sequence
+  static constexpr bool kStream = STREAM;
+  int64_t wide[MAX_PRE + 1];  // wide tiles before each prefix item, for one KV head
+  // streaming tiles before each prefix item, then before each sequence
+  int64_t few[STREAM ? MAX_PRE + kMaxSeq + 1 : 1];
   uint16_t order[kMaxSeq];     // sequences by prefix
   uint16_t rank[kMaxSeq];      // each sequence's place among its prefix's
   int16_t pof[kMaxSeq];        // prefix of each sequence, -1: none
   uint16_t cnt[kMaxSeq];       // sequences of each prefix
   uint16_t first[kMaxSeq];     // where they begin in order
   uint16_t item0[kMaxSeq];     // first item of each prefix
-  uint16_t it_p[kMaxPre];      // prefix of each prefix item
+  int32_t tok[kMaxSeq];        // its tokens
+  uint16_t it_p[MAX_PRE];      // prefix of each prefix item
   int32_t n_pre;               // prefix items
 };
+
+using WidePlan = Plan<max_pre(kPairLog), false>;
+using FewPlan = Plan<max_pre(kFewLog), true>;
 
 // a / b of numbers that are not negative; in 32 bits where they fit, which they
 // nearly always do: a 64-bit division is some 100 dependent instructions.
@@ -111,15 +123,17 @@ __device__ __forceinline__ void warp_sums(int64_t* v, int n) {
   if (lane == 0) v[n] = sum;
 }
 
-__device__ __forceinline__ int pre_rows(const Args& a, const Plan& p, int item) {
+template <typename P>
+__device__ __forceinline__ int pre_rows(const Args& a, const P& p, int item) {
   const int x = p.it_p[item];
-  return min(kPair, p.cnt[x] * a.group - (item - p.item0[x]) * kPair);
+  return min(1 << a.unit_log, p.cnt[x] * a.group - ((item - p.item0[x]) << a.unit_log));
 }
 
 // All threads of the CTA (at least 256); ends with a barrier.  The lengths are
 // loaded at once; a single prefix, the usual case, needs no search for who has
 // which.
-__device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) {
+template <typename Q>
+__device__ __forceinline__ void make_plan(const Args& a, Q& p, int few_tile) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   const int P = a.plen ? a.n_prefix : 0, N = a.n_seq;
   constexpr int kPer = kMaxSeq / 256;
@@ -127,7 +141,7 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) 
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int i = tid + k * nt;
-    own[k] = i < N ? tokens_of(a.len[i], a.cap) : 0;
+    own[k] = Q::kStream && i < N ? tokens_of(a.len[i], a.cap) : 0;
   }
   if (P == 0) {
     for (int i = tid; i < N; i += nt) p.pof[i] = -1;
@@ -135,7 +149,7 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) 
   } else {
     for (int x = tid; x < P; x += nt) {
       p.cnt[x] = 0;
-      p.wide[x] = tokens_of(a.plen[x], a.pcap);  // until the items are known
+      p.tok[x] = (int32_t)tokens_of(a.plen[x], a.pcap);
     }
     for (int i = tid; i < N; i += nt) {
       const int x = a.prefix_of ? a.prefix_of[i] : 0;
@@ -162,7 +176,7 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) 
       for (int b = 0; b < P; b += 32) {
         const int x = b + lane;
         const int c = x >= P ? 0 : a.prefix_of ? p.cnt[x] : x == 0 ? N : 0;
-        const int it = x < P && p.wide[x] > 0 ? (c * a.group + kPair - 1) / kPair : 0;
+        const int it = x < P && p.tok[x] > 0 ? (c * a.group + (1 << a.unit_log) - 1) >> a.unit_log : 0;
         int sc = c, si = it;
         if (P > 1) {
 #pragma unroll
@@ -190,23 +204,24 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p, int few_tile) 
   __syncthreads();
   const int n_pre = p.n_pre;
   for (int i = tid; i < n_pre; i += nt) {
-    const int64_t n = tokens_of(a.plen[p.it_p[i]], a.pcap);
+    const int64_t n = p.tok[p.it_p[i]];
     const bool wide = pre_rows(a, p, i) > kFew;
     p.wide[i] = wide ? (n + kWideTile - 1) / kWideTile : 0;
-    p.few[i] = wide ? 0 : (n + few_tile - 1) / few_tile;
+    if constexpr (Q::kStream) p.few[i] = wide ? 0 : (n + few_tile - 1) / few_tile;
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int i = tid + k * nt;
     if (i < N) {
-      p.few[n_pre + i] = (own[k] + few_tile - 1) / few_tile;
+      if constexpr (Q::kStream) p.few[n_pre + i] = (own[k] + few_tile - 1) / few_tile;
       const int x = p.pof[i];
       if (x >= 0) p.order[p.first[x] + p.rank[i]] = (uint16_t)i;
     }
   }
   __syncthreads();
-  if (tid < 32) warp_sums(p.few, n_pre + N);
-  else if (tid < 64) warp_sums(p.wide, n_pre);
+  if (tid < 32) warp_sums(p.wide, n_pre);
+  if constexpr (Q::kStream)
+    if (tid >= 32 && tid < 64) warp_sums(p.few, n_pre + N);
   __syncthreads();
 }
 
@@ -235,16 +250,16 @@ __device__ __forceinline__ int64_t own_row(const Args& a, int64_t unit, int64_t 
 }
 
 // Where the partials of query row r = (sequence, KV head, head of the group) will be.
-__device__ __forceinline__ Parts parts_of(const Args& a, const Plan& p, int64_t r) {
+__device__ __forceinline__ Parts parts_of(const Args& a, const FewPlan& p, int64_t r) {
   const Share wide(p.wide[p.n_pre] * a.n_heads, a.wide_ctas);
   const Share few(p.few[p.n_pre + a.n_seq] * a.n_heads, a.few_workers);
   const int64_t u = quot(r, a.group);
   const int g = (int)(r - u * a.group), i = (int)quot(u, a.n_heads), h = (int)(u - (int64_t)i * a.n_heads);
   Parts q = {};
   const int x = p.pof[i];
-  const int row = x >= 0 ? p.rank[i] * a.group + g : 0, item = x >= 0 ? p.item0[x] + row / kPair : 0;
+  const int row = x >= 0 ? p.rank[i] * a.group + g : 0, item = x >= 0 ? p.item0[x] + (row >> a.unit_log) : 0;
   if (x >= 0 && item < p.n_pre && p.it_p[item] == x) {  // a prefix of length 0 has no items
-    const int in = row % kPair, rows = pre_rows(a, p, item);
+    const int in = row & ((1 << a.unit_log) - 1), rows = pre_rows(a, p, item);
     const bool is_wide = rows > kFew;
     const Share& share = is_wide ? wide : few;
     const int64_t* sums = is_wide ? p.wide : p.few;

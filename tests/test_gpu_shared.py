@@ -117,7 +117,9 @@ def reference(q, rows, lens, prows, plens, prefix_of, bits):
     return o, tol + 1e-30
 
 
-def run_case(pk, bits, N, H, G, lens, plens, prefix_of, seed=1, spread=0.75, sink=True, given=True):
+def run_case(pk, bits, N, H, G, lens, plens, prefix_of, seed=1, spread=0.75, sink=True, given=True, bound=None):
+    """One call against the formula.  bound: what the host knows of the prefixes' lengths (a cache of that size), which
+    decides whether they are streamed by 16 query rows or taken by the tensor cores."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     cap = max(512, (max(lens) + 511) // 512 * 512)
     q = torch.randn((N, H, G, D), generator=g, device="cuda").to(torch.bfloat16)
@@ -125,9 +127,10 @@ def run_case(pk, bits, N, H, G, lens, plens, prefix_of, seed=1, spread=0.75, sin
     c, rows = make_cache(pk, bits, G, cap, lens, k, v)
     pc, prows = None, None
     if plens:
-        pcap = max(512, (max(plens) + 511) // 512 * 512)
+        pcap = max(512, ((bound or max(plens)) + 511) // 512 * 512)
         k, v = draw_rows(g, len(plens), H, pcap, spread, sink)
         pc, prows = make_cache(pk, bits, G, pcap, plens, k, v)
+        pc.c.n_max = bound or max(plens)
     ws = pk.shared_workspace(c, pc)
     out = torch.full((N, H, G, D), float("nan"), dtype=torch.bfloat16, device="cuda")
     of = torch.tensor(prefix_of, dtype=torch.int32, device="cuda") if given else None
@@ -165,20 +168,24 @@ def test_nothing_at_all(pk):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("N,G", [(1, 4), (5, 3), (31, 4), (32, 4), (33, 4), (43, 3), (64, 4), (65, 4), (70, 8)])
-def test_one_prefix(pk, bits, N, G):
-    """Rows below, at and past 128 (one stream's worth) and 256 (a unit's)."""
+@pytest.mark.parametrize("bound", [None, 65536])
+@pytest.mark.parametrize("N,G", [(1, 4), (5, 3), (4, 8), (9, 4), (16, 4), (31, 4), (32, 4), (33, 4), (43, 3), (64, 4),
+                                 (65, 4), (70, 8)])
+def test_one_prefix(pk, bits, N, G, bound):
+    """Rows below, at and past 16 (streamed), 32 and 64 (copies), 128 (one stream's worth) and 256 (a unit's)."""
     lens = [(37 * i) % 300 for i in range(N)]
-    run_case(pk, bits, N, 2, G, lens, [1000], [0] * N, given=False)
+    for plen in (1000, 1):
+        run_case(pk, bits, N, 2, G, lens, [plen], [0] * N, given=False, bound=bound)
 
 
 @pytest.mark.parametrize("bits", BITS)
-def test_several_prefixes(pk, bits):
+@pytest.mark.parametrize("bound", [None, 65536])
+def test_several_prefixes(pk, bits, bound):
     """Mixed order, sequences without a prefix, an empty prefix and one nobody has."""
     N = 41
     of = [(0, 2, 1, 0, -1, 3, 7, 2)[i % 8] for i in range(N)]
     lens = [(53 * i) % 400 for i in range(N)]
-    run_case(pk, bits, N, 2, 8, lens, [777, 1, 513, 0, 900], of)
+    run_case(pk, bits, N, 2, 8, lens, [777, 1, 513, 0, 900], of, bound=bound)
 
 
 @pytest.mark.parametrize("bits", BITS)
@@ -186,6 +193,30 @@ def test_long_prefix_and_peaked_weights(pk, bits):
     """Many tiles for each CTA, a maximum that rises often, and one that sits in the first token."""
     run_case(pk, bits, 40, 4, 4, [(211 * i) % 900 for i in range(40)], [40001], [0] * 40, spread=1.3)
     run_case(pk, bits, 9, 1, 4, [5] * 9, [70000], [0] * 9, spread=0.2, sink=False, given=False)
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("N,bound", [(1, 2000), (40, 2000), (17, 65536), (40, 65536)])
+def test_rising_maximum_of_a_prefix(pk, bits, N, bound):
+    """Logits that climb along a prefix's rows, streamed, and on the tensor cores with 68 and 160 query rows."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    H, G, n, cap = 1, 4, 2000, 65536
+    q = (1 + 0.1 * torch.randn((N, H, G, D), generator=g, device="cuda")).to(torch.bfloat16)
+    ramp = torch.linspace(-4, 4, n, device="cuda")[None, None, :, None]
+    ramp = torch.cat((ramp, torch.zeros((1, 1, cap - n, 1), device="cuda")), 2)
+    k = (ramp + 0.05 * torch.randn((1, H, cap, D), generator=g, device="cuda")).to(torch.bfloat16)
+    v = torch.randn((1, H, cap, D), generator=g, device="cuda").to(torch.bfloat16)
+    own = [(5 * i) % 70 for i in range(N)]
+    ko, vo = draw_rows(g, N, H, 512)
+    c, rows = make_cache(pk, bits, G, 512, own, ko, vo)
+    pc, prows = make_cache(pk, bits, G, cap, [n], k, v)
+    pc.c.n_max = bound
+    ws = pk.shared_workspace(c, pc)
+    out = torch.empty((N, H, G, D), dtype=torch.bfloat16, device="cuda")
+    (pk.bpkv_shared_attend if bits == 16 else pk.bpkv_shared_attend8)(pc.c, None, c.c, q, out, ws, ws.numel())
+    assert pk.bpkv_read_status(ws) == 0
+    want, tol = reference(q, rows, own, prows, [n], [0] * N, bits)
+    assert ((out.double() - want).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("bits", BITS)
@@ -210,9 +241,10 @@ def test_rising_maximum(pk, bits):
 
 
 @pytest.mark.parametrize("bits", BITS)
-def test_repeats_streams_and_graphs(pk, bits):
+@pytest.mark.parametrize("bound", [None, 65536])
+def test_repeats_streams_and_graphs(pk, bits, bound):
     """The same bits from every call, on another stream, and from two captured graphs that share the workspace."""
-    r = run_case(pk, bits, 33, 2, 4, [(37 * i) % 300 for i in range(33)], [3001], [0] * 33, given=False)
+    r = run_case(pk, bits, 33, 2, 4, [(37 * i) % 300 for i in range(33)], [3001], [0] * 33, given=False, bound=bound)
     args = (r["pc"].c, r["of"], r["c"].c, r["q"])
     first = r["out"].clone()
     s = torch.cuda.Stream()
