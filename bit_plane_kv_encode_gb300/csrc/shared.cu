@@ -130,7 +130,7 @@ struct Walk {
     s.index = p.it_p[item];
     s.row0 = (item - p.item0[s.index]) * kPair;
     s.rows = pre_rows(a, p, item);
-    s.tokens = tokens_of(a.plen[s.index], a.pcap);
+    s.tokens = p.tok[s.index];
     s.unit = (int64_t)item * a.n_heads + s.h;
     s.dual = s.rows > kTile;
     pos += s.tiles;

@@ -48,7 +48,8 @@ struct Walk {
   int tok;
   int64_t pos, end;
   int item, h;
-  int64_t t, tiles, n, row0, unit;
+  int32_t n;
+  int64_t t, tiles, row0, unit;
   int side;  // 0: a prefix, 1: own rows
   int index;
   __device__ __forceinline__ Walk(const FewPlan& plan, const Args& args, int worker, int tile) : p(plan), a(args), tok(tile) {
@@ -77,7 +78,7 @@ struct Walk {
     const int64_t u = (int64_t)index * a.n_heads + h;
     unit = side ? u : (int64_t)item * a.n_heads + h;
     row0 = u * (side ? a.cap : a.pcap);
-    n = side ? tokens_of(a.len[index], a.cap) : tokens_of(a.plen[index], a.pcap);
+    n = side ? p.own[index] : p.tok[index];
   }
   __device__ __forceinline__ bool more() const { return pos < end; }
   // one tile on; true when that is another unit's

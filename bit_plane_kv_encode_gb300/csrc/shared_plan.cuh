@@ -89,6 +89,7 @@ struct Plan {
   uint16_t first[kMaxSeq];     // where they begin in order
   uint16_t item0[kMaxSeq];     // first item of each prefix
   int32_t tok[kMaxSeq];        // its tokens
+  int32_t own[STREAM ? kMaxSeq : 1];  // tokens of each sequence's own
   uint16_t it_p[MAX_PRE];      // prefix of each prefix item
   int32_t n_pre;               // prefix items
 };
@@ -213,6 +214,7 @@ __device__ __forceinline__ void make_plan(const Args& a, Q& p, int few_tile) {
   for (int k = 0; k < kPer; ++k) {
     const int i = tid + k * nt;
     if (i < N) {
+      if constexpr (Q::kStream) p.own[i] = (int32_t)own[k];
       if constexpr (Q::kStream) p.few[n_pre + i] = (own[k] + few_tile - 1) / few_tile;
       const int x = p.pof[i];
       if (x >= 0) p.order[p.first[x] + p.rank[i]] = (uint16_t)i;
