@@ -27,7 +27,7 @@ namespace bpkv {
 namespace shared {
 
 template <int BITS>
-cudaError_t launch_few(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);
+cudaError_t launch_few(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
 int few_tile(int bits);
 
 namespace {
@@ -810,7 +810,7 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
 // 32 sequences of 8 x 4 heads, streamed / wide, in us: 300 tokens 15.2 / 21.6,
 // 1000 tokens 19.3 / 22.0, 2000 tokens (66 MB) 27.7 / 24.2, 4000 tokens 40.2 /
 // 25.0; 8-bit rows: 2000 tokens (33 MB) 22.4 / 29.4, 4000 tokens 31.4 / 30.0.
-constexpr int64_t kStreamBytes = 60000000;
+constexpr int64_t kStreamBytes = 60000000;  // (with 8-bit rows a sixth more)
 
 // One side's rows: K and V (with their exponents for 8-bit rows).
 struct Side {
@@ -852,7 +852,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   const int64_t pn = prefix ? prefix->n : 0, pmax = prefix ? prefix->n_max : 0;
   const int64_t again =
       max64(min64(pn, own.n), (own.n * group + kFew - 1) / kFew) * n_heads * pmax * (BITS == 16 ? 4 * kD : 2 * kD);
-  const bool has_wide = prefix && own.n * group > kFew && again > kStreamBytes;
+  const bool has_wide = prefix && own.n * group > kFew && again > (BITS == 16 ? kStreamBytes : kStreamBytes / 6 * 7);
   a.unit_log = has_wide ? kPairLog : kFewLog;
   // no more CTAs than tiles, as far as the host knows (longer sequences than
   // it knows of only find fewer CTAs)
@@ -874,7 +874,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
     e = launch_pdl(k_shared_wide<BITS>, dim3(a.wide_ctas), dim3(kThreads), (size_t)Shape<BITS>::bytes(dual), st, a, maps);
     if (e != cudaSuccess) return e;
   }
-  return launch_few<BITS>(a, !has_wide, out, st);
+  return launch_few<BITS>(a, own.n_max, !has_wide, out, st);
 }
 
 }  // namespace

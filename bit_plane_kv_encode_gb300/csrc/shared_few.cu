@@ -43,6 +43,7 @@ struct Shape {
 
 // One worker's way through its tiles.
 struct Walk {
+  static constexpr bool kUnit = false;
   const FewPlan& p;
   const Args& a;
   int tok;
@@ -98,6 +99,32 @@ struct Walk {
     return true;
   }
   __device__ __forceinline__ int valid() const { return (int)min64(tok, n - t * tok); }
+};
+
+// A warp's way through one unit of own rows that a CTA takes whole: every
+// W-th tile, W the CTA's warps.
+template <int W>
+struct UnitWalk {
+  static constexpr bool kUnit = true;
+  static constexpr int side = 1;
+  const Args& a;
+  int tok, index, h, n, t, tiles;
+  int64_t row0, unit;
+  __device__ __forceinline__ UnitWalk(const Args& args, int tile) : a(args), tok(tile) {
+    unit = blockIdx.x;
+    index = (int)(blockIdx.x / (uint32_t)a.n_heads);
+    h = (int)(blockIdx.x - (uint32_t)index * a.n_heads);
+    n = (int)tokens_of(a.len[index], a.cap);
+    row0 = unit * a.cap;
+    tiles = (n + tok - 1) / tok;
+    t = threadIdx.x >> 5;
+  }
+  __device__ __forceinline__ bool more() const { return t < tiles; }
+  __device__ __forceinline__ bool next() {
+    t += W;
+    return false;
+  }
+  __device__ __forceinline__ int valid() const { return min(tok, n - t * tok); }
 };
 
 __device__ __forceinline__ void cp16_zero(uint32_t dst, const void* src, bool there, uint64_t policy) {
@@ -161,11 +188,11 @@ __device__ __forceinline__ uint32_t halves(uint32_t codes) {
 }
 
 // Issue the copies of the walk's tile into a stage.
-template <int BITS>
-__device__ __forceinline__ void load_tile(const Walk& w, uint32_t stage, uint32_t exps, uint64_t policy) {
+template <int BITS, typename W>
+__device__ __forceinline__ void load_tile(const W& w, uint32_t stage, uint32_t exps, uint64_t policy) {
   using S = Shape<BITS>;
   const int lane = threadIdx.x & 31, valid = w.valid();
-  const int64_t row = w.row0 + w.t * S::kTok;
+  const int64_t row = w.row0 + (int64_t)w.t * S::kTok;
   constexpr int kChunks = S::kRow / 16;  // 16-byte pieces of a row
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
@@ -181,8 +208,8 @@ __device__ __forceinline__ void load_tile(const Walk& w, uint32_t stage, uint32_
 
 // q of the unit as the 8-side operand of S^T, rows lane / 4 (+ 8), for 8-bit
 // rows as halves under a power-of-two scale of the row.
-template <int BITS, int NB>
-__device__ __forceinline__ void load_q(const Walk& w, int rows, uint32_t (*qb)[8][2], float (*qf)[2]) {
+template <int BITS, int NB, typename W>
+__device__ __forceinline__ void load_q(const W& w, int rows, uint32_t (*qb)[8][2], float (*qf)[2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const Args& a = w.a;
 #pragma unroll
@@ -191,10 +218,12 @@ __device__ __forceinline__ void load_q(const Walk& w, int rows, uint32_t (*qb)[8
     const uint16_t* q = nullptr;
     if (r < rows) {
       int seq = w.index, head = r;
-      if (w.side == 0) {
-        const int x = ((w.item - w.p.item0[w.index]) << a.unit_log) + r;
-        seq = w.p.order[w.p.first[w.index] + x / a.group];
-        head = x % a.group;
+      if constexpr (!W::kUnit) {
+        if (w.side == 0) {
+          const int x = ((w.item - w.p.item0[w.index]) << a.unit_log) + r;
+          seq = w.p.order[w.p.first[w.index] + x / a.group];
+          head = x % a.group;
+        }
       }
       q = a.q + (((int64_t)seq * a.n_heads + w.h) * a.group + head) * kD;
     }
@@ -230,44 +259,34 @@ __device__ __forceinline__ void load_q(const Walk& w, int rows, uint32_t (*qb)[8
   }
 }
 
-template <int BITS, int NB>
-__global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constant__ Args a, int32_t wait_first) {
-  extern __shared__ __align__(1024) unsigned char smem[];
+// What a warp has of its unit's rows: this thread's of O^T (channels g, g + 8 of
+// each 16 for bf16 rows, 2 g, 2 g + 1 for 8-bit ones; rows 2 c, 2 c + 1), m in
+// units of the logits, l of this thread's tokens.
+template <int NB>
+struct State {
+  float o[NB][8][4], m[NB][2], l[NB][2];
+};
+
+// The warp's tiles from `cur` on; the copies of those before `ahead` are already
+// under way.  end(unit, state, rows) after each unit.
+template <int BITS, int NB, typename W, typename R, typename E>
+__device__ __forceinline__ void stream(const Args& a, W& cur, W& ahead, uint32_t ring, const unsigned char* exps,
+                                       uint64_t policy, R&& rows_of, E&& end) {
   using S = Shape<BITS>;
-  FewPlan& plan = *reinterpret_cast<FewPlan*>(smem + S::kRing);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  // Behind the wide kernel of the same call, which starts this one only after
-  // its own wait, what that wait covered is complete: only the end waits, so
-  // that the two overlap.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
-  make_plan(a, plan, S::kTok);
-  const int worker = warp * gridDim.x + blockIdx.x;
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
-  unsigned char* exps = smem + kFewWarps * kStages * kStage + warp * kStages * S::kExps;
-  Walk ahead(plan, a, worker, S::kTok), cur = ahead;
-  const uint64_t policy = evict_first_policy();
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (ahead.more()) {
-      load_tile<BITS>(ahead, ring + i * kStage, smem_u32(exps) + i * S::kExps, policy);
-      ahead.next();
-    }
-    cp_async_commit();
-  }
-  // the join's table, while the first copies come
-  {
-    const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
-    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * tid; r < n; r += (int64_t)gridDim.x * kThreads)
-      a.parts[r] = parts_of(a, plan, r);
-  }
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // logits times this are in powers of two
   uint32_t qb[NB][8][2];
-  float qf[NB][2], o[NB][8][4], m[NB][2], l[NB][2];
+  float qf[NB][2];
+  State<NB> state;
+  auto& o = state.o;
+  auto& m = state.m;
+  auto& l = state.l;
   int rows = 0;
   bool fresh = true;
   int st = 0;
   while (cur.more()) {
     if (fresh) {
-      rows = cur.side ? a.group : pre_rows(a, plan, cur.item);
+      rows = rows_of(cur);
       load_q<BITS, NB>(cur, rows, qb, qf);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -347,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
       }
     }
     // ---- m follows the maximum when that has risen far enough
-    constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;  // x times this is in powers of two
     float top[NB][2];
     bool up = false;
 #pragma unroll
@@ -430,37 +448,146 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
       }
     }
     st = st == kStages - 1 ? 0 : st + 1;
-    // ---- the end of a segment: its partial rows
-    const int64_t at = cur.side ? own_row(a, cur.unit, worker) : few_row(a, cur.unit, worker);
+    const W was = cur;
     fresh = cur.next();
-    if (fresh || !cur.more()) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = nb * 8 + 2 * c + i;
-          float s = l[nb][i];
-#pragma unroll
-          for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-          if (r < rows) {
-            float* po = a.part_o + (at + r) * kD;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if constexpr (BITS == 16) {
-                po[16 * j + g] = o[nb][j][i];
-                po[16 * j + 8 + g] = o[nb][j][2 + i];
-              } else {
-                *reinterpret_cast<float2*>(po + 16 * j + 2 * g) = make_float2(o[nb][j][i], o[nb][j][2 + i]);
-              }
-            }
-            if (g == 0) a.part_ml[at + r] = make_float2(m[nb][i] * kUnit, s);
-          }
-        }
-    }
+    if (fresh || !cur.more()) end(was, state, rows);
   }
   cp_wait<0>();
+}
+
+// This warp's sum of the l of row 2 c + i.
+template <int NB>
+__device__ __forceinline__ float row_sum(const State<NB>& st, int nb, int i) {
+  float s = st.l[nb][i];
+#pragma unroll
+  for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  return s;
+}
+
+// The thread's part of row 2 c + i of O^T to the row at p.
+template <int BITS, int NB>
+__device__ __forceinline__ void put_row(const State<NB>& st, int nb, int i, float* p) {
+  const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (BITS == 16) {
+      p[16 * j + g] = st.o[nb][j][i];
+      p[16 * j + 8 + g] = st.o[nb][j][2 + i];
+    } else {
+      *reinterpret_cast<float2*>(p + 16 * j + 2 * g) = make_float2(st.o[nb][j][i], st.o[nb][j][2 + i]);
+    }
+  }
+}
+
+// Start the first copies of a warp's tiles.
+template <int BITS, typename W>
+__device__ __forceinline__ void prime(W& ahead, uint32_t ring, const unsigned char* exps, uint64_t policy) {
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (ahead.more()) {
+      load_tile<BITS>(ahead, ring + i * kStage, smem_u32(exps) + i * Shape<BITS>::kExps, policy);
+      ahead.next();
+    }
+    cp_async_commit();
+  }
+}
+
+template <int BITS, int NB>
+__global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constant__ Args a, int32_t wait_first) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  using S = Shape<BITS>;
+  constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;
+  FewPlan& plan = *reinterpret_cast<FewPlan*>(smem + S::kRing);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  // Behind the wide kernel of the same call, which starts this one only after
+  // its own wait, what that wait covered is complete: only the end waits, so
+  // that the two overlap.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+  make_plan(a, plan, S::kTok);
+  const int worker = warp * gridDim.x + blockIdx.x;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  const unsigned char* exps = smem + kFewWarps * kStages * kStage + warp * kStages * S::kExps;
+  Walk ahead(plan, a, worker, S::kTok), cur = ahead;
+  const uint64_t policy = evict_first_policy();
+  prime<BITS>(ahead, ring, exps, policy);
+  // the join's table, while the first copies come
+  {
+    const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
+    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * tid; r < n; r += (int64_t)gridDim.x * kThreads)
+      a.parts[r] = parts_of(a, plan, r);
+  }
+  stream<BITS, NB>(
+      a, cur, ahead, ring, exps, policy, [&](const Walk& w) { return w.side ? a.group : pre_rows(a, plan, w.item); },
+      [&](const Walk& w, const State<NB>& st, int rows) {  // the segment's partial rows
+        const int64_t at = w.side ? own_row(a, w.unit, worker) : few_row(a, w.unit, worker);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = nb * 8 + 2 * c + i;
+            const float s = row_sum(st, nb, i);
+            if (r < rows) {
+              put_row<BITS>(st, nb, i, a.part_o + (at + r) * kD);
+              if (g == 0) a.part_ml[at + r] = make_float2(st.m[nb][i] * kUnit, s);
+            }
+          }
+      });
   // the join follows this kernel: it must find the wide kernel complete too
   if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Short sequences without prefixes: a CTA takes a unit whole, its warps join in
+// shared memory, and neither plan nor partials nor join are needed.
+template <int BITS, int W>
+__global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __grid_constant__ Args a, uint16_t* out) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  using S = Shape<BITS>;
+  constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;
+  __shared__ float2 s_ml[W][8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  pdl_enter();
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  const unsigned char* exps = smem + W * kStages * kStage + warp * kStages * S::kExps;
+  UnitWalk<W> ahead(a, S::kTok), cur = ahead;
+  const uint64_t policy = evict_first_policy();
+  prime<BITS>(ahead, ring, exps, policy);
+  if (tid < W * 8) s_ml[tid / 8][tid % 8] = make_float2(-INFINITY, 0.f);
+  __syncthreads();
+  float* rows_o = reinterpret_cast<float*>(smem + warp * kStages * kStage);  // the warp's ring, once it is read
+  stream<BITS, 1>(
+      a, cur, ahead, ring, exps, policy, [&](const UnitWalk<W>&) { return a.group; },
+      [&](const UnitWalk<W>&, const State<1>& st, int rows) {
+        cp_wait<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float s = row_sum(st, 0, i);
+          if (2 * c + i < rows) {
+            put_row<BITS>(st, 0, i, rows_o + (2 * c + i) * kD);
+            if (g == 0) s_ml[warp][2 * c + i] = make_float2(st.m[0][i] * kUnit, s);
+          }
+        }
+      });
+  __syncthreads();
+  for (int x = tid; x < a.group * (kD / 2); x += W * 32) {
+    const int r = x / (kD / 2), d = x % (kD / 2) * 2;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][r].y == 0.f ? -INFINITY : fmaxf(s_ml[w][r].x, -3e38f));
+    float L = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 ml = s_ml[w][r];
+      if (ml.y == 0.f) continue;  // no tile: o was not written
+      const float f = ex2(fmaxf(ml.x, -3e38f) - M);
+      const float2 v = *reinterpret_cast<const float2*>(smem + w * kStages * kStage + (r * kD + d) * sizeof(float));
+      L = fmaf(f, ml.y, L);
+      o0 = fmaf(f, v.x, o0);
+      o1 = fmaf(f, v.y, o1);
+    }
+    const float s = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint32_t*>(out + ((int64_t)blockIdx.x * a.group + r) * kD + d) = pack<16>(o0 * s, o1 * s);
+  }
 }
 
 // ---- join: out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l
@@ -569,9 +696,36 @@ cudaError_t go(const Args& a, int ctas, bool wait_first, cudaStream_t st) {
 
 }  // namespace
 
+// Without prefixes, the longest sequences (as the host knows them) that a CTA
+// takes whole: one launch instead of two, without a plan.  bf16 rows of 8 x 4
+// heads, whole / planned, in us, sequences of up to 500 tokens: 1 of them
+// 4.7 / 7.5, 32 6.6 / 12.0, 128 20.9 / 29.3; 1000: 6.4 / 9.0, 11.4 / 15.7,
+// 37.9 / 46.0; 4000: 16.3 / 14.0 (1 of them).  Beyond 1024 little is won, and
+// a long sequence among short ones would be waited for.
+// Warps of a CTA: 8 while every unit has an SM to itself (32 x 8 units of up to
+// 500 tokens would take 8.3 us), else 4, and 2 for many short units (128 x 8 of
+// up to 100: 7.8 us instead of 10.9; of up to 1000: 40.4 instead of 37.9).
+constexpr int64_t kUnitTokens = 1024;
+
+template <int BITS, int W>
+cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out) {
+  constexpr int kSmem = Shape<BITS>::kRing / kFewWarps * W;
+  static std::atomic<uint64_t> done;
+  const cudaError_t e = allow_smem(k_shared_unit<BITS, W>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_shared_unit<BITS, W>, dim3((unsigned)((int64_t)a.n_seq * a.n_heads)), dim3(W * 32), (size_t)kSmem, st,
+                    a, out);
+}
+
 // The streaming kernel, then the join.  wait_first: no wide kernel came before.
 template <int BITS>
-cudaError_t launch_few(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st) {
+cudaError_t launch_few(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st) {
+  if (!a.plen && own_max <= kUnitTokens) {
+    const int64_t units = (int64_t)a.n_seq * a.n_heads;
+    if (units <= kSms) return go_unit<BITS, 8>(a, st, out);
+    if (units > 4 * kSms && own_max <= kUnitTokens / 2) return go_unit<BITS, 2>(a, st, out);
+    return go_unit<BITS, 4>(a, st, out);
+  }
   const int ctas = a.few_workers / kFewWarps;
   const cudaError_t e = a.plen ? go<BITS, 2>(a, ctas, wait_first, st) : go<BITS, 1>(a, ctas, wait_first, st);
   if (e != cudaSuccess) return e;
@@ -582,8 +736,8 @@ cudaError_t launch_few(const Args& a, bool wait_first, uint16_t* out, cudaStream
                     out);
 }
 
-template cudaError_t launch_few<16>(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);
-template cudaError_t launch_few<8>(const Args& a, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<16>(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<8>(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
 
 int few_tile(int bits) { return bits == 16 ? Shape<16>::kTok : Shape<8>::kTok; }
 

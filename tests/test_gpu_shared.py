@@ -156,6 +156,21 @@ def test_own_rows_only(pk, bits, n):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("N,H,G,longest", [(1, 1, 1, 1024), (76, 2, 8, 300), (77, 2, 5, 700), (305, 2, 4, 512),
+                                           (305, 2, 2, 513), (9, 3, 4, 1025)])
+def test_short_sequences(pk, bits, N, H, G, longest):
+    """Own rows by whole units of 8, 4 and 2 warps and, past 1024 tokens, planned; then with a bound below the lengths."""
+    lens = [(longest - 89 * i) % (longest + 1) for i in range(N)]
+    lens[N // 2:N // 2 + 3] = [0, 1, 17][:len(lens[N // 2:N // 2 + 3])]
+    lens[0] = longest
+    r = run_case(pk, bits, N, H, G, lens, [], [0] * N, given=False)
+    r["c"].c.n_max = 1
+    r["out"].fill_(float("nan"))
+    r["fn"](None, None, r["c"].c, r["q"], r["out"], r["ws"], r["ws"].numel())
+    assert ((r["out"].double() - r["want"]).abs() <= r["tol"]).all()
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("G", [1, 3, 8])
 def test_ragged_batch_with_empty_sequences(pk, bits, G):
     lens = [0, 1, 700, 0, 129, 1500, 128]
@@ -220,17 +235,18 @@ def test_rising_maximum_of_a_prefix(pk, bits, N, bound):
 
 
 @pytest.mark.parametrize("bits", BITS)
-def test_rising_maximum(pk, bits):
+@pytest.mark.parametrize("n", [2000, 1023])
+def test_rising_maximum(pk, bits, n):
     """Logits that climb along the rows: O is rescaled tile after tile."""
     g = torch.Generator(device="cuda").manual_seed(7)
-    N, H, G, n = 3, 1, 4, 2000
+    N, H, G = 3, 1, 4
     q = torch.ones((N, H, G, D), device="cuda").to(torch.bfloat16)
     ramp = torch.linspace(-4, 4, n, device="cuda")[None, None, :, None]
     k = (ramp + 0.05 * torch.randn((N, H, n, D), generator=g, device="cuda")).to(torch.bfloat16)
     v = torch.randn((N, H, n, D), generator=g, device="cuda").to(torch.bfloat16)
     cap = 2048
     pad = torch.zeros((N, H, cap - n, D), dtype=torch.bfloat16, device="cuda")
-    lens = [n, 1100, 64]
+    lens = [n, n * 11 // 20, 64]
     c, rows = make_cache(pk, bits, G, cap, lens, torch.cat((k, pad), 2), torch.cat((v, pad), 2))
     ws = pk.shared_workspace(c)
     out = torch.empty((N, H, G, D), dtype=torch.bfloat16, device="cuda")
