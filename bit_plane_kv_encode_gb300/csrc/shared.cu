@@ -424,184 +424,184 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
   if (warp < 4) {
     // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
     regs_fewer<80>();
-  if (warp == 0) {
-    if (elect_one()) {
-      // ---- loads: K then V of every tile
-      uint32_t stage = 0, phase = 0, issued = 0;
-      const uint64_t policy = evict_first_policy();
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        const int64_t base = (int64_t)g.index * a.n_heads + g.h;
-        for (int t = 0; ok && t < g.tiles; ++t) {
-          const int64_t tok = (g.tile0 + t) * kTile;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_wait(smem_u32(&sm.empty[stage]), phase ^ 1, abort);
-            if (!ok) break;
-            const uint32_t bar = smem_u32(&sm.full[stage]);
-            const uint32_t dst = smem_u32(ring + stage * S::kStage);
-            mbar_expect_tx(bar, S::kStage + (kv ? S::kExps : 0));
-            if constexpr (BITS == 16) {
-              tma_load_4d(dst, &maps.m[kv], bar, 0, (int)tok, 0, (int)base, policy);
-            } else {
-              tma_load_3d(dst, &maps.m[kv], bar, 0, (int)tok, (int)base, policy);
-              if (kv) {
-                const uint32_t e = smem_u32(ring_exps + stage * S::kExps);
-                bulk_load(e, a.exps[0][0] + base * a.pcap + tok, kTile, bar);
-                bulk_load(e + kTile, a.exps[0][1] + base * a.pcap + tok, kTile, bar);
-              }
-            }
-            ++issued;
-            if (++stage == (uint32_t)n_stage) stage = 0, phase ^= 1;
-          }
-        }
-      }
-      if (!ok) {  // the copies in flight must land before the CTA's shared memory is given up
-        uint32_t never = 0;
-        for (uint32_t k = issued > (uint32_t)n_stage ? issued - n_stage : 0; k < issued; ++k)
-          mbar_wait(smem_u32(&sm.full[k % n_stage]), (k / n_stage) & 1, &never);
-      }
-    }
-  } else if (warp == 1) {
-    if (elect_one()) {
-      // ---- products.  Step i of a segment is stream i & 1; S of step i is
-      // issued before O of step i - 1, so the tensor cores work while the
-      // other stream's softmax runs.  Products run in the order issued: S(i)
-      // overwrites P(i - 2) only after O(i - 2) has read it.
-      constexpr uint32_t kDescS = BITS == 16 ? mma_desc(1, 1, 0, kTile, kTile) : mma_desc(0, 0, 0, kTile, kTile);
-      constexpr uint32_t kDescO = BITS == 16 ? mma_desc(1, 1, 1, kTile, kD) : mma_desc(1, 0, 1, kTile, kD);
-      uint32_t tile_no = 0;  // tiles before this segment
-      uint32_t seg = 0, p_phase = 0;
-      bool ok = true;
-      uint32_t k_st = 0, k_ph = 0, v_st = 1, v_ph = 0;
-      auto skip = [&](uint32_t& st, uint32_t& ph) {  // two stages on
-        st += 2;
-        if (st >= (uint32_t)n_stage) st -= n_stage, ph ^= 1;
-      };
-      while (ok && walk.next(g)) {
-        ok = mbar_wait(smem_u32(&sm.q_full), seg & 1, abort);
-        if (!ok) break;
-        const int steps = g.steps();
-        for (int i = 0; ok && i <= steps; ++i) {
-          if (i < steps) {
-            const int s = i & 1;
-            const uint32_t st = k_st;
-            if (!g.dual || s == 0) {
-              ok = mbar_wait(smem_u32(&sm.full[st]), k_ph, abort);
+    if (warp == 0) {
+      if (elect_one()) {
+        // ---- loads: K then V of every tile
+        uint32_t stage = 0, phase = 0, issued = 0;
+        const uint64_t policy = evict_first_policy();
+        bool ok = true;
+        while (ok && walk.next(g)) {
+          const int64_t base = (int64_t)g.index * a.n_heads + g.h;
+          for (int t = 0; ok && t < g.tiles; ++t) {
+            const int64_t tok = (g.tile0 + t) * kTile;
+  #pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              ok = ok && mbar_wait(smem_u32(&sm.empty[stage]), phase ^ 1, abort);
               if (!ok) break;
-            }
-            fence_after();
-            const uint32_t kb = smem_desc(smem_u32(ring + st * S::kStage), 16);
-            const uint32_t qb = smem_desc(smem_u32(q_smem + (g.dual ? s : 0) * S::kQ), 16);
-            const uint32_t d = tmem + s * kTile;
-            if constexpr (BITS == 16) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t o = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-                mma16_ss(d, qb + o, kb + o, kDescS, k > 0);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)  // both pieces of q against the same codes
-                mma8_ss(d, qb + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4), kb + ((k % 4) * 32 >> 4), kDescS, k > 0);
-            }
-            mma_commit(smem_u32(&sm.s_full[s]));
-            if (!g.dual || s) {
-              mma_commit(smem_u32(&sm.empty[st]));
-              skip(k_st, k_ph);
-            }
-            if (i == steps - 1) mma_commit(smem_u32(&sm.q_empty));
-          }
-          if (i > 0) {
-            const int j = i - 1, s = j & 1;
-            const uint32_t st = v_st;
-            const uint32_t pp = (p_phase >> s) & 1;
-            p_phase ^= 1u << s;
-            ok = (g.dual && s) || mbar_wait(smem_u32(&sm.full[st]), v_ph, abort);
-            ok = ok && mbar_wait(smem_u32(&sm.p_half[s]), pp, abort);
-            if (!ok) break;
-            fence_after();
-            const uint32_t vb = smem_desc(smem_u32(ring + st * S::kStage), BITS == 16 ? kTile * 128 : 16);
-            const uint32_t p = tmem + s * kTile, d = tmem + 2 * kTile + s * kD;
-            const uint32_t acc = j >= 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 64 tokens each
-              if (h) {
-                ok = mbar_wait(smem_u32(&sm.p_ready[s]), pp, abort);
-                if (!ok) break;
-                fence_after();
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (BITS == 16) {
-                  const int k = h * 4 + i;
-                  mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, acc | (h | i));
-                } else {  // two products of the high pieces, two of the low
-                  const int k = h * 2 + (i & 1);
-                  mma8_ts(d, p + (i >> 1) * 32 + k * 8, vb + (k * 32 * 128 >> 4), kDescO, acc | (h | i));
+              const uint32_t bar = smem_u32(&sm.full[stage]);
+              const uint32_t dst = smem_u32(ring + stage * S::kStage);
+              mbar_expect_tx(bar, S::kStage + (kv ? S::kExps : 0));
+              if constexpr (BITS == 16) {
+                tma_load_4d(dst, &maps.m[kv], bar, 0, (int)tok, 0, (int)base, policy);
+              } else {
+                tma_load_3d(dst, &maps.m[kv], bar, 0, (int)tok, (int)base, policy);
+                if (kv) {
+                  const uint32_t e = smem_u32(ring_exps + stage * S::kExps);
+                  bulk_load(e, a.exps[0][0] + base * a.pcap + tok, kTile, bar);
+                  bulk_load(e + kTile, a.exps[0][1] + base * a.pcap + tok, kTile, bar);
                 }
               }
+              ++issued;
+              if (++stage == (uint32_t)n_stage) stage = 0, phase ^= 1;
             }
+          }
+        }
+        if (!ok) {  // the copies in flight must land before the CTA's shared memory is given up
+          uint32_t never = 0;
+          for (uint32_t k = issued > (uint32_t)n_stage ? issued - n_stage : 0; k < issued; ++k)
+            mbar_wait(smem_u32(&sm.full[k % n_stage]), (k / n_stage) & 1, &never);
+        }
+      }
+    } else if (warp == 1) {
+      if (elect_one()) {
+        // ---- products.  Step i of a segment is stream i & 1; S of step i is
+        // issued before O of step i - 1, so the tensor cores work while the
+        // other stream's softmax runs.  Products run in the order issued: S(i)
+        // overwrites P(i - 2) only after O(i - 2) has read it.
+        constexpr uint32_t kDescS = BITS == 16 ? mma_desc(1, 1, 0, kTile, kTile) : mma_desc(0, 0, 0, kTile, kTile);
+        constexpr uint32_t kDescO = BITS == 16 ? mma_desc(1, 1, 1, kTile, kD) : mma_desc(1, 0, 1, kTile, kD);
+        uint32_t tile_no = 0;  // tiles before this segment
+        uint32_t seg = 0, p_phase = 0;
+        bool ok = true;
+        uint32_t k_st = 0, k_ph = 0, v_st = 1, v_ph = 0;
+        auto skip = [&](uint32_t& st, uint32_t& ph) {  // two stages on
+          st += 2;
+          if (st >= (uint32_t)n_stage) st -= n_stage, ph ^= 1;
+        };
+        while (ok && walk.next(g)) {
+          ok = mbar_wait(smem_u32(&sm.q_full), seg & 1, abort);
+          if (!ok) break;
+          const int steps = g.steps();
+          for (int i = 0; ok && i <= steps; ++i) {
+            if (i < steps) {
+              const int s = i & 1;
+              const uint32_t st = k_st;
+              if (!g.dual || s == 0) {
+                ok = mbar_wait(smem_u32(&sm.full[st]), k_ph, abort);
+                if (!ok) break;
+              }
+              fence_after();
+              const uint32_t kb = smem_desc(smem_u32(ring + st * S::kStage), 16);
+              const uint32_t qb = smem_desc(smem_u32(q_smem + (g.dual ? s : 0) * S::kQ), 16);
+              const uint32_t d = tmem + s * kTile;
+              if constexpr (BITS == 16) {
+  #pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t o = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+                  mma16_ss(d, qb + o, kb + o, kDescS, k > 0);
+                }
+              } else {
+  #pragma unroll
+                for (int k = 0; k < 8; ++k)  // both pieces of q against the same codes
+                  mma8_ss(d, qb + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4), kb + ((k % 4) * 32 >> 4), kDescS, k > 0);
+              }
+              mma_commit(smem_u32(&sm.s_full[s]));
+              if (!g.dual || s) {
+                mma_commit(smem_u32(&sm.empty[st]));
+                skip(k_st, k_ph);
+              }
+              if (i == steps - 1) mma_commit(smem_u32(&sm.q_empty));
+            }
+            if (i > 0) {
+              const int j = i - 1, s = j & 1;
+              const uint32_t st = v_st;
+              const uint32_t pp = (p_phase >> s) & 1;
+              p_phase ^= 1u << s;
+              ok = (g.dual && s) || mbar_wait(smem_u32(&sm.full[st]), v_ph, abort);
+              ok = ok && mbar_wait(smem_u32(&sm.p_half[s]), pp, abort);
+              if (!ok) break;
+              fence_after();
+              const uint32_t vb = smem_desc(smem_u32(ring + st * S::kStage), BITS == 16 ? kTile * 128 : 16);
+              const uint32_t p = tmem + s * kTile, d = tmem + 2 * kTile + s * kD;
+              const uint32_t acc = j >= 2;
+  #pragma unroll
+              for (int h = 0; h < 2; ++h) {  // 64 tokens each
+                if (h) {
+                  ok = mbar_wait(smem_u32(&sm.p_ready[s]), pp, abort);
+                  if (!ok) break;
+                  fence_after();
+                }
+  #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (BITS == 16) {
+                    const int k = h * 4 + i;
+                    mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, acc | (h | i));
+                  } else {  // two products of the high pieces, two of the low
+                    const int k = h * 2 + (i & 1);
+                    mma8_ts(d, p + (i >> 1) * 32 + k * 8, vb + (k * 32 * 128 >> 4), kDescO, acc | (h | i));
+                  }
+                }
+              }
+              if (!ok) break;
+              if (!g.dual || s) {
+                mma_commit(smem_u32(&sm.empty[st]));
+                skip(v_st, v_ph);
+              }
+              if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
+            }
+          }
+          tile_no += g.tiles;
+          ++seg;
+        }
+        // every product is complete before tensor memory is given up
+        uint32_t never = 0;
+        mma_commit(smem_u32(&sm.done));
+        mbar_wait(smem_u32(&sm.done), 0, &never);
+      }
+    } else {
+      if constexpr (BITS == 8) {
+        // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
+        // segment when the stream does: further ahead, a stage's phase bit would
+        // be that of an earlier fill.
+        const int s = warp - 2;
+        uint32_t tile_no = 0, n = 0, go = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+          const int steps = g.steps_of(s);
+          if (steps > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_go[s]), go, abort));
             if (!ok) break;
-            if (!g.dual || s) {
-              mma_commit(smem_u32(&sm.empty[st]));
-              skip(v_st, v_ph);
+            go ^= 1;
+          }
+          for (int j = 0; j < steps; ++j, ++n) {
+            const int t = g.tile_of(s, j), b = n & 1;
+            const uint32_t use = 2 * (tile_no + t) + 1, st = use % n_stage;
+            ok = mbar_wait(smem_u32(&sm.sc_empty[s][b]), ((n >> 1) & 1) ^ 1, abort) &&
+                 mbar_wait(smem_u32(&sm.full[st]), (use / n_stage) & 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t* e = reinterpret_cast<const uint32_t*>(ring_exps + st * S::kExps);
+            const uint32_t ke = e[lane], ve = e[kTile / 4 + lane];
+            const int valid = g.valid(t) - lane * 4;
+            float kf[4], ev[4], iv[4];
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = min(max((int)((ke >> (8 * i)) & 0xff) - kExpBias, kExpMin), kExpMax);
+              const int v = min(max((int)((ve >> (8 * i)) & 0xff) - kExpBias, kExpMin), kExpMax);
+              kf[i] = i < valid ? exp2i(k) * kLogScale : 0.f;
+              ev[i] = i < valid ? (float)v : 0.f;
+              iv[i] = i < valid ? exp2i(-v) : 0.f;
             }
-            if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
+            *reinterpret_cast<float4*>(&sm.sc.tok[s][b][0][lane * 4]) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+            *reinterpret_cast<float4*>(&sm.sc.tok[s][b][1][lane * 4]) = make_float4(ev[0], ev[1], ev[2], ev[3]);
+            *reinterpret_cast<float4*>(&sm.sc.tok[s][b][2][lane * 4]) = make_float4(iv[0], iv[1], iv[2], iv[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[s][b]));
           }
+          tile_no += g.tiles;
         }
-        tile_no += g.tiles;
-        ++seg;
-      }
-      // every product is complete before tensor memory is given up
-      uint32_t never = 0;
-      mma_commit(smem_u32(&sm.done));
-      mbar_wait(smem_u32(&sm.done), 0, &never);
-    }
-  } else {
-    if constexpr (BITS == 8) {
-      // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
-      // segment when the stream does: further ahead, a stage's phase bit would
-      // be that of an earlier fill.
-      const int s = warp - 2;
-      uint32_t tile_no = 0, n = 0, go = 0;
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        const int steps = g.steps_of(s);
-        if (steps > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_go[s]), go, abort));
-          if (!ok) break;
-          go ^= 1;
-        }
-        for (int j = 0; j < steps; ++j, ++n) {
-          const int t = g.tile_of(s, j), b = n & 1;
-          const uint32_t use = 2 * (tile_no + t) + 1, st = use % n_stage;
-          ok = mbar_wait(smem_u32(&sm.sc_empty[s][b]), ((n >> 1) & 1) ^ 1, abort) &&
-               mbar_wait(smem_u32(&sm.full[st]), (use / n_stage) & 1, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint32_t* e = reinterpret_cast<const uint32_t*>(ring_exps + st * S::kExps);
-          const uint32_t ke = e[lane], ve = e[kTile / 4 + lane];
-          const int valid = g.valid(t) - lane * 4;
-          float kf[4], ev[4], iv[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = min(max((int)((ke >> (8 * i)) & 0xff) - kExpBias, kExpMin), kExpMax);
-            const int v = min(max((int)((ve >> (8 * i)) & 0xff) - kExpBias, kExpMin), kExpMax);
-            kf[i] = i < valid ? exp2i(k) * kLogScale : 0.f;
-            ev[i] = i < valid ? (float)v : 0.f;
-            iv[i] = i < valid ? exp2i(-v) : 0.f;
-          }
-          *reinterpret_cast<float4*>(&sm.sc.tok[s][b][0][lane * 4]) = make_float4(kf[0], kf[1], kf[2], kf[3]);
-          *reinterpret_cast<float4*>(&sm.sc.tok[s][b][1][lane * 4]) = make_float4(ev[0], ev[1], ev[2], ev[3]);
-          *reinterpret_cast<float4*>(&sm.sc.tok[s][b][2][lane * 4]) = make_float4(iv[0], iv[1], iv[2], iv[3]);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[s][b]));
-        }
-        tile_no += g.tiles;
       }
     }
-  }
   } else {
     // ---- softmax of stream s, a thread per row
     regs_more<208>();

@@ -4,12 +4,14 @@
 // A unit is a set of query rows that attend over the same KV rows: the query
 // heads of all sequences of one prefix, 256 at a time (16 where the prefixes are
 // short), for each KV head; and for each sequence and KV head its own rows with
-// its G query heads.  Units of more than kFew rows belong to the tensor-core kernel (k_shared_wide, tiles of
-// kWideTile tokens, a CTA per worker), the others to the streaming kernel
-// (k_shared_few, a warp per worker).  Each kernel's tiles form one list, cut
-// into equal stretches, one per worker; a worker's part of a unit is a segment
-// and leaves its rows' (m, l, o).  Lengths are read on the device, so the cut
-// fits ragged batches; every CTA works the same plan out for itself.
+// its G query heads.  Units of more than kFew rows belong to the tensor-core
+// kernel (k_shared_wide, tiles of kWideTile tokens, a CTA per worker), the
+// others to the streaming kernel (k_shared_few, a warp per worker).  Each
+// kernel's tiles form one list, cut into equal stretches, one per worker; a
+// worker's part of a unit is a segment and leaves its rows' (m, l, o).  Lengths
+// are read on the device, so the cut fits ragged batches; every CTA works the
+// same plan out for itself.  Short sequences without prefixes need none of this
+// (k_shared_unit).
 #pragma once
 
 #include <atomic>
@@ -31,6 +33,15 @@ inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done)
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// L2 policy of rows that are streamed once: they go before anything else, so
+// that a cache larger than L2 does not push out what the next kernels read (the
+// partial results, and the kernels' own instructions).
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 constexpr int kWideTile = 128;       // tokens of a wide tile, rows of a stream

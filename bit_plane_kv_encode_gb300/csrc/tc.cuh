@@ -135,12 +135,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(addr)
-               : "memory");
-}
-
 // ---- float32 arithmetic on pairs ----
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
