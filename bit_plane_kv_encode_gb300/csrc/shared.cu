@@ -9,8 +9,17 @@
 // O += P V, with O in tensor memory too.  The groups are two streams that take
 // turns at the tensor cores: with more than 128 rows each has its own 128 rows
 // and both take every tile; with fewer both hold the same rows and each takes
-// every other tile.  m only follows the maximum when that has risen by a factor
-// of 2^kLazy, so O is seldom rescaled.
+// every other tile.  Rows that fill half or a quarter of the 128 are held twice
+// or four times (the instruction takes 128), each copy's threads weighing their
+// share of the tile's tokens.  m only follows the maximum when that has risen by
+// a factor of 2^kLazy, so O is seldom rescaled.
+//
+// What bounds it: with 256 rows the chain S -> softmax (about 1650 cycles) -> O,
+// of which two streams hide half: the tensor cores are busy 65% of the time.
+// Measured on a GB300 with 128 sequences of 8 x 4 heads over one prefix of
+// 131072 tokens: 203 us for this kernel, 1.35 PFLOP/s; with 32 over 32768 tokens
+// 25 us, 5.4 TB/s.  8-bit rows, 16 sequences of 4 x 8 heads over two prefixes of
+// 131071 tokens: 80 us, 3.4 TB/s, bound by the softmax with its scales.
 //
 // 8-bit rows.  The products take the codes as they lie.  q becomes two e4m3
 // pieces of 4 bits under a power-of-two scale of its row, which is all of a
@@ -751,7 +760,8 @@ struct Space {
 Space space(int64_t n_seq, int64_t n_prefix, int64_t n_heads, int64_t group) {
   Space s;
   // a segment is unit u's part in worker w, slot u + w of its kind
-  const int64_t wide = n_prefix && n_seq * group > kFew ? (units(n_seq, n_prefix, group, kPairLog) * n_heads + kSms) * kPair : 0;
+  const int64_t wide =
+      n_prefix && n_seq * group > kFew ? (units(n_seq, n_prefix, group, kPairLog) * n_heads + kSms) * kPair : 0;
   const int64_t few = n_prefix ? (units(n_seq, n_prefix, group, kFewLog) * n_heads + kSms * kFewWarps) * kFew : 0;
   const int64_t own = (n_seq * n_heads + kSms * kFewWarps) * group;
   s.few0 = wide;
@@ -810,7 +820,10 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
 // 32 sequences of 8 x 4 heads, streamed / wide, in us: 300 tokens 15.2 / 21.6,
 // 1000 tokens 19.3 / 22.0, 2000 tokens (66 MB) 27.7 / 24.2, 4000 tokens 40.2 /
 // 25.0; 8-bit rows: 2000 tokens (33 MB) 22.4 / 29.4, 4000 tokens 31.4 / 30.0.
-constexpr int64_t kStreamBytes = 60000000;  // (with 8-bit rows a sixth more)
+// With three prefixes of 2000 tokens and 64 sequences of 4 x 8 heads over 8-bit
+// rows (66 MB) 35.5 / 47.
+template <int BITS>
+constexpr int64_t kStreamBytes = BITS == 16 ? 60000000 : 70000000;
 
 // One side's rows: K and V (with their exponents for 8-bit rows).
 struct Side {
@@ -852,7 +865,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   const int64_t pn = prefix ? prefix->n : 0, pmax = prefix ? prefix->n_max : 0;
   const int64_t again =
       max64(min64(pn, own.n), (own.n * group + kFew - 1) / kFew) * n_heads * pmax * (BITS == 16 ? 4 * kD : 2 * kD);
-  const bool has_wide = prefix && own.n * group > kFew && again > (BITS == 16 ? kStreamBytes : kStreamBytes / 6 * 7);
+  const bool has_wide = prefix && own.n * group > kFew && again > kStreamBytes<BITS>;
   a.unit_log = has_wide ? kPairLog : kFewLog;
   // no more CTAs than tiles, as far as the host knows (longer sequences than
   // it knows of only find fewer CTAs)

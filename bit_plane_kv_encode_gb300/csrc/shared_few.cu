@@ -15,7 +15,11 @@
 // 8-bit rows: a code is exactly a half, so codes become halves in registers;
 // channels are taken in the order the bytes come in (the same for K and q).
 // K's scales multiply S, V's join the exponent as in the wide kernel: p' = p
-// 2^ev is the weight in the product, p = p' 2^-ev the term of the sum.
+// 2^ev is the weight in the product, p = p' 2^-ev the term of the sum.  p' is a
+// half here, 2^-11 of rounding: the product is of halves anyway.
+//
+// Measured on a GB300: 32 sequences of 8 x 4 heads over 8-bit rows of their own,
+// up to 16384 tokens (542 MB): 85.5 us with the join, 6.3 TB/s.
 #include "rows8_core.cuh"
 #include "shared_plan.cuh"
 
@@ -537,7 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
 }
 
 // Short sequences without prefixes: a CTA takes a unit whole, its warps join in
-// shared memory, and neither plan nor partials nor join are needed.
+// shared memory, and neither plan nor partials nor join are needed.  One
+// sequence of 8 x 4 heads and 500 bf16 tokens takes 4.8 us: the launch, four
+// rounds of loads and products of each warp, and the join, all latency.
 template <int BITS, int W>
 __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __grid_constant__ Args a, uint16_t* out) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
 // W warps a row; each takes every W-th part, with its own running maximum, so
 // that a part's (m, l) and o are loaded together: two round trips in all, the
 // table's and the parts'.  Many rows have few parts each and take one warp,
-// few rows have many and take eight.
+// few rows have many and take eight.  About 5 us behind its kernels, latency.
 
 constexpr int kJoinWarps = 8;
 constexpr int kJoinDeep = 8;  // parts in flight

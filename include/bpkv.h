@@ -467,20 +467,26 @@ int bpkv_qkv_rope(const bpkv_qkv_args *a, void *stream);
  * prefix_of[i] and over its own rows 0 .. seq_len[i] - 1,
  *   o = sum_x softmax_x(q . k_x / sqrt(D)) v_x over both sets together,
  * zeros when both are empty.  A prefix is stored once, as one sequence of the
- * cache `prefix`, and its rows are read once for all the query heads of all
- * the sequences that share it (up to 256 at a time), on the tensor cores.
+ * cache `prefix`.  A long one's rows are read once for up to 256 query heads of
+ * the sequences that share it, on the tensor cores; short ones, and those of
+ * few sequences, are streamed for 16 query heads at a time.
  *   prefix     the P prefixes (NULL: none); same n_kv_heads and group as c
  *   prefix_of  int32 [N] device; values outside 0 .. P - 1 mean no prefix.
  *              NULL: every sequence has prefix 0
  *   q          bf16 [N][H][G][D], out bf16 [N][H][G][D] (16-byte aligned)
  * Logits, softmax statistics and sums are float32; the softmax weights enter
- * the products as bf16 (bpkv_shared_attend) or as two 3-bit pieces
- * (bpkv_shared_attend8, where q enters as two e4m3 pieces of 4 bits).  Rows past
- * the lengths may hold anything.  Stored rows, q and logits must be finite.
+ * the products as bf16 (bpkv_shared_attend), and for bpkv_shared_attend8 as
+ * halves or, on the tensor cores, as two 3-bit pieces with q as two e4m3 pieces
+ * of 4 bits.  Rows past the lengths may hold anything.  Stored rows, q and
+ * logits must be finite.  n_max of the caches sizes the launches and chooses
+ * between the ways above; longer sequences (in a replayed graph) are attended
+ * to in full, but take longer than they need: capture with n_max set to what
+ * the lengths will reach.  Equal calls give equal bits.
  * Device memory only: BPKV_EUNSUPPORTED for residency 1, and for more than
  * BPKV_SHARED_MAX_SEQ sequences or prefixes.  Workspace:
  * bpkv_shared_workspace_size bytes, 256-byte aligned, with nothing kept in it
- * from call to call; its first 256 bytes hold the status word
+ * from call to call (calls that may run at the same time need one each); its
+ * first 256 bytes hold the status word
  * (BPKV_DEV_TIMEOUT when a wait inside the kernel gave up; clear it first).
  */
 #define BPKV_SHARED_MAX_SEQ 512
