@@ -9,7 +9,7 @@
 // Measured on a GB300: 32768 tokens of 8 KV heads quantised (202 MB) in 30.6 us,
 // 6.6 TB/s; 4 x 8191 tokens read back (202 MB) in 32.6 us, 6.2 TB/s.  With one
 // row a group and an exponent byte stored at a time: 36.6 and 36.5 us.  One
-// token of 32 sequences: 2.1 us for both launches, latency.
+// token of 32 sequences: 2.1 us, latency.
 #include "rows8_core.cuh"
 
 namespace bpkv {
@@ -34,7 +34,9 @@ struct AppendArgs {
   const uint16_t* v_new;
   const int64_t* start;
   int32_t* status;
-  int32_t n_seq, n_heads, t_new, bump;
+  int32_t n_seq, n_heads, t_new;
+  int32_t per;   // rows of a CTA
+  int32_t bump;  // the lengths are raised by a launch of their own
 };
 
 template <int R>
@@ -43,22 +45,24 @@ __global__ void __launch_bounds__(kR8Threads) k_rows8_append(const __grid_consta
   __shared__ uint8_t s_exp[2][kR8Groups * R];
   __shared__ int64_t s_dst[kR8Groups * R];  // -1: not written
   const int tid = threadIdx.x, l16 = tid & 15, grp = tid >> 4;
-  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.t_new, r0 = (int64_t)blockIdx.x * (kR8Groups * R);
+  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.t_new, r0 = (int64_t)blockIdx.x * a.per;
+  const int64_t end = min64(rows, r0 + a.per);
   uint4 w[R][2];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int64_t r = r0 + i * kR8Groups + grp;
     w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
+    if (r < end) {
       w[i][0] = __ldcs(reinterpret_cast<const uint4*>(a.k_new + r * kD + l16 * 8));
       w[i][1] = __ldcs(reinterpret_cast<const uint4*>(a.v_new + r * kD + l16 * 8));
     }
   }
+  int64_t s = 0, len = -1;  // of the thread that has a sequence's first row: its new length
   if (tid < kR8Groups * R) {
     const int64_t r = r0 + tid;
     int64_t dst = -1;
-    if (r < rows) {
-      int64_t unit, t, s, h;
+    if (r < end) {
+      int64_t unit, t, h;
       split(r, a.t_new, unit, t);
       split(unit, a.n_heads, s, h);
       const int64_t p = a.start[s];
@@ -67,12 +71,13 @@ __global__ void __launch_bounds__(kR8Threads) k_rows8_append(const __grid_consta
         if (dst < 0)
           set_status(a.status, BPKV_DEV_OVERFLOW);
         else if (!a.bump)
-          a.c.seq_len[s] = p + a.t_new;
+          len = p + a.t_new;
       }
     }
     s_dst[tid] = dst;
   }
   __syncthreads();
+  if (len >= 0) a.c.seq_len[s] = len;  // the CTA has read the old one
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int64_t dst = s_dst[i * kR8Groups + grp];
@@ -107,12 +112,18 @@ cudaError_t launch_rows8_bump(const bpkv_rows8& c, int32_t t_new, cudaStream_t s
 
 cudaError_t launch_rows8_append(const bpkv_rows8& c, const uint16_t* k_new, const uint16_t* v_new, int32_t t_new,
                                 const int64_t* start, int32_t* status, cudaStream_t st) {
-  const bool bump = start == nullptr || start == c.seq_len;
-  AppendArgs a{{c.k8, c.v8, c.kexp, c.vexp, c.seq_len, c.cap_tokens}, k_new, v_new, bump ? c.seq_len : start, status,
-               c.n_seq, c.n_kv_heads, t_new, bump ? 1 : 0};
-  const int64_t rows = (int64_t)c.n_seq * c.n_kv_heads * t_new;
-  const int per = kR8Groups * (many_rows(rows) ? kR8Many : 1);
-  const cudaError_t e = launch_pdl(many_rows(rows) ? k_rows8_append<kR8Many> : k_rows8_append<1>,
+  const bool at_len = start == nullptr || start == c.seq_len;
+  const int64_t rows = (int64_t)c.n_seq * c.n_kv_heads * t_new, of_seq = (int64_t)c.n_kv_heads * t_new;
+  // Lengths that are also the starts may change only when all have read them.
+  // A decode step's rows of a sequence fit one CTA, which then raises the length
+  // itself (32 sequences of 8 heads: 1.9 us a call in a graph, 3.8 outside,
+  // instead of 2.6 and 5.4); for more rows a second launch does.
+  const bool whole = at_len && of_seq <= kR8Groups * kR8Many, bump = at_len && !whole;
+  const bool many = whole ? of_seq > kR8Groups : many_rows(rows);
+  const int per = whole ? (int)of_seq : kR8Groups * (many ? kR8Many : 1);
+  AppendArgs a{{c.k8, c.v8, c.kexp, c.vexp, c.seq_len, c.cap_tokens}, k_new, v_new, at_len ? c.seq_len : start, status,
+               c.n_seq, c.n_kv_heads, t_new, per, bump ? 1 : 0};
+  const cudaError_t e = launch_pdl(many ? k_rows8_append<kR8Many> : k_rows8_append<1>,
                                    dim3((unsigned)((rows + per - 1) / per)), dim3(kR8Threads), 0, st, a);
   if (e != cudaSuccess || !bump) return e;
   return launch_rows8_bump(c, t_new, st);

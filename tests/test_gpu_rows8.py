@@ -108,6 +108,60 @@ def test_append_behind_the_rows_and_overflow(pk):
     assert torch.equal(c.k8[1:], before[1:]) and torch.equal(values(c.k8[0, :, 100:300]), y[0])
 
 
+@pytest.mark.parametrize("N,H,t", [(1, 1, 64), (3, 8, 8), (5, 13, 5), (2, 64, 1), (3, 65, 1), (7, 16, 1), (7, 17, 1)])
+def test_append_raises_the_lengths_once(pk, N, H, t):
+    """Rows of a sequence up to a CTA's 64 and above; one sequence that is full keeps its rows and its length."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    c = pk.Rows8(N, H, 2, 512)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([0 if i else 512 - t + 1 for i in range(N)], device="cuda")
+    c.seq_len.copy_(lens)
+    for x in (c.k8, c.v8):
+        x.zero_()
+    c.kexp.fill_(127)
+    c.vexp.fill_(127)
+    want = [torch.zeros((N, H, 512, D), dtype=torch.float64, device="cuda") for _ in range(2)]
+    for step in range(3):
+        kv = [torch.randn((N, H, t, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+        c.c.n_max = 0
+        pk.bpkv_rows8_append(c.c, kv[0], kv[1], t, None, status)
+        for i in range(1, N):
+            for w, x in zip(want, kv):
+                w[i, :, step * t:(step + 1) * t] = x[i].double()
+    assert int(status) == pk.DEV_OVERFLOW
+    lens[1:] = 3 * t
+    assert torch.equal(c.seq_len, lens)
+    c.seq_len.fill_(512)
+    for got, w in zip(c.read(0, 512), want):
+        # e4m3 after a scale that puts the row's largest at 224 or above: half a step is 2^-4 of a value, or 2^-10
+        assert ((got.double() - w).abs() <= 2.0 ** -4 * w.abs() + 2.0 ** -10 * w.abs().amax(-1, keepdim=True) / 224).all()
+
+
+@pytest.mark.parametrize("N,H,G", [(3, 8, 4), (2, 12, 2), (2, 7, 5), (700, 8, 5), (300, 2, 8)])
+def test_qkv_raises_the_lengths_once(pk, N, H, G):
+    """A token behind the stored ones, positions from the lengths: one CTA a token, several, and one by many tokens."""
+    g = torch.Generator(device="cuda").manual_seed(22)
+    c, d = pk.Rows8(N, H, G, 512), pk.Rows8(N, H, G, 512)
+    start = torch.arange(N, device="cuda") * 7 % 513
+    for x in (c, d):
+        for y in (x.k8, x.v8, x.kexp, x.vexp):
+            y.zero_()
+        x.seq_len.copy_(start)
+    inv = torch.logspace(0, -4, 64, device="cuda")
+    pos = start.clone()
+    for _ in range(2):
+        qkv = torch.randn((N, 1, (G + 2) * H * D), generator=g, device="cuda").to(torch.bfloat16)
+        q1, q2 = [torch.empty((N, 1, H, G, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for x, q, p in ((c, q1, None), (d, q2, pos)):
+            x.c.n_max = 0
+            pk.bpkv_qkv_rope(pk.qkv_args(qkv, q, H, p, inv, rows8=x, status=status))
+        pos = torch.where(pos < 512, pos + 1, pos)
+        assert torch.equal(q1, q2)
+    for a, b in ((c.k8, d.k8), (c.v8, d.v8), (c.kexp, d.kexp), (c.vexp, d.vexp), (c.seq_len, pos), (d.seq_len, pos)):
+        assert torch.equal(a, b)
+
+
 def test_captured_append(pk):
     g = torch.Generator(device="cuda").manual_seed(4)
     N, H = 2, 2
