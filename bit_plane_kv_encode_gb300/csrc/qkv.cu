@@ -16,8 +16,9 @@
 // top 32 bits are the angle within half a turn to 2^-32.
 //
 // Measured on a GB300 (G = 4, H = 8, normed, rotated by halves, bf16 queries):
-// a prompt of 8191 tokens (201 MB) 39.6 us, 5.1 TB/s, 74% of the issue slots in
-// use; with sixteen lanes a head and partners by shuffle it took 72.0 us.  One
+// a prompt of 8191 tokens (201 MB) 38.0 us, 5.3 TB/s, 74% of the issue slots in
+// use; with sixteen lanes a head and partners by shuffle it took 72.0 us, with
+// the 8-bit rows chosen at run time instead of by an instantiation 39.9.  One
 // token 2.9 us, one of each of 32 sequences into 8-bit rows 3.1 us (latency);
 // 3 x 1365 tokens of H = 2, G = 7, float queries, 64 channels rotated in pairs
 // (52 MB) 12.5 us, 4.2 TB/s.
@@ -93,7 +94,7 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* y) {
   }
 }
 
-template <int ROT>
+template <int ROT, bool ROWS8>
 __global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_constant__ QkvArgs a) {
   pdl_enter();
   __shared__ __align__(16) float4 s_tab[2][kQkvTokens][32];
@@ -153,9 +154,9 @@ __global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_consta
         e[2] = sn;
       }
       if ((tid & 63) == 0) {
-        const bool fits = a.c.k8 && rows8_fits(p0, a.t_new, a.c.cap);
+        const bool fits = ROWS8 && rows8_fits(p0, a.t_new, a.c.cap);
         s_tok[buf][i] = {tok, s * a.n_heads * a.t_new + t, fits ? s * a.n_heads * a.c.cap + p0 + t : -1};
-        if (a.c.k8 && t == 0 && head0 == 0) {
+        if (ROWS8 && t == 0 && head0 == 0) {
           if (!fits)
             set_status(a.status, BPKV_DEV_OVERFLOW);
           else if (!a.bump)
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_consta
       }
     }
     __syncthreads();
-    if (a.bump == 2 && tid < n_tok) {  // one token a sequence, and this CTA alone has read its length
+    if (ROWS8 && a.bump == 2 && tid < n_tok) {  // one token a sequence, and this CTA alone has read its length
       const QkvToken& tk = s_tok[buf][tid];
       if (tk.row8 >= 0) a.c.seq_len[tk.tok] = tk.row8 - tk.tok * a.n_heads * a.c.cap + 1;
     }
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_consta
           *reinterpret_cast<uint4*>(rows + ca * 8) = wa;
           *reinterpret_cast<uint4*>(rows + cb * 8) = wb;
         }
-        if (tk.row8 >= 0) {
+        if (ROWS8 && tk.row8 >= 0) {
           const int64_t row = tk.row8 + (int64_t)hk * a.c.cap;
           uint32_t m = __vmaxu2(abs_max(wa), abs_max(wb));
           const uint32_t mask = 0xffu << (tid & 24);
@@ -293,6 +294,13 @@ __global__ void __launch_bounds__(kQkvThreads, 5) k_qkv_rope(const __grid_consta
       h = hn;
     }
   }
+}
+
+template <bool ROWS8>
+void (*pick(int kind))(QkvArgs) {
+  return kind == kRotPairs    ? k_qkv_rope<kRotPairs, ROWS8>
+         : kind == kRotHalves ? k_qkv_rope<kRotHalves, ROWS8>
+                              : k_qkv_rope<kRotAny, ROWS8>;
 }
 
 cudaError_t launch_rows8_bump(const bpkv_rows8& c, int32_t t_new, cudaStream_t st);
@@ -343,8 +351,8 @@ cudaError_t launch_qkv_rope(const bpkv_qkv_args& q, cudaStream_t st) {
   while (a.toks > 1 && (a.toks * a.heads_per_cta > 8 * kQkvHeads || tokens / a.toks < 152 * 8)) a.toks /= 2;
   const dim3 grid((unsigned)min64((tokens + a.toks - 1) / a.toks, 152 * 32),
                   (heads + a.heads_per_cta - 1) / a.heads_per_cta);
-  const auto kernel = a.pairs ? k_qkv_rope<kRotPairs> : a.rot % 16 == 0 ? k_qkv_rope<kRotHalves> : k_qkv_rope<kRotAny>;
-  const cudaError_t e = launch_pdl(kernel, grid, dim3(kQkvThreads), 0, st, a);
+  const int kind = a.pairs ? kRotPairs : a.rot % 16 == 0 ? kRotHalves : kRotAny;
+  const cudaError_t e = launch_pdl(q.rows8 ? pick<true>(kind) : pick<false>(kind), grid, dim3(kQkvThreads), 0, st, a);
   if (e != cudaSuccess || a.bump != 1) return e;
   return launch_rows8_bump(*q.rows8, q.t_new, st);
 }
