@@ -95,6 +95,12 @@ int check_rows8(const bpkv_rows8* c) {
   return BPKV_OK;
 }
 
+// Whether np bytes at p and nq bytes at q share any.
+bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + nq && b < a + np;
+}
+
 // Rows [n_seq][n_heads][t] that the 8-bit row kernels and the projected-heads
 // kernel handle in one launch.
 bool rows_in_range(int64_t n_seq, int64_t n_heads, int64_t t) {
@@ -418,6 +424,13 @@ int bpkv_qkv_rope(const bpkv_qkv_args* a, void* stream) {
   if (a->ld % 8 != 0 || a->ld < (int64_t)(a->group + 2) * a->n_kv_heads * kD) return BPKV_EINVAL;
   if (!a->pos && !a->rows8) return BPKV_EINVAL;
   if (!rows_in_range(a->n_seq, a->n_kv_heads, a->t_new)) return BPKV_EUNSUPPORTED;
+  if (a->ld > ((int64_t)1 << 61) / a->n_seq / a->t_new) return BPKV_EUNSUPPORTED;
+  const int64_t tokens = (int64_t)a->n_seq * a->t_new, row = (int64_t)a->n_kv_heads * kD;
+  const int64_t in = ((tokens - 1) * a->ld + (a->group + 2) * row) * 2, kv = tokens * row * 2;
+  const int64_t qb = tokens * row * a->group * (a->flags & BPKV_QKV_Q_BF16 ? 2 : 4);
+  if (overlap(a->qkv, in, a->q_out, qb) || overlap(a->qkv, in, a->k_out, kv) || overlap(a->qkv, in, a->v_out, kv) ||
+      overlap(a->q_out, qb, a->k_out, kv) || overlap(a->q_out, qb, a->v_out, kv) || overlap(a->k_out, kv, a->v_out, kv))
+    return BPKV_EINVAL;
   bpkv_rows8* c = a->rows8;
   if (c) {
     BPKV_TRY(check_rows8(c));
@@ -451,7 +464,8 @@ int check_shared(const A* prefix, const int32_t* prefix_of, const A& c, const ui
   const size_t need = bpkv_shared_workspace_size(c.n_seq, prefix ? prefix->n_seq : 0, c.n_kv_heads, c.group);
   if (need == 0) return BPKV_EUNSUPPORTED;
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return BPKV_ENOWORKSPACE;
-  return BPKV_OK;
+  const int64_t bytes = (int64_t)c.n_seq * c.n_kv_heads * c.group * kD * 2;
+  return overlap(q, bytes, out, bytes) ? BPKV_EINVAL : BPKV_OK;
 }
 
 }  // namespace

@@ -453,8 +453,9 @@ typedef struct bpkv_qkv_args {
  * pos[i] .. of that cache, exactly as bpkv_rows8_append does with start = pos;
  * pos NULL or rows8->seq_len appends behind the stored tokens.  rows8 must have
  * the same n_seq, n_kv_heads and head_dim.
- * q_out, k_out, v_out and qkv are device memory on 16-byte boundaries and do
- * not overlap.  BPKV_EINVAL for t_new < 1, an odd rot_dim or one outside
+ * q_out, k_out, v_out and qkv (from its first row to its last) are device
+ * memory on 16-byte boundaries and do not overlap.  BPKV_EINVAL when they do,
+ * for t_new < 1, an odd rot_dim or one outside
  * 0 .. D, unknown flags, eps < 0, ld too small or not a multiple of 8, pos and
  * rows8 both NULL, no inv_freq with rot_dim > 0, or as bpkv_rows8_append.
  */
@@ -473,7 +474,8 @@ int bpkv_qkv_rope(const bpkv_qkv_args *a, void *stream);
  *   prefix     the P prefixes (NULL: none); same n_kv_heads and group as c
  *   prefix_of  int32 [N] device; values outside 0 .. P - 1 mean no prefix.
  *              NULL: every sequence has prefix 0
- *   q          bf16 [N][H][G][D], out bf16 [N][H][G][D] (16-byte aligned)
+ *   q          bf16 [N][H][G][D], out bf16 [N][H][G][D] (16-byte aligned, not
+ *              overlapping)
  * Logits, softmax statistics and sums are float32; the softmax weights enter
  * the products as bf16 (bpkv_shared_attend), and for bpkv_shared_attend8 as
  * halves or, on the tensor cores, as two 3-bit pieces with q as two e4m3 pieces

@@ -141,6 +141,64 @@ def test_decode_loop(pk, bits, N, captured):
 
 
 @pytest.mark.parametrize("bits", [16, 8])
+def test_two_calls_at_once(pk, bits):
+    """Calls over the same caches on two streams, each with its own workspace, one of them replayed from a graph."""
+    from test_gpu_shared import run_case
+    r = run_case(pk, bits, 40, 2, 4, [(37 * i) % 300 for i in range(40)], [3001, 70], [i % 3 for i in range(40)],
+                 bound=65536)
+    outs = [torch.empty_like(r["out"]) for _ in range(2)]
+    wss = [pk.shared_workspace(r["c"], r["pc"]) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def call(i):
+        r["fn"](r["pc"].c, r["of"], r["c"].c, r["q"], outs[i], wss[i], wss[i].numel())
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        call(0)
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            call(1)
+    torch.cuda.synchronize()
+    for out, ws in zip(outs, wss):
+        assert torch.equal(out, r["out"]) and pk.bpkv_read_status(ws) == 0
+
+
+def test_first_calls_captured(pk):
+    """A process whose first call of each operator is a captured one."""
+    import subprocess
+    import sys
+    code = """
+import torch, bit_plane_kv_encode_gb300 as pk
+N, H, G = 40, 2, 4
+c, p = pk.Rows8(N, H, G, 512), pk.Rows8(1, H, G, 65536)
+for x in (c.k8, c.v8, p.k8, p.v8): x.fill_(0x38)
+for x in (c.kexp, c.vexp, p.kexp, p.vexp): x.fill_(127)
+p.seq_len.fill_(5000); p.c.n_max = 65536
+ws = pk.shared_workspace(c, p)
+qkv = torch.ones((N, 1, (G + 2) * H * 128), dtype=torch.bfloat16, device="cuda")
+q = torch.empty((N, 1, H, G, 128), dtype=torch.bfloat16, device="cuda"); out = torch.empty_like(q)
+a = pk.qkv_args(qkv, q, H, rows8=c)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    pk.bpkv_qkv_rope(a)
+    pk.bpkv_shared_attend8(p.c, None, c.c, q, out, ws, ws.numel())
+for _ in range(3): g.replay()
+torch.cuda.synchronize()
+assert c.seq_len.tolist() == [3] * N and pk.bpkv_read_status(ws) == 0
+assert (out == 1).all()
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("bits", [16, 8])
 def test_host_bound_below_the_lengths(pk, bits):
     """n_max only sizes the launch: lengths it does not know of (a replayed graph's) are still attended to in full."""
     from test_gpu_shared import run_case

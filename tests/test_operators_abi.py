@@ -68,7 +68,8 @@ def test_rows8_read(L, t0, n, k, v):
 def _qkv(**kw):
     from bit_plane_kv_encode_gb300 import bpkv_qkv_args
     d = dict(n_seq=2, n_kv_heads=2, group=4, head_dim=128, t_new=1, rot_dim=128, flags=0, eps=1e-6, qkv=FAKE,
-             ld=12 * 128, pos=FAKE * 2, inv_freq=FAKE, q_weight=None, k_weight=None, q_out=FAKE, k_out=FAKE, v_out=FAKE)
+             ld=12 * 128, pos=FAKE * 2, inv_freq=FAKE, q_weight=None, k_weight=None, q_out=FAKE * 3, k_out=FAKE * 4,
+             v_out=FAKE * 5)
     d.update(kw)
     return bpkv_qkv_args(**d)
 
@@ -79,7 +80,11 @@ def _qkv(**kw):
     (dict(flags=4), EINVAL), (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(ld=12 * 128 - 8), EINVAL),
     (dict(ld=12 * 128 + 4), EINVAL), (dict(qkv=None), EINVAL), (dict(q_out=None), EINVAL), (dict(qkv=FAKE + 2), EINVAL),
     (dict(k_out=FAKE + 8), EINVAL), (dict(pos=None), EINVAL), (dict(pos=FAKE + 4), EINVAL),
-    (dict(q_weight=FAKE + 2), EINVAL), (dict(n_seq=65536), EUNSUP)])
+    (dict(q_weight=FAKE + 2), EINVAL), (dict(n_seq=65536), EUNSUP), (dict(ld=1 << 61), EUNSUP),
+    # outputs in the input (its last row), in one another
+    (dict(q_out=FAKE + 12 * 128 * 2), EINVAL), (dict(k_out=FAKE + 2 * 12 * 128 * 2 - 16), EINVAL),
+    (dict(v_out=FAKE), EINVAL), (dict(k_out=FAKE * 3 + 2 * 8 * 128 * 4 - 16), EINVAL), (dict(v_out=FAKE * 3 - 16), EINVAL),
+    (dict(v_out=FAKE * 4 + 16), EINVAL)])
 def test_qkv(L, bad, rc):
     a = _qkv(**bad)
     assert L.bpkv_qkv_rope(ctypes.byref(a), None) == rc
@@ -148,5 +153,7 @@ def test_shared_attend(L, bits):
     assert call(w=None) == ENOWS and call(w=FAKE + 128) == ENOWS and call(n=1000) == ENOWS
     need = L.bpkv_shared_workspace_size(2, 1, 2, 4)
     assert call(prefix=p, n=need - 1) == ENOWS
+    size = 2 * 2 * 4 * 128 * 2
+    assert call() == EINVAL and call(out=FAKE + size - 16) == EINVAL and call(q=FAKE + 16) == EINVAL
     if bits == 16:
         assert call(own=mk(residency=1)) == EUNSUP and call(prefix=mk(residency=1, n_seq=1)) == EUNSUP
