@@ -36,7 +36,7 @@ namespace bpkv {
 namespace shared {
 
 template <int BITS>
-cudaError_t launch_few(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
+cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
 int few_tile(int bits);
 
 namespace {
@@ -815,13 +815,23 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Short prefixes are streamed by units of 16 rows, from L2 again for each, and
+// Short calls are one launch of k_shared_unit: tokens of a prefix and a sequence
+// together (as the host knows them), of a sequence alone when there are more
+// units than SMs (a long one among short ones would be waited for), and rows of
+// prefixes that all units together read.  One call / planned, in us, 8 x 4 heads,
+// bf16 rows; sequences of up to 500 tokens: 1 of them 4.7 / 7.5, 32 6.6 / 12.0,
+// 128 20.9 / 29.3; 2000: 9.9 / 12.1, 21 / 24, 74 / 80; 4000: 16.3 / 14.0.  Over
+// one prefix of 300 tokens: 1 sequence 4.5 / 9.2, 32 6.1 / 15.0, 96 15.3 / 19.3;
+// of 900: 6.8 / 10.7, 10.4 / 18.4, 27.6 / 27.5 (691200 rows); of 2000: 10.4 /
+// 13.9, 17.8 / 24.0, 49.6 / 29.3.  8-bit rows are alike.
+constexpr int64_t kWholeTokens = 2048, kWholeMany = 1024, kWholeRows = 600000;
+
+// Longer prefixes are streamed by units of 16 rows, from L2 again for each, and
 // the wide kernel is left out, while that reads at most this many bytes.  With
-// 32 sequences of 8 x 4 heads, streamed / wide, in us: 300 tokens 15.2 / 21.6,
-// 1000 tokens 19.3 / 22.0, 2000 tokens (66 MB) 27.7 / 24.2, 4000 tokens 40.2 /
-// 25.0; 8-bit rows: 2000 tokens (33 MB) 22.4 / 29.4, 4000 tokens 31.4 / 30.0.
-// With three prefixes of 2000 tokens and 64 sequences of 4 x 8 heads over 8-bit
-// rows (66 MB) 35.5 / 47.
+// 32 sequences of 8 x 4 heads, streamed / wide, in us: 1000 tokens 19.3 / 22.0,
+// 2000 tokens (66 MB) 27.7 / 24.2, 4000 tokens 40.2 / 25.0; 8-bit rows: 2000
+// tokens (33 MB) 22.4 / 29.4, 4000 tokens 31.4 / 30.0.  With three prefixes of
+// 2000 tokens and 64 sequences of 4 x 8 heads over 8-bit rows (66 MB) 35.5 / 47.
 template <int BITS>
 constexpr int64_t kStreamBytes = BITS == 16 ? 60000000 : 70000000;
 
@@ -865,7 +875,10 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   const int64_t pn = prefix ? prefix->n : 0, pmax = prefix ? prefix->n_max : 0;
   const int64_t again =
       max64(min64(pn, own.n), (own.n * group + kFew - 1) / kFew) * n_heads * pmax * (BITS == 16 ? 4 * kD : 2 * kD);
-  const bool has_wide = prefix && own.n * group > kFew && again > kStreamBytes<BITS>;
+  const int64_t total = own.n_max + pmax;
+  const int64_t n_own = (int64_t)own.n * n_heads;
+  const bool whole = total <= kWholeTokens && (n_own <= kSms || own.n_max <= kWholeMany) && n_own * pmax <= kWholeRows;
+  const bool has_wide = !whole && prefix && own.n * group > kFew && again > kStreamBytes<BITS>;
   a.unit_log = has_wide ? kPairLog : kFewLog;
   // no more CTAs than tiles, as far as the host knows (longer sequences than
   // it knows of only find fewer CTAs)
@@ -887,7 +900,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
     e = launch_pdl(k_shared_wide<BITS>, dim3(a.wide_ctas), dim3(kThreads), (size_t)Shape<BITS>::bytes(dual), st, a, maps);
     if (e != cudaSuccess) return e;
   }
-  return launch_few<BITS>(a, own.n_max, !has_wide, out, st);
+  return launch_few<BITS>(a, whole ? total : -1, !has_wide, out, st);
 }
 
 }  // namespace

@@ -105,27 +105,42 @@ struct Walk {
   __device__ __forceinline__ int valid() const { return (int)min64(tok, n - t * tok); }
 };
 
-// A warp's way through one unit of own rows that a CTA takes whole: every
-// W-th tile, W the CTA's warps.
+// A warp's way through all rows of one sequence and KV head that a CTA takes
+// whole, the prefix's and then its own: every W-th tile, W the CTA's warps.
 template <int W>
 struct UnitWalk {
   static constexpr bool kUnit = true;
-  static constexpr int side = 1;
   const Args& a;
-  int tok, index, h, n, t, tiles;
-  int64_t row0, unit;
+  int tok, index, h, side, x, tiles, pre_tiles, t, n, n_pre, n_own;
+  int64_t row0, pre_row0;
   __device__ __forceinline__ UnitWalk(const Args& args, int tile) : a(args), tok(tile) {
-    unit = blockIdx.x;
     index = (int)(blockIdx.x / (uint32_t)a.n_heads);
     h = (int)(blockIdx.x - (uint32_t)index * a.n_heads);
-    n = (int)tokens_of(a.len[index], a.cap);
-    row0 = unit * a.cap;
-    tiles = (n + tok - 1) / tok;
-    t = threadIdx.x >> 5;
+    n_pre = 0;
+    n_own = (int)tokens_of(a.len[index], a.cap);
+    pre_row0 = 0;
+    if (a.plen) {
+      const int p = a.prefix_of ? a.prefix_of[index] : 0;
+      if (p >= 0 && p < a.n_prefix) {
+        n_pre = (int)tokens_of(a.plen[p], a.pcap);
+        pre_row0 = ((int64_t)p * a.n_heads + h) * a.pcap;
+      }
+    }
+    pre_tiles = (n_pre + tok - 1) / tok;
+    tiles = pre_tiles + (n_own + tok - 1) / tok;
+    x = threadIdx.x >> 5;
+    set();
   }
-  __device__ __forceinline__ bool more() const { return t < tiles; }
+  __device__ __forceinline__ void set() {
+    side = x < pre_tiles ? 0 : 1;
+    t = side ? x - pre_tiles : x;
+    n = side ? n_own : n_pre;
+    row0 = side ? blockIdx.x * a.cap : pre_row0;
+  }
+  __device__ __forceinline__ bool more() const { return x < tiles; }
   __device__ __forceinline__ bool next() {
-    t += W;
+    x += W;
+    set();
     return false;
   }
   __device__ __forceinline__ int valid() const { return min(tok, n - t * tok); }
@@ -540,8 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
   if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Short sequences without prefixes: a CTA takes a unit whole, its warps join in
-// shared memory, and neither plan nor partials nor join are needed.  One
+// Short sequences and prefixes: a CTA takes all rows of one sequence and KV head,
+// its warps join in shared memory, and neither plan nor partials nor join are
+// needed; a prefix is read again for every sequence, from L2.  One
 // sequence of 8 x 4 heads and 500 bf16 tokens takes 4.8 us: the launch, four
 // rounds of loads and products of each warp, and the join, all latency.
 template <int BITS, int W>
@@ -702,16 +718,11 @@ cudaError_t go(const Args& a, int ctas, bool wait_first, cudaStream_t st) {
 
 }  // namespace
 
-// Without prefixes, the longest sequences (as the host knows them) that a CTA
-// takes whole: one launch instead of two, without a plan.  bf16 rows of 8 x 4
-// heads, whole / planned, in us, sequences of up to 500 tokens: 1 of them
-// 4.7 / 7.5, 32 6.6 / 12.0, 128 20.9 / 29.3; 1000: 6.4 / 9.0, 11.4 / 15.7,
-// 37.9 / 46.0; 4000: 16.3 / 14.0 (1 of them).  Beyond 1024 little is won, and
-// a long sequence among short ones would be waited for.
-// Warps of a CTA: 8 while every unit has an SM to itself (32 x 8 units of up to
-// 500 tokens would take 8.3 us), else 4, and 2 for many short units (128 x 8 of
-// up to 100: 7.8 us instead of 10.9; of up to 1000: 40.4 instead of 37.9).
-constexpr int64_t kUnitTokens = 1024;
+// Warps of a CTA that takes a unit whole: 8 while every unit has an SM to
+// itself (32 x 8 units of up to 500 tokens would take 8.3 us instead of 6.6),
+// else 4, and 2 for many short units (128 x 8 of up to 100: 7.8 us instead of
+// 10.9; of up to 1000: 40.4 instead of 37.9).
+constexpr int64_t kShortUnit = 512;
 
 template <int BITS, int W>
 cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out) {
@@ -723,13 +734,14 @@ cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out) {
                     a, out);
 }
 
-// The streaming kernel, then the join.  wait_first: no wide kernel came before.
+// whole: tokens of a unit at most, for CTAs that take units whole; else -1, for
+// the streaming kernel and the join.  wait_first: no wide kernel came before.
 template <int BITS>
-cudaError_t launch_few(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st) {
-  if (!a.plen && own_max <= kUnitTokens) {
+cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st) {
+  if (whole >= 0) {
     const int64_t units = (int64_t)a.n_seq * a.n_heads;
     if (units <= kSms) return go_unit<BITS, 8>(a, st, out);
-    if (units > 4 * kSms && own_max <= kUnitTokens / 2) return go_unit<BITS, 2>(a, st, out);
+    if (units > 4 * kSms && whole <= kShortUnit) return go_unit<BITS, 2>(a, st, out);
     return go_unit<BITS, 4>(a, st, out);
   }
   const int ctas = a.few_workers / kFewWarps;
@@ -742,8 +754,8 @@ cudaError_t launch_few(const Args& a, int64_t own_max, bool wait_first, uint16_t
                     out);
 }
 
-template cudaError_t launch_few<16>(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
-template cudaError_t launch_few<8>(const Args& a, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<16>(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<8>(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
 
 int few_tile(int bits) { return bits == 16 ? Shape<16>::kTok : Shape<8>::kTok; }
 

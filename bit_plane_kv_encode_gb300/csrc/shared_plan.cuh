@@ -10,7 +10,7 @@
 // kernel's tiles form one list, cut into equal stretches, one per worker; a
 // worker's part of a unit is a segment and leaves its rows' (m, l, o).  Lengths
 // are read on the device, so the cut fits ragged batches; every CTA works the
-// same plan out for itself.  Short sequences without prefixes need none of this
+// same plan out for itself.  Short sequences and prefixes need none of this
 // (k_shared_unit).
 #pragma once
 

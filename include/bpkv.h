@@ -469,8 +469,8 @@ int bpkv_qkv_rope(const bpkv_qkv_args *a, void *stream);
  *   o = sum_x softmax_x(q . k_x / sqrt(D)) v_x over both sets together,
  * zeros when both are empty.  A prefix is stored once, as one sequence of the
  * cache `prefix`.  A long one's rows are read once for up to 256 query heads of
- * the sequences that share it, on the tensor cores; short ones, and those of
- * few sequences, are streamed for 16 query heads at a time.
+ * the sequences that share it, on the tensor cores; shorter ones, and those of
+ * few sequences, are streamed for 16 query heads or one sequence at a time.
  *   prefix     the P prefixes (NULL: none); same n_kv_heads and group as c
  *   prefix_of  int32 [N] device; values outside 0 .. P - 1 mean no prefix.
  *              NULL: every sequence has prefix 0

@@ -119,7 +119,8 @@ def reference(q, rows, lens, prows, plens, prefix_of, bits):
 
 def run_case(pk, bits, N, H, G, lens, plens, prefix_of, seed=1, spread=0.75, sink=True, given=True, bound=None):
     """One call against the formula.  bound: what the host knows of the prefixes' lengths (a cache of that size), which
-    decides whether they are streamed by 16 query rows or taken by the tensor cores."""
+    decides whether a CTA takes each sequence with its prefix (none given and short), they are streamed by 16 query rows
+    (3000) or taken by the tensor cores (65536)."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     cap = max(512, (max(lens) + 511) // 512 * 512)
     q = torch.randn((N, H, G, D), generator=g, device="cuda").to(torch.bfloat16)
@@ -157,9 +158,10 @@ def test_own_rows_only(pk, bits, n):
 
 @pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("N,H,G,longest", [(1, 1, 1, 1024), (76, 2, 8, 300), (77, 2, 5, 700), (305, 2, 4, 512),
-                                           (305, 2, 2, 513), (9, 3, 4, 1025)])
+                                           (305, 2, 2, 513), (9, 3, 4, 2048), (9, 3, 4, 2049), (77, 2, 3, 1025)])
 def test_short_sequences(pk, bits, N, H, G, longest):
-    """Own rows by whole units of 8, 4 and 2 warps and, past 1024 tokens, planned; then with a bound below the lengths."""
+    """Own rows by whole units of 8, 4 and 2 warps and, past 2048 tokens (1024 of many units), planned; then with a
+    bound below the lengths."""
     lens = [(longest - 89 * i) % (longest + 1) for i in range(N)]
     lens[N // 2:N // 2 + 3] = [0, 1, 17][:len(lens[N // 2:N // 2 + 3])]
     lens[0] = longest
@@ -183,7 +185,7 @@ def test_nothing_at_all(pk):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("bound", [None, 65536])
+@pytest.mark.parametrize("bound", [None, 3000, 65536])
 @pytest.mark.parametrize("N,G", [(1, 4), (5, 3), (4, 8), (9, 4), (16, 4), (31, 4), (32, 4), (33, 4), (43, 3), (64, 4),
                                  (65, 4), (70, 8)])
 def test_one_prefix(pk, bits, N, G, bound):
@@ -194,7 +196,7 @@ def test_one_prefix(pk, bits, N, G, bound):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("bound", [None, 65536])
+@pytest.mark.parametrize("bound", [None, 3000, 65536])
 def test_several_prefixes(pk, bits, bound):
     """Mixed order, sequences without a prefix, an empty prefix and one nobody has."""
     N = 41
@@ -211,9 +213,9 @@ def test_long_prefix_and_peaked_weights(pk, bits):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("N,bound", [(1, 2000), (40, 2000), (17, 65536), (40, 65536)])
+@pytest.mark.parametrize("N,bound", [(1, 1900), (1, 2000), (40, 1900), (40, 2000), (17, 65536), (40, 65536)])
 def test_rising_maximum_of_a_prefix(pk, bits, N, bound):
-    """Logits that climb along a prefix's rows, streamed, and on the tensor cores with 68 and 160 query rows."""
+    """Logits that climb along a prefix's rows, in whole units, streamed, and on the tensor cores with 68 and 160 query rows."""
     g = torch.Generator(device="cuda").manual_seed(8)
     H, G, n, cap = 1, 4, 2000, 65536
     q = (1 + 0.1 * torch.randn((N, H, G, D), generator=g, device="cuda")).to(torch.bfloat16)
@@ -257,7 +259,7 @@ def test_rising_maximum(pk, bits, n):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("bound", [None, 65536])
+@pytest.mark.parametrize("bound", [None, 3000, 65536])
 def test_repeats_streams_and_graphs(pk, bits, bound):
     """The same bits from every call, on another stream, and from two captured graphs that share the workspace."""
     r = run_case(pk, bits, 33, 2, 4, [(37 * i) % 300 for i in range(33)], [3001], [0] * 33, given=False, bound=bound)
