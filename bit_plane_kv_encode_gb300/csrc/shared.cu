@@ -38,6 +38,7 @@ namespace shared {
 template <int BITS>
 cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
 int few_tile(int bits);
+int unit_split(int64_t units, int64_t tokens);
 
 namespace {
 
@@ -815,15 +816,18 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Short calls are one launch of k_shared_unit: tokens of a prefix and a sequence
-// together (as the host knows them), of a sequence alone when there are more
-// units than SMs (a long one among short ones would be waited for), and rows of
+// Short calls are one launch of k_shared_unit, by the tokens of a prefix and a
+// sequence together and of a sequence alone (as the host knows them; a long one
+// among short ones would be waited for) for each CTA of a unit, and the rows of
 // prefixes that all units together read.  One call / planned, in us, 8 x 4 heads,
-// bf16 rows; sequences of up to 500 tokens: 1 of them 4.7 / 7.5, 32 6.6 / 12.0,
-// 128 20.9 / 29.3; 2000: 9.9 / 12.1, 21 / 24, 74 / 80; 4000: 16.3 / 14.0.  Over
-// one prefix of 300 tokens: 1 sequence 4.5 / 9.2, 32 6.1 / 15.0, 96 15.3 / 19.3;
-// of 900: 6.8 / 10.7, 10.4 / 18.4, 27.6 / 27.5 (691200 rows); of 2000: 10.4 /
-// 13.9, 17.8 / 24.0, 49.6 / 29.3.  8-bit rows are alike.
+// bf16 rows (8-bit rows in brackets).
+//   Own rows only: 1 sequence of up to 500 tokens 4.7 / 7.5, 4000 6.4 / 13.9,
+//   32000 20 / 26 (20 / 21); 8 of 4000 13.1 / 15.0 (11.7 / 13.0), of 8000 22.6 /
+//   23.6 (19.5 / 17.0); 32 of 500 6.6 / 12.0, of 2000 21 / 24 (18 / 18).
+//   Over a prefix: 1 over 300 4.5 / 9.2, over 4000 6.6 / 16.4, over 32000 22 / 30;
+//   8 over 8000 18.7 / 25.5 (19.5 / 21.2), over 16000 32 / 29; 32 over 900 10.4 /
+//   18.4, over 2000 17.8 / 24.0; 96 over 300 15.3 / 19.3, over 900 (691200 rows)
+//   27.6 / 27.5.
 constexpr int64_t kWholeTokens = 2048, kWholeMany = 1024, kWholeRows = 600000;
 
 // Longer prefixes are streamed by units of 16 rows, from L2 again for each, and
@@ -877,7 +881,10 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
       max64(min64(pn, own.n), (own.n * group + kFew - 1) / kFew) * n_heads * pmax * (BITS == 16 ? 4 * kD : 2 * kD);
   const int64_t total = own.n_max + pmax;
   const int64_t n_own = (int64_t)own.n * n_heads;
-  const bool whole = total <= kWholeTokens && (n_own <= kSms || own.n_max <= kWholeMany) && n_own * pmax <= kWholeRows;
+  const int split = unit_split(n_own, total);
+  const bool whole = total <= (split > 1 ? 2 : 1) * split * kWholeTokens &&
+                     own.n_max <= (n_own > kSms ? kWholeMany : (split > 2 ? 2 : 1) * split * kWholeTokens) &&
+                     n_own * pmax <= kWholeRows;
   const bool has_wide = !whole && prefix && own.n * group > kFew && again > kStreamBytes<BITS>;
   a.unit_log = has_wide ? kPairLog : kFewLog;
   // no more CTAs than tiles, as far as the host knows (longer sequences than

@@ -20,6 +20,8 @@
 //
 // Measured on a GB300: 32 sequences of 8 x 4 heads over 8-bit rows of their own,
 // up to 16384 tokens (542 MB): 85.5 us with the join, 6.3 TB/s.
+#include <cooperative_groups.h>
+
 #include "rows8_core.cuh"
 #include "shared_plan.cuh"
 
@@ -105,17 +107,22 @@ struct Walk {
   __device__ __forceinline__ int valid() const { return (int)min64(tok, n - t * tok); }
 };
 
-// A warp's way through all rows of one sequence and KV head that a CTA takes
-// whole, the prefix's and then its own: every W-th tile, W the CTA's warps.
-template <int W>
+namespace cg = cooperative_groups;
+constexpr int kMaxCluster = 8;
+
+// A warp's way through all rows of one sequence and KV head that a CTA or a
+// cluster of them takes whole, the prefix's and then its own: every step-th
+// tile, step the warps of all.
 struct UnitWalk {
   static constexpr bool kUnit = true;
   const Args& a;
-  int tok, index, h, side, x, tiles, pre_tiles, t, n, n_pre, n_own;
-  int64_t row0, pre_row0;
-  __device__ __forceinline__ UnitWalk(const Args& args, int tile) : a(args), tok(tile) {
-    index = (int)(blockIdx.x / (uint32_t)a.n_heads);
-    h = (int)(blockIdx.x - (uint32_t)index * a.n_heads);
+  int tok, index, h, side, x, step, tiles, pre_tiles, t, n, n_pre, n_own;
+  int64_t row0, own_row0, pre_row0;
+  __device__ __forceinline__ UnitWalk(const Args& args, int tile, uint32_t unit, int first, int stride)
+      : a(args), tok(tile), x(first), step(stride) {
+    index = (int)(unit / (uint32_t)a.n_heads);
+    h = (int)(unit - (uint32_t)index * a.n_heads);
+    own_row0 = unit * a.cap;
     n_pre = 0;
     n_own = (int)tokens_of(a.len[index], a.cap);
     pre_row0 = 0;
@@ -128,18 +135,17 @@ struct UnitWalk {
     }
     pre_tiles = (n_pre + tok - 1) / tok;
     tiles = pre_tiles + (n_own + tok - 1) / tok;
-    x = threadIdx.x >> 5;
     set();
   }
   __device__ __forceinline__ void set() {
     side = x < pre_tiles ? 0 : 1;
     t = side ? x - pre_tiles : x;
     n = side ? n_own : n_pre;
-    row0 = side ? blockIdx.x * a.cap : pre_row0;
+    row0 = side ? own_row0 : pre_row0;
   }
   __device__ __forceinline__ bool more() const { return x < tiles; }
   __device__ __forceinline__ bool next() {
-    x += W;
+    x += step;
     set();
     return false;
   }
@@ -559,26 +565,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
 // its warps join in shared memory, and neither plan nor partials nor join are
 // needed; a prefix is read again for every sequence, from L2.  One
 // sequence of 8 x 4 heads and 500 bf16 tokens takes 4.8 us: the launch, four
-// rounds of loads and products of each warp, and the join, all latency.
-template <int BITS, int W>
+// rounds of loads and products of each warp, and the join, all latency.  Few
+// units are dealt to a cluster of CTAs each (CLUSTER), which join through
+// distributed shared memory: over 32000 tokens (131 MB) 22 us, 6 TB/s.
+template <int BITS, int W, bool CLUSTER>
 __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __grid_constant__ Args a, uint16_t* out) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = Shape<BITS>;
   constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;
   __shared__ float2 s_ml[W][8];
+  uint32_t ctas = 1, rank = 0;
+  if constexpr (CLUSTER) {
+    ctas = cg::this_cluster().num_blocks();
+    rank = cg::this_cluster().block_rank();
+  }
+  const uint32_t unit = blockIdx.x / ctas;
+  __shared__ float2 s_part[CLUSTER ? 8 : 1][kD / 2], s_part_ml[8];  // the CTA's o, (m, l)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_enter();
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const unsigned char* exps = smem + W * kStages * kStage + warp * kStages * S::kExps;
-  UnitWalk<W> ahead(a, S::kTok), cur = ahead;
+  UnitWalk ahead(a, S::kTok, unit, rank * W + warp, ctas * W), cur = ahead;
   const uint64_t policy = evict_first_policy();
   prime<BITS>(ahead, ring, exps, policy);
   if (tid < W * 8) s_ml[tid / 8][tid % 8] = make_float2(-INFINITY, 0.f);
   __syncthreads();
   float* rows_o = reinterpret_cast<float*>(smem + warp * kStages * kStage);  // the warp's ring, once it is read
   stream<BITS, 1>(
-      a, cur, ahead, ring, exps, policy, [&](const UnitWalk<W>&) { return a.group; },
-      [&](const UnitWalk<W>&, const State<1>& st, int rows) {
+      a, cur, ahead, ring, exps, policy, [&](const UnitWalk&) { return a.group; },
+      [&](const UnitWalk&, const State<1>& st, int rows) {
         cp_wait<0>();
         __syncwarp();
 #pragma unroll
@@ -607,8 +622,42 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
       o0 = fmaf(f, v.x, o0);
       o1 = fmaf(f, v.y, o1);
     }
-    const float s = L == 0.f ? 0.f : 1.f / L;
-    *reinterpret_cast<uint32_t*>(out + ((int64_t)blockIdx.x * a.group + r) * kD + d) = pack<16>(o0 * s, o1 * s);
+    if constexpr (CLUSTER) {
+      s_part[r][d / 2] = make_float2(o0, o1);
+      if (d == 0) s_part_ml[r] = make_float2(M, L);
+    } else {
+      const float s = L == 0.f ? 0.f : 1.f / L;
+      *reinterpret_cast<uint32_t*>(out + ((int64_t)unit * a.group + r) * kD + d) = pack<16>(o0 * s, o1 * s);
+    }
+  }
+  if constexpr (CLUSTER) {
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int x = rank * (W * 32) + tid; x < a.group * (kD / 2); x += ctas * W * 32) {
+      const int r = x / (kD / 2), d = x % (kD / 2) * 2;
+      float2 ml[kMaxCluster], v[kMaxCluster];
+      float M = -INFINITY, L = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (i < ctas) {
+          ml[i] = *cl.map_shared_rank(&s_part_ml[r], i);
+          v[i] = *cl.map_shared_rank(&s_part[r][d / 2], i);
+        }
+        M = fmaxf(M, ml[i].x);
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) {
+        if (ml[i].y == 0.f) continue;
+        const float f = ex2(ml[i].x - M);
+        L = fmaf(f, ml[i].y, L);
+        o0 = fmaf(f, v[i].x, o0);
+        o1 = fmaf(f, v[i].y, o1);
+      }
+      const float s = L == 0.f ? 0.f : 1.f / L;
+      *reinterpret_cast<uint32_t*>(out + ((int64_t)unit * a.group + r) * kD + d) = pack<16>(o0 * s, o1 * s);
+    }
+    cl.sync();  // no CTA leaves while another reads its shared memory
   }
 }
 
@@ -718,20 +767,34 @@ cudaError_t go(const Args& a, int ctas, bool wait_first, cudaStream_t st) {
 
 }  // namespace
 
+int unit_split(int64_t units, int64_t tokens);
+
 // Warps of a CTA that takes a unit whole: 8 while every unit has an SM to
 // itself (32 x 8 units of up to 500 tokens would take 8.3 us instead of 6.6),
 // else 4, and 2 for many short units (128 x 8 of up to 100: 7.8 us instead of
 // 10.9; of up to 1000: 40.4 instead of 37.9).
 constexpr int64_t kShortUnit = 512;
 
-template <int BITS, int W>
-cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out) {
+template <int BITS, int W, bool CLUSTER = false>
+cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out, int ctas = 1) {
   constexpr int kSmem = Shape<BITS>::kRing / kFewWarps * W;
   static std::atomic<uint64_t> done;
-  const cudaError_t e = allow_smem(k_shared_unit<BITS, W>, kSmem, done);
+  const auto kernel = k_shared_unit<BITS, W, CLUSTER>;
+  const cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_shared_unit<BITS, W>, dim3((unsigned)((int64_t)a.n_seq * a.n_heads)), dim3(W * 32), (size_t)kSmem, st,
-                    a, out);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.n_seq * a.n_heads * ctas));
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, out);
 }
 
 // whole: tokens of a unit at most, for CTAs that take units whole; else -1, for
@@ -740,6 +803,8 @@ template <int BITS>
 cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st) {
   if (whole >= 0) {
     const int64_t units = (int64_t)a.n_seq * a.n_heads;
+    const int split = unit_split(units, whole);
+    if (split > 1) return go_unit<BITS, 8, true>(a, st, out, split);
     if (units <= kSms) return go_unit<BITS, 8>(a, st, out);
     if (units > 4 * kSms && whole <= kShortUnit) return go_unit<BITS, 2>(a, st, out);
     return go_unit<BITS, 4>(a, st, out);
@@ -756,6 +821,16 @@ cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* 
 
 template cudaError_t launch_few<16>(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
 template cudaError_t launch_few<8>(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
+
+// CTAs that share a unit (k_shared_unit): as many as leave all units resident at
+// once, clusters of 8 finding room for 12 at least.  In us for one / two / four /
+// eight CTAs, bf16 rows of 8 x 4 heads: 1 sequence of up to 500 tokens 4.8 / 4.8 /
+// 4.6 / 4.8, 1000 6.5 / 5.9 / 5.2 / 4.8, 2000 9.9 / 8.0 / 6.1 / 5.4, 4000 16.8 /
+// 12.9 / 8.0 / 6.4; below 600 tokens the cluster's barriers cost what they save.
+int unit_split(int64_t units, int64_t tokens) {
+  if (tokens < 600) return 1;
+  return units <= 12 ? 8 : units <= 32 ? 4 : units <= 72 ? 2 : 1;
+}
 
 int few_tile(int bits) { return bits == 16 ? Shape<16>::kTok : Shape<8>::kTok; }
 

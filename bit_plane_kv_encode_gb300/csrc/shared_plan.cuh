@@ -43,7 +43,6 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-
 constexpr int kWideTile = 128;       // tokens of a wide tile, rows of a stream
 constexpr int kPair = 2 * kWideTile; // rows of a wide unit at most
 constexpr int kPairLog = 8;

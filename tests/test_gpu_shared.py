@@ -158,10 +158,13 @@ def test_own_rows_only(pk, bits, n):
 
 @pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("N,H,G,longest", [(1, 1, 1, 1024), (76, 2, 8, 300), (77, 2, 5, 700), (305, 2, 4, 512),
-                                           (305, 2, 2, 513), (9, 3, 4, 2048), (9, 3, 4, 2049), (77, 2, 3, 1025)])
+                                           (305, 2, 2, 513), (76, 2, 4, 2048), (76, 2, 4, 2049), (77, 2, 3, 1025), (1, 1, 8, 599),
+                                           (4, 3, 8, 600), (2, 1, 5, 32768), (1, 1, 1, 32769), (13, 1, 4, 601),
+                                           (8, 4, 3, 16384), (8, 4, 3, 16385), (33, 1, 4, 600), (36, 2, 8, 4096),
+                                           (36, 2, 8, 4097)])
 def test_short_sequences(pk, bits, N, H, G, longest):
-    """Own rows by whole units of 8, 4 and 2 warps and, past 2048 tokens (1024 of many units), planned; then with a
-    bound below the lengths."""
+    """Own rows by whole units of 8, 4 and 2 warps and of clusters of 8, 4 and 2 CTAs, and past these lengths planned;
+    then with a bound below the lengths."""
     lens = [(longest - 89 * i) % (longest + 1) for i in range(N)]
     lens[N // 2:N // 2 + 3] = [0, 1, 17][:len(lens[N // 2:N // 2 + 3])]
     lens[0] = longest
@@ -193,6 +196,15 @@ def test_one_prefix(pk, bits, N, G, bound):
     lens = [(37 * i) % 300 for i in range(N)]
     for plen in (1000, 1):
         run_case(pk, bits, N, 2, G, lens, [plen], [0] * N, given=False, bound=bound)
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("N,H,plen,longest", [(3, 4, 30000, 2000), (8, 4, 12000, 4000), (18, 4, 4000, 4000), (5, 1, 20000, 0)])
+def test_clusters_over_prefixes(pk, bits, N, H, plen, longest):
+    """Units of 8, 4 and 2 CTAs over a prefix, an empty one and none, with and without rows of their own."""
+    lens = [(997 * i) % (longest + 1) for i in range(N)]
+    lens[-1] = longest
+    run_case(pk, bits, N, H, 4, lens, [plen, 0], [(0, 0, 1, 5)[i % 4] for i in range(N)])
 
 
 @pytest.mark.parametrize("bits", BITS)
