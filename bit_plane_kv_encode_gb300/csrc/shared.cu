@@ -36,7 +36,7 @@ namespace bpkv {
 namespace shared {
 
 template <int BITS>
-cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
+cudaError_t launch_few(const Args& a, int64_t whole, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
 int few_tile(int bits);
 int unit_split(int64_t units, int64_t tokens);
 
@@ -431,6 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
   Walk walk(sm.plan, a);
   Segment g;
 
+  if (a.finish && (warp == 2 || warp == 3)) {
+    const int64_t n = (int64_t)a.n_seq * a.n_heads * a.group;
+    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * (tid - 64); r < n; r += (int64_t)gridDim.x * 64)
+      a.parts[r] = parts_of(a, sm.plan, r);
+  }
   if (warp < 4) {
     // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
     regs_fewer<80>();
@@ -830,6 +835,18 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
 //   27.6 / 27.5.
 constexpr int64_t kWholeTokens = 2048, kWholeMany = 1024, kWholeRows = 600000;
 
+// Behind the wide kernel, sequences that are short enough for k_shared_unit take
+// it too and join the prefix's partials there, which saves the streaming kernel's
+// plan and the join's launch: while a row has few partials (as the sequences
+// divide evenly among the prefixes) and there are not many CTAs with next to
+// nothing to do.  This / streamed and joined, in us, 8 x 4 heads, bf16 rows: 32
+// sequences of up to 1000 tokens over 32768 42.3 / 49.0, over 8000 31.2 / 38.8
+// (8-bit 33.1 / 42.2), of 60 over 4000 21.0 / 25.3; 64 of 300 over 8000 38.3 /
+// 41.6; 96 of 500 over 2000 41.3 / 46.0, of 300 over 8000 52.9 / 51.5, of 60 over
+// 2000 34.2 / 29.7; with 80 partials a row, 8 of 100 over 60000, 56.1 / 52.7.
+constexpr int kFinishParts = 32;
+constexpr int64_t kFinishRows = 300000;
+
 // Longer prefixes are streamed by units of 16 rows, from L2 again for each, and
 // the wide kernel is left out, while that reads at most this many bytes.  With
 // 32 sequences of 8 x 4 heads, streamed / wide, in us: 1000 tokens 19.3 / 22.0,
@@ -887,6 +904,12 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
                      n_own * pmax <= kWholeRows;
   const bool has_wide = !whole && prefix && own.n * group > kFew && again > kStreamBytes<BITS>;
   a.unit_log = has_wide ? kPairLog : kFewLog;
+  const int64_t sets = max64(1, min64(pn, own.n)), set_rows = (own.n * group + sets - 1) / sets;
+  const int64_t set_units = sets * n_heads * ((set_rows + kPair - 1) / kPair);
+  a.finish = has_wide && own.n_max <= (n_own > kSms ? kWholeMany : kWholeTokens) &&
+             (n_own <= 4 * kSms || n_own * own.n_max >= kFinishRows) &&
+             copies_of((int)set_rows) * (kSms / set_units + 1) <= kFinishParts;
+  a.few_rows = a.finish ? 0 : kFew;
   // no more CTAs than tiles, as far as the host knows (longer sequences than
   // it knows of only find fewer CTAs)
   const int64_t n_units = units(own.n, pn, group, a.unit_log), tok = few_tile(BITS);
@@ -907,7 +930,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
     e = launch_pdl(k_shared_wide<BITS>, dim3(a.wide_ctas), dim3(kThreads), (size_t)Shape<BITS>::bytes(dual), st, a, maps);
     if (e != cudaSuccess) return e;
   }
-  return launch_few<BITS>(a, whole ? total : -1, !has_wide, out, st);
+  return launch_few<BITS>(a, whole ? total : -1, own.n_max, !has_wide, out, st);
 }
 
 }  // namespace

@@ -109,6 +109,7 @@ struct Walk {
 
 namespace cg = cooperative_groups;
 constexpr int kMaxCluster = 8;
+enum { kAlone, kCluster, kFinish };  // what a CTA of k_shared_unit joins besides its own warps
 
 // A warp's way through all rows of one sequence and KV head that a CTA or a
 // cluster of them takes whole, the prefix's and then its own: every step-th
@@ -561,28 +562,91 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
   if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A lane's four channels of a row, and the row's maximum and sum.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+};
+
+constexpr int kJoinDeep = 8;  // parts in flight
+
+// Every step-th of a row's n parts from the first-th on, by one warp, each
+// part's (m, l) and o loaded together, under a running maximum.
+__device__ __forceinline__ void join_parts(const Args& a, const Parts& q, int n, int first, int step, int lane, Joined& j) {
+  const int n_pre = q.pre_n * q.pre_sub;
+  for (int k0 = first; k0 < n; k0 += step * kJoinDeep) {
+    float2 ml[kJoinDeep];
+    float4 o[kJoinDeep];
+#pragma unroll
+    for (int i = 0; i < kJoinDeep; ++i) {
+      const int k = k0 + i * step;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (k < n) {
+        const uint32_t seg = q.pre_sub > 1 ? (uint32_t)k / (uint32_t)q.pre_sub : k;
+        const int64_t row = k < n_pre ? q.pre + (int64_t)seg * q.pre_step + (k - (int)seg * q.pre_sub) * q.pre_span
+                                      : q.own + (int64_t)(k - n_pre) * a.group;
+        ml[i] = a.part_ml[row];
+        o[i] = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
+      }
+    }
+    float top = j.m;
+#pragma unroll
+    for (int i = 0; i < kJoinDeep; ++i) {
+      if (ml[i].y != 0.f) ml[i].x = fmaxf(ml[i].x, -3e38f);  // a sum that is NaN stays one
+      top = fmaxf(top, ml[i].y != 0.f ? ml[i].x : -INFINITY);
+    }
+    if (top == -INFINITY) continue;
+    const float f = ex2(j.m - top);
+    j.m = top;
+    j.l *= f;
+    j.o.x *= f;
+    j.o.y *= f;
+    j.o.z *= f;
+    j.o.w *= f;
+#pragma unroll
+    for (int i = 0; i < kJoinDeep; ++i) {
+      if (ml[i].y == 0.f) continue;  // no tokens: o was not written
+      const float w = ex2(ml[i].x - j.m);
+      j.l = fmaf(w, ml[i].y, j.l);
+      j.o.x = fmaf(w, o[i].x, j.o.x);
+      j.o.y = fmaf(w, o[i].y, j.o.y);
+      j.o.z = fmaf(w, o[i].z, j.o.z);
+      j.o.w = fmaf(w, o[i].w, j.o.w);
+    }
+  }
+}
+
 // Short sequences and prefixes: a CTA takes all rows of one sequence and KV head,
 // its warps join in shared memory, and neither plan nor partials nor join are
 // needed; a prefix is read again for every sequence, from L2.  One
 // sequence of 8 x 4 heads and 500 bf16 tokens takes 4.8 us: the launch, four
 // rounds of loads and products of each warp, and the join, all latency.  Few
 // units are dealt to a cluster of CTAs each (CLUSTER), which join through
-// distributed shared memory: over 32000 tokens (131 MB) 22 us, 6 TB/s.
-template <int BITS, int W, bool CLUSTER>
+// distributed shared memory: over 32000 tokens (131 MB) 22 us, 6 TB/s.  Behind
+// the wide kernel (kFinish) a CTA streams its sequence's own rows and joins them
+// with the prefix's partials, a warp or several for each row.
+template <int BITS, int W, int JOIN>
 __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __grid_constant__ Args a, uint16_t* out) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = Shape<BITS>;
   constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;
   __shared__ float2 s_ml[W][8];
   uint32_t ctas = 1, rank = 0;
-  if constexpr (CLUSTER) {
+  if constexpr (JOIN == kCluster) {
     ctas = cg::this_cluster().num_blocks();
     rank = cg::this_cluster().block_rank();
   }
   const uint32_t unit = blockIdx.x / ctas;
-  __shared__ float2 s_part[CLUSTER ? 8 : 1][kD / 2], s_part_ml[8];  // the CTA's o, (m, l)
+  // kCluster: the CTA's o, (m, l) of each row; kFinish: a warp's of a prefix's partials
+  __shared__ __align__(16) float2 s_part[JOIN != kAlone ? 8 : 1][kD / 2];
+  __shared__ float2 s_part_ml[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  pdl_enter();
+  if constexpr (JOIN == kFinish) {
+    // behind the wide kernel of the same call, which has waited for what came before it
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else {
+    pdl_enter();
+  }
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const unsigned char* exps = smem + W * kStages * kStage + warp * kStages * S::kExps;
   UnitWalk ahead(a, S::kTok, unit, rank * W + warp, ctas * W), cur = ahead;
@@ -605,12 +669,26 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
           }
         }
       });
+  const int split = JOIN == kFinish && a.group <= W / 2 ? W / a.group : 1;  // warps of a row's partials
+  if constexpr (JOIN == kFinish) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int t = warp; t < a.group * split; t += W) {
+      const int r = t % a.group;
+      const Parts q = a.parts[(int64_t)unit * a.group + r];
+      Joined j;
+      join_parts(a, q, q.pre_n * q.pre_sub, t / a.group, split, lane, j);
+      *reinterpret_cast<float4*>(&s_part[t][lane * 2]) = j.o;
+      if (lane == 0) s_part_ml[t] = make_float2(j.m, j.l);
+    }
+  }
   __syncthreads();
   for (int x = tid; x < a.group * (kD / 2); x += W * 32) {
     const int r = x / (kD / 2), d = x % (kD / 2) * 2;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][r].y == 0.f ? -INFINITY : fmaxf(s_ml[w][r].x, -3e38f));
+    if constexpr (JOIN == kFinish)
+      for (int t = r; t < a.group * split; t += a.group) M = fmaxf(M, s_part_ml[t].x);
     float L = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -622,7 +700,17 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
       o0 = fmaf(f, v.x, o0);
       o1 = fmaf(f, v.y, o1);
     }
-    if constexpr (CLUSTER) {
+    if constexpr (JOIN == kFinish) {
+      for (int t = r; t < a.group * split; t += a.group) {
+        const float2 ml = s_part_ml[t], v = s_part[t][d / 2];
+        if (ml.y == 0.f) continue;
+        const float f = ex2(ml.x - M);
+        L = fmaf(f, ml.y, L);
+        o0 = fmaf(f, v.x, o0);
+        o1 = fmaf(f, v.y, o1);
+      }
+    }
+    if constexpr (JOIN == kCluster) {
       s_part[r][d / 2] = make_float2(o0, o1);
       if (d == 0) s_part_ml[r] = make_float2(M, L);
     } else {
@@ -630,7 +718,7 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
       *reinterpret_cast<uint32_t*>(out + ((int64_t)unit * a.group + r) * kD + d) = pack<16>(o0 * s, o1 * s);
     }
   }
-  if constexpr (CLUSTER) {
+  if constexpr (JOIN == kCluster) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     for (int x = rank * (W * 32) + tid; x < a.group * (kD / 2); x += ctas * W * 32) {
@@ -669,7 +757,6 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
 // few rows have many and take eight.  About 5 us behind its kernels, latency.
 
 constexpr int kJoinWarps = 8;
-constexpr int kJoinDeep = 8;  // parts in flight
 
 template <int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_constant__ Args a, uint16_t* out) {
@@ -679,62 +766,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part0 = warp % W;
   const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.group;
   const int64_t r = (int64_t)blockIdx.x * (kJoinWarps / W) + warp / W;
-  float M = -INFINITY, L = 0.f;
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  Joined j;
   if (r < rows) {
     const Parts q = a.parts[r];
-    const int n_pre = q.pre_n * q.pre_sub, n = n_pre + q.own_n;
-    for (int k0 = part0; k0 < n; k0 += W * kJoinDeep) {
-      float2 ml[kJoinDeep];
-      float4 o[kJoinDeep];
-#pragma unroll
-      for (int i = 0; i < kJoinDeep; ++i) {
-        const int k = k0 + i * W;
-        ml[i] = make_float2(-INFINITY, 0.f);
-        if (k < n) {
-          const uint32_t seg = q.pre_sub > 1 ? (uint32_t)k / (uint32_t)q.pre_sub : k;
-          const int64_t row = k < n_pre
-                                  ? q.pre + (int64_t)seg * q.pre_step + (k - (int)seg * q.pre_sub) * q.pre_span
-                                  : q.own + (int64_t)(k - n_pre) * a.group;
-          ml[i] = a.part_ml[row];
-          o[i] = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
-        }
-      }
-      float top = M;
-#pragma unroll
-      for (int i = 0; i < kJoinDeep; ++i) {
-        if (ml[i].y != 0.f) ml[i].x = fmaxf(ml[i].x, -3e38f);  // a sum that is NaN stays one
-        top = fmaxf(top, ml[i].y != 0.f ? ml[i].x : -INFINITY);
-      }
-      if (top == -INFINITY) continue;
-      const float f = ex2(M - top);
-      M = top;
-      L *= f;
-      O.x *= f;
-      O.y *= f;
-      O.z *= f;
-      O.w *= f;
-#pragma unroll
-      for (int i = 0; i < kJoinDeep; ++i) {
-        if (ml[i].y == 0.f) continue;  // no tokens: o was not written
-        const float w = ex2(ml[i].x - M);
-        L = fmaf(w, ml[i].y, L);
-        O.x = fmaf(w, o[i].x, O.x);
-        O.y = fmaf(w, o[i].y, O.y);
-        O.z = fmaf(w, o[i].z, O.z);
-        O.w = fmaf(w, o[i].w, O.w);
-      }
-    }
+    join_parts(a, q, q.pre_n * q.pre_sub + q.own_n, part0, W, lane, j);
   }
+  float L = j.l;
+  float4 O = j.o;
   if constexpr (W > 1) {
     s_o[warp][lane] = O;
-    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    if (lane == 0) s_ml[warp] = make_float2(j.m, L);
     __syncthreads();
     if (part0 != 0) return;
-    float top = M;
+    float top = j.m;
 #pragma unroll
     for (int w = 1; w < W; ++w) top = fmaxf(top, s_ml[warp + w].x);
-    const float f = top == -INFINITY ? 0.f : ex2(M - top);
+    const float f = top == -INFINITY ? 0.f : ex2(j.m - top);
     L *= f;
     O = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
 #pragma unroll
@@ -775,11 +822,11 @@ int unit_split(int64_t units, int64_t tokens);
 // 10.9; of up to 1000: 40.4 instead of 37.9).
 constexpr int64_t kShortUnit = 512;
 
-template <int BITS, int W, bool CLUSTER = false>
+template <int BITS, int W, int JOIN = kAlone>
 cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out, int ctas = 1) {
   constexpr int kSmem = Shape<BITS>::kRing / kFewWarps * W;
   static std::atomic<uint64_t> done;
-  const auto kernel = k_shared_unit<BITS, W, CLUSTER>;
+  const auto kernel = k_shared_unit<BITS, W, JOIN>;
   const cudaError_t e = allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -793,21 +840,31 @@ cudaError_t go_unit(const Args& a, cudaStream_t st, uint16_t* out, int ctas = 1)
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = CLUSTER ? 2 : 1;
+  cfg.numAttrs = JOIN == kCluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, out);
 }
 
 // whole: tokens of a unit at most, for CTAs that take units whole; else -1, for
-// the streaming kernel and the join.  wait_first: no wide kernel came before.
+// the streaming kernel and the join, or for k_shared_unit behind the wide kernel
+// (a.finish).  own_max: tokens of a sequence at most.  wait_first: no wide kernel
+// came before.
 template <int BITS>
-cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st) {
+cudaError_t launch_few(const Args& a, int64_t whole, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st) {
   if (whole >= 0) {
     const int64_t units = (int64_t)a.n_seq * a.n_heads;
     const int split = unit_split(units, whole);
-    if (split > 1) return go_unit<BITS, 8, true>(a, st, out, split);
+    if (split > 1) return go_unit<BITS, 8, kCluster>(a, st, out, split);
     if (units <= kSms) return go_unit<BITS, 8>(a, st, out);
     if (units > 4 * kSms && whole <= kShortUnit) return go_unit<BITS, 2>(a, st, out);
     return go_unit<BITS, 4>(a, st, out);
+  }
+  if (a.finish) {
+    Args own = a;
+    own.plen = nullptr;
+    const int64_t units = (int64_t)a.n_seq * a.n_heads;
+    if (units <= kSms) return go_unit<BITS, 8, kFinish>(own, st, out);
+    if (units > 4 * kSms && own_max <= kShortUnit) return go_unit<BITS, 2, kFinish>(own, st, out);
+    return go_unit<BITS, 4, kFinish>(own, st, out);
   }
   const int ctas = a.few_workers / kFewWarps;
   const cudaError_t e = a.plen ? go<BITS, 2>(a, ctas, wait_first, st) : go<BITS, 1>(a, ctas, wait_first, st);
@@ -819,8 +876,8 @@ cudaError_t launch_few(const Args& a, int64_t whole, bool wait_first, uint16_t* 
                     out);
 }
 
-template cudaError_t launch_few<16>(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
-template cudaError_t launch_few<8>(const Args& a, int64_t whole, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<16>(const Args& a, int64_t whole, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<8>(const Args& a, int64_t whole, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
 
 // CTAs that share a unit (k_shared_unit): as many as leave all units resident at
 // once, clusters of 8 finding room for 12 at least.  In us for one / two / four /

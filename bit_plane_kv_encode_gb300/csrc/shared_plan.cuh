@@ -80,6 +80,8 @@ struct Args {
   int32_t wide_ctas, few_workers;
   int32_t unit_log;           // rows of a prefix unit: kPairLog, or kFewLog without the wide kernel
   int32_t stages;             // of the wide kernel's ring
+  int32_t few_rows;           // rows of the largest prefix unit that is streamed: kFew, or 0
+  int32_t finish;             // k_shared_unit joins: the wide kernel writes the table of partials
 };
 
 // Prefix items there can be with units of 2^log rows: one more for every full unit.
@@ -216,7 +218,7 @@ __device__ __forceinline__ void make_plan(const Args& a, Q& p, int few_tile) {
   const int n_pre = p.n_pre;
   for (int i = tid; i < n_pre; i += nt) {
     const int64_t n = p.tok[p.it_p[i]];
-    const bool wide = pre_rows(a, p, i) > kFew;
+    const bool wide = pre_rows(a, p, i) > a.few_rows;
     p.wide[i] = wide ? (n + kWideTile - 1) / kWideTile : 0;
     if constexpr (Q::kStream) p.few[i] = wide ? 0 : (n + few_tile - 1) / few_tile;
   }
@@ -249,7 +251,7 @@ struct Share {
 // Copies of a wide unit's rows among the 128 of a stream.  With 64 rows or
 // fewer the copies' softmax threads share the tile's tokens, so that all four
 // warps work; each copy has its own m, l and o.
-__device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 4 ? 4 : rows <= kWideTile / 2 ? 2 : 1; }
+__host__ __device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 4 ? 4 : rows <= kWideTile / 2 ? 2 : 1; }
 
 // Partial rows of segment (unit, worker): the segments in order have ascending
 // unit + worker, each its own.
@@ -262,9 +264,10 @@ __device__ __forceinline__ int64_t own_row(const Args& a, int64_t unit, int64_t 
 }
 
 // Where the partials of query row r = (sequence, KV head, head of the group) will be.
-__device__ __forceinline__ Parts parts_of(const Args& a, const FewPlan& p, int64_t r) {
+template <typename P>
+__device__ __forceinline__ Parts parts_of(const Args& a, const P& p, int64_t r) {
   const Share wide(p.wide[p.n_pre] * a.n_heads, a.wide_ctas);
-  const Share few(p.few[p.n_pre + a.n_seq] * a.n_heads, a.few_workers);
+  const Share few(P::kStream ? p.few[p.n_pre + a.n_seq] * a.n_heads : 0, a.few_workers);
   const int64_t u = quot(r, a.group);
   const int g = (int)(r - u * a.group), i = (int)quot(u, a.n_heads), h = (int)(u - (int64_t)i * a.n_heads);
   Parts q = {};
@@ -272,7 +275,7 @@ __device__ __forceinline__ Parts parts_of(const Args& a, const FewPlan& p, int64
   const int row = x >= 0 ? p.rank[i] * a.group + g : 0, item = x >= 0 ? p.item0[x] + (row >> a.unit_log) : 0;
   if (x >= 0 && item < p.n_pre && p.it_p[item] == x) {  // a prefix of length 0 has no items
     const int in = row & ((1 << a.unit_log) - 1), rows = pre_rows(a, p, item);
-    const bool is_wide = rows > kFew;
+    const bool is_wide = !P::kStream || rows > a.few_rows;
     const Share& share = is_wide ? wide : few;
     const int64_t* sums = is_wide ? p.wide : p.few;
     const int64_t tiles = sums[item + 1] - sums[item], at = sums[item] * a.n_heads + h * tiles;
@@ -289,12 +292,14 @@ __device__ __forceinline__ Parts parts_of(const Args& a, const FewPlan& p, int64
       q.pre_step = kFew;
     }
   }
-  const int own = p.n_pre + i;
-  const int64_t tiles = p.few[own + 1] - p.few[own], at = p.few[own] * a.n_heads + h * tiles;
-  if (tiles > 0) {
-    const int64_t w0 = few.owner(at);
-    q.own_n = (int)(few.owner(at + tiles - 1) - w0) + 1;
-    q.own = own_row(a, u, w0) + g;
+  if constexpr (P::kStream) {
+    const int own = p.n_pre + i;
+    const int64_t tiles = p.few[own + 1] - p.few[own], at = p.few[own] * a.n_heads + h * tiles;
+    if (tiles > 0) {
+      const int64_t w0 = few.owner(at);
+      q.own_n = (int)(few.owner(at + tiles - 1) - w0) + 1;
+      q.own = own_row(a, u, w0) + g;
+    }
   }
   return q;
 }

@@ -199,6 +199,20 @@ def test_one_prefix(pk, bits, N, G, bound):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("N,H,G,plens,longest", [(40, 4, 3, [900], 2048), (40, 8, 5, [5000], 1024), (77, 8, 2, [300], 600),
+                                                 (160, 4, 8, [2000], 469), (44, 8, 8, [700, 0, 1, 200], 300), (44, 8, 1, [700, 0, 1, 200], 300),
+                                                 (500, 2, 1, [130, 900], 1024), (40, 4, 7, [900], 2049)])
+def test_own_rows_behind_the_wide_kernel(pk, bits, N, H, G, plens, longest):
+    """Joined with the prefix's partials in units of 8, 4 and 2 warps; prefixes of few sequences and of none; and one
+    token more than that takes."""
+    lens = [(89 * i) % (longest + 1) for i in range(N)]
+    lens[1] = longest
+    P = len(plens)
+    of = [(0, 0, 0, 0, 1, 0, 0, 2, 3, -1)[i % 10] for i in range(N)] if P > 2 else [i % P for i in range(N)]
+    run_case(pk, bits, N, H, G, lens, plens, of, bound=65536)
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("N,H,plen,longest", [(3, 4, 30000, 2000), (8, 4, 12000, 4000), (18, 4, 4000, 4000), (5, 1, 20000, 0)])
 def test_clusters_over_prefixes(pk, bits, N, H, plen, longest):
     """Units of 8, 4 and 2 CTAs over a prefix, an empty one and none, with and without rows of their own."""
