@@ -213,6 +213,16 @@ def test_own_rows_behind_the_wide_kernel(pk, bits, N, H, G, plens, longest):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("bound", [None, 3000, 65536])
+@pytest.mark.parametrize("plens,of", [([0], 0), ([0, 0], 1), ([900], -1), ([900, 5], 2)])
+def test_prefixes_that_give_nothing(pk, bits, bound, plens, of):
+    """Only empty prefixes, or prefixes that no sequence has, every way; also with no rows of their own."""
+    for lens in ([(37 * i) % 300 for i in range(40)], [0] * 40):
+        r = run_case(pk, bits, 40, 4, 4, lens, plens, [of] * 40, bound=bound)
+    assert (r["out"] == 0).all()
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("N,H,plen,longest", [(3, 4, 30000, 2000), (8, 4, 12000, 4000), (18, 4, 4000, 4000), (5, 1, 20000, 0)])
 def test_clusters_over_prefixes(pk, bits, N, H, plen, longest):
     """Units of 8, 4 and 2 CTAs over a prefix, an empty one and none, with and without rows of their own."""
