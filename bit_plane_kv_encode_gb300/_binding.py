@@ -126,25 +126,37 @@ def header_symbols() -> list:
 
 # ------------------------------------------------------------------ marshalling
 
+# Addresses go in as plain integers (every parameter they fill is declared a
+# void pointer): a call of few microseconds has no time for a ctypes object each.
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return ctypes.c_void_p(x)
-    return ctypes.c_void_p(x.data_ptr())
+    if x is None or isinstance(x, int):
+        return x
+    return x.data_ptr()
+
+
+_current = None
+
+
+def _current_stream():
+    """Handle of torch's current stream: from the raw call, as building a Stream object costs 3 us."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is None or device is None:
+            _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _current = lambda: raw(device())  # noqa: E731
+    return _current()
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        # the handle itself: building a Stream object costs 3 us, more than a small call
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        return ctypes.c_void_p(raw(torch.cuda.current_device()))
+        return _current_stream()
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check(fn: str, rc: int) -> int:
