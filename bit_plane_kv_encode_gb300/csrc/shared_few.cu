@@ -1,6 +1,7 @@
 // Attention of few query rows over long rows of KV: each sequence's G heads
-// over its own rows, and prefixes of at most 16 query rows (the streaming half
-// of bpkv_shared_attend / bpkv_shared_attend8; the plan is in shared_plan.cuh).
+// over its own rows, and units of at most 16 query rows over a prefix (the
+// streaming half of bpkv_shared_attend / bpkv_shared_attend8; the plan is in
+// shared_plan.cuh, which kernel takes what in shared.cu's launch).
 //
 // Bound by the bytes of K and V, so every warp is a worker with its own ring of
 // asynchronous copies (three stages of 8 KB: 16 tokens of bf16, 32 of codes)
@@ -621,7 +622,7 @@ __device__ __forceinline__ void join_parts(const Args& a, const Parts& q, int n,
 // needed; a prefix is read again for every sequence, from L2.  One
 // sequence of 8 x 4 heads and 500 bf16 tokens takes 4.8 us: the launch, four
 // rounds of loads and products of each warp, and the join, all latency.  Few
-// units are dealt to a cluster of CTAs each (CLUSTER), which join through
+// units are dealt to a cluster of CTAs each (kCluster), which join through
 // distributed shared memory: over 32000 tokens (131 MB) 22 us, 6 TB/s.  Behind
 // the wide kernel (kFinish) a CTA streams its sequence's own rows and joins them
 // with the prefix's partials, a warp or several for each row.
@@ -876,8 +877,8 @@ cudaError_t launch_few(const Args& a, int64_t whole, int64_t own_max, bool wait_
                     out);
 }
 
-template cudaError_t launch_few<16>(const Args& a, int64_t whole, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
-template cudaError_t launch_few<8>(const Args& a, int64_t whole, int64_t own_max, bool wait_first, uint16_t* out, cudaStream_t st);
+template cudaError_t launch_few<16>(const Args&, int64_t, int64_t, bool, uint16_t*, cudaStream_t);
+template cudaError_t launch_few<8>(const Args&, int64_t, int64_t, bool, uint16_t*, cudaStream_t);
 
 // CTAs that share a unit (k_shared_unit): as many as leave all units resident at
 // once, clusters of 8 finding room for 12 at least.  In us for one / two / four /
