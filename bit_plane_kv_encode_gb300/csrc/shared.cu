@@ -11,13 +11,14 @@
 // and both take every tile; with fewer both hold the same rows and each takes
 // every other tile.  Rows that fill half or a quarter of the 128 are held twice
 // or four times (the instruction takes 128), each copy's threads weighing their
-// share of the tile's tokens.  m only follows the maximum when that has risen by
-// a factor of 2^kLazy, so O is seldom rescaled.
+// share of the tile's tokens; the copies are joined when the segment ends.  m
+// only follows the maximum when that has risen by a factor of 2^kLazy, so O is
+// seldom rescaled.
 //
 // What bounds it: with 256 rows the chain S -> softmax (about 1650 cycles) -> O,
 // of which two streams hide half: the tensor cores are busy 65% of the time.
 // Measured on a GB300 with 128 sequences of 8 x 4 heads over one prefix of
-// 131072 tokens: 203 us for this kernel, 1.35 PFLOP/s; with 32 over 32768 tokens
+// 131072 tokens: 195 us for this kernel, 1.41 PFLOP/s; with 32 over 32768 tokens
 // 25 us, 5.4 TB/s.  8-bit rows, 16 sequences of 4 x 8 heads over two prefixes of
 // 131071 tokens: 80 us, 3.4 TB/s, bound by the softmax with its scales.
 //
@@ -693,42 +694,102 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
         o_phase ^= 1;
       }
       m *= BITS == 16 ? kLogScale : 1.f;
-      // streams that hold the same rows join them: each writes half of the channels
+      // Streams that hold the same rows join them, each half of the channels, and
+      // so do a row's copies: the upper half of the copies through shared memory
+      // (the rows of q, which are read), then of four the second.
       float f0 = 1.f, f1 = 0.f;
-      if (!g.dual) {
-        sm.ml[s][row] = make_float2(m, l);
+      auto meet = [&] {  // of all softmax warps
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.fin));
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.fin), fin_phase, abort));
-        if (!ok) break;
         fin_phase ^= 1;
-        const float2 a0 = sm.ml[0][row], a1 = sm.ml[1][row];
-        m = fmaxf(a0.x, a1.x);
-        f0 = a0.y == 0.f ? 0.f : ex2(a0.x - m);
-        f1 = a1.y == 0.f ? 0.f : ex2(a1.x - m);
-        l = f0 * a0.y + f1 * a1.y;
+        return ok;
+      };
+      if (!g.dual) {
+        sm.ml[s][row] = make_float2(m, l);
+        if (!meet()) break;
+        m = -INFINITY;
+        for (int c = r; c < kTile; c += kTile / copies) m = fmaxf(m, fmaxf(sm.ml[0][c].x, sm.ml[1][c].x));
+        l = 0.f;
+        for (int c = r; c < kTile; c += kTile / copies) {
+          const float2 a0 = sm.ml[0][c], a1 = sm.ml[1][c];
+          const float g0 = a0.y == 0.f ? 0.f : ex2(a0.x - m), g1 = a1.y == 0.f ? 0.f : ex2(a1.x - m);
+          if (c == row) f0 = g0, f1 = g1;
+          l += g0 * a0.y + g1 * a1.y;
+        }
       }
-      if (active && g.steps_of(0) > 0) {
-        fence_after();
+      fence_after();
+      const int c0 = g.dual ? 0 : s * 64, c1 = g.dual ? kD : c0 + 64;
+      const uint32_t o0 = g.dual ? to : tmem + lanes + 2 * kTile;
+      const bool both = !g.dual && g.steps_of(1) > 0;
+      auto own = [&](int k, uint32_t (&o)[16]) {  // 16 channels of this thread's row
+        tmem_ld16(o0 + k, o);
+        if (both) {
+          uint32_t v[16];
+          tmem_ld16(o0 + kD + k, v);
+          wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(v[i]) * f1));
+        } else {
+          wait_ld();
+          if (copies > 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+          }
+        }
+      };
+      // 16 bytes of a slot, one of 64 rows of this stream's channels
+      auto slot = [&](int x, int k, int i) {
+        return reinterpret_cast<float4*>(q_smem + s * (kTile * kD) + x * 256 + (((((k - c0) >> 2) + i) ^ (x & 15)) << 4));
+      };
+      auto put = [&](int x, int k, const uint32_t (&o)[16]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *slot(x, k, i) = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+      };
+      auto add = [&](int x, int k, uint32_t (&o)[16]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = *slot(x, k, i);
+          o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) + v.x);
+          o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) + v.y);
+          o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) + v.z);
+          o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) + v.w);
+        }
+      };
+      uint32_t o[16];
+      if (copies > 1) {
+        if (active && copy >= copies / 2) {
+#pragma unroll 1
+          for (int k = c0; k < c1; k += 16) {
+            own(k, o);
+            put(row - kTile / 2, k, o);
+          }
+        }
+        if (!meet()) break;
+        if (copies == 4) {
+          if (active && copy == 1) {
+#pragma unroll 1
+            for (int k = c0; k < c1; k += 16) {
+              own(k, o);
+              add(row, k, o);
+              put(row, k, o);
+            }
+          }
+          if (!meet()) break;
+        }
+      }
+      if (active && copy == 0) {
         const int64_t at = wide_row(a, g.unit, blockIdx.x) + (g.dual ? s * kTile : 0) + row;
-        const int q = lane & 3, c0 = g.dual ? 0 : s * 64, c1 = g.dual ? kD : c0 + 64;
-        const uint32_t o0 = g.dual ? to : tmem + lanes + 2 * kTile;
-        const bool both = !g.dual && g.steps_of(1) > 0;
+        const int q = lane & 3;
         float* po = a.part_o + (at - q) * kD + q * 4;
 #pragma unroll 1
         for (int k = c0; k < c1; k += 16) {
-          uint32_t o[16];
-          tmem_ld16(o0 + k, o);
-          if (both) {
-            uint32_t v[16];
-            tmem_ld16(o0 + kD + k, v);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(v[i]) * f1));
-          } else {
-            wait_ld();
-          }
+          own(k, o);
+          if (copies > 1) add(row, k, o);
+          if (copies == 4) add(row + 32, k, o);
           quads(o);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -736,8 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
               *reinterpret_cast<uint4*>(po + i * kD + k) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
         if ((g.dual || s == 0) && r < rows) a.part_ml[at] = make_float2(m, l);
-        fence_before();
       }
+      fence_before();
+      if (copies > 1 && !meet()) break;  // the slots are read before the next rows of q come
       tile_no += g.tiles;
       ++seg;
     }
@@ -837,24 +899,23 @@ constexpr int64_t kWholeTokens = 2048, kWholeMany = 1024, kWholeRows = 600000;
 
 // Behind the wide kernel, sequences that are short enough for k_shared_unit take
 // it too and join the prefix's partials there, which saves the streaming kernel's
-// plan and the join's launch: while a row has few partials (as the sequences
-// divide evenly among the prefixes) and there are not many CTAs with next to
-// nothing to do.  This / streamed and joined, in us, 8 x 4 heads, bf16 rows: 32
-// sequences of up to 1000 tokens over 32768 42.3 / 49.0, over 8000 31.2 / 38.8
-// (8-bit 33.1 / 42.2), of 60 over 4000 21.0 / 25.3; 64 of 300 over 8000 38.3 /
-// 41.6; 96 of 500 over 2000 41.3 / 46.0, of 300 over 8000 52.9 / 51.5, of 60 over
-// 2000 34.2 / 29.7; with 80 partials a row, 8 of 100 over 60000, 56.1 / 52.7.
-constexpr int kFinishParts = 32;
-constexpr int64_t kFinishRows = 300000;
+// plan and the join's launch.  This / streamed and joined, in us, 8 x 4 heads,
+// bf16 rows (8-bit rows in brackets): 32 sequences of up to 1000 tokens over
+// 32768 39.3 / 49.7; over 20000 8 of 2000 31 / 38 (33 / 38), 18 of 4000 45 / 52
+// (43 / 52), 8 of 8000 53 / 50 (54 / 47); 96 of 1000 72 / 81 (98 / 109), of 2000
+// 91 / 106 (107 / 123).  The bounds are as long as a long sequence among short
+// ones may be waited for; of many units a CTA has fewer warps.
+constexpr int64_t kFinishTokens = 4096, kFinishMany = 2048;
 
-// Longer prefixes are streamed by units of 16 rows, from L2 again for each, and
-// the wide kernel is left out, while that reads at most this many bytes.  With
-// 32 sequences of 8 x 4 heads, streamed / wide, in us: 1000 tokens 19.3 / 22.0,
-// 2000 tokens (66 MB) 27.7 / 24.2, 4000 tokens 40.2 / 25.0; 8-bit rows: 2000
-// tokens (33 MB) 22.4 / 29.4, 4000 tokens 31.4 / 30.0.  With three prefixes of
-// 2000 tokens and 64 sequences of 4 x 8 heads over 8-bit rows (66 MB) 35.5 / 47.
+// Prefixes are streamed by units of 16 rows, from L2 again for each, and the wide
+// kernel is left out, while that reads at most this many bytes.  Streamed / wide,
+// in us: 40 sequences of 2 x 4 heads over five prefixes of up to 3000 tokens (31
+// MB) 16.3 / 23.3 (8-bit 16.2 / 27.5); 96 of 8 x 1 over two of 1500 (38 MB) 22.8 /
+// 20.3 (22.0 / 23.9); 20 of 8 x 4 over 2500 (51 MB) 24.0 / 15.4 (21.0 / 19.7); 17
+// of 1 x 4 over 20000 (51 MB) 24.5 / 18.3 (24.3 / 22.0); 80 of 8 x 4 over 1000 in
+// 8 bits (41 MB) 24.6 / 28.5.
 template <int BITS>
-constexpr int64_t kStreamBytes = BITS == 16 ? 60000000 : 70000000;
+constexpr int64_t kStreamBytes = BITS == 16 ? 40000000 : 50000000;
 
 // One side's rows: K and V (with their exponents for 8-bit rows).
 struct Side {
@@ -904,11 +965,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
                      n_own * pmax <= kWholeRows;
   const bool has_wide = !whole && prefix && own.n * group > kFew && again > kStreamBytes<BITS>;
   a.unit_log = has_wide ? kPairLog : kFewLog;
-  const int64_t sets = max64(1, min64(pn, own.n)), set_rows = (own.n * group + sets - 1) / sets;
-  const int64_t set_units = sets * n_heads * ((set_rows + kPair - 1) / kPair);
-  a.finish = has_wide && own.n_max <= (n_own > kSms ? kWholeMany : kWholeTokens) &&
-             (n_own <= 4 * kSms || n_own * own.n_max >= kFinishRows) &&
-             copies_of((int)set_rows) * (kSms / set_units + 1) <= kFinishParts;
+  a.finish = has_wide && own.n_max <= (n_own > kSms ? kFinishMany : kFinishTokens);
   a.few_rows = a.finish ? 0 : kFew;
   // no more CTAs than tiles, as far as the host knows (longer sequences than
   // it knows of only find fewer CTAs)

@@ -574,7 +574,6 @@ constexpr int kJoinDeep = 8;  // parts in flight
 // Every step-th of a row's n parts from the first-th on, by one warp, each
 // part's (m, l) and o loaded together, under a running maximum.
 __device__ __forceinline__ void join_parts(const Args& a, const Parts& q, int n, int first, int step, int lane, Joined& j) {
-  const int n_pre = q.pre_n * q.pre_sub;
   for (int k0 = first; k0 < n; k0 += step * kJoinDeep) {
     float2 ml[kJoinDeep];
     float4 o[kJoinDeep];
@@ -583,9 +582,8 @@ __device__ __forceinline__ void join_parts(const Args& a, const Parts& q, int n,
       const int k = k0 + i * step;
       ml[i] = make_float2(-INFINITY, 0.f);
       if (k < n) {
-        const uint32_t seg = q.pre_sub > 1 ? (uint32_t)k / (uint32_t)q.pre_sub : k;
-        const int64_t row = k < n_pre ? q.pre + (int64_t)seg * q.pre_step + (k - (int)seg * q.pre_sub) * q.pre_span
-                                      : q.own + (int64_t)(k - n_pre) * a.group;
+        const int64_t row =
+            k < q.pre_n ? q.pre + (int64_t)k * q.pre_step : q.own + (int64_t)(k - q.pre_n) * a.group;
         ml[i] = a.part_ml[row];
         o[i] = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
       }
@@ -677,7 +675,7 @@ __global__ void __launch_bounds__(W * 32, kFewWarps / W) k_shared_unit(const __g
       const int r = t % a.group;
       const Parts q = a.parts[(int64_t)unit * a.group + r];
       Joined j;
-      join_parts(a, q, q.pre_n * q.pre_sub, t / a.group, split, lane, j);
+      join_parts(a, q, q.pre_n, t / a.group, split, lane, j);
       *reinterpret_cast<float4*>(&s_part[t][lane * 2]) = j.o;
       if (lane == 0) s_part_ml[t] = make_float2(j.m, j.l);
     }
@@ -770,7 +768,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const __grid_co
   Joined j;
   if (r < rows) {
     const Parts q = a.parts[r];
-    join_parts(a, q, q.pre_n * q.pre_sub + q.own_n, part0, W, lane, j);
+    join_parts(a, q, q.pre_n + q.own_n, part0, W, lane, j);
   }
   float L = j.l;
   float4 O = j.o;

@@ -52,16 +52,15 @@ constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
 constexpr int kSms = 152;
 constexpr int kFewWarps = 8;         // per CTA of the streaming kernel
 
-// A query row's partials, as rows of the partial buffers: of each of pre_n
-// segments pre_sub copies, then of each of own_n segments one.
+// A query row's partials, as rows of the partial buffers: of pre_n segments of
+// its prefix, then of own_n segments of its own rows.
 struct Parts {
   int64_t pre, own;   // first
   int32_t pre_n, own_n;
-  int32_t pre_sub;    // copies of the row
-  int32_t pre_span;   // rows from one copy to the next
   int32_t pre_step;   // rows from one segment to the next
   int32_t pad;
 };
+static_assert(sizeof(Parts) == 32, "two 16-byte loads");
 
 struct Args {
   const int32_t* prefix_of;
@@ -250,8 +249,8 @@ struct Share {
 
 // Copies of a wide unit's rows among the 128 of a stream.  With 64 rows or
 // fewer the copies' softmax threads share the tile's tokens, so that all four
-// warps work; each copy has its own m, l and o.
-__host__ __device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 4 ? 4 : rows <= kWideTile / 2 ? 2 : 1; }
+// warps work; each copy has its own m, l and o until the segment's end.
+__device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 4 ? 4 : rows <= kWideTile / 2 ? 2 : 1; }
 
 // Partial rows of segment (unit, worker): the segments in order have ascending
 // unit + worker, each its own.
@@ -283,12 +282,9 @@ __device__ __forceinline__ Parts parts_of(const Args& a, const P& p, int64_t r) 
     q.pre_n = (int)(share.owner(at + tiles - 1) - w0) + 1;
     if (is_wide) {
       q.pre = wide_row(a, unit, w0) + in;
-      q.pre_sub = copies_of(rows);
-      q.pre_span = kWideTile / copies_of(rows);
       q.pre_step = kPair;
     } else {
       q.pre = few_row(a, unit, w0) + in;
-      q.pre_sub = 1;
       q.pre_step = kFew;
     }
   }

@@ -199,9 +199,10 @@ def test_one_prefix(pk, bits, N, G, bound):
 
 
 @pytest.mark.parametrize("bits", BITS)
-@pytest.mark.parametrize("N,H,G,plens,longest", [(40, 4, 3, [900], 2048), (40, 8, 5, [5000], 1024), (77, 8, 2, [300], 600),
+@pytest.mark.parametrize("N,H,G,plens,longest", [(38, 4, 3, [900], 4096), (40, 8, 5, [5000], 2048), (77, 8, 2, [300], 600),
                                                  (160, 4, 8, [2000], 469), (44, 8, 8, [700, 0, 1, 200], 300), (44, 8, 1, [700, 0, 1, 200], 300),
-                                                 (500, 2, 1, [130, 900], 1024), (40, 4, 7, [900], 2049)])
+                                                 (500, 2, 1, [130, 900], 1024), (38, 4, 7, [900], 4097), (40, 4, 7, [900], 2049),
+                                                 (20, 1, 1, [9000], 50), (70, 1, 1, [9000], 50), (24, 3, 2, [3000], 70)])
 def test_own_rows_behind_the_wide_kernel(pk, bits, N, H, G, plens, longest):
     """Joined with the prefix's partials in units of 8, 4 and 2 warps; prefixes of few sequences and of none; and one
     token more than that takes."""
