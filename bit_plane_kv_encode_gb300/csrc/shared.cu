@@ -187,13 +187,15 @@ __device__ __forceinline__ void load_q(const Args& a, const WidePlan& p, const S
   const int l16 = t & 15, rows = g.rows_of(s), span = kTile / g.copies();
   const uint32_t base = g.row0 + (g.dual ? s * kTile : 0), first = p.first[g.index], group = a.group;
   unsigned char* half = dst + (l16 / 8) * (kTile * 128);
+  const uint16_t* q = a.q + (int64_t)g.h * a.group * kD + l16 * 8;
+  const uint32_t seq_step = a.n_heads * a.group * kD;
 #pragma unroll 4
   for (int r = t / 16; r < kTile; r += n / 16) {
     const uint32_t of = r & (span - 1);
     if ((int)of < rows) {
-      const uint32_t x = base + of, seq = p.order[first + x / group], head = x % group;
+      const uint32_t x = base + of, i = x * a.group_inv >> 16, seq = p.order[first + i];
       cp_async16(half + (BITS == 16 ? swz(r, l16 & 7) : (uint32_t)(r * 128 + (l16 & 7) * 16)),
-                 a.q + ((((int64_t)seq * a.n_heads + g.h) * a.group + head) * kD + l16 * 8));
+                 q + (uint64_t)seq * seq_step + (x - i * group) * kD);
     }
   }
   cp_async_commit();
@@ -947,6 +949,7 @@ cudaError_t launch(const Side* prefix, const Side& own, const int32_t* prefix_of
   a.n_seq = own.n;
   a.n_heads = n_heads;
   a.group = group;
+  a.group_inv = ((1u << 16) + group - 1) / group;
   a.q = q;
   a.parts = reinterpret_cast<Parts*>(w + sp.parts);
   a.part_ml = reinterpret_cast<float2*>(w + sp.ml);

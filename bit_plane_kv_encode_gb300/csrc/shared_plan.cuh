@@ -68,6 +68,7 @@ struct Args {
   const int64_t* len;
   int64_t pcap, cap;
   int32_t n_prefix, n_seq, n_heads, group;
+  uint32_t group_inv;  // 2^16 / group rounded up: x group_inv >> 16 is x / group for every row x of a prefix
   const uint16_t* q;
   const void* rows[2][2];     // [prefix, own][K, V]
   const uint8_t* exps[2][2];  // scale exponents of 8-bit rows
@@ -134,6 +135,8 @@ __device__ __forceinline__ void warp_sums(int64_t* v, int n) {
   }
   if (lane == 0) v[n] = sum;
 }
+
+static_assert(kMaxSeq * BPKV_MAX_GROUP * (BPKV_MAX_GROUP - 1) < 1 << 16, "x / group by group_inv");
 
 template <typename P>
 __device__ __forceinline__ int pre_rows(const Args& a, const P& p, int item) {
