@@ -20,7 +20,7 @@
 // Measured on a GB300 with 128 sequences of 8 x 4 heads over one prefix of
 // 131072 tokens: 195 us for this kernel, 1.41 PFLOP/s; with 32 over 32768 tokens
 // 25 us, 5.4 TB/s.  8-bit rows, 16 sequences of 4 x 8 heads over two prefixes of
-// 131071 tokens: 80 us, 3.4 TB/s, bound by the softmax with its scales.
+// 131071 tokens: 72 us, 3.7 TB/s, bound by the softmax with its scales.
 //
 // 8-bit rows.  The products take the codes as they lie.  q becomes two e4m3
 // pieces of 4 bits under a power-of-two scale of its row, which is all of a
