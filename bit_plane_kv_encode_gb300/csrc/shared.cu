@@ -31,6 +31,7 @@
 // half.
 #include "rows8_core.cuh"
 #include "shared_plan.cuh"
+#include "shared_ring.cuh"
 #include "tc.cuh"
 
 namespace bpkv {
@@ -44,13 +45,9 @@ int unit_split(int64_t units, int64_t tokens);
 namespace {
 
 using namespace tc;
+using namespace wide;
 
-constexpr int kTile = kWideTile;
-constexpr int kSoftmaxWarps = 8;                 // four a stream, a thread per row
 constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
-constexpr int kRing16 = 32 * 1024;               // bytes of a stage: 128 rows of bf16
-constexpr int kRing8 = 16 * 1024;                // 128 rows of codes
-constexpr int kMaxStages = 10;
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
 constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
 
@@ -64,29 +61,6 @@ struct Range {
 
 struct Maps {
   CUtensorMap m[2];  // K, V
-};
-
-template <int BITS>
-struct Scales {};
-
-template <>
-struct Scales<8> {
-  float qf[2][2][kTile];  // scales of the rows of q, by segment parity and stream
-  __align__(16) float tok[2][2][3][kTile];  // by stream, twice: 2^ek log2(e)/sqrt(D), ev, 2^-ev of a tile's tokens
-};
-
-template <int BITS>
-struct Smem {
-  Scales<BITS> sc;
-  WidePlan plan;
-  uint32_t tmem;
-  uint32_t abort;
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t s_full[2], p_ready[2], o_done[2];
-  uint64_t q_full, q_empty, done;
-  uint64_t sc_go[2], sc_full[2][2], sc_empty[2][2];
-  uint64_t p_half[2], fin;
-  float2 ml[2][kTile];  // each row's maximum and sum, where both streams hold the rows
 };
 
 // One CTA's part of a unit.
@@ -148,24 +122,6 @@ struct Walk {
     return true;
   }
 };
-
-// ---- shared memory: Smem, then 1024-byte aligned the rows of q, then the ring
-
-template <int BITS>
-struct Shape {
-  static constexpr int kQ = kTile * kD * 2;                       // one stream's rows of q (16 bits, or two 8-bit pieces)
-  static constexpr int kStage = BITS == 16 ? kRing16 : kRing8;    // K or V tile
-  static constexpr int kExps = BITS == 16 ? 0 : 2 * kTile;        // exponent bytes that come with V
-  static constexpr int kSmemMax = 227 * 1024;
-  static constexpr int kBase = (sizeof(Smem<BITS>) + 1023) / 1024 * 1024 + 1024;
-  static constexpr int stages(bool dual) {
-    const int n = (kSmemMax - kBase - (dual ? 2 : 1) * kQ) / (kStage + kExps);
-    return n < kMaxStages ? n : kMaxStages;
-  }
-  static int bytes(bool dual) { return kBase + (dual ? 2 : 1) * kQ + stages(dual) * (kStage + kExps); }
-};
-
-static_assert(Shape<16>::stages(true) >= 4 && Shape<8>::stages(true) >= 8, "two tiles of K and V at least");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -579,8 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
     } else {
       if constexpr (BITS == 8) {
         // ---- warp 2 + s: the scales of stream s's tiles as floats.  It begins a
-        // segment when the stream does: further ahead, a stage's phase bit would
-        // be that of an earlier fill.
+        // segment when the stream does, and in it keeps at most two of the stream's
+        // tiles ahead of the softmax (sc_empty): further ahead, a stage's phase bit
+        // could be that of an earlier fill (kMaxStages).
         const int s = warp - 2;
         uint32_t tile_no = 0, n = 0, go = 0;
         bool ok = true;
