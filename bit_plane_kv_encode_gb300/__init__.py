@@ -105,6 +105,23 @@ class Cache:
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
 
+def _check_arg(fn, name, x, dtype, shape, device):
+    """A tensor that a kernel reads or writes at its address alone: raises unless it is what the kernel takes it for.
+    None and raw addresses pass."""
+    if x is None or isinstance(x, int):
+        return
+    if x.shape != shape or x.dtype is not dtype or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{fn}: {name} must be {dtype} {shape}, contiguous, on {device}; "
+                         f"got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+
+
+def _check_status(fn, status, device):
+    """A status word: the first four bytes of a tensor (a workspace has one too)."""
+    if status is not None and not isinstance(status, int) and (
+            status.device != device or status.numel() * status.element_size() < 4):
+        raise ValueError(f"{fn}: status must have four bytes on {device}")
+
+
 class Rows8:
     """One layer's cache of 8-bit K and V rows (e4m3 codes, one power-of-two
     scale per row) for N sequences x H KV heads, in device memory."""
@@ -129,8 +146,17 @@ class Rows8:
 
     def append(self, k_new, v_new, start=None, status=None, stream=None):
         """Quantise k_new/v_new [N][H][t][D] bf16 (device) behind every
-        sequence's rows, or at rows start[i] .. (int64 [N], device)."""
-        bpkv_rows8_append(self.c, k_new, v_new, k_new.shape[2], start, status, stream)
+        sequence's rows, or at rows start[i] .. (int64 [N], device).  ValueError
+        for tensors of another type, shape or device, or with other strides."""
+        import torch
+        device = self.k8.device
+        t = k_new.shape[2] if k_new.dim() == 4 else 0
+        shape = (self.c.n_seq, self.c.n_kv_heads, t, HEAD_DIM)
+        _check_arg("Rows8.append", "k_new", k_new, torch.bfloat16, shape, device)
+        _check_arg("Rows8.append", "v_new", v_new, torch.bfloat16, shape, device)
+        _check_arg("Rows8.append", "start", start, torch.int64, shape[:1], device)
+        _check_status("Rows8.append", status, device)
+        bpkv_rows8_append(self.c, k_new, v_new, t, start, status, stream)
 
     def read(self, t0: int, n: int, stream=None):
         """(K, V) rows t0 .. t0 + n - 1 of every sequence, bf16 [N][H][n][D]; zeros past its length."""
