@@ -172,8 +172,8 @@ def qkv_args(qkv, q_out, n_kv_heads: int, pos=None, inv_freq=None, q_weight=None
              pairs: bool = False, k_out=None, v_out=None, rows8=None, status=None):
     """bpkv_qkv_args for qkv [N][t][>= (G + 2) H D] bf16 (its last dimension
     dense) and q_out [N][t][H][G][D] float32 or bf16; inv_freq [rot / 2]
-    float32 says how many channels are rotated; rows8: a Rows8.  The struct
-    keeps the tensors it points to alive."""
+    float32 says how many channels are rotated; rows8: a Rows8.  All on one
+    device.  The struct keeps the tensors it points to alive."""
     import torch
     N, t = qkv.shape[0], qkv.shape[1]
     H, G = q_out.shape[2], q_out.shape[3]
@@ -187,12 +187,17 @@ def qkv_args(qkv, q_out, n_kv_heads: int, pos=None, inv_freq=None, q_weight=None
     need(H == n_kv_heads and q_out.shape == (N, t, H, G, HEAD_DIM) and q_out.is_contiguous(), "q_out's shape")
     need(q_out.dtype in (torch.float32, torch.bfloat16), "q_out must be float32 or bf16")
     need(qkv.shape[2] >= (G + 2) * H * HEAD_DIM, "qkv's rows hold (G + 2) H heads")
-    for x, dt, shape in ((pos, torch.int64, (N,)), (q_weight, torch.float32, (HEAD_DIM,)),
-                         (k_weight, torch.float32, (HEAD_DIM,)), (k_out, torch.bfloat16, (N, H, t, HEAD_DIM)),
-                         (v_out, torch.bfloat16, (N, H, t, HEAD_DIM))):
-        need(x is None or (x.dtype == dt and tuple(x.shape) == shape and x.is_contiguous()), f"expected {dt} {shape}")
-    need(inv_freq is None or (inv_freq.dtype == torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()),
-         "inv_freq must be float32 [rot / 2]")
+    device = qkv.device
+    need(q_out.device == device and (rows8 is None or rows8.k8.device == device), "tensors on several devices")
+    for name, x, dt, shape in (("pos", pos, torch.int64, (N,)), ("q_weight", q_weight, torch.float32, (HEAD_DIM,)),
+                               ("k_weight", k_weight, torch.float32, (HEAD_DIM,)),
+                               ("k_out", k_out, torch.bfloat16, (N, H, t, HEAD_DIM)),
+                               ("v_out", v_out, torch.bfloat16, (N, H, t, HEAD_DIM))):
+        _check_arg("qkv_args", name, x, dt, shape, device)
+    if inv_freq is not None:
+        need(inv_freq.dim() == 1, "inv_freq must be float32 [rot / 2]")
+        _check_arg("qkv_args", "inv_freq", inv_freq, torch.float32, tuple(inv_freq.shape), device)
+    _check_status("qkv_args", status, device)
     # one token of one sequence has no stride between tokens; of several sequences it is theirs
     ld = qkv.stride(1) if t > 1 else qkv.stride(0) if N > 1 else qkv.shape[2] // 8 * 8
 

@@ -60,3 +60,39 @@ def test_append_takes_what_fits(cache):
     one = new((N, H, T + 4, D))[:, :, :1].contiguous()
     cache.append(one, one, stream=0)
     assert cache.calls[-1][3] == 1
+
+
+def heads(G=4, **kw):
+    """Arguments of qkv_args that fit, with those of kw in their place."""
+    d = dict(qkv=new((N, T, (G + 2) * H * D)), q_out=torch.zeros((N, T, H, G, D)), n_kv_heads=H,
+             pos=torch.zeros(N, dtype=torch.int64), inv_freq=torch.ones(D // 2), q_weight=torch.ones(D),
+             k_weight=torch.ones(D), k_out=new(), v_out=new())
+    d.update(kw)
+    return d
+
+
+def test_qkv_args_takes_what_fits():
+    pk.qkv_args(**heads())
+    pk.qkv_args(**heads(rows8=pk.Rows8(N, H, 4, 512, device="cpu"), status=torch.zeros(1, dtype=torch.int32)))
+    pk.qkv_args(**heads(status=torch.zeros(256, dtype=torch.uint8), pos=None, q_weight=None, k_out=None, v_out=None,
+                        rows8=pk.Rows8(N, H, 4, 512, device="cpu")))
+
+
+@pytest.mark.parametrize("name", ["q_out", "pos", "inv_freq", "q_weight", "k_weight", "k_out", "v_out", "status", "rows8"])
+def test_qkv_args_refuses_tensors_of_another_device(name):
+    d = heads(status=torch.zeros(1, dtype=torch.int32), rows8=pk.Rows8(N, H, 4, 512, device="cpu"))
+    if name == "rows8":
+        d["rows8"].k8 = d["rows8"].k8.to("meta")
+    else:
+        d[name] = d[name].to("meta")
+    with pytest.raises(ValueError):
+        pk.qkv_args(**d)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(inv_freq=torch.ones(D)[::2]), dict(inv_freq=torch.ones((D // 2, 1))), dict(pos=torch.zeros((N, 1), dtype=torch.int64)),
+    dict(q_weight=torch.ones(2 * D)[::2]), dict(k_out=new((N, T, H, D)).transpose(1, 2)),
+    dict(status=torch.zeros(0, dtype=torch.int32))])
+def test_qkv_args_refuses_other_tensors(kw):
+    with pytest.raises(ValueError):
+        pk.qkv_args(**heads(**kw))
