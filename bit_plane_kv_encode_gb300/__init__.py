@@ -142,7 +142,16 @@ class Rows8:
 
     @property
     def n_max(self) -> int:
+        """What the host knows the sequences' lengths to be at most.  Every
+        append adds its tokens, also one that overwrites rows (start given):
+        set it when the lengths are known to be less, or more."""
         return int(self.c.n_max)
+
+    @n_max.setter
+    def n_max(self, tokens: int):
+        if not 0 <= tokens <= self.c.cap_tokens:
+            raise ValueError(f"n_max must be 0 .. {self.c.cap_tokens}")
+        self.c.n_max = int(tokens)
 
     def append(self, k_new, v_new, start=None, status=None, stream=None):
         """Quantise k_new/v_new [N][H][t][D] bf16 (device) behind every

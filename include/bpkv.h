@@ -403,7 +403,10 @@ typedef struct bpkv_rows8 {
  * keeps its rows and its length, and BPKV_DEV_OVERFLOW is set in *status
  * (device, NULL to skip).  n_max becomes min(n_max + t_new, cap_tokens).
  * With start given its values bound nothing on the host: raise n_max yourself
- * when one is above n_max.
+ * when one is above n_max, and lower it to what you know of the lengths when
+ * rows are overwritten again and again, since each call adds t_new all the same
+ * (at cap_tokens, appending behind the rows is refused and the attention takes
+ * its way for long sequences).
  * BPKV_EINVAL when t_new < 1, t_new > cap_tokens, or (start NULL) n_max + t_new
  * > cap_tokens.
  */

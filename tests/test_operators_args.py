@@ -96,3 +96,14 @@ def test_qkv_args_refuses_tensors_of_another_device(name):
 def test_qkv_args_refuses_other_tensors(kw):
     with pytest.raises(ValueError):
         pk.qkv_args(**heads(**kw))
+
+
+def test_n_max_is_the_callers_to_set():
+    c = pk.Rows8(N, H, 4, 512, device="cpu")
+    for n in (512, 0, 77):
+        c.n_max = n
+        assert c.n_max == n == c.c.n_max
+    for n in (-1, 513):
+        with pytest.raises(ValueError):
+            c.n_max = n
+    assert c.n_max == 77
