@@ -1,4 +1,5 @@
-"""Longer uses of the serving operators: drafted tokens that are rejected."""
+"""Longer uses of the serving operators: drafted tokens that are rejected,
+prompts of many turns."""
 import pytest
 import torch
 
@@ -50,3 +51,37 @@ def test_drafted_tokens_overwritten_again_and_again(pk):
     kr, vr = c.read(0, cap)
     assert torch.equal(kr.double(), torch.where(there, want, 0.0))
     assert torch.equal(vr.double(), torch.where(there, -want, 0.0))
+
+
+@pytest.mark.parametrize("N,t,H,G,rot,pairs", [(10, 8001, 1, 1, 128, False), (5, 8001, 2, 8, 64, True),
+                                               (3, 13337, 1, 1, 18, False)])
+def test_projected_heads_of_many_turns(pk, N, t, H, G, rot, pairs):
+    """A CTA's second and third turn: more tokens than the grid's 4864 CTAs take at once, eight each."""
+    from test_gpu_rows8 import check, qkv_reference
+    assert N * t > 8 * 4864
+    g = torch.Generator(device="cuda").manual_seed(t)
+    cap = (t + 1100 + 511) // 512 * 512
+    qkv = torch.randn((N, t, (G + 2) * H * D), generator=g, device="cuda").to(torch.bfloat16)
+    pos = 1000 - 97 * torch.arange(N, device="cuda")
+    inv = (1e4 ** (-torch.arange(0, rot, 2, device="cuda").double() / rot)).float()
+    w = 1 + 0.3 * torch.randn(D, generator=g, device="cuda")
+    c, d = pk.Rows8(N, H, G, cap), pk.Rows8(N, H, G, cap)
+    for x in (c, d):
+        for y in (x.k8, x.v8, x.kexp, x.vexp):
+            y.zero_()
+    q = torch.full((N, t, H, G, D), float("nan"), device="cuda")
+    k = torch.full((N, H, t, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, float("nan"))
+    q2 = torch.empty((N, t, H, G, D), dtype=torch.bfloat16, device="cuda")
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    pk.bpkv_qkv_rope(pk.qkv_args(qkv, q, H, pos, inv, w, w, pairs=pairs, k_out=k, v_out=v))
+    pk.bpkv_qkv_rope(pk.qkv_args(qkv, q2, H, pos, inv, w, w, pairs=pairs, k_out=k2, v_out=v2, rows8=c))
+    (wq, tq), (wk, tk), wv = qkv_reference(qkv, N, t, H, G, pos, inv, w, w, 1e-6, pairs)
+    for got, want, tol in ((q, wq, tq), (q2, wq, tq), (k, wk, tk), (k2, wk, tk)):
+        check(got, want, tol)
+    assert torch.equal(v.double(), wv) and torch.equal(v2, v)
+    # into the 8-bit rows: as the append of the bf16 rows does it
+    d.append(k2, v2, pos)
+    for a, b in ((c.k8, d.k8), (c.v8, d.v8), (c.kexp, d.kexp), (c.vexp, d.vexp), (c.seq_len, d.seq_len)):
+        assert torch.equal(a, b)
+    assert torch.equal(c.seq_len, pos + t)
