@@ -1,5 +1,5 @@
 """Longer uses of the serving operators: drafted tokens that are rejected,
-prompts of many turns."""
+prompts of many turns, device lengths above the host's bound."""
 import pytest
 import torch
 
@@ -85,3 +85,30 @@ def test_projected_heads_of_many_turns(pk, N, t, H, G, rot, pairs):
     for a, b in ((c.k8, d.k8), (c.v8, d.v8), (c.kexp, d.kexp), (c.vexp, d.vexp), (c.seq_len, d.seq_len)):
         assert torch.equal(a, b)
     assert torch.equal(c.seq_len, pos + t)
+
+
+LOW = [
+    # prefix on the tensor cores; own rows behind it in whole units; the same, joined by the streaming kernel's join
+    (40, 2, 4, 900, [60001], 900, 20000), (40, 2, 4, 5000, [60001], 300, 20000), (40, 2, 4, 5600, [30001], 5000, 20000),
+    # no prefix, planned; a prefix that is streamed by 16 query rows; with several
+    (1, 2, 4, 60000, [], 40000, 0), (40, 2, 4, 700, [9001], 300, 3000), (41, 2, 8, 400, [5003, 0, 2000], 300, 1800),
+    # clusters of 8 and 2 CTAs; whole units of 8, 4 and 2 warps
+    (2, 2, 5, 9000, [7001], 2000, 3000), (9, 4, 4, 2500, [6001], 700, 1000), (20, 4, 8, 3000, [2001], 300, 1000),
+    (40, 4, 3, 3000, [900], 900, 300), (200, 4, 2, 700, [300], 300, 100),
+]
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("N,H,G,longest,plens,own_bound,prefix_bound", LOW)
+def test_lengths_above_the_hosts_bound(pk, bits, N, H, G, longest, plens, own_bound, prefix_bound):
+    """n_max chooses the way and sizes its launches; longer sequences and prefixes are attended to in full, every way."""
+    from test_gpu_shared import run_case
+    lens = [(longest - 89 * i) % (longest + 1) for i in range(N)]
+    r = run_case(pk, bits, N, H, G, lens, plens, [i % len(plens) if plens else 0 for i in range(N)])
+    r["c"].c.n_max = own_bound
+    if plens:
+        r["pc"].c.n_max = prefix_bound
+    r["out"].fill_(float("nan"))
+    r["fn"](r["pc"].c if plens else None, r["of"], r["c"].c, r["q"], r["out"], r["ws"], r["ws"].numel())
+    assert ((r["out"].double() - r["want"]).abs() <= r["tol"]).all()
+    assert pk.bpkv_read_status(r["ws"]) == 0
