@@ -6,14 +6,18 @@
 // lanes hold a head, and both channels of a rotated pair are the thread's own
 // (halves: channels 8 l .. and rot/2 + 8 l .., for rot/2 a multiple of 8; other
 // rot read the partner a second time).  The mean square is three shuffles.  A
-// CTA takes several tokens in turn; cosines and sines are worked out once for
-// all of a token's heads into shared memory, in the order in which the lanes
-// read them as 16-byte pieces without bank conflicts, and each thread's next
-// loads are issued before a head is worked on.
+// CTA takes up to eight tokens at once, a turn; cosines and sines are worked out
+// once for all of a token's heads into shared memory, in the order in which the
+// lanes read them as 16-byte pieces without bank conflicts, and each thread's
+// next loads are issued before a head is worked on.  The grid has a CTA for each
+// turn up to 4864 of them; only longer prompts give a CTA a second one.
 //
 // Angles: the position times the frequency in turns, as 64-bit fixed point
-// whose wrap-around drops whole turns, is exact however far the position; the
-// top 32 bits are the angle within half a turn to 2^-32.
+// whose wrap-around drops whole turns.  Only the frequency is rounded, down to
+// 2^-64 of a turn from a 64-bit 2^64 / (2 pi) that is cut off too: a position p
+// is off by less than |p| (1 + frequency) 2^-64 turns (2^-44 at a million, 2^-23
+// at 2^40).  The top 32 bits are the angle within half a turn to 2^-31, which a
+// float holds to 2^-24.
 //
 // Measured on a GB300 (G = 4, H = 8, normed, rotated by halves, bf16 queries):
 // a prompt of 8191 tokens (201 MB) 38.0 us, 5.3 TB/s, 74% of the issue slots in
@@ -52,7 +56,8 @@ struct QkvArgs {
 };
 
 // Turns per position of a frequency in radians, modulo one, in 2^-64 turns:
-// the frequency's 24-bit mantissa times 2^64 / (2 pi), shifted by its exponent.
+// the frequency's 24-bit mantissa times 2^64 / (2 pi), shifted by its exponent;
+// below the exact number by less than 1 + frequency.
 __device__ __forceinline__ uint64_t turns64(float inv_freq) {
   const uint32_t b = __float_as_uint(inv_freq);
   const int e = (int)((b >> 23) & 0xff);

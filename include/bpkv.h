@@ -450,8 +450,9 @@ typedef struct bpkv_qkv_args {
  * x_j^2 + eps) w_j (weight given; float32), its first rot_dim channels are
  * rotated by the angle of the token's position p = pos[i] + t,
  *   (y_a, y_b) -> (y_a cos u - y_b sin u, y_b cos u + y_a sin u), u = p inv_freq[i],
- * with the product p inv_freq[i] taken exactly and reduced to a turn in 64-bit
- * fixed point, and rounded once to its output type.  Values are copied.
+ * and rounded once to its output type.  Values are copied.  The angle is taken
+ * modulo a turn in 64-bit fixed point: it is off by less than |p| (1 +
+ * inv_freq[i]) 2^-64 turns, and by 2^-24 of half a turn for being a float32.
  * With rows8 the keys (as rounded to bf16) and values are quantised into rows
  * pos[i] .. of that cache, exactly as bpkv_rows8_append does with start = pos;
  * pos NULL or rows8->seq_len appends behind the stored tokens.  rows8 must have

@@ -112,3 +112,44 @@ def test_lengths_above_the_hosts_bound(pk, bits, N, H, G, longest, plens, own_bo
     r["fn"](r["pc"].c if plens else None, r["of"], r["c"].c, r["q"], r["out"], r["ws"], r["ws"].numel())
     assert ((r["out"].double() - r["want"]).abs() <= r["tol"]).all()
     assert pk.bpkv_read_status(r["ws"]) == 0
+
+
+def turns(p, f):
+    """p f / (2 pi) modulo one, from whole numbers of 200 bits (pi by Machin's formula)."""
+    one = 1 << 200
+
+    def arctan_of_inverse(x):
+        term, total, n = one // x, 0, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+
+    two_pi = 8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))
+    a, b = float(f).as_integer_ratio()
+    return p * a * one * one // (b * two_pi) % one / one
+
+
+@pytest.mark.parametrize("first", [1 << 31, (1 << 36) + 12345, (1 << 40) + 7, (1 << 50) + 1, -3, -(1 << 35)])
+def test_far_positions(pk, first):
+    """The angle's bound: |p| (1 + f) 2^-64 turns, the fixed point's last bit (2^-32 turns), the float's rounding (2^-25
+    half turns); then sincospi 2^-23, and the two products and the sum 3 2^-24 of |a| + |b|."""
+    import math
+    H, G, t = 1, 1, 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    qkv = torch.randn((1, t, 3 * D), generator=g, device="cuda").to(torch.bfloat16)
+    inv = (5e5 ** (-torch.arange(0, D, 2, device="cuda").double() / D)).float()
+    inv[1] = 3.0
+    q = torch.empty((1, t, H, G, D), device="cuda")
+    pk.bpkv_qkv_rope(pk.qkv_args(qkv, q, H, torch.tensor([first], device="cuda"), inv))
+    x, y = qkv[0, :, :D].double().cpu(), q[0, :, 0, 0].double().cpu()
+    for i in range(t):
+        p = first + i
+        for j, f in enumerate(inv.tolist()):
+            u = 2 * math.pi * turns(p, f)
+            a, b = float(x[i, j]), float(x[i, j + D // 2])
+            off = 2 * math.pi * (abs(p) * (1 + f) * 2.0 ** -64 + 2.0 ** -32) + math.pi * 2.0 ** -25
+            tol = (off + 2.0 ** -23 + 3 * 2.0 ** -24) * (abs(a) + abs(b))
+            assert abs(float(y[i, j]) - (a * math.cos(u) - b * math.sin(u))) <= tol
+            assert abs(float(y[i, j + D // 2]) - (b * math.cos(u) + a * math.sin(u))) <= tol
