@@ -6,7 +6,9 @@
 // memory stages, one thread issues the products, and two groups of four warps
 // do the softmax, a thread per query row: S = Q K^T (128 x 128 x 128) into
 // tensor memory, p = exp2(S - m) written back over S as the A operand of
-// O += P V, with O in tensor memory too.  The groups are two streams that take
+// O += P V, with O in tensor memory too.  p is rounded to bf16 there (2^-8),
+// since a product's operands have one type and V is bf16; S, m, O and the sum of
+// the unrounded p are float32.  The groups are two streams that take
 // turns at the tensor cores: with more than 128 rows each has its own 128 rows
 // and both take every tile; with fewer both hold the same rows and each takes
 // every other tile.  Rows that fill half or a quarter of the 128 are held twice
@@ -444,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
         // overwrites P(i - 2) only after O(i - 2) has read it.
         constexpr uint32_t kDescS = BITS == 16 ? mma_desc(1, 1, 0, kTile, kTile) : mma_desc(0, 0, 0, kTile, kTile);
         constexpr uint32_t kDescO = BITS == 16 ? mma_desc(1, 1, 1, kTile, kD) : mma_desc(1, 0, 1, kTile, kD);
-        uint32_t tile_no = 0;  // tiles before this segment
         uint32_t seg = 0, p_phase = 0;
         bool ok = true;
         uint32_t k_st = 0, k_ph = 0, v_st = 1, v_ph = 0;
@@ -524,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
               if (j + 2 >= steps) mma_commit(smem_u32(&sm.o_done[s]));
             }
           }
-          tile_no += g.tiles;
           ++seg;
         }
         // every product is complete before tensor memory is given up
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_wide(const __grid_consta
         }
       }
       if (active && copy == 0) {
-        const int64_t at = wide_row(a, g.unit, blockIdx.x) + (g.dual ? s * kTile : 0) + row;
+        const int64_t at = wide_row(g.unit, blockIdx.x) + (g.dual ? s * kTile : 0) + row;
         const int q = lane & 3;
         float* po = a.part_o + (at - q) * kD + q * 4;
 #pragma unroll 1
@@ -854,6 +854,9 @@ bool make_map(CUtensorMap* m, const void* rows, int64_t units, int64_t cap) {
 //   8 over 8000 18.7 / 25.5 (19.5 / 21.2), over 16000 32 / 29; 32 over 900 10.4 /
 //   18.4, over 2000 17.8 / 24.0; 96 over 300 15.3 / 19.3, over 900 (691200 rows)
 //   27.6 / 27.5.
+// A sequence of many units has half the bound: with one of 2000 tokens among 31
+// of 500 a call takes 19.2 / 17.7 (of 100 15.3 / 17.6, all of 2000 35 / 40; 8-bit
+// rows, of 100, 12.8 / 17.1).
 constexpr int64_t kWholeTokens = 2048, kWholeMany = 1024, kWholeRows = 600000;
 
 // Behind the wide kernel, sequences that are short enough for k_shared_unit take

@@ -9,7 +9,8 @@
 // anything else.  Products are S^T = K Q^T and O^T = V^T P^T, so that the 16
 // side of the warp-level matrix instruction holds tokens or channels and the 8
 // side the query rows: no part of a product is padding for G = 8, and P^T is
-// S^T's own registers through one 8 x 8 transpose.  The 5th-generation tensor
+// S^T's own registers through one 8 x 8 transpose.  P^T enters its product as
+// bf16 (2^-8), the type of V; its sum takes it unrounded, in float32.  The 5th-generation tensor
 // instructions take 128 rows at least, and the units here change every few
 // tiles: there a switch of unit cost 2.5 us, more than the tiles between two.
 //
@@ -526,8 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared_few(const __grid_constan
   FewPlan& plan = *reinterpret_cast<FewPlan*>(smem + S::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   // Behind the wide kernel of the same call, which starts this one only after
-  // its own wait, what that wait covered is complete: only the end waits, so
-  // that the two overlap.
+  // its own wait, what that wait covered is complete: only the end waits.  Both
+  // kernels want an SM's whole shared memory, so no two of their CTAs share one;
+  // this one's begin where the wide kernel has no CTA, or its CTA has ended.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
   make_plan(a, plan, S::kTok);

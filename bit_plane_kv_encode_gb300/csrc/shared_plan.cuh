@@ -10,8 +10,12 @@
 // kernel's tiles form one list, cut into equal stretches, one per worker; a
 // worker's part of a unit is a segment and leaves its rows' (m, l, o).  Lengths
 // are read on the device, so the cut fits ragged batches; every CTA works the
-// same plan out for itself.  Short sequences and prefixes need none of this
-// (k_shared_unit).
+// same plan out for itself.
+//
+// Where all sequences' own rows are short, there is no streaming kernel behind
+// the wide one (Args::finish): the wide kernel takes every prefix unit, also
+// those of at most kFew rows, and k_shared_unit each sequence's own rows.  Short
+// sequences and prefixes need no plan at all (k_shared_unit alone).
 #pragma once
 
 #include <atomic>
@@ -257,7 +261,7 @@ __device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 
 
 // Partial rows of segment (unit, worker): the segments in order have ascending
 // unit + worker, each its own.
-__device__ __forceinline__ int64_t wide_row(const Args& a, int64_t unit, int64_t cta) { return (unit + cta) * kPair; }
+__device__ __forceinline__ int64_t wide_row(int64_t unit, int64_t cta) { return (unit + cta) * kPair; }
 __device__ __forceinline__ int64_t few_row(const Args& a, int64_t unit, int64_t worker) {
   return a.few0 + (unit + worker) * kFew;
 }
@@ -284,7 +288,7 @@ __device__ __forceinline__ Parts parts_of(const Args& a, const P& p, int64_t r) 
     const int64_t w0 = share.owner(at), unit = (int64_t)item * a.n_heads + h;
     q.pre_n = (int)(share.owner(at + tiles - 1) - w0) + 1;
     if (is_wide) {
-      q.pre = wide_row(a, unit, w0) + in;
+      q.pre = wide_row(unit, w0) + in;
       q.pre_step = kPair;
     } else {
       q.pre = few_row(a, unit, w0) + in;
