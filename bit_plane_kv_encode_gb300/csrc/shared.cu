@@ -234,7 +234,7 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int copy,
   if (first) {
     m = top;
   } else {
-    const bool up = top > m + Range<BITS>::kLazy / kUnit;
+    const bool up = top > lazy_top<BITS>(m, Range<BITS>::kLazy / kUnit);
     if (__any_sync(0xffffffffu, up)) {
       // S of this step is complete, so O of the stream's step before it is too
       const float f = up ? ex2((m - top) * kUnit) : 1.f;
@@ -251,7 +251,7 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, int copy,
       }
     }
   }
-  const float base = m == -INFINITY ? 0.f : fmaf(m, kUnit, -Range<BITS>::kShift);
+  const float base = m == -INFINITY ? 0.f : shifted<BITS>(m, kUnit, Range<BITS>::kShift);
   const F2 base2(-base, -base), unit2(kUnit, kUnit);
   F2 ls[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll

@@ -403,7 +403,7 @@ __device__ __forceinline__ void stream(const Args& a, W& cur, W& ahead, uint32_t
         top[nb][i] = fmaxf(x[0][nb][i], x[0][nb][2 + i]);
 #pragma unroll
         for (int b = 1; b < S::kSub; ++b) top[nb][i] = fmaxf(top[nb][i], fmaxf(x[b][nb][i], x[b][nb][2 + i]));
-        up |= top[nb][i] > m[nb][i] + S::kLazy / kUnit;
+        up |= top[nb][i] > lazy_top<BITS>(m[nb][i], S::kLazy / kUnit);
       }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -430,7 +430,7 @@ __device__ __forceinline__ void stream(const Args& a, W& cur, W& ahead, uint32_t
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        base[nb][i] = m[nb][i] == -INFINITY ? 0.f : fmaf(m[nb][i], kUnit, -S::kShift);
+        base[nb][i] = m[nb][i] == -INFINITY ? 0.f : shifted<BITS>(m[nb][i], kUnit, S::kShift);
     // ---- P^T, and O^T += V^T P^T
 #pragma unroll
     for (int b = 0; b < S::kSub; ++b) {

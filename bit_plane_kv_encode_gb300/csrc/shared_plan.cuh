@@ -259,6 +259,20 @@ struct Share {
 // warps work; each copy has its own m, l and o until the segment's end.
 __device__ __forceinline__ int copies_of(int rows) { return rows <= kWideTile / 4 ? 4 : rows <= kWideTile / 2 ? 2 : 1; }
 
+// What a logit may reach before m follows it, and what is taken from the logits
+// (times unit) before exp2.  8-bit rows' weights have the range of a half: both
+// are rounded so that x <= lazy_top(m) never makes more than 2^(lazy + shift),
+// also where the logits' last bit is worth more than the shift.  bf16 weights
+// have float32's range.
+template <int BITS>
+__device__ __forceinline__ float lazy_top(float m, float lazy) {
+  return BITS == 8 ? __fadd_rd(m, lazy) : m + lazy;
+}
+template <int BITS>
+__device__ __forceinline__ float shifted(float m, float unit, float shift) {
+  return BITS == 8 ? __fadd_ru(m, -shift) : fmaf(m, unit, -shift);
+}
+
 // Partial rows of segment (unit, worker): the segments in order have ascending
 // unit + worker, each its own.
 __device__ __forceinline__ int64_t wide_row(int64_t unit, int64_t cta) { return (unit + cta) * kPair; }

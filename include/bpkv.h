@@ -483,9 +483,10 @@ int bpkv_qkv_rope(const bpkv_qkv_args *a, void *stream);
  * Logits, softmax statistics and sums are float32; the softmax weights enter
  * the products as bf16 (bpkv_shared_attend), and for bpkv_shared_attend8 as
  * halves or, on the tensor cores, as two 3-bit pieces with q as two e4m3 pieces
- * of 4 bits.  Rows past the lengths may hold anything.  Stored rows, q and
- * logits must be finite.  n_max of the caches sizes the launches and chooses
- * between the ways above; longer sequences (in a replayed graph) are attended
+ * of 4 bits.  Rows past the lengths may hold anything.  Stored rows and q must
+ * be finite, logits below 2^28 and bf16 values below 2^96 in magnitude (float32
+ * holds no weighted sums of larger ones).  n_max of the caches sizes the
+ * launches and chooses between the ways above; longer sequences (in a replayed graph) are attended
  * to in full, but take longer than they need: capture with n_max set to what
  * the lengths will reach.  Equal calls give equal bits.
  * Device memory only: BPKV_EUNSUPPORTED for residency 1, and for more than
