@@ -448,7 +448,8 @@ typedef struct bpkv_qkv_args {
  * From a layer's projections to what the caches and the attention take, in one
  * pass over the heads: every query and key head is normed, y = x / sqrt(mean_j
  * x_j^2 + eps) w_j (weight given; in float32, which holds the squares of |x_j|
- * below 2^60), its first rot_dim channels are rotated by the angle of the token's position p = pos[i] + t,
+ * below 2^60), its first rot_dim channels are rotated by the angle of the token's
+ * position p = pos[i] + t,
  *   (y_a, y_b) -> (y_a cos u - y_b sin u, y_b cos u + y_a sin u), u = p inv_freq[i],
  * and rounded once to its output type.  Values are copied.  The angle is taken
  * modulo a turn in 64-bit fixed point: it is off by less than |p| (1 +
