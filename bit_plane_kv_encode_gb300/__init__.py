@@ -14,7 +14,8 @@ from ._binding import (  # noqa: F401
     BpkvError, bpkv_alloc_depths, bpkv_cache, bpkv_calibrate_channels, bpkv_clear_status, bpkv_decode_step,
     bpkv_dense_attend, bpkv_encode_append, bpkv_fixed_depths, bpkv_read_status, bpkv_rotate, bpkv_row_cache_stats, bpkv_scan, bpkv_scan_topk, bpkv_scan_topk_noalloc, bpkv_selection_map, bpkv_selftest_wait, bpkv_sparse_attend, bpkv_sparse_attend_vdepth,
     bpkv_qkv_args, bpkv_qkv_rope, bpkv_rows8, bpkv_rows8_append, bpkv_rows8_read, bpkv_shared_attend,
-    bpkv_shared_attend8, bpkv_shared_workspace_size, bpkv_status_string, bpkv_step_args, bpkv_topk, bpkv_union, bpkv_version, bpkv_workspace_size, header_symbols, load)
+    bpkv_shared_attend8, bpkv_shared_workspace_size, bpkv_prompt_args, bpkv_prompt_attend,
+    bpkv_prompt_workspace_size, bpkv_rows8_accept, bpkv_tree_attend, bpkv_tree_attend8, bpkv_status_string, bpkv_step_args, bpkv_topk, bpkv_union, bpkv_version, bpkv_workspace_size, header_symbols, load)
 
 HEAD_DIM = 128
 WS_SCAN_TOPK, WS_ATTEND, WS_DENSE, WS_STEP = 1, 2, 4, 8
@@ -167,6 +168,21 @@ class Rows8:
         _check_status("Rows8.append", status, device)
         bpkv_rows8_append(self.c, k_new, v_new, t, start, status, stream)
 
+    def accept(self, k_new, v_new, start, count, path=None, status=None, stream=None):
+        """Of k_new/v_new [N][H][t][D] bf16 (device) keep tokens path[i][j], j < count[i] (int32 [N][t], None: the
+        first count[i]; int32 [N]), quantised into rows start[i] + j (int64 [N]); the lengths become start + count."""
+        import torch
+        device = self.k8.device
+        t = k_new.shape[2] if k_new.dim() == 4 else 0
+        N = self.c.n_seq
+        shape = (N, self.c.n_kv_heads, t, HEAD_DIM)
+        for name, x, dt, want in (("k_new", k_new, torch.bfloat16, shape), ("v_new", v_new, torch.bfloat16, shape),
+                                  ("start", start, torch.int64, (N,)), ("count", count, torch.int32, (N,)),
+                                  ("path", path, torch.int32, (N, t))):
+            _check_arg("Rows8.accept", name, x, dt, want, device)
+        _check_status("Rows8.accept", status, device)
+        bpkv_rows8_accept(self.c, k_new, v_new, t, start, path, count, status, stream)
+
     def read(self, t0: int, n: int, stream=None):
         """(K, V) rows t0 .. t0 + n - 1 of every sequence, bf16 [N][H][n][D]; zeros past its length."""
         import torch
@@ -234,6 +250,82 @@ def shared_workspace(cache, prefix=None):
     return ws
 
 
+def prompt_args(q, out, q_start, k=None, v=None, cache=None):
+    """bpkv_prompt_args for q [T][H][G][D] bf16 (a token's heads dense, any stride between tokens) and out of the same
+    shape, dense; q_start [N + 1] int64.  k, v: bf16 [T][H][D] (a token's heads dense, any stride between tokens), or
+    each sequence's [H][t][D] one behind the other as [T H][D], or [N][H][t][D] for equal lengths; or cache: a Cache or
+    Rows8 whose sequences end in the new tokens.  All on one device.  The struct keeps the tensors it points to alive."""
+    import torch
+
+    def need(ok, what):
+        if not ok:
+            raise ValueError(f"prompt_args: {what}")
+
+    need(q.dim() == 4 and q.shape[3] == HEAD_DIM and q.dtype == torch.bfloat16, "q must be bf16 [T][H][G][D]")
+    T, H, G = q.shape[:3]
+    N = q_start.shape[0] - 1 if q_start.dim() == 1 else 0
+    device = q.device
+    need(T > 0 and N > 0, "no tokens, or no sequences")
+    need(_dense_from(q, 1), "a token's heads of q must be dense")
+    _check_arg("prompt_args", "out", out, torch.bfloat16, (T, H, G, HEAD_DIM), device)
+    _check_arg("prompt_args", "q_start", q_start, torch.int64, (N + 1,), device)
+    need((k is None) == (v is None) and (k is None) != (cache is None), "either k and v or cache")
+    ld = [0, 0]
+    if cache is not None:
+        c = cache.c
+        need((c.n_seq, c.n_kv_heads, c.group) == (N, H, G), "the cache's sequences and heads")
+        need((cache.k8 if isinstance(cache, Rows8) else cache.seq_len).device == device, "tensors on several devices")
+    else:
+        need(k.dim() == v.dim(), "k and v laid out alike")
+        for i, (name, x) in enumerate((("k", k), ("v", v))):
+            if x.dim() == 3:
+                need(x.shape == (T, H, HEAD_DIM) and x.dtype == torch.bfloat16 and x.device == device
+                     and _dense_from(x, 1), f"{name} must be bf16 [T][H][D], a token's heads dense, on {device}")
+                ld[i] = x.stride(0) if T > 1 else H * HEAD_DIM
+            else:
+                shape = (T * H, HEAD_DIM) if x.dim() == 2 else (N, H, T // N, HEAD_DIM)
+                need(x.dim() == 2 or T % N == 0, "k and v of equal lengths")
+                _check_arg("prompt_args", name, x, torch.bfloat16, shape, device)
+    a = bpkv_prompt_args(N, H, G, HEAD_DIM, T, q_start.data_ptr(), q.data_ptr(),
+                         q.stride(0) if T > 1 else H * G * HEAD_DIM, out.data_ptr(),
+                         None if k is None else k.data_ptr(), None if v is None else v.data_ptr(), ld[0], ld[1],
+                         ctypes.pointer(cache.c) if isinstance(cache, Cache) else None,
+                         ctypes.pointer(cache.c) if isinstance(cache, Rows8) else None)
+    a.keep = (q, out, q_start, k, v, cache)
+    return a
+
+
+def _dense_from(x, dim):
+    """Whether x's dimensions from dim on are dense (those of size 1 have no stride)."""
+    n = 1
+    for size, stride in zip(reversed(x.shape[dim:]), reversed(x.stride()[dim:])):
+        if size != 1 and stride != n:
+            return False
+        n *= size
+    return True
+
+
+def _prompt_workspace(n_new, group, device):
+    import torch
+    n = bpkv_prompt_workspace_size(n_new, group)
+    if n == 0:
+        raise BpkvError("bpkv_prompt_workspace_size", -4)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def prompt_workspace(args):
+    """Workspace (uint8, device) of bpkv_prompt_attend for these arguments; its status word is clear."""
+    return _prompt_workspace(args.n_tokens, args.group, args.keep[0].device)
+
+
+def tree_workspace(cache, t: int):
+    """Workspace (uint8, device) of bpkv_tree_attend / bpkv_tree_attend8 for trees of t nodes over a Cache or Rows8;
+    its status word is clear."""
+    return _prompt_workspace(t, cache.c.group, cache.device)
+
+
 def cache_array(caches):
     """ctypes array of the bpkv_cache structs of several layers (for bpkv_decode_step)."""
     arr = (bpkv_cache * len(caches))(*[c.c for c in caches])
@@ -246,5 +338,5 @@ def sync_n_max(caches, arr):
         c.c.n_max = s.n_max
 
 
-__all__ = [n for n in dir() if n.startswith("bpkv_")] + ["Cache", "Rows8", "cache_array", "qkv_args", "shared_workspace", "sync_n_max", "BpkvError"]
+__all__ = [n for n in dir() if n.startswith("bpkv_")] + ["Cache", "Rows8", "cache_array", "prompt_args", "prompt_workspace", "qkv_args", "shared_workspace", "sync_n_max", "tree_workspace", "BpkvError"]
 _ = ctypes

@@ -61,6 +61,14 @@ class bpkv_qkv_args(ctypes.Structure):
     ]
 
 
+class bpkv_prompt_args(ctypes.Structure):
+    _fields_ = [
+        ("n_seq", i32), ("n_kv_heads", i32), ("group", i32), ("head_dim", i32), ("n_tokens", i64), ("q_start", P),
+        ("q", P), ("ld_q", i64), ("out", P), ("k", P), ("v", P), ("ld_k", i64), ("ld_v", i64),
+        ("cache", ctypes.POINTER(bpkv_cache)), ("rows8", ctypes.POINTER(bpkv_rows8)),
+    ]
+
+
 _SIGS = {
     "bpkv_version": ([], i32),
     "bpkv_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -90,6 +98,11 @@ _SIGS = {
     "bpkv_shared_workspace_size": ([i32, i32, i32, i32], sz),
     "bpkv_shared_attend": ([P, P, P, P, P, P, sz, P], ctypes.c_int),
     "bpkv_shared_attend8": ([P, P, P, P, P, P, sz, P], ctypes.c_int),
+    "bpkv_prompt_workspace_size": ([i64, i32], sz),
+    "bpkv_prompt_attend": ([P, P, sz, P], ctypes.c_int),
+    "bpkv_tree_attend": ([P, i32, P, P, P, P, sz, P], ctypes.c_int),
+    "bpkv_tree_attend8": ([P, i32, P, P, P, P, sz, P], ctypes.c_int),
+    "bpkv_rows8_accept": ([P, P, P, i32, P, P, P, P, P], ctypes.c_int),
 }
 
 _lib = None
@@ -329,3 +342,30 @@ def bpkv_shared_attend8(prefix, prefix_of, cache, q, out, ws, ws_bytes: int, str
                   load().bpkv_shared_attend8(None if prefix is None else ctypes.byref(prefix), _ptr(prefix_of),
                                              ctypes.byref(cache), _ptr(q), _ptr(out), _ptr(ws), int(ws_bytes),
                                              _stream(stream)))
+
+
+def bpkv_prompt_workspace_size(n_new: int, group: int) -> int:
+    return int(load().bpkv_prompt_workspace_size(int(n_new), int(group)))
+
+
+def bpkv_prompt_attend(args, ws, ws_bytes: int, stream=None):
+    return _check("bpkv_prompt_attend",
+                  load().bpkv_prompt_attend(ctypes.byref(args), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def bpkv_tree_attend(cache, t: int, tree, q, out, ws, ws_bytes: int, stream=None):
+    return _check("bpkv_tree_attend",
+                  load().bpkv_tree_attend(ctypes.byref(cache), int(t), _ptr(tree), _ptr(q), _ptr(out), _ptr(ws),
+                                          int(ws_bytes), _stream(stream)))
+
+
+def bpkv_tree_attend8(cache, t: int, tree, q, out, ws, ws_bytes: int, stream=None):
+    return _check("bpkv_tree_attend8",
+                  load().bpkv_tree_attend8(ctypes.byref(cache), int(t), _ptr(tree), _ptr(q), _ptr(out), _ptr(ws),
+                                           int(ws_bytes), _stream(stream)))
+
+
+def bpkv_rows8_accept(c, k_new, v_new, t: int, start, path, count, status=None, stream=None):
+    return _check("bpkv_rows8_accept",
+                  load().bpkv_rows8_accept(ctypes.byref(c), _ptr(k_new), _ptr(v_new), int(t), _ptr(start), _ptr(path),
+                                           _ptr(count), _ptr(status), _stream(stream)))

@@ -55,6 +55,15 @@ cudaError_t launch_shared(const bpkv_cache* prefix, const int32_t* prefix_of, co
                           uint16_t* out, void* ws, cudaStream_t st);
 cudaError_t launch_shared8(const bpkv_rows8* prefix, const int32_t* prefix_of, const bpkv_rows8& c, const uint16_t* q,
                            uint16_t* out, void* ws, cudaStream_t st);
+cudaError_t launch_rows8_accept(const bpkv_rows8& c, const uint16_t* k_new, const uint16_t* v_new, int32_t t,
+                                const int64_t* start, const int32_t* path, const int32_t* count, int32_t* status,
+                                cudaStream_t st);
+size_t prompt_bytes(int64_t n_new, int64_t group);
+cudaError_t launch_prompt(const bpkv_prompt_args& a, void* ws, cudaStream_t st);
+cudaError_t launch_tree(const bpkv_cache& c, int32_t t, const uint64_t* mask, const uint16_t* q, uint16_t* out, void* ws,
+                        cudaStream_t st);
+cudaError_t launch_tree8(const bpkv_rows8& c, int32_t t, const uint64_t* mask, const uint16_t* q, uint16_t* out, void* ws,
+                         cudaStream_t st);
 
 namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -468,6 +477,41 @@ int check_shared(const A* prefix, const int32_t* prefix_of, const A& c, const ui
   return overlap(q, bytes, out, bytes) ? BPKV_EINVAL : BPKV_OK;
 }
 
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // a tile's coordinates and what is added to them are 32 bits
+constexpr int64_t kMaxLd = (int64_t)1 << 32;
+
+int32_t residency(const bpkv_cache& c) { return c.residency; }
+int32_t residency(const bpkv_rows8&) { return 0; }
+
+template <typename A>
+int check_prompt_rows(const A& c) {
+  if (residency(c) != 0 || c.n_seq > BPKV_SHARED_MAX_SEQ || c.cap_tokens > kMaxTokens ||
+      (int64_t)c.n_seq * c.n_kv_heads > kMaxTokens)
+    return BPKV_EUNSUPPORTED;
+  return BPKV_OK;
+}
+
+bool overlaps_rows(const bpkv_cache& c, const void* out, int64_t bytes) {
+  const int64_t n = (int64_t)c.n_seq * c.n_kv_heads * c.cap_tokens * kD * 2;
+  return overlap(c.k_rows, n, out, bytes) || overlap(c.v_rows, n, out, bytes);
+}
+bool overlaps_rows(const bpkv_rows8& c, const void* out, int64_t bytes) {
+  const int64_t n = (int64_t)c.n_seq * c.n_kv_heads * c.cap_tokens;
+  return overlap(c.k8, n * kD, out, bytes) || overlap(c.v8, n * kD, out, bytes) || overlap(c.kexp, n, out, bytes) ||
+         overlap(c.vexp, n, out, bytes);
+}
+
+template <typename A>
+int check_tree(const A& c, int32_t t, const uint64_t* tree, const uint16_t* q, const uint16_t* out, const void* ws,
+               size_t ws_bytes) {
+  if (t < 1 || t > 64 || !q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(tree, 8)) return BPKV_EINVAL;
+  BPKV_TRY(check_prompt_rows(c));
+  const int64_t bytes = (int64_t)c.n_seq * t * c.n_kv_heads * c.group * kD * 2;
+  if (overlap(q, bytes, out, bytes) || overlaps_rows(c, out, bytes)) return BPKV_EINVAL;
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < prompt_bytes(t, c.group)) return BPKV_ENOWORKSPACE;
+  return BPKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -487,6 +531,77 @@ int bpkv_shared_attend8(const bpkv_rows8* prefix, const int32_t* prefix_of, cons
   if (prefix) BPKV_TRY(check_rows8(prefix));
   BPKV_TRY(check_shared(prefix, prefix_of, *c, q, out, ws, ws_bytes));
   return cuda_status(launch_shared8(prefix, prefix_of, *c, q, out, ws, as_stream(stream)));
+}
+
+int bpkv_rows8_accept(bpkv_rows8* c, const uint16_t* k_new, const uint16_t* v_new, int32_t t, const int64_t* start,
+                      const int32_t* path, const int32_t* count, int32_t* status, void* stream) {
+  BPKV_TRY(check_rows8(c));
+  if (t < 1 || t > c->cap_tokens || !k_new || !v_new || !start || !count || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+      !aligned(start, 8) || !aligned(path, 4) || !aligned(count, 4) || !aligned(status, 4))
+    return BPKV_EINVAL;
+  if (start == c->seq_len && c->n_max + t > c->cap_tokens) return BPKV_EINVAL;
+  if (!rows_in_range(c->n_seq, c->n_kv_heads, t)) return BPKV_EUNSUPPORTED;
+  BPKV_TRY(cuda_status(launch_rows8_accept(*c, k_new, v_new, t, start, path, count, status, as_stream(stream))));
+  c->n_max = min64(c->n_max + t, c->cap_tokens);
+  return BPKV_OK;
+}
+
+size_t bpkv_prompt_workspace_size(int64_t n_new, int32_t group) {
+  if (n_new < 1 || n_new > kMaxTokens || group < 1 || group > BPKV_MAX_GROUP) return 0;
+  return prompt_bytes(n_new, group);
+}
+
+int bpkv_prompt_attend(const bpkv_prompt_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a) return BPKV_EINVAL;
+  if (a->head_dim != kD) return BPKV_EUNSUPPORTED;
+  const int64_t N = a->n_seq, H = a->n_kv_heads, G = a->group, T = a->n_tokens;
+  if (N < 1 || H < 1 || G < 1 || G > BPKV_MAX_GROUP || T < 1) return BPKV_EINVAL;
+  if (N > BPKV_SHARED_MAX_SEQ || H > 65535 || T > kMaxTokens || T * H > kMaxTokens) return BPKV_EUNSUPPORTED;
+  if (!a->q_start || !a->q || !a->out || !aligned(a->q_start, 8) || !aligned(a->q, 16) || !aligned(a->out, 16))
+    return BPKV_EINVAL;
+  if (a->ld_q % 8 != 0 || a->ld_q < H * G * kD) return BPKV_EINVAL;
+  const bool own = a->k || a->v;
+  if (own + (a->cache != nullptr) + (a->rows8 != nullptr) != 1) return BPKV_EINVAL;
+  // what a tensor's address arithmetic and a tile's strides hold
+  if (a->ld_q > kMaxLd || a->ld_k > kMaxLd || a->ld_v > kMaxLd) return BPKV_EUNSUPPORTED;
+  const int64_t out = T * H * G * kD * 2;
+  if (overlap(a->q, ((T - 1) * a->ld_q + H * G * kD) * 2, a->out, out)) return BPKV_EINVAL;
+  if (own) {
+    if (!a->k || !a->v || !aligned(a->k, 16) || !aligned(a->v, 16)) return BPKV_EINVAL;
+    if ((a->ld_k == 0) != (a->ld_v == 0)) return BPKV_EINVAL;
+    for (int64_t ld : {a->ld_k, a->ld_v})
+      if (ld % 8 != 0 || (ld != 0 && ld < H * kD)) return BPKV_EINVAL;
+    const int64_t row = H * kD;
+    for (int kv = 0; kv < 2; ++kv) {
+      const int64_t ld = kv ? a->ld_v : a->ld_k;
+      if (overlap(kv ? a->v : a->k, ((T - 1) * (ld ? ld : row) + row) * 2, a->out, out)) return BPKV_EINVAL;
+    }
+  } else {
+    const bool wide = a->cache != nullptr;
+    BPKV_TRY(wide ? check_cache(a->cache) : check_rows8(a->rows8));
+    const int32_t n = wide ? a->cache->n_seq : a->rows8->n_seq, h = wide ? a->cache->n_kv_heads : a->rows8->n_kv_heads,
+                  g = wide ? a->cache->group : a->rows8->group;
+    if (n != a->n_seq || h != a->n_kv_heads || g != a->group) return BPKV_EINVAL;
+    BPKV_TRY(wide ? check_prompt_rows(*a->cache) : check_prompt_rows(*a->rows8));
+    if (wide && overlaps_rows(*a->cache, a->out, out)) return BPKV_EINVAL;
+    if (!wide && overlaps_rows(*a->rows8, a->out, out)) return BPKV_EINVAL;
+  }
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < prompt_bytes(T, G)) return BPKV_ENOWORKSPACE;
+  return cuda_status(launch_prompt(*a, ws, as_stream(stream)));
+}
+
+int bpkv_tree_attend(const bpkv_cache* c, int32_t t, const uint64_t* tree, const uint16_t* q, uint16_t* out, void* ws,
+                     size_t ws_bytes, void* stream) {
+  BPKV_TRY(check_cache(c));
+  BPKV_TRY(check_tree(*c, t, tree, q, out, ws, ws_bytes));
+  return cuda_status(launch_tree(*c, t, tree, q, out, ws, as_stream(stream)));
+}
+
+int bpkv_tree_attend8(const bpkv_rows8* c, int32_t t, const uint64_t* tree, const uint16_t* q, uint16_t* out, void* ws,
+                      size_t ws_bytes, void* stream) {
+  BPKV_TRY(check_rows8(c));
+  BPKV_TRY(check_tree(*c, t, tree, q, out, ws, ws_bytes));
+  return cuda_status(launch_tree8(*c, t, tree, q, out, ws, as_stream(stream)));
 }
 
 int bpkv_decode_step(bpkv_cache* layers, int32_t n_layers, const bpkv_step_args* a, void* ws, size_t ws_bytes,

@@ -1,0 +1,235 @@
+// How the attention of several new tokens a sequence (bpkv_prompt_attend,
+// bpkv_tree_attend, bpkv_tree_attend8) is laid out: units, tiles, the cut of the
+// tiles over CTAs, and the shared memory of its kernel.
+//
+// A unit is a run of a sequence's new tokens with the G query heads of one KV
+// head, at most two streams of 128 rows (token by token, head by head, whole
+// tokens only: 2 floor(128 / G) tokens), over the keys that its last token sees,
+// in tiles of 128.  The units in order (sequence, KV head, run) form one list;
+// a unit counts its tiles and kOver more for its start and end.  The list is cut
+// into equal stretches, one per CTA; a unit that a cut goes through leaves partial
+// rows (m, l, o) in two slots a CTA has, one for a unit that began before it and
+// one for a unit that goes on behind it, and k_prompt_join joins them in order.
+// Where units are short they are not cut: each counts one.
+//
+// Lengths are read on the device; every CTA works the cut out for itself.
+#pragma once
+
+#include "shared_plan.cuh"
+
+namespace bpkv {
+namespace prompt {
+
+using shared::quot;
+
+constexpr int kTile = 128;      // keys of a tile, rows of a stream
+constexpr int kRows = 256;      // rows of a unit at most
+constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
+constexpr int kSms = 152;
+constexpr int kSoftmaxWarps = 8;
+// What a unit's start and end cost, in tiles: its rows of q, the first S and the
+// last O, that nothing of its own overlaps.
+constexpr int kOver = 2;
+
+enum Rows : int32_t { kToken, kSeq, kCache };  // where keys and values lie
+
+// What the CTA that a cut unit begins in leaves for the join.
+struct Cut {
+  int64_t token;   // first token of the unit in q
+  int32_t h;       // KV head
+  int32_t tokens;
+  int32_t pieces;  // 0: this CTA's last unit is whole
+  int32_t pad;
+};
+
+struct Args {
+  const int64_t* q_start;  // NULL: sequence i has the tokens i t .. (i + 1) t - 1
+  const int64_t* len;      // rows of each sequence of a cache; NULL: the keys are those of the new tokens
+  const uint64_t* tree;    // NULL: causal
+  uint16_t* out;
+  const uint8_t* exps[2];  // scale exponents of 8-bit rows
+  int64_t cap, tokens;     // rows a sequence of the cache can have; tokens of q
+  int32_t n_seq, n_heads, group, t;
+  int32_t rows;            // Rows
+  int32_t run;             // tokens of a stream: 128 / G
+  uint32_t group_inv;      // 2^16 / group rounded up: x group_inv >> 16 is x / group for x below 256
+  int32_t split;           // units may be cut
+  int32_t slot_rows;       // rows of a slot of partial rows
+  float* part_o;           // [slots][slot_rows][D]
+  float2* part_ml;         // [slots][slot_rows] maximum (log2 domain) and sum
+  Cut* cuts;               // [CTAs]
+  int32_t* status;
+};
+
+struct Plan {
+  int64_t cum[kMaxSeq + 1];   // what the sequences before count together
+  int32_t start[kMaxSeq];     // a sequence's first token in q
+  int32_t n[kMaxSeq];         // its new tokens
+  int32_t off[kMaxSeq];       // keys before the first of them (negative: that many of them have none)
+  // where this CTA's stretch begins
+  int32_t seq, h, run;
+  int32_t pad;
+  int64_t at, left;           // within that unit, and the stretch's length
+  int64_t total, ctas;
+};
+
+// Runs of a sequence, keys and tiles of its run b.
+__device__ __forceinline__ int runs_of(const Args& a, int t) { return (t + 2 * a.run - 1) / (2 * a.run); }
+__device__ __forceinline__ int tiles_of(const Args& a, int t, int off, int b) {
+  const int last = a.tree ? t : min(t, (b + 1) * 2 * a.run);
+  return max(1, (off + last + kTile - 1) >> 7);
+}
+__device__ __forceinline__ int count_of(const Args& a, int tiles) { return a.split ? tiles + kOver : 1; }
+
+// All threads of the CTA; ends with a barrier.
+__device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, N = a.n_seq;
+  for (int i = tid; i < N; i += nt) {
+    const int64_t lo = a.q_start ? max64(0, min64(a.q_start[i], a.tokens)) : (int64_t)i * a.t;
+    const int64_t hi = a.q_start ? max64(lo, min64(a.q_start[i + 1], a.tokens)) : lo + a.t;
+    const int64_t len = a.len ? shared::tokens_of(a.len[i], a.cap) : hi - lo;
+    p.start[i] = (int32_t)lo;
+    p.n[i] = (int32_t)(hi - lo);
+    p.off[i] = (int32_t)(len - (hi - lo));
+  }
+  __syncthreads();
+  for (int i = warp; i < N; i += nt / 32) {
+    const int t = p.n[i], off = p.off[i], runs = runs_of(a, t);
+    int64_t sum = 0;
+    for (int b = lane; b < runs; b += 32) sum += count_of(a, tiles_of(a, t, off, b));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) p.cum[i] = sum * a.n_heads;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    shared::warp_sums(p.cum, N);
+    __syncwarp();
+    const int64_t total = p.cum[N], ctas = min64(gridDim.x, total), c = blockIdx.x;
+    int64_t lo = 0, hi = 0, at = 0;
+    int seq = 0, h = 0, b = 0;
+    if (c < ctas) {
+      lo = quot(c * total, ctas);
+      hi = quot((c + 1) * total, ctas);
+      int x = 0, y = N - 1;  // the last sequence that begins at or before lo: empty ones end where they begin
+      while (x < y) {
+        const int mid = (x + y + 1) / 2;
+        if (p.cum[mid] <= lo) x = mid;
+        else y = mid - 1;
+      }
+      seq = x;
+      const int64_t per = quot(p.cum[seq + 1] - p.cum[seq], a.n_heads);
+      h = (int)quot(lo - p.cum[seq], per);
+      at = lo - p.cum[seq] - h * per;
+      const int t = p.n[seq], off = p.off[seq];
+      for (;; b += 32) {  // 32 runs at a time
+        const int64_t n = count_of(a, tiles_of(a, t, off, b + lane));
+        int64_t sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += u;
+        }
+        const uint32_t in = __ballot_sync(0xffffffffu, at < sum);
+        if (in) {
+          const int k = __ffs(in) - 1;
+          at -= __shfl_sync(0xffffffffu, sum - n, k);
+          b += k;
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, sum, 31);
+      }
+    }
+    if (lane == 0) {
+      p.seq = seq;
+      p.h = h;
+      p.run = b;
+      p.at = at;
+      p.left = hi - lo;
+      p.total = total;
+      p.ctas = ctas;
+    }
+  }
+  __syncthreads();
+}
+
+// One CTA's part of a unit.
+struct Segment {
+  int32_t seq, h;
+  int32_t token;    // the unit's first in q
+  int32_t first;    // and in its sequence
+  int32_t tokens;   // of the unit
+  bool dual;        // two streams of rows, each over every tile; else one that both hold, every other tile each
+  int32_t tile0, tiles;
+  bool whole;       // all of the unit's tiles
+  int32_t pieces;   // of a unit that begins here and goes on, else 0
+  int32_t t, off;   // of the sequence
+  __device__ int steps() const { return dual ? 2 * tiles : tiles; }
+  __device__ int steps_of(int s) const { return dual ? tiles : (tiles + 1 - s) / 2; }
+  __device__ int tile_of(int s, int j) const { return tile0 + (dual ? j : 2 * j + s); }
+  // the segment's slot of partial rows
+  __device__ int slot() const { return 2 * blockIdx.x + (tile0 == 0); }
+};
+
+// Walks the segments of one CTA; every role of the CTA walks alike.  Kept in shared
+// memory, a warp's own: registers are short.
+struct Walk {
+  int64_t at, left;
+  int32_t seq, h, run;
+  Segment g;
+  __device__ void begin(const Plan& p) {
+    at = p.at;
+    left = p.left;
+    seq = p.seq;
+    h = p.h;
+    run = p.run;
+  }
+  __device__ bool next(const Plan& p, const Args& a) {
+    Segment s;
+    while (left > 0) {
+      while (p.n[seq] == 0) ++seq;  // what is left lies in a sequence further on
+      const int t = p.n[seq], off = p.off[seq], n = tiles_of(a, t, off, run), count = count_of(a, n);
+      const int64_t take = min64(left, count - at), done = p.left - left;
+      s.seq = seq;
+      s.h = h;
+      s.t = t;
+      s.off = off;
+      s.first = run * 2 * a.run;
+      s.token = p.start[seq] + s.first;
+      s.tokens = min(t - s.first, 2 * a.run);
+      s.dual = s.tokens > a.run;
+      s.pieces = 0;
+      s.tile0 = 0;
+      s.tiles = n;
+      if (a.split) {
+        s.tile0 = (int)min64(at, n);
+        s.tiles = (int)min64(at + take, n) - s.tile0;
+      }
+      s.whole = s.tiles == n;
+      if (!s.whole && s.tile0 == 0) {
+        // the CTA that has the unit's last tile
+        const int64_t last = quot(blockIdx.x * p.total, p.ctas) + done + n - 1;
+        s.pieces = (int)(quot((last + 1) * p.ctas - 1, p.total) - blockIdx.x) + 1;
+      }
+      left -= take;
+      at += take;
+      if (at == count) {
+        at = 0;
+        if (s.first + 2 * a.run < t) {
+          ++run;
+        } else {
+          run = 0;
+          if (++h == a.n_heads) h = 0, ++seq;
+        }
+      }
+      if (s.tiles > 0) {
+        g = s;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+}  // namespace prompt
+}  // namespace bpkv

@@ -129,6 +129,106 @@ cudaError_t launch_rows8_append(const bpkv_rows8& c, const uint16_t* k_new, cons
   return launch_rows8_bump(c, t_new, st);
 }
 
+struct AcceptArgs {
+  Rows8Out c;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  const int64_t* start;
+  const int32_t* path;   // NULL: token j itself
+  const int32_t* count;
+  int32_t* status;
+  int32_t n_seq, n_heads, t;
+  int32_t bump;  // the lengths are set by a launch of their own
+};
+
+__device__ __forceinline__ bool accept_fits(int64_t start, int32_t count, int32_t t, int64_t cap) {
+  return count >= 0 && count <= t && rows8_fits(start, count, cap);
+}
+
+// As k_rows8_append, but of a sequence's t tokens only the first count rows are
+// there, and each goes by way of the path: one more dependent load before the
+// row's own, which the R rows of a group take together.
+template <int R>
+__global__ void __launch_bounds__(kR8Threads) k_rows8_accept(const __grid_constant__ AcceptArgs a) {
+  pdl_enter();
+  __shared__ uint8_t s_exp[2][kR8Groups * R];
+  __shared__ int64_t s_dst[kR8Groups * R];  // -1: not written
+  const int tid = threadIdx.x, l16 = tid & 15, grp = tid >> 4;
+  const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.t, r0 = (int64_t)blockIdx.x * (kR8Groups * R);
+  int64_t from[R], dst[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + i * kR8Groups + grp;
+    from[i] = dst[i] = -1;
+    if (r < rows) {
+      int64_t unit, j, s, h;
+      split(r, a.t, unit, j);
+      split(unit, a.n_heads, s, h);
+      const int64_t p = a.start[s];
+      const int32_t n = a.count[s];
+      const int32_t node = a.path ? a.path[s * a.t + j] : (int32_t)j;
+      const bool fits = accept_fits(p, n, a.t, a.c.cap);
+      const bool there = fits && j < n, known = node >= 0 && node < a.t;
+      if (there) {
+        from[i] = unit * a.t + min(max(node, 0), a.t - 1);
+        dst[i] = unit * a.c.cap + p + j;
+      }
+      if (l16 == 0 && h == 0) {
+        if ((there && !known) || (j == 0 && !fits)) set_status(a.status, BPKV_DEV_OVERFLOW);
+        if (j == 0 && fits && !a.bump) a.c.seq_len[s] = p + n;
+      }
+    }
+    if (l16 == 0) s_dst[i * kR8Groups + grp] = dst[i];
+  }
+  uint4 w[R][2];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+    if (from[i] >= 0) {
+      w[i][0] = __ldg(reinterpret_cast<const uint4*>(a.k_new + from[i] * kD + l16 * 8));
+      w[i][1] = __ldg(reinterpret_cast<const uint4*>(a.v_new + from[i] * kD + l16 * 8));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int ke = row_exponent(w[i][0]), ve = row_exponent(w[i][1]);
+    if (l16 == 0) {
+      s_exp[0][i * kR8Groups + grp] = (uint8_t)(ke + kExpBias);
+      s_exp[1][i * kR8Groups + grp] = (uint8_t)(ve + kExpBias);
+    }
+    if (dst[i] >= 0) {
+      *reinterpret_cast<uint2*>(a.c.k8 + dst[i] * kD + l16 * 8) = row_codes(w[i][0], ke);
+      *reinterpret_cast<uint2*>(a.c.v8 + dst[i] * kD + l16 * 8) = row_codes(w[i][1], ve);
+    }
+  }
+  __syncthreads();
+  if (tid < 2 * kR8Groups * R) {
+    const int kv = tid / (kR8Groups * R), x = tid % (kR8Groups * R);
+    if (s_dst[x] >= 0) (kv ? a.c.vexp : a.c.kexp)[s_dst[x]] = s_exp[kv][x];
+  }
+}
+
+// Lengths that are also the starts, once every CTA has read them.
+__global__ void k_rows8_accept_len(const __grid_constant__ AcceptArgs a) {
+  pdl_enter();
+  const int s = blockIdx.x * blockDim.x + threadIdx.x;
+  if (s < a.n_seq && accept_fits(a.c.seq_len[s], a.count[s], a.t, a.c.cap)) a.c.seq_len[s] += a.count[s];
+}
+
+cudaError_t launch_rows8_accept(const bpkv_rows8& c, const uint16_t* k_new, const uint16_t* v_new, int32_t t,
+                                const int64_t* start, const int32_t* path, const int32_t* count, int32_t* status,
+                                cudaStream_t st) {
+  const int64_t rows = (int64_t)c.n_seq * c.n_kv_heads * t;
+  const bool many = many_rows(rows), bump = start == c.seq_len;
+  const int per = kR8Groups * (many ? kR8Many : 1);
+  const AcceptArgs a{{c.k8, c.v8, c.kexp, c.vexp, c.seq_len, c.cap_tokens}, k_new, v_new, start, path, count, status,
+                     c.n_seq, c.n_kv_heads, t, bump ? 1 : 0};
+  const cudaError_t e = launch_pdl(many ? k_rows8_accept<kR8Many> : k_rows8_accept<1>,
+                                   dim3((unsigned)((rows + per - 1) / per)), dim3(kR8Threads), 0, st, a);
+  if (e != cudaSuccess || !bump) return e;
+  return launch_pdl(k_rows8_accept_len, dim3((c.n_seq + 127) / 128), dim3(128), 0, st, a);
+}
+
 struct ReadArgs {
   const uint8_t* codes[2];
   const uint8_t* exps[2];

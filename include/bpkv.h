@@ -505,6 +505,88 @@ int bpkv_shared_attend(const bpkv_cache *prefix, const int32_t *prefix_of, const
 int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, const bpkv_rows8 *c, const uint16_t *q,
                         uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------- several new tokens at once */
+/*
+ * Attention of several new tokens of each sequence: with D = 128 and logits
+ * q . k / sqrt(D), every query head attends over the keys that its token sees,
+ *   o = sum_x softmax_x(q . k_x / sqrt(D)) v_x,
+ * zeros where a token sees none.  Logits, softmax statistics and sums are
+ * float32; the softmax weights enter the products as bf16.  8-bit rows count as
+ * the values they stand for.  A sequence's keys, values and rows of q must be
+ * finite, logits below 2^28 and values below 2^96 in magnitude; what lies past
+ * its rows, and other sequences, may hold anything.  Equal calls give equal bits.
+ * At most BPKV_SHARED_MAX_SEQ sequences, 2^30 tokens, rows of a sequence or rows
+ * of H T keys (BPKV_EUNSUPPORTED for more, and for residency 1).
+ * Workspace: bpkv_prompt_workspace_size bytes for the largest number of new
+ * tokens that one sequence of the call may have, 256-byte aligned, with nothing
+ * kept in it from call to call (calls that may run at the same time need one
+ * each); its first 256 bytes hold the status word (BPKV_DEV_TIMEOUT when a wait
+ * inside the kernel gave up; clear it first).
+ */
+size_t bpkv_prompt_workspace_size(int64_t n_new, int32_t group);
+
+typedef struct bpkv_prompt_args {
+  int32_t n_seq, n_kv_heads, group, head_dim;
+  int64_t n_tokens;         /* T: tokens of q and out */
+  const int64_t *q_start;   /* [N + 1] device: sequence i has the tokens q_start[i] .. q_start[i + 1] - 1 */
+  const uint16_t *q;        /* bf16 [T][H][G][D] */
+  int64_t ld_q;             /* elements from one token of q to the next: a multiple of 8, >= H G D */
+  uint16_t *out;            /* bf16 [T][H][G][D] */
+  const uint16_t *k;        /* bf16; NULL with cache or rows8 */
+  const uint16_t *v;
+  int64_t ld_k, ld_v;       /* elements from one token of k (v) to the next, multiples of 8, >= H D: [T][H][D];
+                               both 0: every sequence's [H][t][D], one behind the other (k_out, v_out of
+                               bpkv_qkv_rope for one sequence, or for several of equal length) */
+  const bpkv_cache *cache;  /* or the rows of a cache */
+  const bpkv_rows8 *rows8;
+} bpkv_prompt_args;
+
+/*
+ * Causal attention of prompts of different lengths, packed one behind the other.
+ * With k and v token j of a sequence sees the sequence's tokens 0 .. j.  With
+ * cache or rows8 (one of the three) the t new tokens of sequence i are the last t
+ * of its seq_len[i] rows, already appended, and token j sees the rows 0 ..
+ * seq_len[i] - t + j; n_max sizes the launch, as for bpkv_shared_attend.  q_start
+ * ascends from 0 or more to T at most (values outside are taken as the nearest);
+ * sequences may be empty, and rows of out that belong to none are left as they are.
+ * q, k, v and out start on 16-byte boundaries; out overlaps none of the others.
+ * BPKV_EINVAL when it does, for none or several sources, or strides as above.
+ */
+int bpkv_prompt_attend(const bpkv_prompt_args *a, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of a tree of t drafted tokens of each sequence (1 .. 64), the last t
+ * of its rows (appended before, e.g. with `start`): node j sees the rows before the
+ * tree and, of the tree, the nodes whose bits are set in its mask.
+ *   tree   uint64 [N][t] device: bit x of a node's mask is node x, itself included;
+ *          bits from t on say nothing.  NULL: a chain, node j sees 0 .. j
+ *   q, out bf16 [N][t][H][G][D] (16-byte aligned, not overlapping)
+ * Of a sequence with fewer than t rows the first nodes have none: nobody sees them.
+ */
+int bpkv_tree_attend(const bpkv_cache *c, int32_t t, const uint64_t *tree, const uint16_t *q, uint16_t *out, void *ws,
+                     size_t ws_bytes, void *stream);
+int bpkv_tree_attend8(const bpkv_rows8 *c, int32_t t, const uint64_t *tree, const uint16_t *q, uint16_t *out, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/*
+ * Of t drafted tokens of each sequence keep those that were accepted: rows start[i]
+ * + j, j = 0 .. count[i] - 1, become token path[i][j] of k_new/v_new [N][H][t][D]
+ * (bf16, 16-byte aligned), quantised as bpkv_rows8_append does, and seq_len[i] =
+ * start[i] + count[i].
+ *   start  int64 [N] device
+ *   path   int32 [N][t] device; NULL: token j itself (prompts of different lengths,
+ *          padded to t, appended at once)
+ *   count  int32 [N] device, 0 .. t
+ * A sequence whose rows would leave 0 .. cap_tokens or whose count is outside 0 .. t
+ * keeps its rows and its length; a path's token outside 0 .. t - 1 is taken as the
+ * nearest.  For both BPKV_DEV_OVERFLOW is set in *status (device, NULL to skip).  n_max becomes
+ * min(n_max + t, cap_tokens), as for bpkv_rows8_append with start: set it to what
+ * you know.  start may be seq_len itself (then n_max + t must not pass cap_tokens).
+ * BPKV_EINVAL when t < 1 or t > cap_tokens.
+ */
+int bpkv_rows8_accept(bpkv_rows8 *c, const uint16_t *k_new, const uint16_t *v_new, int32_t t, const int64_t *start,
+                      const int32_t *path, const int32_t *count, int32_t *status, void *stream);
+
 /* ------------------------------------------------------------- decode step */
 #define BPKV_DEPTH_WATERFILL 0  /* bpkv_alloc_depths with sigma2 and budget_q */
 #define BPKV_DEPTH_FIXED 1      /* bpkv_fixed_depths(fixed_channels, fixed_depth) */
