@@ -59,6 +59,7 @@ cudaError_t launch_rows8_accept(const bpkv_rows8& c, const uint16_t* k_new, cons
                                 const int64_t* start, const int32_t* path, const int32_t* count, int32_t* status,
                                 cudaStream_t st);
 size_t prompt_bytes(int64_t n_new, int64_t group);
+bool prompt_in_range(int64_t tokens, int64_t n_seq, int64_t n_heads, int64_t group, int64_t keys);
 cudaError_t launch_prompt(const bpkv_prompt_args& a, void* ws, cudaStream_t st);
 cudaError_t launch_tree(const bpkv_cache& c, int32_t t, const uint64_t* mask, const uint16_t* q, uint16_t* out, void* ws,
                         cudaStream_t st);
@@ -508,6 +509,7 @@ int check_tree(const A& c, int32_t t, const uint64_t* tree, const uint16_t* q, c
   BPKV_TRY(check_prompt_rows(c));
   const int64_t bytes = (int64_t)c.n_seq * t * c.n_kv_heads * c.group * kD * 2;
   if (overlap(q, bytes, out, bytes) || overlaps_rows(c, out, bytes)) return BPKV_EINVAL;
+  if (!prompt_in_range((int64_t)c.n_seq * t, c.n_seq, c.n_kv_heads, c.group, c.cap_tokens)) return BPKV_EUNSUPPORTED;
   if (!ws || !aligned(ws, kAlign) || ws_bytes < prompt_bytes(t, c.group)) return BPKV_ENOWORKSPACE;
   return BPKV_OK;
 }
@@ -586,6 +588,8 @@ int bpkv_prompt_attend(const bpkv_prompt_args* a, void* ws, size_t ws_bytes, voi
     if (wide && overlaps_rows(*a->cache, a->out, out)) return BPKV_EINVAL;
     if (!wide && overlaps_rows(*a->rows8, a->out, out)) return BPKV_EINVAL;
   }
+  if (!prompt_in_range(T, N, H, G, own ? T : a->cache ? a->cache->cap_tokens : a->rows8->cap_tokens))
+    return BPKV_EUNSUPPORTED;
   if (!ws || !aligned(ws, kAlign) || ws_bytes < prompt_bytes(T, G)) return BPKV_ENOWORKSPACE;
   return cuda_status(launch_prompt(*a, ws, as_stream(stream)));
 }

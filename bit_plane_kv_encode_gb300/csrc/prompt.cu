@@ -26,6 +26,9 @@
 #include "tc.cuh"
 
 namespace bpkv {
+
+int64_t prompt_units(int64_t tokens, int64_t n_seq, int64_t n_heads, int64_t group);
+
 namespace prompt {
 
 namespace {
@@ -45,18 +48,23 @@ struct Shape {
   static constexpr int kThreads = BITS == 16 ? 384 : 512;
   static constexpr int kStages = BITS == 16 ? 4 : 3;       // K of tile t as fill 2 t, V as 2 t + 1
   static constexpr int kCodeStages = BITS == 16 ? 0 : 3;   // of codes, in the same order
+  static constexpr int kReaders = 3 + 8 + (BITS == 16 ? 0 : 4);  // of segments: loads, products, the other warps
 };
+constexpr int kSegments = 2;  // that are known at once
 
 template <int BITS>
 struct Smem {
   Plan plan;
-  Walk walk[Shape<BITS>::kThreads / 32];
+  Segment seg[kSegments];
   uint32_t tmem;
   uint32_t abort;
   uint64_t full[4], empty[4];
   uint64_t code_full[3], code_empty[3];
   uint64_t s_full[2], p_half[2], p_ready[2], o_done[2];
+  uint64_t turn[2];
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t q_full, q_empty, done, fin;
+  __align__(16) unsigned char turn_stage[BITS == 16 ? kSoftmaxWarps : 1][2048];
   float2 ml[2][kTile];  // each row's maximum and sum, where both streams hold the rows
 };
 
@@ -70,6 +78,19 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
+// Waits for the phase of the given parity to complete.  Gives up (false) after some
+// seconds, raising *abort, or once another wait of the CTA has.  Short: it stands in
+// many places, and instructions that are not in the cache cost more than the wait.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+#pragma unroll 1
+  for (uint32_t i = 0; i < kMbarRounds && !*abort && now_ns() - t0 <= kMbarNs; ++i)
+    if (mbar_try(bar, parity)) return true;
+  *abort = 1;
+  return false;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -80,9 +101,6 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// 16 bytes of row r, chunk c of a 128-byte-row tile in the 128-byte swizzle
-__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
 // Where the keys of a KV head of a sequence begin, as a tile's coordinates.
 struct Place {
@@ -121,106 +139,150 @@ __device__ __forceinline__ Sees sees_tree(int at, uint64_t mask) {
   return s;
 }
 
-// One tile of one query row: S from tensor memory to weights over it, m and l of the
-// row so far, and O when m moves.  The first 64 keys' weights are announced on `half`.
-__device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool masked, const Sees& sees, bool first,
-                                             uint32_t half, float& m, float& l) {
-  float x[kTile];
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int k = 0; k < 64; k += 32) tmem_ld32(ts + k, reinterpret_cast<uint32_t*>(x) + k);
-  wait_ld();
-#pragma unroll
-  for (int k = 64; k < 128; k += 32) tmem_ld32(ts + k, reinterpret_cast<uint32_t*>(x) + k);  // while the first is looked at
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    if (part) wait_ld();
-    if (masked) {
-#pragma unroll
-      for (int k = part * 64; k < part * 64 + 64; ++k)
-        if (!((sees.w[k / 32] >> (k % 32)) & 1u)) x[k] = -INFINITY;
-    }
-#pragma unroll
-    for (int k = part * 64; k < part * 64 + 64; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
-  }
-  const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-  if (first) {
-    m = top;
-  } else {
-    const bool up = top > m + kLazy / kLogScale;
-    if (__any_sync(0xffffffffu, up)) {
-      // S of this step is complete, so O of the stream's step before it is too
-      const float f = up ? ex2((m - top) * kLogScale) : 1.f;
-      l *= f;
-      if (up) m = top;
-#pragma unroll 1
-      for (int k = 0; k < kD; k += 16) {
-        uint32_t o[16];
-        tmem_ld16(to + k, o);
-        wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-        tmem_st16(to + k, o);
-      }
-    }
-  }
+// 64 logits of a row to weights in bf16, and their sum (of the weights unrounded).
+__device__ __forceinline__ void weights(const float* x, float m, uint32_t* w, F2& sum) {
   const float base = m == -INFINITY ? 0.f : m * kLogScale;
   const F2 base2(-base, -base), unit2(kLogScale, kLogScale);
   F2 ls[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
-  for (int k = 0; k < kTile; k += 32) {
-    uint32_t w[16];
+  for (int i = 0; i < 32; ++i) {
+    float p0, p1;
+    fma2(F2(x[2 * i], x[2 * i + 1]), unit2, base2).get(p0, p1);
+    p0 = ex2(p0);
+    p1 = ex2(p1);
+    ls[i & 1] = add2(ls[i & 1], F2(p0, p1));
+    w[i] = bf16x2(p0, p1);
+  }
+  sum = add2(ls[0], ls[1]);
+}
+
+__device__ __forceinline__ void load_half(uint32_t ts, float* x) {
+  tmem_ld32(ts, reinterpret_cast<uint32_t*>(x));
+  tmem_ld32(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
+}
+
+// Hides what a row does not see of 64 keys; the largest of the rest.
+__device__ __forceinline__ float look(float* x, bool masked, uint32_t see0, uint32_t see1) {
+  if (masked) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float p0, p1;
-      fma2(F2(x[k + 2 * i], x[k + 2 * i + 1]), unit2, base2).get(p0, p1);
-      p0 = ex2(p0);
-      p1 = ex2(p1);
-      ls[i & 1] = add2(ls[i & 1], F2(p0, p1));
-      w[i] = bf16x2(p0, p1);
-    }
-    tmem_st16(ts + k / 2, w);
-    if (k == 32) {
-      wait_st();
-      fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(half);
+    for (int k = 0; k < 64; ++k)
+      if (!(((k < 32 ? see0 : see1) >> (k % 32)) & 1u)) x[k] = -INFINITY;
+  }
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], x[k], x[k + 1]);
+  return max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+}
+
+// One tile of one query row: S from tensor memory to weights over it, m and l of the
+// row so far, and O when m moves.  The first 64 keys' weights are announced on `half`.
+__device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool masked, const Sees& sees, bool first,
+                                             uint32_t half, float& m, float& l) {
+  float x[64], y[64];
+  load_half(ts, x);
+  wait_ld();
+  load_half(ts + 64, y);  // while the first is looked at
+  float top = look(x, masked, sees.w[0], sees.w[1]);
+  wait_ld();
+  top = fmaxf(top, look(y, masked, sees.w[2], sees.w[3]));
+  const bool up = top > m + kLazy / kLogScale;
+  if (first) {
+    m = top;
+  } else if (__any_sync(0xffffffffu, up)) {
+    // S of this step is complete, so O of the stream's step before it is too
+    const float f = up ? ex2((m - top) * kLogScale) : 1.f;
+    l *= f;
+    if (up) m = top;
+#pragma unroll 1
+    for (int k = 0; k < kD; k += 16) {
+      uint32_t o[16];
+      tmem_ld16(to + k, o);
+      wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      tmem_st16(to + k, o);
     }
   }
+  uint32_t w[32];
+  F2 sum, rest;
+  weights(x, m, w, sum);
+  tmem_st16(ts, w);
+  tmem_st16(ts + 16, w + 16);
+  wait_st();
+  fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(half);
+  weights(y, m, w, rest);
+  tmem_st16(ts + 32, w);
+  tmem_st16(ts + 48, w + 16);
   float l0, l1;
-  add2(ls[0], ls[1]).get(l0, l1);
+  add2(sum, rest).get(l0, l1);
   l += l0 + l1;
 }
 
-// Sixteen words of this warp's rows, a row a lane, to sixteen bytes of four
-// neighbouring rows a lane: lane q of four ends with the rows' q-th four words.
-__device__ __forceinline__ void quads(uint32_t (&r)[16]) {
-  const int q = threadIdx.x & 3;
+// Sixteen words of this warp's rows, a row a lane, to sixteen bytes of four rows a
+// lane: lane q of four ends with the q-th four words of rows turned_row(0) .. (3).
+// Through shared memory, or by exchanges where there is no room.
+template <int BITS>
+__device__ __forceinline__ int turned_row(int i) {
+  const int lane = threadIdx.x & 31;
+  return BITS == 16 ? (lane >> 2) + 8 * i : (lane & ~3) + i;
+}
+template <int BITS>
+__device__ __forceinline__ void turn(uint32_t (&r)[16], unsigned char* stage) {
+  const int lane = threadIdx.x & 31, q = lane & 3;
+  if constexpr (BITS == 16) {
+    // a row's chunks in an order that keeps eight lanes' stores, and loads, in different banks
+    __syncwarp();
 #pragma unroll
-  for (int u = 0; u < 4; u += 2)
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 1 ? r[4 * u + i] : r[4 * u + 4 + i], 1);
-      if (q & 1) r[4 * u + i] = y;
-      else r[4 * u + 4 + i] = y;
+      const int row = turned_row<BITS>(i);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((q ^ ((row >> 1) & 3)) << 4));
+      r[4 * i] = v.x;
+      r[4 * i + 1] = v.y;
+      r[4 * i + 2] = v.z;
+      r[4 * i + 3] = v.w;
     }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 2 ? r[i] : r[8 + i], 2);
-    if (q & 2) r[i] = y;
-    else r[8 + i] = y;
+    for (int u = 0; u < 4; u += 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 1 ? r[4 * u + i] : r[4 * u + 4 + i], 1);
+        if (q & 1) r[4 * u + i] = y;
+        else r[4 * u + 4 + i] = y;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 2 ? r[i] : r[8 + i], 2);
+      if (q & 2) r[i] = y;
+      else r[8 + i] = y;
+    }
   }
 }
 
-// Four codes as two pairs of bf16, times 2^(e + 120) each (exact): the code's bits
-// moved to a bf16 number's are 2^-120 of its value.
-__device__ __forceinline__ uint32_t bf16_codes(uint32_t spread, uint32_t f0, uint32_t f1) {
-  // spread: a code in the upper byte of each half
-  const uint32_t bits = ((spread >> 4) & 0x07f007f0u) | (spread & 0x80008000u);
+// Two codes to bf16, times `f` each.  A code's magnitude moved to where a bf16 number
+// has its own is 2^-120 of it; the sign comes from the byte above, a copy of it.
+template <int PAIR>
+__device__ __forceinline__ uint32_t bf16_codes(uint32_t w, uint32_t f) {
   uint32_t r;
-  asm("{\n .reg .b32 t;\n mul.rn.bf16x2 t, %1, %2;\n mul.rn.bf16x2 %0, t, %3;\n}" : "=r"(r) : "r"(bits), "r"(f0), "r"(f1));
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(PAIR ? 0xb3a2 : 0x9180));
+  const uint32_t bits = (r << 4) & 0x87f087f0u;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(f));
   return r;
 }
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t f) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
+  return r;
+}
+// a power of two twice
+__device__ __forceinline__ uint32_t twice2(int e) { return (uint32_t)(e + 127) << 7 | (uint32_t)(e + 127) << 23; }
 
 template <int BITS>
 __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __grid_constant__ Args a,
@@ -238,7 +300,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     sm.abort = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.full[i]), BITS == 16 ? 1 : 4);
-      mbar_init(smem_u32(&sm.empty[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), 2);
     }
     for (int i = 0; i < kCodeStages; ++i) {
       mbar_init(smem_u32(&sm.code_full[i]), 1);
@@ -249,10 +311,15 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
       mbar_init(smem_u32(&sm.p_half[s]), 4);
       mbar_init(smem_u32(&sm.p_ready[s]), 4);
       mbar_init(smem_u32(&sm.o_done[s]), 1);
+      mbar_init(smem_u32(&sm.turn[s]), 1);
+    }
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(smem_u32(&sm.seg_full[i]), 1);
+      mbar_init(smem_u32(&sm.seg_empty[i]), Shape<BITS>::kReaders);
     }
     mbar_init(smem_u32(&sm.q_full), 1);
-    mbar_init(smem_u32(&sm.q_empty), 1);
-    mbar_init(smem_u32(&sm.done), 1);
+    mbar_init(smem_u32(&sm.q_empty), 2);
+    mbar_init(smem_u32(&sm.done), 2);
     mbar_init(smem_u32(&sm.fin), kSoftmaxWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_shared();
@@ -264,21 +331,21 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
   make_plan(a, sm.plan);  // ends with a barrier of the CTA
   fence_after();
   const uint32_t tmem = sm.tmem;
-  Walk& walk = sm.walk[warp];
-  const Segment& g = walk.g;
-  if (lane == 0) walk.begin(sm.plan);
-  __syncwarp();
-  auto next = [&] { return walk.next(sm.plan, a); };  // by one thread of the warp
-  auto next_all = [&] {                               // by all of it
-    __syncwarp();
-    const bool more = __shfl_sync(0xffffffffu, lane == 0 && next(), 0);
-    __syncwarp();
-    return more;
+  // Segments come from one thread, each role takes them in order: its n-th, until
+  // `end_segment`, which gives its place back.  By one thread, or by all of a warp.
+  uint32_t seg_no = 0;
+  Segment g;
+  auto next = [&](bool& ok) {
+    const uint32_t i = seg_no % kSegments;
+    ok = ok && wait(smem_u32(&sm.seg_full[i]), (seg_no / kSegments) & 1, abort);
+    if (ok) g = sm.seg[i];
+    return ok && g.tiles > 0;
   };
+  auto end_segment = [&] { mbar_arrive(smem_u32(&sm.seg_empty[seg_no++ % kSegments])); };
 
   if (warp < 4) {
     // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168; 8-bit rows:
-    // 256 x 48 + 256 x 208 of 512 x 128
+    // 128 x 48 + 256 x 200 + 128 x 64 of 512 x 128
     regs_fewer<BITS == 16 ? 80 : 48>();
     if (warp == 0) {
       if (elect_one()) {
@@ -289,12 +356,13 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         uint32_t stage = 0, phase = 0, issued = 0;
         const uint64_t policy = shared::evict_first_policy();
         bool ok = true;
-        while (ok && next()) {
+        while (next(ok)) {
           const Place at = place_of(a, sm.plan, g);
+#pragma unroll 1
           for (int t = g.tile0; ok && t < g.tile0 + g.tiles; ++t) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-              ok = ok && mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort);
+              ok = ok && wait(smem_u32(&empty[stage]), phase ^ 1, abort);
               if (!ok) break;
               const uint32_t bar = smem_u32(&full[stage]);
               const CUtensorMap* m = kv ? &maps.v : &maps.k;
@@ -311,114 +379,150 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
               if (++stage == (uint32_t)kRing) stage = 0, phase ^= 1;
             }
           }
+          end_segment();
         }
         if (!ok) {  // the copies in flight must land before the CTA's shared memory is given up
           uint32_t never = 0;
+#pragma unroll 1
           for (uint32_t k = issued > (uint32_t)kRing ? issued - kRing : 0; k < issued; ++k)
-            mbar_wait(smem_u32(&full[k % kRing]), (k / kRing) & 1, &never);
+            wait(smem_u32(&full[k % kRing]), (k / kRing) & 1, &never);
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
       if (elect_one()) {
-        // ---- products.  Steps follow one another through all segments; a step's S is
-        // issued before O of the step before, which is another stream's, so that the
-        // tensor cores work while that one's softmax runs (of the same stream, O comes
-        // first: S takes the place of P).  Products run in the order issued.
+        // ---- products of stream s, in its own thread: S of a step is issued right
+        // behind O of the step before, whose P it takes the place of, so that the tensor
+        // cores work while the other stream's softmax runs.  (One thread for both
+        // streams spent more cycles on its waits than on the products.)
+        const int s = warp >> 1;
         constexpr uint32_t kDescS = mma_desc(1, 1, 0, kTile, kTile);
         constexpr uint32_t kDescO = mma_desc(1, 1, 1, kTile, kD);
-        uint32_t seg = 0, p_phase = 0, tile_no = 0;
+        const uint32_t d_s = tmem + s * kTile, d_o = tmem + 2 * kTile + s * kD;
+        uint32_t p_phase = 0, tile_no = 0, turns = 0;
         bool ok = true;
-        // the O that is still to be issued
-        bool pend = false, p_dual = false, p_last = false, p_acc = false;
-        int p_s = 0;
-        uint32_t p_use = 0;
-        auto flush = [&] {
-          pend = false;
-          const int s = p_s;
-          const uint32_t st = p_use % kStages;
-          const uint32_t pp = (p_phase >> s) & 1;
-          p_phase ^= 1u << s;
-          ok = (p_dual && s) || mbar_wait(smem_u32(&sm.full[st]), (p_use / kStages) & 1, abort);
-          ok = ok && mbar_wait(smem_u32(&sm.p_half[s]), pp, abort);
-          if (!ok) return;
-          fence_after();
-          const uint32_t vb = smem_desc(smem_u32(ring + st * kStage), kTile * 128);
-          const uint32_t p = tmem + s * kTile, d = tmem + 2 * kTile + s * kD;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, p_acc | (k > 0));
-          ok = mbar_wait(smem_u32(&sm.p_ready[s]), pp, abort);
-          if (!ok) return;
-          fence_after();
-#pragma unroll
-          for (int k = 4; k < 8; ++k) mma16_ts(d, p + k * 8, vb + (k * 16 * 128 >> 4), kDescO, 1);
-          if (!p_dual || s) mma_commit(smem_u32(&sm.empty[st]));
-          if (p_last) mma_commit(smem_u32(&sm.o_done[s]));
+        // Streams of their own rows take turns, a turn being the rest of O and the next S:
+        // left alone they fall into step, and neither's products hide the other's softmax.
+        auto begin_turn = [&] {
+          ok = ok && wait(smem_u32(&sm.turn[s]), (turns & 1) ^ (s ? 0 : 1), abort);
+          ++turns;
+          return ok;
         };
-        while (ok && next()) {
-          // a segment's last O does not wait for the next one's rows of q
-          if (pend && !mbar_try(smem_u32(&sm.q_full), seg & 1)) flush();
-          ok = ok && mbar_wait(smem_u32(&sm.q_full), seg & 1, abort);
+        auto end_turn = [&] { mbar_arrive(smem_u32(&sm.turn[s ^ 1])); };
+        // Every fill of the ring is waited for by both threads, and released by both: a
+        // wait reads one bit of the stage's phase, which must not run ahead of it.
+        auto await = [&](uint32_t use) {
+          ok = ok && wait(smem_u32(&sm.full[use % kStages]), (use / kStages) & 1, abort);
+          return ok;
+        };
+        auto skip = [&](uint32_t use) {  // of the other stream's tile
+          if (await(use)) mbar_arrive(smem_u32(&sm.empty[use % kStages]));
+        };
+        auto release = [&](uint32_t use) { mma_commit(smem_u32(&sm.empty[use % kStages])); };
+        while (next(ok)) {
+          ok = wait(smem_u32(&sm.q_full), seg_no & 1, abort);
           if (!ok) break;
-          const int steps = g.steps();
-          for (int i = 0; ok && i < steps; ++i) {
-            const int s = i & 1;
-            const uint32_t use = 2 * (tile_no + (g.dual ? i >> 1 : i)), st = use % kStages;
-            if (pend && p_s == s) flush();
-            if (!g.dual || s == 0) ok = ok && mbar_wait(smem_u32(&sm.full[st]), (use / kStages) & 1, abort);
-            if (!ok) break;
-            fence_after();
-            const uint32_t kb = smem_desc(smem_u32(ring + st * kStage), 16);
-            const uint32_t qb = smem_desc(smem_u32(q_smem + (g.dual ? s : 0) * kQ), 16);
+          const bool dual = g.dual;
+          const int tiles = g.tiles;
+          const uint32_t qb = smem_desc(smem_u32(q_smem + (dual ? s : 0) * kQ), 16);
+          const int step = dual ? 1 : 2, t0 = dual ? 0 : s;
+          if (t0 >= tiles) mbar_arrive(smem_u32(&sm.q_empty));
+          if (!dual && s) {
+            skip(2 * tile_no);
+            skip(2 * tile_no + 1);
+          }
+          // S of tile t, and what the barriers wait for: it, the rows of q, the stage
+          auto scores = [&](int t) {
+            const uint32_t use = 2 * (tile_no + t);
+            const uint32_t kb = smem_desc(smem_u32(ring + use % kStages * kStage), 16);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint32_t o = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-              mma16_ss(tmem + s * kTile, qb + o, kb + o, kDescS, k > 0);
+              mma16_ss(d_s, qb + o, kb + o, kDescS, k > 0);
             }
             mma_commit(smem_u32(&sm.s_full[s]));
-            if (!g.dual || s) mma_commit(smem_u32(&sm.empty[st]));
-            if (i == steps - 1) mma_commit(smem_u32(&sm.q_empty));
-            if (pend) flush();
-            pend = true;
-            p_dual = g.dual;
-            p_last = i + 2 >= steps;
-            p_acc = i >= 2;
-            p_s = s;
-            p_use = use + 1;
+            if (t + step >= tiles) mma_commit(smem_u32(&sm.q_empty));
+          };
+          if (t0 < tiles && await(2 * (tile_no + t0)) && (!dual || begin_turn())) {
+            fence_after();
+            scores(t0);
+            release(2 * (tile_no + t0));
+            if (dual) end_turn();
           }
-          tile_no += g.tiles;
-          ++seg;
+#pragma unroll 1
+          for (int t = t0; ok && t < tiles; t += step) {
+            const uint32_t use = 2 * (tile_no + t);
+            const bool more = t + step < tiles, other = !dual && t + 1 < tiles;
+            if (!await(use + 1)) break;
+            if (other) skip(use + 2);
+            const uint32_t vb = smem_desc(smem_u32(ring + (use + 1) % kStages * kStage), kTile * 128);
+            ok = ok && wait(smem_u32(&sm.p_half[s]), p_phase, abort);
+            if (!ok) break;
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma16_ts(d_o, d_s + k * 8, vb + (k * 16 * 128 >> 4), kDescO, (t > t0) | (k > 0));
+            // a tile that comes from memory is not waited for before V of this one is given back
+            if (dual) {
+              if (more) await(use + 2);
+              begin_turn();
+            }
+            ok = ok && wait(smem_u32(&sm.p_ready[s]), p_phase, abort);
+            if (!ok) break;
+            p_phase ^= 1;
+            fence_after();
+#pragma unroll
+            for (int k = 4; k < 8; ++k) mma16_ts(d_o, d_s + k * 8, vb + (k * 16 * 128 >> 4), kDescO, 1);
+            if (!more) mma_commit(smem_u32(&sm.o_done[s]));
+            if (!dual) release(use + 1);
+            if (other) skip(use + 3);
+            if (more && (dual || await(use + 4))) scores(t + step);
+            if (dual) {
+              end_turn();
+              release(use + 1);
+            }
+            if (more) release(use + 2 * step);
+          }
+          tile_no += tiles;
+          end_segment();
         }
-        if (ok && pend) flush();
         // every product is complete before tensor memory is given up
         uint32_t never = 0;
         mma_commit(smem_u32(&sm.done));
-        mbar_wait(smem_u32(&sm.done), 0, &never);
+        wait(smem_u32(&sm.done), 0, &never);
       }
     } else if (warp == 2) {
       if (elect_one()) {
-        // ---- loads: the rows of q of every segment, once the products have read the last one's
+        // ---- the segments, and the loads of their rows of q, once the products have read the last one's
         const uint32_t bytes = 128 * a.group * a.run, bar = smem_u32(&sm.q_full);
         const uint64_t policy = shared::evict_first_policy();
-        uint32_t seg = 0;
+        Walk walk(sm.plan, a);
+        uint32_t loads = 0;
         bool ok = true;
-        while (ok && next()) {
-          if (seg > 0) ok = mbar_wait(smem_u32(&sm.q_empty), (seg - 1) & 1, abort);
+        for (;; ++seg_no) {
+          const uint32_t i = seg_no % kSegments;
+          g = walk.next();
+          ok = wait(smem_u32(&sm.seg_empty[i]), ((seg_no / kSegments) & 1) ^ 1, abort);
+          if (!ok) break;
+          sm.seg[i] = g;
+          mbar_arrive(smem_u32(&sm.seg_full[i]));
+          if (g.tiles == 0) break;
+          if (seg_no > 0) ok = wait(smem_u32(&sm.q_empty), (seg_no - 1) & 1, abort);
           if (!ok) break;
           const int n = g.dual ? 2 : 1;
           mbar_expect_tx(bar, 2 * n * bytes);
+#pragma unroll 1
           for (int s = 0; s < n; ++s)
             for (int half = 0; half < 2; ++half)  // 64 channels each
               tma_load_3d(smem_u32(q_smem + s * kQ + half * (kTile * 128)), &maps.q, bar, half * 64, g.h * a.group,
                           g.token + s * a.run, policy);
-          ++seg;
+          ++loads;
         }
         uint32_t never = 0;  // the last ones' landing is nobody's to wait for when another role gave up
-        if (seg > 0) mbar_wait(bar, (seg - 1) & 1, &never);
+        if (loads > 0) wait(bar, (loads - 1) & 1, &never);
       }
     }
   } else if (warp < 4 + kSoftmaxWarps) {
     // ---- softmax of stream s, a thread per row
-    regs_more<208>();
+    regs_more<BITS == 16 ? 208 : 200>();
     const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
@@ -426,7 +530,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     uint32_t tile_no = 0, s_phase = 0, o_phase = 0, fin_phase = 0;
     Cut cut = {};
     bool ok = true;
-    while (ok && next_all()) {
+    while (__all_sync(0xffffffffu, next(ok))) {
       const int steps = g.steps_of(s), first_tok = g.dual ? s * a.run : 0;
       const bool there = tok < a.run && first_tok + tok < g.tokens;  // a row of the unit
       // keys before this row's end; rows that are not there are not masked
@@ -437,15 +541,18 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         mask = a.tree[(int64_t)g.seq * a.t + own] & (a.t >= 64 ? ~0ull : (1ull << a.t) - 1);
       const int keys = g.off + g.t;
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const int t = g.tile_of(s, j), key0 = t * kTile;
-        ok = mbar_wait(smem_u32(&sm.s_full[s]), s_phase, abort);
-        if (BITS == 16 && keys < key0 + kTile && (!g.dual || s == 0)) {
-          // rows of V past the last key may hold anything: zeros, so that 0 x does not become NaN
+        ok = wait(smem_u32(&sm.s_full[s]), s_phase, abort);
+        if (BITS == 16 && keys < key0 + kTile) {
+          // rows of V past the last key may hold anything: zeros, so that 0 x does not
+          // become NaN (of two streams both write them, each before its own product)
           const uint32_t use = 2 * (tile_no + t - g.tile0) + 1, stage = use % kStages;
-          ok = ok && mbar_wait(smem_u32(&sm.full[stage]), (use / kStages) & 1, abort);
+          ok = ok && wait(smem_u32(&sm.full[stage]), (use / kStages) & 1, abort);
           if (ok) {
             const int valid = max(0, keys - key0);
+#pragma unroll 1
             for (int x = row; x < (kTile - valid) * 16; x += kTile) {
               const int v = valid + x / 16, c = x % 16;
               *reinterpret_cast<uint4*>(ring + stage * kStage + (c / 8) * (kTile * 128) + v * 128 + (c % 8) * 16) =
@@ -476,8 +583,33 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
       }
       if (!ok) break;
       tile_no += g.tiles;
+      // what the segment's end takes of it; the walk to the next one hides behind the last O
+      const bool dual = g.dual, whole = g.whole, both = !dual && g.steps_of(1) > 0;
+      const int rows = min(a.run, g.tokens - first_tok) * a.group, token = g.token + first_tok, h = g.h, slot = g.slot();
+      cut = {g.token, g.h, g.tokens, g.pieces, 0};  // of the last segment
+      const bool writes = (dual || both || s == 0) && w4 * 32 < rows;
+      const int c0 = both ? s * 64 : 0, c1 = both ? c0 + 64 : kD;
+      const int64_t at = (int64_t)slot * a.slot_rows + (dual ? s * kTile : 0) + w4 * 32;
+      // The four rows that the lane stores, 16 bytes of every 64.
+      unsigned char* dst[4];
+      if (writes) {
+        unsigned char* base = whole ? reinterpret_cast<unsigned char*>(
+                                          a.out + (((int64_t)token * a.n_heads + h) * a.group) * kD + c0)
+                                    : reinterpret_cast<unsigned char*>(a.part_o + at * kD + c0);
+        const uint32_t tok_step = a.n_heads * a.group * kD * 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = turned_row<BITS>(i), x = (w4 * 32 + r) * a.group_inv >> 16;
+          dst[i] = base + (lane & 3) * 16 +
+                   (whole ? (uint64_t)x * tok_step + (w4 * 32 + r - x * a.group) * (kD * 2) : (uint64_t)r * (kD * 4));
+          if (w4 * 32 + r >= rows) dst[i] = nullptr;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) end_segment();
+      else ++seg_no;
       if (steps > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.o_done[s]), o_phase, abort));
+        ok = __all_sync(0xffffffffu, wait(smem_u32(&sm.o_done[s]), o_phase, abort));
         if (!ok) break;
         o_phase ^= 1;
       }
@@ -486,11 +618,10 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
       auto meet = [&] {  // of all softmax warps
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.fin));
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.fin), fin_phase, abort));
+        ok = __all_sync(0xffffffffu, wait(smem_u32(&sm.fin), fin_phase, abort));
         fin_phase ^= 1;
         return ok;
       };
-      const bool both = !g.dual && g.steps_of(1) > 0;
       if (both) {  // streams that hold the same rows join them, each half of the channels
         sm.ml[s][row] = make_float2(m, l);
         if (!meet()) break;
@@ -501,69 +632,55 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         l = f0 * a0.y + f1 * a1.y;
       }
       fence_after();
-      if (g.dual || both || s == 0) {
-        const int c0 = both ? s * 64 : 0, c1 = both ? c0 + 64 : kD;
-        const uint32_t o0 = g.dual ? to : tmem + lanes + 2 * kTile;
-        if (g.whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // a sum that is NaN stays one
+      if (writes) {
+        const uint32_t o0 = (dual ? to : tmem + lanes + 2 * kTile) + c0;
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : __frcp_rn(l);  // a sum that is NaN stays one
           f0 *= inv;
           f1 *= inv;
+        } else if (row < rows && c0 == 0) {
+          a.part_ml[at + lane] = make_float2(m, l);
         }
-        auto load = [&](int k, uint32_t* o) {  // 16 channels of this thread's row
-          tmem_ld16(o0 + k, o);
+        unsigned char* stage = sm.turn_stage[BITS == 16 ? warp - 4 : 0];
+        uint32_t o[32], w[16];
+        tmem_ld32(o0, o);
+#pragma unroll 1
+        for (int k = 0; k < c1 - c0; k += 32) {
+          wait_ld();
           if (both) {
-            uint32_t v[16];
-            tmem_ld16(o0 + kD + k, v);
+            uint32_t v[32];
+            tmem_ld32(o0 + kD + k, v);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
               o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(v[i]) * f1));
           } else {
-            wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
           }
-        };
-        const int q = lane & 3;
-        const int rows = min(a.run, g.tokens - first_tok) * a.group;
-        if (g.whole) {
-          uint16_t* dst[4];  // the four rows that the lane stores
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = row - q + i, x = r * a.group_inv >> 16;
-            dst[i] = a.out + ((((int64_t)g.token + first_tok + x) * a.n_heads + g.h) * a.group + (r - x * a.group)) * kD + q * 8;
-            if (r >= rows) dst[i] = nullptr;
-          }
-#pragma unroll 1
-          for (int k = c0; k < c1; k += 32) {
-            uint32_t o[32], w[16];
-            load(k, o);
-            load(k + 16, o + 16);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-            quads(w);
+          auto store = [&](int off) {
+            turn<BITS>(w, stage);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (dst[i])
-                *reinterpret_cast<uint4*>(dst[i] + k) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          }
-        } else {
-          const int64_t at = (int64_t)g.slot() * a.slot_rows + (g.dual ? s * kTile : 0) + row;
-          float* po = a.part_o + (at - q) * kD + q * 4;
-#pragma unroll 1
-          for (int k = c0; k < c1; k += 16) {
-            uint32_t o[16];
-            load(k, o);
-            quads(o);
+                __stcs(reinterpret_cast<uint4*>(dst[i] + off), make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+          };
+          if (whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (row - q + i < rows)
-                *reinterpret_cast<uint4*>(po + i * kD + k) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 16; ++i) w[i] = bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            if (k + 32 < c1 - c0) tmem_ld32(o0 + k + 32, o);  // comes while this part leaves
+            store(k * 2);
+          } else {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = o[16 * part + i];
+              if (part && k + 32 < c1 - c0) tmem_ld32(o0 + k + 32, o);
+              store(k * 4 + 64 * part);
+            }
           }
-          if (row < rows && c0 == 0) a.part_ml[at] = make_float2(m, l);
         }
       }
-      cut = {g.token, g.h, g.tokens, g.pieces, 0};  // of the last segment
       fence_before();
       // O and the rows' maxima are read before the next segment's take their place
       if (both && !meet()) break;
@@ -571,46 +688,47 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     if (a.split && s == 0 && row == 0) a.cuts[blockIdx.x] = cut;
   } else if constexpr (BITS == 8) {
     // ---- codes to bf16, all four warps each tile
-    regs_fewer<48>();
-    const int t128 = tid - 384, c = t128 & 7;
+    regs_fewer<64>();
+    // A thread a row, in chunks of 16 codes in such an order that eight neighbouring
+    // threads' loads, and their stores, meet in no bank.
+    const int r = tid - 384, r7 = r & 7;
+    const uint32_t src0 = r * 128 + (r7 << 4);
+    const uint32_t dst0 = r * 128 + ((r7 & 4) << 12) + (((2 * (r7 & 3)) ^ r7) << 4);
     uint32_t n = 0;
     bool ok = true;
-    while (ok && next_all()) {
+    while (__all_sync(0xffffffffu, next(ok))) {
       const int keys = g.off + g.t;
+#pragma unroll 1
       for (int t = g.tile0; ok && t < g.tile0 + g.tiles; ++t) {
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const uint32_t from = n % kCodeStages, to = n % kStages;
-          ok = mbar_wait(smem_u32(&sm.code_full[from]), (n / kCodeStages) & 1, abort) &&
-               mbar_wait(smem_u32(&sm.empty[to]), ((n / kStages) & 1) ^ 1, abort);
+          ok = wait(smem_u32(&sm.code_full[from]), (n / kCodeStages) & 1, abort) &&
+               wait(smem_u32(&sm.empty[to]), ((n / kStages) & 1) ^ 1, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const unsigned char* src = codes + from * kCodeStage;
-          // of 16 codes, a row's c-th, as two 16-byte chunks; the upper half of a row
-          // stores its odd chunk first, so that eight lanes' stores meet in no bank
-          unsigned char* dst = ring + to * kStage + (c >> 2) * (kTile * 128);
-          const int k0 = (c & 3) * 2 + (c >> 2), k1 = k0 ^ 1;
-          const int valid = keys - t * kTile;
-#pragma unroll 2
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 16 + (t128 >> 3);
-            uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + c * 16);
-            if (kv && r >= valid) x = make_uint4(0, 0, 0, 0);  // may hold anything: zeros, so that 0 x does not become NaN
-            const int e = min(max((int)src[kCodes + r] - kExpBias, kExpMin), kExpMax);
-            // 2^(e + 120) passes bf16's range: 2^60, then the rest
-            const uint32_t f0 = (uint32_t)(60 + 127) << 7, f1 = (uint32_t)(e + 60 + 127) << 7;
-            const uint32_t m0 = f0 | f0 << 16, m1 = f1 | f1 << 16;
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
+          unsigned char* dst = ring + to * kStage;
+          const bool there = r < keys - t * kTile;
+          const int e = min(max((int)src[kCodes + r] - kExpBias, kExpMin), kExpMax);
+          // 2^(e + 120), as far as bf16 has it; the rest below.  Rows past the last key
+          // may hold anything: zeros, so that 0 x does not become NaN
+          const uint32_t f = twice2(min(e, 7) + 120);
+          const bool big = __any_sync(0xffffffffu, e > 7);
+          const uint32_t f2 = twice2(max(e - 7, 0));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[2 * k] = bf16_codes(__byte_perm(w[k], 0, 0x1404), m0, m1);
-              y[2 * k + 1] = bf16_codes(__byte_perm(w[k], 0, 0x3424), m0, m1);
+          for (int i = 0; i < 8; ++i) {
+            uint4 x = *reinterpret_cast<const uint4*>(src + (src0 ^ (i << 4)));
+            if (!there) x = make_uint4(0, 0, 0, 0);
+            uint4 a0 = make_uint4(bf16_codes<0>(x.x, f), bf16_codes<1>(x.x, f), bf16_codes<0>(x.y, f), bf16_codes<1>(x.y, f));
+            uint4 a1 = make_uint4(bf16_codes<0>(x.z, f), bf16_codes<1>(x.z, f), bf16_codes<0>(x.w, f), bf16_codes<1>(x.w, f));
+            if (big) {
+              a0 = make_uint4(times(a0.x, f2), times(a0.y, f2), times(a0.z, f2), times(a0.w, f2));
+              a1 = make_uint4(times(a1.x, f2), times(a1.y, f2), times(a1.z, f2), times(a1.w, f2));
             }
-            const bool odd = c >> 2;
-            *reinterpret_cast<uint4*>(dst + swz(r, k0)) =
-                odd ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(dst + swz(r, k1)) =
-                odd ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
+            const uint32_t at = dst0 ^ ((i & 4) << 12) ^ ((i & 3) << 5);
+            *reinterpret_cast<uint4*>(dst + at) = a0;
+            *reinterpret_cast<uint4*>(dst + (at ^ 16)) = a1;
           }
           fence_async_shared();
           __syncwarp();
@@ -620,6 +738,9 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) end_segment();
+      else ++seg_no;
     }
   }
   fence_before();
@@ -766,8 +887,7 @@ cudaError_t launch(Args& a, const Maps& maps, int64_t longest, int64_t keys, voi
   a.part_o = reinterpret_cast<float*>(w + sp.o);
   a.slot_rows = sp.slot_rows;
   a.status = static_cast<int32_t*>(ws);
-  // units and their tiles at most
-  const int64_t units = a.n_heads * (a.tokens / (2 * a.run) + min64(a.n_seq, a.tokens));
+  const int64_t units = prompt_units(a.tokens, a.n_seq, a.n_heads, a.group);
   const int64_t tiles = max64(1, (keys + kTile - 1) / kTile);
   a.split = tiles > 4;
   const int ctas = (int)max64(1, min64(kSms, a.split ? units * (tiles + 1) / 2 : units));
@@ -784,6 +904,15 @@ cudaError_t launch(Args& a, const Maps& maps, int64_t longest, int64_t keys, voi
 }  // namespace prompt
 
 using namespace prompt;
+
+int64_t prompt_units(int64_t tokens, int64_t n_seq, int64_t n_heads, int64_t group) {
+  return n_heads * (tokens / (2 * (kTile / group)) + min64(n_seq, tokens));
+}
+
+// Whether what the units count (with `keys` keys each at most) stays below 2^31.
+bool prompt_in_range(int64_t tokens, int64_t n_seq, int64_t n_heads, int64_t group, int64_t keys) {
+  return prompt_units(tokens, n_seq, n_heads, group) <= (((int64_t)1 << 31) - 1) / (keys / kTile + 1 + kOver);
+}
 
 size_t prompt_bytes(int64_t tokens, int64_t group) { return space(tokens, group).total; }
 

@@ -20,8 +20,6 @@
 namespace bpkv {
 namespace prompt {
 
-using shared::quot;
-
 constexpr int kTile = 128;      // keys of a tile, rows of a stream
 constexpr int kRows = 256;      // rows of a unit at most
 constexpr int kMaxSeq = BPKV_SHARED_MAX_SEQ;
@@ -61,16 +59,16 @@ struct Args {
   int32_t* status;
 };
 
+// Counts are below 2^31: the host makes sure.
 struct Plan {
-  int64_t cum[kMaxSeq + 1];   // what the sequences before count together
+  int32_t cum[kMaxSeq + 1];   // what the sequences before count together
   int32_t start[kMaxSeq];     // a sequence's first token in q
   int32_t n[kMaxSeq];         // its new tokens
   int32_t off[kMaxSeq];       // keys before the first of them (negative: that many of them have none)
   // where this CTA's stretch begins
   int32_t seq, h, run;
-  int32_t pad;
-  int64_t at, left;           // within that unit, and the stretch's length
-  int64_t total, ctas;
+  int32_t at, left;           // within that unit, and the stretch's length
+  int32_t per;                // a stretch's length (the last ones may be shorter)
 };
 
 // Runs of a sequence, keys and tiles of its run b.
@@ -81,9 +79,20 @@ __device__ __forceinline__ int tiles_of(const Args& a, int t, int off, int b) {
 }
 __device__ __forceinline__ int count_of(const Args& a, int tiles) { return a.split ? tiles + kOver : 1; }
 
+// Sum of x of this lane and those below.
+__device__ __forceinline__ int below(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  return x;
+}
+
 // All threads of the CTA; ends with a barrier.
 __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, N = a.n_seq;
+#pragma unroll 1
   for (int i = tid; i < N; i += nt) {
     const int64_t lo = a.q_start ? max64(0, min64(a.q_start[i], a.tokens)) : (int64_t)i * a.t;
     const int64_t hi = a.q_start ? max64(lo, min64(a.q_start[i + 1], a.tokens)) : lo + a.t;
@@ -93,43 +102,44 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
     p.off[i] = (int32_t)(len - (hi - lo));
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = warp; i < N; i += nt / 32) {
     const int t = p.n[i], off = p.off[i], runs = runs_of(a, t);
-    int64_t sum = 0;
+    int sum = 0;
+#pragma unroll 1
     for (int b = lane; b < runs; b += 32) sum += count_of(a, tiles_of(a, t, off, b));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) p.cum[i] = sum * a.n_heads;
   }
   __syncthreads();
   if (warp == 0) {
-    shared::warp_sums(p.cum, N);
+    int total = 0;
+#pragma unroll 1
+    for (int b = 0; b < N; b += 32) {
+      const int t = b + lane < N ? p.cum[b + lane] : 0, c = below(t, lane);
+      if (b + lane < N) p.cum[b + lane] = total + c - t;
+      total += __shfl_sync(0xffffffffu, c, 31);
+    }
+    if (lane == 0) p.cum[N] = total;
     __syncwarp();
-    const int64_t total = p.cum[N], ctas = min64(gridDim.x, total), c = blockIdx.x;
-    int64_t lo = 0, hi = 0, at = 0;
-    int seq = 0, h = 0, b = 0;
-    if (c < ctas) {
-      lo = quot(c * total, ctas);
-      hi = quot((c + 1) * total, ctas);
+    const int per = (uint32_t)(total + gridDim.x - 1) / gridDim.x, lo = min((int64_t)blockIdx.x * per, (int64_t)total);
+    int at = 0, seq = 0, h = 0, b = 0;
+    if (lo < total) {
       int x = 0, y = N - 1;  // the last sequence that begins at or before lo: empty ones end where they begin
+#pragma unroll 1
       while (x < y) {
         const int mid = (x + y + 1) / 2;
         if (p.cum[mid] <= lo) x = mid;
         else y = mid - 1;
       }
       seq = x;
-      const int64_t per = quot(p.cum[seq + 1] - p.cum[seq], a.n_heads);
-      h = (int)quot(lo - p.cum[seq], per);
-      at = lo - p.cum[seq] - h * per;
+      const int head = (uint32_t)(p.cum[seq + 1] - p.cum[seq]) / a.n_heads;
+      h = (uint32_t)(lo - p.cum[seq]) / head;
+      at = lo - p.cum[seq] - h * head;
       const int t = p.n[seq], off = p.off[seq];
+#pragma unroll 1
       for (;; b += 32) {  // 32 runs at a time
-        const int64_t n = count_of(a, tiles_of(a, t, off, b + lane));
-        int64_t sum = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += u;
-        }
+        const int n = count_of(a, tiles_of(a, t, off, b + lane)), sum = below(n, lane);
         const uint32_t in = __ballot_sync(0xffffffffu, at < sum);
         if (in) {
           const int k = __ffs(in) - 1;
@@ -145,9 +155,8 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
       p.h = h;
       p.run = b;
       p.at = at;
-      p.left = hi - lo;
-      p.total = total;
-      p.ctas = ctas;
+      p.left = min(per, total - lo);
+      p.per = per;
     }
   }
   __syncthreads();
@@ -171,25 +180,22 @@ struct Segment {
   __device__ int slot() const { return 2 * blockIdx.x + (tile0 == 0); }
 };
 
-// Walks the segments of one CTA; every role of the CTA walks alike.  Kept in shared
-// memory, a warp's own: registers are short.
+// Walks the segments of one CTA: one thread, which leaves them for the others.
 struct Walk {
-  int64_t at, left;
-  int32_t seq, h, run;
-  Segment g;
-  __device__ void begin(const Plan& p) {
-    at = p.at;
-    left = p.left;
-    seq = p.seq;
-    h = p.h;
-    run = p.run;
-  }
-  __device__ bool next(const Plan& p, const Args& a) {
-    Segment s;
+  const Plan& p;
+  const Args& a;
+  int32_t at, left, seq, h, run;
+  __device__ Walk(const Plan& plan, const Args& args)
+      : p(plan), a(args), at(p.at), left(p.left), seq(p.seq), h(p.h), run(p.run) {}
+  // The next one; without tiles behind the last.
+  __device__ Segment next() {
+    Segment s = {};
+#pragma unroll 1
     while (left > 0) {
+#pragma unroll 1
       while (p.n[seq] == 0) ++seq;  // what is left lies in a sequence further on
       const int t = p.n[seq], off = p.off[seq], n = tiles_of(a, t, off, run), count = count_of(a, n);
-      const int64_t take = min64(left, count - at), done = p.left - left;
+      const int take = min(left, count - at), done = p.left - left;
       s.seq = seq;
       s.h = h;
       s.t = t;
@@ -202,14 +208,12 @@ struct Walk {
       s.tile0 = 0;
       s.tiles = n;
       if (a.split) {
-        s.tile0 = (int)min64(at, n);
-        s.tiles = (int)min64(at + take, n) - s.tile0;
+        s.tile0 = min(at, n);
+        s.tiles = min(at + take, n) - s.tile0;
       }
       s.whole = s.tiles == n;
       if (!s.whole && s.tile0 == 0) {
-        // the CTA that has the unit's last tile
-        const int64_t last = quot(blockIdx.x * p.total, p.ctas) + done + n - 1;
-        s.pieces = (int)(quot((last + 1) * p.ctas - 1, p.total) - blockIdx.x) + 1;
+        s.pieces = (uint32_t)(done + n - 1) / p.per + 1;  // up to the CTA that has the unit's last tile
       }
       left -= take;
       at += take;
@@ -222,12 +226,10 @@ struct Walk {
           if (++h == a.n_heads) h = 0, ++seq;
         }
       }
-      if (s.tiles > 0) {
-        g = s;
-        return true;
-      }
+      if (s.tiles > 0) return s;
     }
-    return false;
+    s.tiles = 0;
+    return s;
   }
 };
 

@@ -516,7 +516,8 @@ int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, cons
  * finite, logits below 2^28 and values below 2^96 in magnitude; what lies past
  * its rows, and other sequences, may hold anything.  Equal calls give equal bits.
  * At most BPKV_SHARED_MAX_SEQ sequences, 2^30 tokens, rows of a sequence or rows
- * of H T keys (BPKV_EUNSUPPORTED for more, and for residency 1).
+ * of H T keys, and 2^31 tiles of 128 keys by 2 floor(128 / G) tokens and KV head
+ * (BPKV_EUNSUPPORTED for more, and for residency 1).
  * Workspace: bpkv_prompt_workspace_size bytes for the largest number of new
  * tokens that one sequence of the call may have, 256-byte aligned, with nothing
  * kept in it from call to call (calls that may run at the same time need one
