@@ -64,7 +64,6 @@ struct Smem {
   uint64_t turn[2];
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t q_full, q_empty, done, fin;
-  __align__(16) unsigned char turn_stage[BITS == 16 ? kSoftmaxWarps : 1][2048];
   float2 ml[2][kTile];  // each row's maximum and sum, where both streams hold the rows
 };
 
@@ -87,6 +86,24 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
 #pragma unroll 1
   for (uint32_t i = 0; i < kMbarRounds && !*abort && now_ns() - t0 <= kMbarNs; ++i)
     if (mbar_try(bar, parity)) return true;
+  *abort = 1;
+  return false;
+}
+
+// The same without the hardware's suspension of a waiting thread: where a hundred cycles count.
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  const uint64_t t0 = now_ns();
+#pragma unroll 1
+  for (uint32_t i = 0; i < kMbarRounds; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 63u) == 63u && (*abort || now_ns() - t0 > kMbarNs)) break;
+  }
   *abort = 1;
   return false;
 }
@@ -220,49 +237,15 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool mask
   l += l0 + l1;
 }
 
-// Sixteen words of this warp's rows, a row a lane, to sixteen bytes of four rows a
-// lane: lane q of four ends with the q-th four words of rows turned_row(0) .. (3).
-// Through shared memory, or by exchanges where there is no room.
-template <int BITS>
-__device__ __forceinline__ int turned_row(int i) {
-  const int lane = threadIdx.x & 31;
-  return BITS == 16 ? (lane >> 2) + 8 * i : (lane & ~3) + i;
-}
-template <int BITS>
-__device__ __forceinline__ void turn(uint32_t (&r)[16], unsigned char* stage) {
-  const int lane = threadIdx.x & 31, q = lane & 3;
-  if constexpr (BITS == 16) {
-    // a row's chunks in an order that keeps eight lanes' stores, and loads, in different banks
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-          make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = turned_row<BITS>(i);
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((q ^ ((row >> 1) & 3)) << 4));
-      r[4 * i] = v.x;
-      r[4 * i + 1] = v.y;
-      r[4 * i + 2] = v.z;
-      r[4 * i + 3] = v.w;
-    }
+// 32 bytes of a row; at an address that is only a multiple of 16 in two stores.
+__device__ __forceinline__ void store32(unsigned char* p, const uint32_t* w, bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
   } else {
-#pragma unroll
-    for (int u = 0; u < 4; u += 2)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 1 ? r[4 * u + i] : r[4 * u + 4 + i], 1);
-        if (q & 1) r[4 * u + i] = y;
-        else r[4 * u + 4 + i] = y;
-      }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t y = __shfl_xor_sync(0xffffffffu, q & 2 ? r[i] : r[8 + i], 2);
-      if (q & 2) r[i] = y;
-      else r[8 + i] = y;
-    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -403,7 +386,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         // Streams of their own rows take turns, a turn being the rest of O and the next S:
         // left alone they fall into step, and neither's products hide the other's softmax.
         auto begin_turn = [&] {
-          ok = ok && wait(smem_u32(&sm.turn[s]), (turns & 1) ^ (s ? 0 : 1), abort);
+          ok = ok && spin(smem_u32(&sm.turn[s]), (turns & 1) ^ (s ? 0 : 1), abort);
           ++turns;
           return ok;
         };
@@ -455,7 +438,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
             if (!await(use + 1)) break;
             if (other) skip(use + 2);
             const uint32_t vb = smem_desc(smem_u32(ring + (use + 1) % kStages * kStage), kTile * 128);
-            ok = ok && wait(smem_u32(&sm.p_half[s]), p_phase, abort);
+            ok = ok && spin(smem_u32(&sm.p_half[s]), p_phase, abort);
             if (!ok) break;
             fence_after();
 #pragma unroll
@@ -465,7 +448,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
               if (more) await(use + 2);
               begin_turn();
             }
-            ok = ok && wait(smem_u32(&sm.p_ready[s]), p_phase, abort);
+            ok = ok && spin(smem_u32(&sm.p_ready[s]), p_phase, abort);
             if (!ok) break;
             p_phase ^= 1;
             fence_after();
@@ -590,21 +573,13 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
       const bool writes = (dual || both || s == 0) && w4 * 32 < rows;
       const int c0 = both ? s * 64 : 0, c1 = both ? c0 + 64 : kD;
       const int64_t at = (int64_t)slot * a.slot_rows + (dual ? s * kTile : 0) + w4 * 32;
-      // The four rows that the lane stores, 16 bytes of every 64.
-      unsigned char* dst[4];
-      if (writes) {
-        unsigned char* base = whole ? reinterpret_cast<unsigned char*>(
-                                          a.out + (((int64_t)token * a.n_heads + h) * a.group) * kD + c0)
-                                    : reinterpret_cast<unsigned char*>(a.part_o + at * kD + c0);
-        const uint32_t tok_step = a.n_heads * a.group * kD * 2;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = turned_row<BITS>(i), x = (w4 * 32 + r) * a.group_inv >> 16;
-          dst[i] = base + (lane & 3) * 16 +
-                   (whole ? (uint64_t)x * tok_step + (w4 * 32 + r - x * a.group) * (kD * 2) : (uint64_t)r * (kD * 4));
-          if (w4 * 32 + r >= rows) dst[i] = nullptr;
-        }
-      }
+      // this thread's row, from channel c0 on
+      const int x = there ? tok : 0;
+      unsigned char* dst =
+          whole ? reinterpret_cast<unsigned char*>(
+                      a.out + ((((int64_t)token + x) * a.n_heads + h) * a.group + row - x * a.group) * kD + c0)
+                : reinterpret_cast<unsigned char*>(a.part_o + (at + lane) * kD + c0);
+      const bool aligned = !whole || (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
       __syncwarp();
       if (lane == 0) end_segment();
       else ++seg_no;
@@ -641,8 +616,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         } else if (row < rows && c0 == 0) {
           a.part_ml[at + lane] = make_float2(m, l);
         }
-        unsigned char* stage = sm.turn_stage[BITS == 16 ? warp - 4 : 0];
-        uint32_t o[32], w[16];
+        uint32_t o[32];
         tmem_ld32(o0, o);
 #pragma unroll 1
         for (int k = 0; k < c1 - c0; k += 32) {
@@ -658,26 +632,21 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
           }
-          auto store = [&](int off) {
-            turn<BITS>(w, stage);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (dst[i])
-                __stcs(reinterpret_cast<uint4*>(dst[i] + off), make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
-          };
           if (whole) {
+            uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
             if (k + 32 < c1 - c0) tmem_ld32(o0 + k + 32, o);  // comes while this part leaves
-            store(k * 2);
-          } else {
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = o[16 * part + i];
-              if (part && k + 32 < c1 - c0) tmem_ld32(o0 + k + 32, o);
-              store(k * 4 + 64 * part);
+            if (row < rows) {
+              store32(dst + k * 2, w, aligned);
+              store32(dst + k * 2 + 32, w + 8, aligned);
             }
+          } else {
+            if (row < rows) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) store32(dst + k * 4 + 32 * i, o + 8 * i, true);
+            }
+            if (k + 32 < c1 - c0) tmem_ld32(o0 + k + 32, o);
           }
         }
       }
