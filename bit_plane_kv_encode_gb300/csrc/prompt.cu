@@ -237,6 +237,12 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool mask
   l += l0 + l1;
 }
 
+__device__ __forceinline__ uint64_t normal_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // 32 bytes of a row; at an address that is only a multiple of 16 in two stores.
 __device__ __forceinline__ void store32(unsigned char* p, const uint32_t* w, bool aligned) {
   if (aligned) {
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
 
   if (warp < 4) {
     // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168; 8-bit rows:
-    // 128 x 48 + 256 x 200 + 128 x 64 of 512 x 128
+    // 128 x 48 + 256 x 184 + 128 x 96 of 512 x 128
     regs_fewer<BITS == 16 ? 80 : 48>();
     if (warp == 0) {
       if (elect_one()) {
@@ -337,7 +343,8 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         uint64_t* full = BITS == 16 ? sm.full : sm.code_full;
         uint64_t* empty = BITS == 16 ? sm.empty : sm.code_empty;
         uint32_t stage = 0, phase = 0, issued = 0;
-        const uint64_t policy = shared::evict_first_policy();
+        // keys that only one unit reads go through L2 before anything else
+        const uint64_t policy = a.once ? shared::evict_first_policy() : normal_policy();
         bool ok = true;
         while (next(ok)) {
           const Place at = place_of(a, sm.plan, g);
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     }
   } else if (warp < 4 + kSoftmaxWarps) {
     // ---- softmax of stream s, a thread per row
-    regs_more<BITS == 16 ? 208 : 200>();
+    regs_more<BITS == 16 ? 208 : 184>();
     const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     if (a.split && s == 0 && row == 0) a.cuts[blockIdx.x] = cut;
   } else if constexpr (BITS == 8) {
     // ---- codes to bf16, all four warps each tile
-    regs_fewer<64>();
+    regs_fewer<96>();
     // A thread a row, in chunks of 16 codes in such an order that eight neighbouring
     // threads' loads, and their stores, meet in no bank.
     const int r = tid - 384, r7 = r & 7;
@@ -672,9 +679,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const uint32_t from = n % kCodeStages, to = n % kStages;
-          ok = wait(smem_u32(&sm.code_full[from]), (n / kCodeStages) & 1, abort) &&
-               wait(smem_u32(&sm.empty[to]), ((n / kStages) & 1) ^ 1, abort);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, wait(smem_u32(&sm.code_full[from]), (n / kCodeStages) & 1, abort));
           if (!ok) break;
           const unsigned char* src = codes + from * kCodeStage;
           unsigned char* dst = ring + to * kStage;
@@ -683,28 +688,38 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
           // 2^(e + 120), as far as bf16 has it; the rest below.  Rows past the last key
           // may hold anything: zeros, so that 0 x does not become NaN
           const uint32_t f = twice2(min(e, 7) + 120);
-          const bool big = __any_sync(0xffffffffu, e > 7);
-          const uint32_t f2 = twice2(max(e - 7, 0));
+          uint4 x[8], y[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            uint4 x = *reinterpret_cast<const uint4*>(src + (src0 ^ (i << 4)));
-            if (!there) x = make_uint4(0, 0, 0, 0);
-            uint4 a0 = make_uint4(bf16_codes<0>(x.x, f), bf16_codes<1>(x.x, f), bf16_codes<0>(x.y, f), bf16_codes<1>(x.y, f));
-            uint4 a1 = make_uint4(bf16_codes<0>(x.z, f), bf16_codes<1>(x.z, f), bf16_codes<0>(x.w, f), bf16_codes<1>(x.w, f));
-            if (big) {
-              a0 = make_uint4(times(a0.x, f2), times(a0.y, f2), times(a0.z, f2), times(a0.w, f2));
-              a1 = make_uint4(times(a1.x, f2), times(a1.y, f2), times(a1.z, f2), times(a1.w, f2));
-            }
+            x[i] = *reinterpret_cast<const uint4*>(src + (src0 ^ (i << 4)));
+            if (!there) x[i] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[2 * i] = make_uint4(bf16_codes<0>(x[i].x, f), bf16_codes<1>(x[i].x, f), bf16_codes<0>(x[i].y, f),
+                                  bf16_codes<1>(x[i].y, f));
+            y[2 * i + 1] = make_uint4(bf16_codes<0>(x[i].z, f), bf16_codes<1>(x[i].z, f), bf16_codes<0>(x[i].w, f),
+                                      bf16_codes<1>(x[i].w, f));
+          }
+          if (__any_sync(0xffffffffu, e > 7)) {
+            const uint32_t f2 = twice2(max(e - 7, 0));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              y[i] = make_uint4(times(y[i].x, f2), times(y[i].y, f2), times(y[i].z, f2), times(y[i].w, f2));
+          }
+          if (lane == 0) mbar_arrive(smem_u32(&sm.code_empty[from]));
+          // only the stores wait for the stage
+          ok = __all_sync(0xffffffffu, wait(smem_u32(&sm.empty[to]), ((n / kStages) & 1) ^ 1, abort));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
             const uint32_t at = dst0 ^ ((i & 4) << 12) ^ ((i & 3) << 5);
-            *reinterpret_cast<uint4*>(dst + at) = a0;
-            *reinterpret_cast<uint4*>(dst + (at ^ 16)) = a1;
+            *reinterpret_cast<uint4*>(dst + at) = y[2 * i];
+            *reinterpret_cast<uint4*>(dst + (at ^ 16)) = y[2 * i + 1];
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&sm.full[to]));
-            mbar_arrive(smem_u32(&sm.code_empty[from]));
-          }
+          if (lane == 0) mbar_arrive(smem_u32(&sm.full[to]));
         }
       }
       __syncwarp();
@@ -855,6 +870,7 @@ cudaError_t launch(Args& a, const Maps& maps, int64_t longest, int64_t keys, voi
   a.part_ml = reinterpret_cast<float2*>(w + sp.ml);
   a.part_o = reinterpret_cast<float*>(w + sp.o);
   a.slot_rows = sp.slot_rows;
+  a.once = longest <= 2 * a.run;
   a.status = static_cast<int32_t*>(ws);
   const int64_t units = prompt_units(a.tokens, a.n_seq, a.n_heads, a.group);
   const int64_t tiles = max64(1, (keys + kTile - 1) / kTile);

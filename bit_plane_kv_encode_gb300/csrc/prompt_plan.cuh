@@ -52,6 +52,7 @@ struct Args {
   int32_t run;             // tokens of a stream: 128 / G
   uint32_t group_inv;      // 2^16 / group rounded up: x group_inv >> 16 is x / group for x below 256
   int32_t split;           // units may be cut
+  int32_t once;            // a sequence's tokens are one unit of a KV head
   int32_t slot_rows;       // rows of a slot of partial rows
   float* part_o;           // [slots][slot_rows][D]
   float2* part_ml;         // [slots][slot_rows] maximum (log2 domain) and sum
