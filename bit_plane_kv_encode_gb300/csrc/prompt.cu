@@ -735,16 +735,15 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
 }
 
 // The rows of units that were cut: out = sum_pieces 2^(m - M) o / sum_pieces 2^(m - M) l,
-// a warp a row, eight pieces at a time.
+// a warp a row, four pieces at a time.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinDeep = 8;
+constexpr int kJoinDeep = 4;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) k_prompt_join(const __grid_constant__ Args a) {
   pdl_enter();
   const Cut cut = a.cuts[blockIdx.x];
-  const int lane = threadIdx.x & 31, rows = cut.tokens * a.group;
-  if (cut.pieces == 0) return;
-  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows; r += gridDim.y * kJoinWarps) {
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (cut.pieces > 0 && r < cut.tokens * a.group) {
     const int x = r * a.group_inv >> 16, s = x >= a.run;
     const int64_t in = r + s * (kTile - a.run * a.group);
     float M = -INFINITY, L = 0.f;
@@ -881,7 +880,7 @@ cudaError_t launch(Args& a, const Maps& maps, int64_t longest, int64_t keys, voi
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_prompt<BITS>, dim3(ctas), dim3(Shape<BITS>::kThreads), (size_t)kSmem<BITS>, st, a, maps);
   if (e != cudaSuccess || !a.split) return e;
-  return launch_pdl(k_prompt_join, dim3(ctas, 4), dim3(kJoinWarps * 32), 0, st, a);
+  return launch_pdl(k_prompt_join, dim3(ctas, a.slot_rows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a);
 }
 
 }  // namespace

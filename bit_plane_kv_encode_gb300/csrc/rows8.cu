@@ -147,19 +147,18 @@ __device__ __forceinline__ bool accept_fits(int64_t start, int32_t count, int32_
 
 // As k_rows8_append, but of a sequence's t tokens only the first count rows are
 // there, and each goes by way of the path: one more dependent load before the
-// row's own, which the R rows of a group take together.
+// row's own.  A thread a row finds out where it comes from and goes.
 template <int R>
 __global__ void __launch_bounds__(kR8Threads) k_rows8_accept(const __grid_constant__ AcceptArgs a) {
   pdl_enter();
   __shared__ uint8_t s_exp[2][kR8Groups * R];
-  __shared__ int64_t s_dst[kR8Groups * R];  // -1: not written
+  __shared__ int64_t s_from[kR8Groups * R], s_dst[kR8Groups * R];  // -1: not written
   const int tid = threadIdx.x, l16 = tid & 15, grp = tid >> 4;
   const int64_t rows = (int64_t)a.n_seq * a.n_heads * a.t, r0 = (int64_t)blockIdx.x * (kR8Groups * R);
-  int64_t from[R], dst[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t r = r0 + i * kR8Groups + grp;
-    from[i] = dst[i] = -1;
+  bool mine = false;
+  if (tid < kR8Groups * R) {
+    const int64_t r = r0 + tid;
+    int64_t from = -1, dst = -1;
     if (r < rows) {
       int64_t unit, j, s, h;
       split(r, a.t, unit, j);
@@ -168,25 +167,31 @@ __global__ void __launch_bounds__(kR8Threads) k_rows8_accept(const __grid_consta
       const int32_t n = a.count[s];
       const int32_t node = a.path ? a.path[s * a.t + j] : (int32_t)j;
       const bool fits = accept_fits(p, n, a.t, a.c.cap);
-      const bool there = fits && j < n, known = node >= 0 && node < a.t;
-      if (there) {
-        from[i] = unit * a.t + min(max(node, 0), a.t - 1);
-        dst[i] = unit * a.c.cap + p + j;
+      if (fits && j < n) {
+        mine = true;
+        from = unit * a.t + min(max(node, 0), a.t - 1);
+        dst = unit * a.c.cap + p + j;
+        if (h == 0 && (node < 0 || node >= a.t)) set_status(a.status, BPKV_DEV_OVERFLOW);
       }
-      if (l16 == 0 && h == 0) {
-        if ((there && !known) || (j == 0 && !fits)) set_status(a.status, BPKV_DEV_OVERFLOW);
-        if (j == 0 && fits && !a.bump) a.c.seq_len[s] = p + n;
+      if (h == 0 && j == 0) {
+        if (!fits) set_status(a.status, BPKV_DEV_OVERFLOW);
+        else if (!a.bump) a.c.seq_len[s] = p + n;
       }
     }
-    if (l16 == 0) s_dst[i * kR8Groups + grp] = dst[i];
+    s_from[tid] = from;
+    s_dst[tid] = dst;
   }
+  if (!__syncthreads_or(mine)) return;  // padding
   uint4 w[R][2];
+  int64_t dst[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
+    const int64_t from = s_from[i * kR8Groups + grp];
+    dst[i] = s_dst[i * kR8Groups + grp];
     w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-    if (from[i] >= 0) {
-      w[i][0] = __ldg(reinterpret_cast<const uint4*>(a.k_new + from[i] * kD + l16 * 8));
-      w[i][1] = __ldg(reinterpret_cast<const uint4*>(a.v_new + from[i] * kD + l16 * 8));
+    if (from >= 0) {
+      w[i][0] = __ldg(reinterpret_cast<const uint4*>(a.k_new + from * kD + l16 * 8));
+      w[i][1] = __ldg(reinterpret_cast<const uint4*>(a.v_new + from * kD + l16 * 8));
     }
   }
 #pragma unroll
