@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["encode.cu", "depths.cu", "scan.cu", "select.cu", "attend.cu", "abi.cu", "noalloc.cu",
-           "calibrate.cu", "vdepth.cu", "rows8.cu", "qkv.cu", "shared.cu", "shared_few.cu", "prompt.cu"]
+           "calibrate.cu", "vdepth.cu", "rows8.cu", "qkv.cu", "shared.cu", "shared_few.cu", "prompt.cu", "prompt_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -31,6 +31,9 @@ int64_t prompt_units(int64_t tokens, int64_t n_seq, int64_t n_heads, int64_t gro
 
 namespace prompt {
 
+template <int BITS>
+cudaError_t launch_tree_few(const FewArgs& a, int ctas, cudaStream_t st);
+
 namespace {
 
 using namespace tc;
@@ -211,13 +214,14 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool mask
     l *= f;
     if (up) m = top;
 #pragma unroll 1
-    for (int k = 0; k < kD; k += 16) {
-      uint32_t o[16];
-      tmem_ld16(to + k, o);
+    for (int k = 0; k < kD; k += 32) {
+      uint32_t o[32];
+      tmem_ld32(to + k, o);
       wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
       tmem_st16(to + k, o);
+      tmem_st16(to + k + 16, o + 16);
     }
   }
   uint32_t w[32];
@@ -956,9 +960,45 @@ cudaError_t launch_prompt(const bpkv_prompt_args& p, void* ws, cudaStream_t st) 
   return launch<16>(a, maps, T, T, ws, st);
 }
 
+// CTAs of a cluster that streams a unit (16 rows at most of a sequence and KV head) of a
+// tree, 0: the tensor cores take the call.  As many CTAs as leave all units resident at
+// once (clusters of 8 find room for 12 at least).
+//
+// Streamed / tensor cores, in us, trees of t nodes of 4 heads for each of 8 KV heads, bf16
+// rows (8-bit rows in brackets).  Up to 16 rows the keys are read once either way:
+//   1 sequence, t = 1, 300 keys 5.0 / 8.9 (5.8 / 11.2), 4000 6.8 / 12.0 (7.0 / 14.5), 64000
+//   42 / 44 (39 / 50); 16 sequences of 4000 39 / 45 (22 / 54); 64 of 4000 146 / 163 (88 / 187);
+//   t = 4: 1 of 4000 10.1 / 13.0 (9.9 / 14.8), of 16000 19.1 / 17.4 (18.7 / 22.0), of 64000
+//   53 / 45 (52 / 50); 4 of 64000 151 / 154 (97 / 161); 64 of 1000 53 / 52 (47 / 77), of 4000
+//   158 / 163 (112 / 188).
+// More rows read them again, from L2, for every 16:
+//   t = 8: 1 of 1000 8.5 / 10.8 (8.5 / 13.4), of 4000 13.1 / 12.6 (12.9 / 15.2), of 16000
+//   31 / 18 (30 / 23); 4 of 1000 10.4 / 12.7 (10.4 / 15.8), of 4000 19.5 / 17.9 (19.0 / 23.6);
+//   16 of 300 15.2 / 10.4 (16.0 / 12.7); t = 16: 1 of 4000 13.2 / 13.5 (12.9 / 16.2); 4 of 1000
+//   12.2 / 13.6 (11.8 / 16.6), of 4000 28 / 20 (28 / 25).
+int few_ctas(int bits, int64_t units, int rows, int groups, int64_t keys) {
+  const int64_t n = units * groups;
+  const int ctas = n <= 12 ? 8 : n <= 32 ? 4 : n <= 72 ? 2 : 1;
+  if (keys < 600 && ctas == 8) return 4;  // the wider cluster's barriers cost what it saves
+  if (groups > 1) return n <= kSms && keys <= (bits == 16 ? 1000 : 2000) * ctas ? ctas : 0;
+  // 64 to 96 CTAs with two products for each load of a tile
+  if (bits == 16 && rows > 8 && ctas == 8 && keys > 12000) return 0;
+  return ctas;
+}
+
 template <typename C>
 static cudaError_t tree(const C& c, int32_t t, const uint64_t* mask, const uint16_t* q, uint16_t* out, void* ws,
                         cudaStream_t st) {
+  constexpr int BITS = sizeof(C) == sizeof(bpkv_cache) ? 16 : 8;
+  const PromptRows r = rows_of(c);
+  const int32_t per = t * c.group <= 8 ? 8 : 16, groups = (t * c.group + per - 1) / per;
+  const int ctas = few_ctas(BITS, (int64_t)c.n_seq * c.n_kv_heads, t * c.group, groups, c.n_max);
+  if (ctas) {
+    const FewArgs a = {r.len,   mask,     q,          out,     {{r.k, r.v}}, {{r.kexp, r.vexp}},
+                       r.cap,   c.n_seq,  c.n_kv_heads, c.group, t,            groups,
+                       per};
+    return launch_tree_few<BITS>(a, ctas, st);
+  }
   Args a = {};
   Maps maps;
   a.tree = mask;
@@ -970,8 +1010,7 @@ static cudaError_t tree(const C& c, int32_t t, const uint64_t* mask, const uint1
   a.tokens = (int64_t)c.n_seq * t;
   const int64_t heads = (int64_t)c.n_kv_heads * c.group;
   if (!map_q(&maps.q, q, a.tokens, heads, heads * kD, c.group, kTile / c.group)) return cudaErrorInvalidValue;
-  constexpr int BITS = sizeof(C) == sizeof(bpkv_cache) ? 16 : 8;
-  return over_cache<BITS>(a, maps, rows_of(c), t, ws, st);
+  return over_cache<BITS>(a, maps, r, t, ws, st);
 }
 static_assert(sizeof(bpkv_cache) != sizeof(bpkv_rows8), "which of the two a template has");
 

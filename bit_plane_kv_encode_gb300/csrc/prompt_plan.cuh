@@ -60,6 +60,19 @@ struct Args {
   int32_t* status;
 };
 
+// What the streaming kernel of trees takes (prompt_few.cu).
+struct FewArgs {
+  const int64_t* len;
+  const uint64_t* tree;       // NULL: a chain
+  const uint16_t* q;
+  uint16_t* out;
+  const void* rows[1][2];     // K, V
+  const uint8_t* exps[1][2];  // scale exponents of 8-bit rows
+  int64_t cap;
+  int32_t n_seq, n_heads, group, t;
+  int32_t groups, per;        // a tree's query rows, per (8 or 16) at a time
+};
+
 // Counts are below 2^31: the host makes sure.
 struct Plan {
   int32_t cum[kMaxSeq + 1];   // what the sequences before count together

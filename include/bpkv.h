@@ -511,7 +511,7 @@ int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, cons
  * q . k / sqrt(D), every query head attends over the keys that its token sees,
  *   o = sum_x softmax_x(q . k_x / sqrt(D)) v_x,
  * zeros where a token sees none.  Logits, softmax statistics and sums are
- * float32; the softmax weights enter the products as bf16.  8-bit rows count as
+ * float32; the softmax weights enter the products as bf16, or as halves.  8-bit rows count as
  * the values they stand for.  A sequence's keys, values and rows of q must be
  * finite, logits below 2^28 and values below 2^96 in magnitude; what lies past
  * its rows, and other sequences, may hold anything.  Equal calls give equal bits.
