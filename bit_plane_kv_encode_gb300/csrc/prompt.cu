@@ -214,14 +214,13 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool mask
     l *= f;
     if (up) m = top;
 #pragma unroll 1
-    for (int k = 0; k < kD; k += 32) {
-      uint32_t o[32];
-      tmem_ld32(to + k, o);
+    for (int k = 0; k < kD; k += 16) {
+      uint32_t o[16];
+      tmem_ld16(to + k, o);
       wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
       tmem_st16(to + k, o);
-      tmem_st16(to + k + 16, o + 16);
     }
   }
   uint32_t w[32];

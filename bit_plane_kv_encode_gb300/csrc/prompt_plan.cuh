@@ -76,7 +76,7 @@ struct FewArgs {
 // Counts are below 2^31: the host makes sure.
 struct Plan {
   int32_t cum[kMaxSeq + 1];   // what the sequences before count together
-  int32_t start[kMaxSeq];     // a sequence's first token in q
+  int32_t start[kMaxSeq + 1]; // a sequence's first token in q
   int32_t n[kMaxSeq];         // its new tokens
   int32_t off[kMaxSeq];       // keys before the first of them (negative: that many of them have none)
   // where this CTA's stretch begins
@@ -107,23 +107,39 @@ __device__ __forceinline__ int below(int x, int lane) {
 __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, N = a.n_seq;
 #pragma unroll 1
-  for (int i = tid; i < N; i += nt) {
-    const int64_t lo = a.q_start ? max64(0, min64(a.q_start[i], a.tokens)) : (int64_t)i * a.t;
-    const int64_t hi = a.q_start ? max64(lo, min64(a.q_start[i + 1], a.tokens)) : lo + a.t;
-    const int64_t len = a.len ? shared::tokens_of(a.len[i], a.cap) : hi - lo;
-    p.start[i] = (int32_t)lo;
-    p.n[i] = (int32_t)(hi - lo);
-    p.off[i] = (int32_t)(len - (hi - lo));
+  for (int i = tid; i <= N; i += nt) {
+    p.start[i] = a.q_start ? (int32_t)max64(0, min64(a.q_start[i], a.tokens)) : i * a.t;
+    if (i < N) p.off[i] = a.len ? (int32_t)shared::tokens_of(a.len[i], a.cap) : 0;
+  }
+  __syncthreads();
+  if (a.q_start && warp == 0) {  // one that lies before the last one's counts as that: no two sequences share a token
+    int top = 0;
+#pragma unroll 1
+    for (int b = 0; b <= N; b += 32) {
+      int x = b + lane <= N ? p.start[b + lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x = max(x, u);
+      }
+      x = max(x, top);
+      if (b + lane <= N) p.start[b + lane] = x;
+      top = __shfl_sync(0xffffffffu, x, 31);
+    }
   }
   __syncthreads();
 #pragma unroll 1
   for (int i = warp; i < N; i += nt / 32) {
-    const int t = p.n[i], off = p.off[i], runs = runs_of(a, t);
+    const int t = p.start[i + 1] - p.start[i], off = a.len ? p.off[i] - t : 0, runs = runs_of(a, t);
     int sum = 0;
 #pragma unroll 1
     for (int b = lane; b < runs; b += 32) sum += count_of(a, tiles_of(a, t, off, b));
     sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) p.cum[i] = sum * a.n_heads;
+    if (lane == 0) {
+      p.n[i] = t;
+      p.off[i] = off;
+      p.cum[i] = sum * a.n_heads;
+    }
   }
   __syncthreads();
   if (warp == 0) {

@@ -8,7 +8,10 @@ Bounds.  With p the exact softmax weights, A = sum p |v| and o = sum p v:
     / sqrt(D) at most, which moves a weight by B and the sum by B: 2 B A;
   - sums over n keys in float32, n 2^-23 A; exp2 2^-21;
   - the output is bf16: 2^-8 |o|.
-8-bit rows count as the values they stand for, which bf16 holds exactly."""
+8-bit rows count as the values they stand for, which bf16 holds exactly; where they are
+streamed, a weight times its row's scale 2^e is a half in which the largest is 2^11 or
+more: off by 2^-11 of itself, and by 2^-25 (half the smallest step) of a code of 448 at
+most, together n 2^-27 of the largest p 2^e."""
 import math
 
 import pytest
@@ -19,8 +22,8 @@ pytestmark = pytest.mark.gpu
 D = 128
 
 
-def attention(q, k, v, sees):
-    """(o, bound) in 64 bits of q [t][H][G][D] over k, v [H][n][D], sees [t][n]."""
+def attention(q, k, v, sees, scale=None):
+    """(o, bound) in 64 bits of q [t][H][G][D] over k, v [H][n][D], sees [t][n]; scale [H][n]: of 8-bit rows of v."""
     n = k.shape[1]
     if n == 0:
         o = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
@@ -32,6 +35,8 @@ def attention(q, k, v, sees):
     o, A = w @ v, w @ v.abs()
     B = 130 * 2.0 ** -24 * ((qd.abs() @ k.abs().transpose(-1, -2)) * sees).amax(-1, keepdim=True) / math.sqrt(D)
     tol = (2.0 ** -8 + 2 * B + n * 2.0 ** -23 + 2.0 ** -21) * A + 2.0 ** -8 * o.abs() + 1e-30
+    if scale is not None:
+        tol = tol + n * 2.0 ** -27 * (w * scale[:, None, None]).amax(-1, keepdim=True)
     return o.permute(2, 0, 1, 3), tol.permute(2, 0, 1, 3)
 
 
@@ -142,9 +147,14 @@ def test_any_bound_of_the_lengths(pk, bits, n_max):
     run_prompt(pk, "cache", [50, 70], [1500, 2000], 2, 4, seed=3, bits=bits, n_max=n_max)
 
 
+WAYS = [None, 32768]
+
+
 def run_tree(pk, bits, N, t, H, G, lens, seed=0, tree="random", n_max=None):
+    """One call against the formula.  n_max: what the host knows of the lengths, which decides whether a cluster streams
+    a tree's rows or, above 16 rows, the tensor cores take it (32768)."""
     g = torch.Generator(device="cuda").manual_seed(seed)
-    cap = max(512, (max(lens) + 511) // 512 * 512)
+    cap = max(512, (max(max(lens), n_max or 0) + 511) // 512 * 512)
     k, v = draw_rows(g, N, H, cap)
     c, vals = make_cache(pk, bits, G, cap, lens, k, v)
     if n_max is not None:
@@ -171,7 +181,7 @@ def run_tree(pk, bits, N, t, H, G, lens, seed=0, tree="random", n_max=None):
         sees = torch.ones((t, max(n, t)), dtype=torch.bool, device="cuda")
         sees[:, max(n, t) - t:] = bit[i]
         sees = sees[:, max(n, t) - n:]  # a short sequence's first nodes have no rows
-        want, tol = attention(q[i], vals[0][i, :, :n], vals[1][i, :, :n], sees)
+        want, tol = attention(q[i], vals[0][i, :, :n], vals[1][i, :, :n], sees, None if bits == 16 else vals[2][i, :, :n])
         check(out[i], want, tol, f"sequence {i}")
     return dict(c=c, mask=mask, q=q, out=out, ws=ws, fn=fn)
 
@@ -179,29 +189,34 @@ def run_tree(pk, bits, N, t, H, G, lens, seed=0, tree="random", n_max=None):
 @pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("tree", ["chain", "random", "full", "none"])
 @pytest.mark.parametrize("t", [1, 2, 8, 32, 33, 64])
-def test_trees(pk, bits, tree, t):
-    run_tree(pk, bits, 3, t, 2, 4, [t, 500, 130 + t], seed=t, tree=tree)
+@pytest.mark.parametrize("n_max", WAYS)
+def test_trees(pk, bits, tree, t, n_max):
+    run_tree(pk, bits, 3, t, 2, 4, [t, 500, 130 + t], seed=t, tree=tree, n_max=n_max)
 
 
 @pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("G,t", [(1, 64), (2, 64), (3, 50), (5, 64), (6, 7), (7, 64), (8, 64), (8, 16), (8, 17)])
-def test_tree_groups(pk, bits, G, t):
-    run_tree(pk, bits, 2, t, 1, G, [1000, 4097], seed=G)
+@pytest.mark.parametrize("n_max", WAYS)
+def test_tree_groups(pk, bits, G, t, n_max):
+    run_tree(pk, bits, 2, t, 1, G, [1000, 4097], seed=G, n_max=n_max)
 
 
 @pytest.mark.parametrize("bits", [16, 8])
-def test_tree_at_every_place_of_a_tile(pk, bits):
+@pytest.mark.parametrize("n_max", WAYS)
+def test_tree_at_every_place_of_a_tile(pk, bits, n_max):
     """The tree begins and ends inside tiles, on their edges and across them."""
     t = 40
     lens = [t + x for x in (0, 1, 23, 63, 64, 65, 87, 88, 89, 90, 127, 128, 129, 200, 216, 217)]
-    run_tree(pk, bits, len(lens), t, 1, 4, lens, seed=5)
+    run_tree(pk, bits, len(lens), t, 1, 4, lens, seed=5, n_max=n_max)
+    run_tree(pk, bits, len(lens), 3, 1, 4, [x - t + 3 for x in lens], seed=6, n_max=n_max)
 
 
 @pytest.mark.parametrize("bits", [16, 8])
-def test_trees_of_short_sequences(pk, bits):
+@pytest.mark.parametrize("n_max", WAYS)
+def test_trees_of_short_sequences(pk, bits, n_max):
     """Fewer rows than nodes: the first nodes have none."""
-    run_tree(pk, bits, 5, 20, 2, 4, [0, 1, 19, 20, 21], seed=7)
-    run_tree(pk, bits, 4, 64, 1, 8, [0, 1, 63, 65], seed=8)
+    run_tree(pk, bits, 5, 20, 2, 4, [0, 1, 19, 20, 21], seed=7, n_max=n_max)
+    run_tree(pk, bits, 4, 64, 1, 8, [0, 1, 63, 65], seed=8, n_max=n_max)
 
 
 @pytest.mark.parametrize("bits", [16, 8])
