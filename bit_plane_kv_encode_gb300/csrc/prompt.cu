@@ -82,20 +82,38 @@ struct Maps {
 
 // Waits for the phase of the given parity to complete.  Gives up (false) after some
 // seconds, raising *abort, or once another wait of the CTA has.  Short: it stands in
-// many places, and instructions that are not in the cache cost more than the wait.
+// many places, and instructions that are not in the cache cost more than the wait.  The
+// SM's own clock bounds it: reading the global timer takes longer than most waits.
+constexpr int64_t kWaitCycles = 4000000000;
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
   if (mbar_try(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
+  const int64_t t0 = clock64();
 #pragma unroll 1
-  for (uint32_t i = 0; i < kMbarRounds && !*abort && now_ns() - t0 <= kMbarNs; ++i)
+  for (uint32_t i = 0; i < kMbarRounds; ++i) {
     if (mbar_try(bar, parity)) return true;
+    if (*abort || clock64() - t0 > kWaitCycles) break;
+  }
+  *abort = 1;
+  return false;
+}
+
+// The same for waits that are long and not urgent: the others keep the issue slots.
+template <int NS>
+__device__ __forceinline__ bool doze(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  const int64_t t0 = clock64();
+#pragma unroll 1
+  for (uint32_t i = 0; i < kMbarRounds; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if (*abort || clock64() - t0 > kWaitCycles) break;
+    __nanosleep(NS);
+  }
   *abort = 1;
   return false;
 }
 
 // The same without the hardware's suspension of a waiting thread: where a hundred cycles count.
 __device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-  const uint64_t t0 = now_ns();
+  const int64_t t0 = clock64();
 #pragma unroll 1
   for (uint32_t i = 0; i < kMbarRounds; ++i) {
     uint32_t done;
@@ -105,7 +123,7 @@ __device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, volatile uin
         : "r"(bar), "r"(parity)
         : "memory");
     if (done) return true;
-    if ((i & 63u) == 63u && (*abort || now_ns() - t0 > kMbarNs)) break;
+    if ((i & 63u) == 63u && (*abort || clock64() - t0 > kWaitCycles)) break;
   }
   *abort = 1;
   return false;
@@ -336,9 +354,9 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
   auto end_segment = [&] { mbar_arrive(smem_u32(&sm.seg_empty[seg_no++ % kSegments])); };
 
   if (warp < 4) {
-    // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168; 8-bit rows:
+    // registers: 128 x 96 + 256 x 200 of the launch's 384 x 168; 8-bit rows:
     // 128 x 48 + 256 x 184 + 128 x 96 of 512 x 128
-    regs_fewer<BITS == 16 ? 80 : 48>();
+    regs_fewer<BITS == 16 ? 96 : 48>();
     if (warp == 0) {
       if (elect_one()) {
         // ---- loads: K then V of every tile
@@ -493,12 +511,12 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         for (;; ++seg_no) {
           const uint32_t i = seg_no % kSegments;
           g = walk.next();
-          ok = wait(smem_u32(&sm.seg_empty[i]), ((seg_no / kSegments) & 1) ^ 1, abort);
+          ok = doze<100>(smem_u32(&sm.seg_empty[i]), ((seg_no / kSegments) & 1) ^ 1, abort);
           if (!ok) break;
           sm.seg[i] = g;
           mbar_arrive(smem_u32(&sm.seg_full[i]));
           if (g.tiles == 0) break;
-          if (seg_no > 0) ok = wait(smem_u32(&sm.q_empty), (seg_no - 1) & 1, abort);
+          if (seg_no > 0) ok = doze<100>(smem_u32(&sm.q_empty), (seg_no - 1) & 1, abort);
           if (!ok) break;
           const int n = g.dual ? 2 : 1;
           mbar_expect_tx(bar, 2 * n * bytes);
@@ -515,7 +533,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     }
   } else if (warp < 4 + kSoftmaxWarps) {
     // ---- softmax of stream s, a thread per row
-    regs_more<BITS == 16 ? 208 : 184>();
+    regs_more<BITS == 16 ? 200 : 184>();
     const int s = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
