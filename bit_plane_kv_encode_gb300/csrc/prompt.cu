@@ -231,9 +231,10 @@ __device__ __forceinline__ float look(float* x, bool masked, uint32_t see0, uint
 __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool masked, const Sees& sees, bool first,
                                              uint32_t half, float& m, float& l) {
   float x[64], y[64];
-  load_half(ts, x);
+  tmem_ld32(ts, reinterpret_cast<uint32_t*>(x));
+  tmem_ld32(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
+  load_half(ts + 64, y);
   wait_ld();
-  load_half(ts + 64, y);  // while the first is looked at
   float top = look(x, masked, sees.w[0], sees.w[1]);
   wait_ld();
   top = fmaxf(top, look(y, masked, sees.w[2], sees.w[3]));
