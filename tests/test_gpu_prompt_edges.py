@@ -391,3 +391,24 @@ def test_drafting_loop(pk, bits):
             c.seq_len.copy_(torch.tensor(lens))
             c.c.n_max = max(lens)
         assert c.seq_len.tolist() == lens and pk.bpkv_read_status(tw) == 0
+
+
+def test_drafted_tokens_rolled_back(pk):
+    """A Cache whose length is set back behind drafted tokens, and appended to again, holds what one does that never saw
+    them: rows, planes and scales."""
+    H, n, t, keep, more = 2, 100, 40, 3, 50
+    g = torch.Generator(device="cuda").manual_seed(8)
+    k, v = draw_rows(g, 1, H, n + t + more)
+    c, want = pk.Cache(1, H, 4, 512), pk.Cache(1, H, 4, 512)
+    c.append(k[:, :, :n].contiguous(), v[:, :, :n].contiguous())
+    c.append(k[:, :, n:n + t].contiguous() * 8, v[:, :, n:n + t].contiguous())  # larger keys: other scales
+    c.seq_len.fill_(n + keep)
+    c.c.n_max = n + keep
+    rest = [x[:, :, n + t:].contiguous() for x in (k, v)]
+    c.append(*rest)
+    want.append(torch.cat((k[:, :, :n], k[:, :, n:n + keep] * 8), 2), v[:, :, :n + keep].contiguous())
+    want.append(*rest)
+    end, nb = n + keep + more, (n + keep + more + 63) // 64
+    assert c.seq_len.tolist() == want.seq_len.tolist() == [end]
+    assert torch.equal(c.k_rows[:, :, :end], want.k_rows[:, :, :end]) and torch.equal(c.v_rows[:, :, :end], want.v_rows[:, :, :end])
+    assert torch.equal(c.planes[..., :nb], want.planes[..., :nb]) and torch.equal(c.scales[..., :nb], want.scales[..., :nb])
