@@ -46,7 +46,7 @@ int64_t prompt_units(int64_t tokens, int64_t n_seq, int64_t n_heads, int64_t gro
 namespace prompt {
 
 template <int BITS>
-cudaError_t launch_tree_few(const FewArgs& a, int ctas, cudaStream_t st);
+cudaError_t launch_few_tokens(const FewArgs& a, int ctas, cudaStream_t st);
 
 namespace {
 
@@ -970,31 +970,14 @@ PromptRows rows_of(const bpkv_rows8& c) { return {c.k8, c.v8, c.kexp, c.vexp, c.
 
 }  // namespace
 
-cudaError_t launch_prompt(const bpkv_prompt_args& p, void* ws, cudaStream_t st) {
-  Args a = {};
-  Maps maps;
-  a.q_start = p.q_start;
-  a.out = p.out;
-  a.tokens = p.n_tokens;
-  a.n_seq = p.n_seq;
-  a.n_heads = p.n_kv_heads;
-  a.group = p.group;
-  const int64_t H = p.n_kv_heads, T = p.n_tokens;
-  if (!map_q(&maps.q, p.q, T, H * p.group, p.ld_q, p.group, kTile / p.group)) return cudaErrorInvalidValue;
-  if (p.cache) return over_cache<16>(a, maps, rows_of(*p.cache), T, ws, st);
-  if (p.rows8) return over_cache<8>(a, maps, rows_of(*p.rows8), T, ws, st);
-  const bool by_token = p.ld_k != 0;
-  a.rows = by_token ? kToken : kSeq;
-  const bool ok = by_token ? map_rows(&maps.k, p.k, T, p.ld_k, H, kD) && map_rows(&maps.v, p.v, T, p.ld_v, H, kD)
-                           : map_rows(&maps.k, p.k, T * H, kD, 1, T * H * kD) &&
-                                 map_rows(&maps.v, p.v, T * H, kD, 1, T * H * kD);
-  if (!ok) return cudaErrorInvalidValue;
-  return launch<16>(a, maps, T, T, ws, st);
-}
+// Tokens of a call of bpkv_prompt_attend that may be streamed: a row's mask has 64 bits.
+constexpr int64_t kFewTokens = 64;
 
-// CTAs of a cluster that streams a unit (16 rows at most of a sequence and KV head) of a
-// tree, 0: the tensor cores take the call.  As many CTAs as leave all units resident at
-// once (clusters of 8 find room for 12 at least).
+// CTAs of a cluster that streams each of n units (16 rows at most of a sequence and KV
+// head), 0: the tensor cores take the call.  As many CTAs as leave all units resident at
+// once (clusters of 8 find room for 12 at least).  rows: of a sequence and KV head at
+// most; again: the units of a sequence are several, which read its keys each; wide: units
+// of the tensor cores.
 //
 // Streamed / tensor cores, in us, trees of t nodes of 4 heads for each of 8 KV heads, bf16
 // rows (8-bit rows in brackets).  Up to 16 rows the keys are read once either way:
@@ -1008,14 +991,63 @@ cudaError_t launch_prompt(const bpkv_prompt_args& p, void* ws, cudaStream_t st) 
 //   31 / 18 (30 / 23); 4 of 1000 10.4 / 12.7 (10.4 / 15.8), of 4000 19.5 / 17.9 (19.0 / 23.6);
 //   16 of 300 15.2 / 10.4 (16.0 / 12.7); t = 16: 1 of 4000 13.2 / 13.5 (12.9 / 16.2); 4 of 1000
 //   12.2 / 13.6 (11.8 / 16.6), of 4000 28 / 20 (28 / 25).
-int few_ctas(int bits, int64_t units, int rows, int groups, int64_t keys) {
-  const int64_t n = units * groups;
-  const int ctas = n <= 12 ? 8 : n <= 32 ? 4 : n <= 72 ? 2 : 1;
-  if (keys < 600 && ctas == 8) return 4;  // the wider cluster's barriers cost what it saves
-  if (groups > 1) return n <= kSms && keys <= (bits == 16 ? 1000 : 2000) * ctas ? ctas : 0;
+// Prompts over their own keys: 1 token 4.1 / 6.8, 17 5.4 / 6.9, 64 6.0 / 8.7, 32 of 1
+//   token 7.6 / 12.4; of 32 heads in groups of 1, 64 tokens 6.6 / 7.0.
+int few_ctas(int bits, int64_t n, int64_t wide, int rows, bool again, int64_t keys) {
+  // no wider than there are tiles for, below 600 keys not as wide: the barriers cost what it saves
+  const int ctas = keys <= 128 ? 1 : n <= 12 ? (keys < 600 ? 4 : 8) : n <= 32 ? 4 : n <= 72 ? 2 : 1;
+  // of few keys a unit takes some 4.5 us of its SM streamed, and 3.5, behind 5.5 once, on the tensor cores
+  if (keys <= kFewTokens) return n <= kSms * 3 / 4 * (1 + (wide + kSms - 1) / kSms) ? ctas : 0;
+  if (again) return n <= kSms && keys <= (bits == 16 ? 1000 : 2000) * ctas ? ctas : 0;
   // 64 to 96 CTAs with two products for each load of a tile
   if (bits == 16 && rows > 8 && ctas == 8 && keys > 12000) return 0;
   return ctas;
+}
+
+static void few_rows(FewArgs& f, const PromptRows& r, int64_t step) {
+  f.len = r.len;
+  f.rows[0][0] = r.k;
+  f.rows[0][1] = r.v;
+  f.exps[0][0] = r.kexp;
+  f.exps[0][1] = r.vexp;
+  f.cap = r.cap;
+  f.step[0] = f.step[1] = step;
+  f.where = kCache;
+}
+
+cudaError_t launch_prompt(const bpkv_prompt_args& p, void* ws, cudaStream_t st) {
+  Args a = {};
+  Maps maps;
+  a.q_start = p.q_start;
+  a.out = p.out;
+  a.tokens = p.n_tokens;
+  a.n_seq = p.n_seq;
+  a.n_heads = p.n_kv_heads;
+  a.group = p.group;
+  const int64_t H = p.n_kv_heads, T = p.n_tokens;
+  const bool by_token = p.ld_k != 0;
+  if (T <= kFewTokens) {
+    // groups of rows at most: one more for every sequence that has tokens
+    const int64_t per = T * p.group <= 8 ? 8 : 16, some = min64(p.n_seq, T);
+    const int groups = (int)(T * p.group / per + some);
+    FewArgs f = {p.q_start, nullptr, nullptr, p.q, p.out, {{p.k, p.v}}, {{nullptr, nullptr}}, 0, p.ld_q,
+                 {kD * 2, kD * 2}, (int32_t)T, p.n_seq, p.n_kv_heads, p.group, 0, by_token ? kToken : kSeq, groups, (int32_t)per};
+    if (by_token) f.step[0] = p.ld_k * 2, f.step[1] = p.ld_v * 2;
+    if (p.cache) few_rows(f, rows_of(*p.cache), kD * 2);
+    if (p.rows8) few_rows(f, rows_of(*p.rows8), kD);
+    const int64_t keys = p.cache ? p.cache->n_max : p.rows8 ? p.rows8->n_max : T;
+    const int ctas = few_ctas(p.rows8 ? 8 : 16, H * groups, prompt_units(T, p.n_seq, H, p.group), (int)(T * p.group), 2 * groups > 3 * some, keys);
+    if (ctas) return p.rows8 ? launch_few_tokens<8>(f, ctas, st) : launch_few_tokens<16>(f, ctas, st);
+  }
+  if (!map_q(&maps.q, p.q, T, H * p.group, p.ld_q, p.group, kTile / p.group)) return cudaErrorInvalidValue;
+  if (p.cache) return over_cache<16>(a, maps, rows_of(*p.cache), T, ws, st);
+  if (p.rows8) return over_cache<8>(a, maps, rows_of(*p.rows8), T, ws, st);
+  a.rows = by_token ? kToken : kSeq;
+  const bool ok = by_token ? map_rows(&maps.k, p.k, T, p.ld_k, H, kD) && map_rows(&maps.v, p.v, T, p.ld_v, H, kD)
+                           : map_rows(&maps.k, p.k, T * H, kD, 1, T * H * kD) &&
+                                 map_rows(&maps.v, p.v, T * H, kD, 1, T * H * kD);
+  if (!ok) return cudaErrorInvalidValue;
+  return launch<16>(a, maps, T, T, ws, st);
 }
 
 template <typename C>
@@ -1024,12 +1056,13 @@ static cudaError_t tree(const C& c, int32_t t, const uint64_t* mask, const uint1
   constexpr int BITS = sizeof(C) == sizeof(bpkv_cache) ? 16 : 8;
   const PromptRows r = rows_of(c);
   const int32_t per = t * c.group <= 8 ? 8 : 16, groups = (t * c.group + per - 1) / per;
-  const int ctas = few_ctas(BITS, (int64_t)c.n_seq * c.n_kv_heads, t * c.group, groups, c.n_max);
+  const int ctas = few_ctas(BITS, (int64_t)c.n_seq * c.n_kv_heads * groups,
+                            prompt_units((int64_t)c.n_seq * t, c.n_seq, c.n_kv_heads, c.group), t * c.group, groups > 1, c.n_max);
   if (ctas) {
-    const FewArgs a = {r.len,   mask,     q,          out,     {{r.k, r.v}}, {{r.kexp, r.vexp}},
-                       r.cap,   c.n_seq,  c.n_kv_heads, c.group, t,            groups,
-                       per};
-    return launch_tree_few<BITS>(a, ctas, st);
+    FewArgs a = {nullptr, nullptr, mask, q, out, {{nullptr, nullptr}}, {{nullptr, nullptr}}, 0, (int64_t)c.n_kv_heads * c.group * kD,
+                 {0, 0}, c.n_seq * t, c.n_seq, c.n_kv_heads, c.group, t, kCache, groups, per};
+    few_rows(a, r, BITS == 16 ? kD * 2 : kD);
+    return launch_few_tokens<BITS>(a, ctas, st);
   }
   Args a = {};
   Maps maps;

@@ -1,6 +1,5 @@
-// Trees of few drafted tokens, or single new ones: the streaming half of
-// bpkv_tree_attend and bpkv_tree_attend8 (which call takes which half in
-// prompt.cu's launch).
+// Few new tokens, in a tree or not: the streaming half of bpkv_tree_attend,
+// bpkv_tree_attend8 and bpkv_prompt_attend (which call takes which half in prompt.cu).
 //
 // A cluster of CTAs takes up to 16 query rows of a sequence and KV head over all of
 // its rows of the cache; every warp streams its own tiles (shared_stream.cuh), the
@@ -36,22 +35,73 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // A warp's way through the rows of one unit: every step-th tile, step the warps of all its CTAs.
-struct TreeWalk {
-  static constexpr bool kMasked = true;
+struct FewWalk {
+  static constexpr bool kMasked = true, kStrided = true;
   static constexpr int side = 0;
   const FewArgs& a;
-  int tok, index, h, row0_q, x, step, tiles, t, n;
-  int64_t row0, base;
-  __device__ __forceinline__ TreeWalk(const FewArgs& args, int tile, uint32_t unit, int first, int stride)
-      : a(args), tok(tile), t(first), step(stride) {
+  int tok, index, h, row0_q, step, tiles, t, n, count, start;
+  int64_t row0, base, first[2];
+  __device__ __forceinline__ FewWalk(const FewArgs& args, int tile, uint32_t unit, int begin, int stride)
+      : a(args), tok(tile), t(begin), step(stride) {
     const uint32_t head = unit / (uint32_t)a.groups;
-    row0_q = (int)(unit - head * a.groups) * a.per;
-    index = (int)(head / (uint32_t)a.n_heads);
-    h = (int)(head - (uint32_t)index * a.n_heads);
-    row0 = head * a.cap;
-    n = (int)shared::tokens_of(a.len[index], a.cap);
-    base = n - a.t;
-    tiles = (n + tok - 1) / tok;
+    uint32_t group = unit - head * a.groups;
+    if (a.q_start) {  // heads, then the groups of all sequences
+      h = (int)head;
+      find(group);
+    } else {
+      index = (int)(head / (uint32_t)a.n_heads);
+      h = (int)(head - (uint32_t)index * a.n_heads);
+      count = a.t;
+      start = index * a.t;
+    }
+    row0_q = (int)group * a.per;
+    n = a.len ? (int)shared::tokens_of(a.len[index], a.cap) : count;
+    base = n - count;
+    tiles = rows() > 0 ? (n + tok - 1) / tok : 0;
+    row0 = a.where == kCache ? ((int64_t)index * a.n_heads + h) * a.cap
+           : a.where == kSeq ? (int64_t)start * a.n_heads + (int64_t)h * count
+                             : start;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) first[kv] = row0 * a.step[kv] + (a.where == kToken ? h * (kD * 2) : 0);
+  }
+  // The sequence that a group of rows belongs to, and its place there; none: no tokens.
+  // Starts as prompt_plan.cuh takes them: within the tokens, none before the last.
+  __device__ __forceinline__ void find(uint32_t& group) {
+    const int lane = threadIdx.x & 31;
+    int top = 0, before = 0;
+    index = count = start = 0;
+#pragma unroll 1
+    for (int b = 0; b < a.n_seq; b += 32) {
+      const int i = min(b + lane, a.n_seq - 1);
+      int lo = b + lane < a.n_seq ? (int)max64(0, min64(a.q_start[i], a.tokens)) : 0;
+      const int next = (int)max64(0, min64(a.q_start[i + 1], a.tokens));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, lo, o);
+        if (lane >= o) lo = max(lo, u);
+      }
+      lo = max(lo, top);
+      const int hi = max(lo, next), mine = b + lane < a.n_seq ? hi - lo : 0;
+      const int groups = (mine * a.group + a.per - 1) / a.per;
+      int sum = groups;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, (int)group < before + sum);
+      if (in) {
+        const int k = __ffs(in) - 1;
+        index = b + k;
+        count = __shfl_sync(0xffffffffu, mine, k);
+        start = __shfl_sync(0xffffffffu, lo, k);
+        group -= before + __shfl_sync(0xffffffffu, sum - groups, k);
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+      top = __shfl_sync(0xffffffffu, hi, 31);
+    }
+    group = 0;
   }
   __device__ __forceinline__ bool more() const { return t < tiles; }
   __device__ __forceinline__ bool next() {
@@ -59,13 +109,22 @@ struct TreeWalk {
     return false;
   }
   __device__ __forceinline__ int valid() const { return min(tok, n - t * tok); }
-  __device__ __forceinline__ int rows() const { return min(a.per, a.t * a.group - row0_q); }
-  // element of q and out where row r begins
-  __device__ __forceinline__ int64_t at(int r) const {
-    const int node = (row0_q + r) / a.group, head = row0_q + r - node * a.group;
-    return ((((int64_t)index * a.t + node) * a.n_heads + h) * a.group + head) * kD;
+  __device__ __forceinline__ int rows() const { return min(a.per, count * a.group - row0_q); }
+  // token and head of the group of row r
+  __device__ __forceinline__ void place(int r, int& node, int& head) const {
+    node = (row0_q + r) / a.group;
+    head = row0_q + r - node * a.group;
   }
-  __device__ __forceinline__ const uint16_t* q_of(int r) const { return a.q + at(r); }
+  __device__ __forceinline__ const uint16_t* q_of(int r) const {
+    int node, head;
+    place(r, node, head);
+    return a.q + (int64_t)(start + node) * a.ld_q + (h * a.group + head) * kD;
+  }
+  __device__ __forceinline__ uint16_t* out_of(int r) const {
+    int node, head;
+    place(r, node, head);
+    return a.out + (((int64_t)(start + node) * a.n_heads + h) * a.group + head) * kD;
+  }
   __device__ __forceinline__ uint64_t mask_of(int r) const {
     const int node = (row0_q + r) / a.group;
     if (!a.tree) return (2ull << node) - 1;
@@ -74,7 +133,7 @@ struct TreeWalk {
 };
 
 template <int BITS, int NB, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 1) k_tree_unit(const __grid_constant__ FewArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_few_unit(const __grid_constant__ FewArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = Shape<BITS>;
   constexpr float kUnit = BITS == 16 ? kLogScale : 1.f;
@@ -92,17 +151,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_unit(const __grid_constant
   pdl_enter();
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const unsigned char* exps = smem + kWarps * kStages * kStage + warp * kStages * S::kExps;
-  TreeWalk ahead(a, S::kTok, blockIdx.x / ctas, rank * kWarps + warp, ctas * kWarps), cur = ahead;
+  FewWalk ahead(a, S::kTok, blockIdx.x / ctas, rank * kWarps + warp, ctas * kWarps), cur = ahead;
   const uint64_t policy = shared::evict_first_policy();
   prime<BITS>(ahead, ring, exps, policy);
   const int rows = cur.rows();
-  const TreeWalk unit = cur;
+  if (rows <= 0) return;  // of no sequence: the whole cluster
+  const FewWalk unit = cur;
   for (int i = tid; i < kWarps * kR; i += kThreads) s_ml[i / kR][i % kR] = make_float2(-INFINITY, 0.f);
   __syncthreads();
   float* rows_o = reinterpret_cast<float*>(smem + warp * kStages * kStage);  // the warp's ring, once it is read
   stream<BITS, NB>(
-      cur, ahead, ring, exps, policy, [&](const TreeWalk&) { return rows; },
-      [&](const TreeWalk&, const State<NB>& st, int) {
+      cur, ahead, ring, exps, policy, [&](const FewWalk&) { return rows; },
+      [&](const FewWalk&, const State<NB>& st, int) {
         cp_wait<0>();
         __syncwarp();
 #pragma unroll
@@ -139,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_unit(const __grid_constant
       if (d == 0) s_part_ml[r] = make_float2(M, L);
     } else {
       const float s = L == 0.f ? 0.f : 1.f / L;
-      *reinterpret_cast<uint32_t*>(a.out + unit.at(r) + d) = pack<16>(o0 * s, o1 * s);
+      *reinterpret_cast<uint32_t*>(unit.out_of(r) + d) = pack<16>(o0 * s, o1 * s);
     }
   }
   if constexpr (CLUSTER) {
@@ -167,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_unit(const __grid_constant
         o1 = fmaf(f, v[i].y, o1);
       }
       const float s = L == 0.f ? 0.f : 1.f / L;
-      *reinterpret_cast<uint32_t*>(a.out + unit.at(r) + d) = pack<16>(o0 * s, o1 * s);
+      *reinterpret_cast<uint32_t*>(unit.out_of(r) + d) = pack<16>(o0 * s, o1 * s);
     }
     cl.sync();  // no CTA leaves while another reads its shared memory
   }
@@ -177,11 +237,11 @@ template <int BITS, int NB, bool CLUSTER>
 cudaError_t go(const FewArgs& a, int ctas, cudaStream_t st) {
   constexpr int kSmem = Shape<BITS>::kRing;
   static std::atomic<uint64_t> done;
-  const auto kernel = k_tree_unit<BITS, NB, CLUSTER>;
+  const auto kernel = k_few_unit<BITS, NB, CLUSTER>;
   const cudaError_t e = shared::allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.n_seq * a.n_heads * a.groups * ctas));
+  cfg.gridDim = dim3((unsigned)((a.q_start ? 1 : (int64_t)a.n_seq) * a.n_heads * a.groups * ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -199,12 +259,12 @@ cudaError_t go(const FewArgs& a, int ctas, cudaStream_t st) {
 
 // ctas: of a unit's cluster
 template <int BITS>
-cudaError_t launch_tree_few(const FewArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch_few_tokens(const FewArgs& a, int ctas, cudaStream_t st) {
   if (a.per == 8) return ctas > 1 ? go<BITS, 1, true>(a, ctas, st) : go<BITS, 1, false>(a, 1, st);
   return ctas > 1 ? go<BITS, 2, true>(a, ctas, st) : go<BITS, 2, false>(a, 1, st);
 }
-template cudaError_t launch_tree_few<16>(const FewArgs&, int, cudaStream_t);
-template cudaError_t launch_tree_few<8>(const FewArgs&, int, cudaStream_t);
+template cudaError_t launch_few_tokens<16>(const FewArgs&, int, cudaStream_t);
+template cudaError_t launch_few_tokens<8>(const FewArgs&, int, cudaStream_t);
 
 }  // namespace prompt
 }  // namespace bpkv

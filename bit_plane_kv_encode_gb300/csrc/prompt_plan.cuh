@@ -62,17 +62,21 @@ struct Args {
   int32_t* status;
 };
 
-// What the streaming kernel of trees takes (prompt_few.cu).
+// What the streaming kernel of few new tokens takes (prompt_few.cu).
 struct FewArgs {
-  const int64_t* len;
+  const int64_t* q_start;     // NULL: t tokens of each sequence
+  const int64_t* len;         // NULL: the keys are those of the new tokens
   const uint64_t* tree;       // NULL: a chain
   const uint16_t* q;
   uint16_t* out;
   const void* rows[1][2];     // K, V
   const uint8_t* exps[1][2];  // scale exponents of 8-bit rows
-  int64_t cap;
+  int64_t cap, ld_q;
+  int64_t step[2];            // bytes from one row to the next
+  int32_t tokens;             // of q
   int32_t n_seq, n_heads, group, t;
-  int32_t groups, per;        // a tree's query rows, per (8 or 16) at a time
+  int32_t where;              // Rows
+  int32_t groups, per;        // a tree's query rows, per (8 or 16) at a time; groups: of a sequence, or of all
 };
 
 // Counts are below 2^31: the host makes sure.

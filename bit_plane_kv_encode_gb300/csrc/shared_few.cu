@@ -39,7 +39,7 @@ constexpr int kSmem = Shape<BITS>::kRing + (int)sizeof(FewPlan);
 
 // One worker's way through its tiles.
 struct Walk {
-  static constexpr bool kMasked = false;
+  static constexpr bool kMasked = false, kStrided = false;
   const FewPlan& p;
   const Args& a;
   int tok;
@@ -114,7 +114,7 @@ enum { kAlone, kCluster, kFinish };  // what a CTA of k_shared_unit joins beside
 // cluster of them takes whole, the prefix's and then its own: every step-th
 // tile, step the warps of all.
 struct UnitWalk {
-  static constexpr bool kMasked = false;
+  static constexpr bool kMasked = false, kStrided = false;
   const Args& a;
   int tok, index, h, side, x, step, tiles, pre_tiles, t, n, n_pre, n_own;
   int64_t row0, own_row0, pre_row0;

@@ -3,8 +3,9 @@
 //
 // A walk W says which tiles: tok (tokens of a tile), t, valid(), more(), next(), row0,
 // side, a (Args with rows[side][K, V] and exps), q_of(r), the address of query row r,
-// and, where a row does not see all of the last rows (kMasked), base, the first of
-// those, and mask_of(r), a bit for each.
+// where a row does not see all of the last rows (kMasked), base, the first of those, and
+// mask_of(r), a bit for each, and where rows do not lie one behind the other (kStrided)
+// first[K, V], the bytes before them, and a.step[K, V], from one to the next.
 #pragma once
 
 #include "rows8_core.cuh"
@@ -98,11 +99,15 @@ __device__ __forceinline__ void load_tile(const W& w, uint32_t stage, uint32_t e
   constexpr int kChunks = S::kRow / 16;  // 16-byte pieces of a row
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    const unsigned char* src = static_cast<const unsigned char*>(w.a.rows[w.side][kv]) + row * S::kRow;
+    const unsigned char* src = static_cast<const unsigned char*>(w.a.rows[w.side][kv]);
+    if constexpr (W::kStrided) src += w.first[kv] + (int64_t)w.t * S::kTok * w.a.step[kv];
+    else src += row * S::kRow;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int x = i * 32 + lane, tok = x / kChunks, c = x % kChunks;
-      cp16_zero(stage + kv * (kStage / 2) + tok * S::kRow + ((c ^ (tok & 7)) << 4), src + x * 16, tok < valid, policy);
+      const unsigned char* from = src + x * 16;
+      if constexpr (W::kStrided) from = src + tok * w.a.step[kv] + c * 16;
+      cp16_zero(stage + kv * (kStage / 2) + tok * S::kRow + ((c ^ (tok & 7)) << 4), from, tok < valid, policy);
     }
     if (BITS == 8 && lane < 2) cp16_zero(exps + kv * S::kTok + lane * 16, w.a.exps[w.side][kv] + row + lane * 16, true, policy);
   }

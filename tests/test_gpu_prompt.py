@@ -20,6 +20,7 @@ from test_gpu_shared import draw_rows, make_cache, pk  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 D = 128
+WAYS = [None, 32768]  # what the host knows of the lengths
 
 
 def attention(q, k, v, sees, scale=None):
@@ -63,7 +64,7 @@ def run_prompt(pk, rows, new, past, H, G, seed=0, lens=None, spread=0.75, pad=0,
     q_start = torch.tensor(start, dtype=torch.int64, device="cuda")
     if rows == "cache":
         lens = lens or [a + b for a, b in zip(new, past)]
-        cap = max(512, (max(lens) + 511) // 512 * 512)
+        cap = max(512, (max(max(lens), n_max or 0) + 511) // 512 * 512)
         k, v = draw_rows(g, N, H, cap, spread)
         c, vals = make_cache(pk, bits, G, cap, lens, k, v)
         if n_max is not None:
@@ -128,16 +129,25 @@ def test_prompts_that_are_cut(pk, G, t):
 @pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("new,past", [([1], [0]), ([1], [511]), ([1, 1, 1], [0, 128, 4000]), ([7, 0, 130], [100, 9, 1000]),
                                       ([64, 33], [4090, 127]), ([300, 2], [700, 9000])])
-def test_behind_cached_rows(pk, bits, new, past):
-    run_prompt(pk, "cache", new, past, 2, 4, seed=sum(new), bits=bits, pad=2)
+@pytest.mark.parametrize("n_max", WAYS)
+def test_behind_cached_rows(pk, bits, new, past, n_max):
+    run_prompt(pk, "cache", new, past, 2, 4, seed=sum(new), bits=bits, pad=2, n_max=n_max)
 
 
 @pytest.mark.parametrize("bits", [16, 8])
-def test_more_new_tokens_than_rows(pk, bits):
+@pytest.mark.parametrize("new,n_max", [([40, 3, 200, 5], None), ([40, 3, 2, 5], None), ([40, 3, 2, 5], 32768)])
+def test_more_new_tokens_than_rows(pk, bits, new, n_max):
     """Tokens without a row see nothing: zeros."""
-    new, lens = [40, 3, 200, 5], [10, 0, 150, 600]
-    got = run_prompt(pk, "cache", new, None, 2, 4, lens=lens, bits=bits)
+    got = run_prompt(pk, "cache", new, None, 2, 4, lens=[10, 0, 150, 600], bits=bits, n_max=n_max)
     assert (got["out"][:30] == 0).all() and (got["out"][40:43] == 0).all()
+
+
+@pytest.mark.parametrize("rows", LAYOUTS)
+@pytest.mark.parametrize("new", [[0, 1, 0, 0, 2, 60], [1] * 33 + [0] * 40 + [1] * 30, [5, 0, 17, 3], [64]])
+@pytest.mark.parametrize("G", [1, 3, 8])
+def test_few_tokens_of_many_prompts(pk, rows, new, G):
+    """Prompts of 64 tokens together at most, which are streamed; empty ones among them."""
+    run_prompt(pk, rows, new, None, 3, G, seed=len(new), pad=1, ld=16)
 
 
 @pytest.mark.parametrize("bits", [16, 8])
@@ -145,9 +155,6 @@ def test_more_new_tokens_than_rows(pk, bits):
 def test_any_bound_of_the_lengths(pk, bits, n_max):
     """n_max sizes the launch and chooses the way, never the result."""
     run_prompt(pk, "cache", [50, 70], [1500, 2000], 2, 4, seed=3, bits=bits, n_max=n_max)
-
-
-WAYS = [None, 32768]
 
 
 def run_tree(pk, bits, N, t, H, G, lens, seed=0, tree="random", n_max=None):
