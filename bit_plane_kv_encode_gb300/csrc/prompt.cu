@@ -1,7 +1,8 @@
 // Attention of several new tokens of each sequence at once, on the 5th-generation
 // tensor cores: causal over packed prompts or over the rows of a cache that they
 // end (bpkv_prompt_attend), or as a tree of drafted tokens over a cache
-// (bpkv_tree_attend, bpkv_tree_attend8).  The plan is in prompt_plan.cuh.
+// (bpkv_tree_attend, bpkv_tree_attend8).  The plan is in prompt_plan.cuh; calls of few
+// tokens are streamed instead (prompt_few.cu, few_ctas below).
 //
 // For every query row, o = sum_x softmax_x(q . k_x / sqrt(D)) v_x over the keys x
 // that its token sees, with a running maximum and sum: one pass over the keys.
@@ -24,17 +25,17 @@
 // streams' tiles, of which the products are 2048.  And the power limit: a call of 400 us
 // runs at 2.0 GHz, calls back to back at 1.8.  Between segments 6500 cycles: the last O,
 // 256 rows through the load-store unit (4000, whatever way they were turned), the next S.
-// Measured on a GB300, 8 x 4 heads: 8191 tokens 390 us, 1.41 PFLOP/s (404 in a long
-// run); 16383 tokens 1.44 ms, 1.52 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 640
-// us, 1.20; 512 tokens of four sequences behind 32256 rows 322 us, 1.38; trees of 32
-// nodes of 16 sequences of up to 8192 rows 55 us, 5.0 TB/s.
+// Measured on a GB300, 8 x 4 heads: 8191 tokens 384 us, 1.43 PFLOP/s (404 in a long
+// run); 16383 tokens 1.40 ms, 1.57 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 632
+// us, 1.21; 512 tokens of four sequences behind 32256 rows 325 us, 1.37; trees of 32
+// nodes of 16 sequences of up to 8192 rows 53 us, 5.2 TB/s.
 //
 // 8-bit rows.  A group of four more warps turns the tiles of codes, as they come,
 // into tiles of bf16: a code times its power of two is exactly a bf16 number, so
 // that products, softmax and results are those of bf16 rows of the same values.  A
 // tile of K is turned in some 1400 cycles, and there is room for three tiles of bf16
-// only, which bounds them: 1000 tokens behind 100000 rows 1.28 ms, 1.29 PFLOP/s;
-// trees of 64 nodes of 4 sequences of up to 131071 rows 222 us, 1.24 PFLOP/s.
+// only, which bounds them: 1000 tokens behind 100000 rows 1.27 ms, 1.30 PFLOP/s;
+// trees of 64 nodes of 4 sequences of up to 131071 rows 220 us, 1.25 PFLOP/s.
 #include "prompt_plan.cuh"
 #include "rows8_core.cuh"
 #include "tc.cuh"
@@ -231,12 +232,10 @@ __device__ __forceinline__ float look(float* x, bool masked, uint32_t see0, uint
 __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool masked, const Sees& sees, bool first,
                                              uint32_t half, float& m, float& l) {
   float x[64], y[64];
-  tmem_ld32(ts, reinterpret_cast<uint32_t*>(x));
-  tmem_ld32(ts + 32, reinterpret_cast<uint32_t*>(x) + 32);
+  load_half(ts, x);
   load_half(ts + 64, y);
   wait_ld();
   float top = look(x, masked, sees.w[0], sees.w[1]);
-  wait_ld();
   top = fmaxf(top, look(y, masked, sees.w[2], sees.w[3]));
   const bool up = top > m + kLazy / kLogScale;
   if (first) {
@@ -407,12 +406,11 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
           }
           end_segment();
         }
-        if (!ok) {  // the copies in flight must land before the CTA's shared memory is given up
-          uint32_t never = 0;
+        // the copies in flight must land before the CTA's shared memory is given up
+        uint32_t never = 0;
 #pragma unroll 1
-          for (uint32_t k = issued > (uint32_t)kRing ? issued - kRing : 0; k < issued; ++k)
-            wait(smem_u32(&full[k % kRing]), (k / kRing) & 1, &never);
-        }
+        for (uint32_t k = issued > (uint32_t)kRing ? issued - kRing : 0; k < issued; ++k)
+          wait(smem_u32(&full[k % kRing]), (k / kRing) & 1, &never);
       }
     } else if (warp == 1 || warp == 3) {
       if (elect_one()) {
@@ -542,7 +540,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
                           g.token + s * a.run, policy);
           ++loads;
         }
-        uint32_t never = 0;  // the last ones' landing is nobody's to wait for when another role gave up
+        uint32_t never = 0;  // as above
         if (loads > 0) wait(bar, (loads - 1) & 1, &never);
       }
     }
