@@ -518,10 +518,10 @@ int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, cons
  * At most BPKV_SHARED_MAX_SEQ sequences, 2^30 tokens, rows of a sequence or rows
  * of H T keys, and 2^31 tiles of 128 keys by 2 floor(128 / G) tokens and KV head
  * (BPKV_EUNSUPPORTED for more, and for residency 1).
- * Workspace: bpkv_prompt_workspace_size bytes for the largest number of new
- * tokens that one sequence of the call may have, 256-byte aligned, with nothing
- * kept in it from call to call (calls that may run at the same time need one
- * each); its first 256 bytes hold the status word (BPKV_DEV_TIMEOUT when a wait
+ * Workspace: bpkv_prompt_workspace_size bytes, 256-byte aligned, for n_new = T,
+ * the call's tokens, or a tree's t (BPKV_ENOWORKSPACE for less), with nothing kept
+ * in it from call to call (calls that may run at the same time need one each); its
+ * first 256 bytes hold the status word (BPKV_DEV_TIMEOUT when a wait
  * inside the kernel gave up; clear it first).
  */
 size_t bpkv_prompt_workspace_size(int64_t n_new, int32_t group);
