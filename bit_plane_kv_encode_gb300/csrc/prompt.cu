@@ -25,17 +25,20 @@
 // streams' tiles, of which the products are 2048.  And the power limit: a call of 400 us
 // runs at 2.0 GHz, calls back to back at 1.8.  Between segments 6500 cycles: the last O,
 // 256 rows through the load-store unit (4000, whatever way they were turned), the next S.
-// Measured on a GB300, 8 x 4 heads: 8191 tokens 384 us, 1.43 PFLOP/s (404 in a long
-// run); 16383 tokens 1.40 ms, 1.57 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 632
-// us, 1.21; 512 tokens of four sequences behind 32256 rows 325 us, 1.37; trees of 32
-// nodes of 16 sequences of up to 8192 rows 53 us, 5.2 TB/s.
+// Without any softmax the products, loads and ends take 303 us of 8191 tokens' 383; without
+// the exponentials, or most of the maximum, 372 and 365.
+// Measured on a GB300, 8 x 4 heads: 8191 tokens 375 us, 1.47 PFLOP/s (394 in a long
+// run); 16383 tokens 1.36 ms, 1.62 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 617
+// us, 1.24; up to 512 tokens of four sequences behind up to 32256 rows 297 us, 1.49 (325
+// where each run reads the rows when it comes to them); trees of 32 nodes of 16 sequences
+// of up to 8192 rows 53 us, 5.2 TB/s.
 //
 // 8-bit rows.  A group of four more warps turns the tiles of codes, as they come,
 // into tiles of bf16: a code times its power of two is exactly a bf16 number, so
 // that products, softmax and results are those of bf16 rows of the same values.  A
 // tile of K is turned in some 1400 cycles, and there is room for three tiles of bf16
-// only, which bounds them: 1000 tokens behind 100000 rows 1.27 ms, 1.30 PFLOP/s;
-// trees of 64 nodes of 4 sequences of up to 131071 rows 220 us, 1.25 PFLOP/s.
+// only, which bounds them: 1000 tokens behind 100000 rows 1.26 ms, 1.31 PFLOP/s;
+// trees of 64 nodes of 4 sequences of up to 131071 rows 224 us, 1.22 PFLOP/s.
 #include "prompt_plan.cuh"
 #include "rows8_core.cuh"
 #include "tc.cuh"
@@ -74,6 +77,7 @@ template <int BITS>
 struct Smem {
   Plan plan;
   Segment seg[kSegments];
+  Cut cut;  // of the last segment
   uint32_t tmem;
   uint32_t abort;
   uint64_t full[4], empty[4];
@@ -90,6 +94,14 @@ constexpr int kBase = (sizeof(Smem<BITS>) + 1023) / 1024 * 1024 + 1024;
 template <int BITS>
 constexpr int kSmem = kBase<BITS> + 2 * kQ + Shape<BITS>::kStages * kStage + Shape<BITS>::kCodeStages * kCodeStage;
 static_assert(kSmem<16> <= 227 * 1024 && kSmem<8> <= 227 * 1024, "shared memory of a CTA");
+
+// Bytes of a cache's keys and values from which runs go side by side (prompt_plan.cuh):
+// about what L2 holds.  With / without, in us, 8 x 4 heads, bf16 rows: 512 tokens behind
+// 16000 rows (66 MB) 98.7 / 97.4, 32000 (131 MB) 175 / 182, 64000 325 / 359; 128 behind
+// 8000 31.2 / 30.9, 64000 99 / 106; 256 of 4 sequences of 4000 (66 MB) 68.0 / 67.1, 8000
+// 105 / 109, 16000 181 / 197; 512 of 8 of 3000 (98 MB) 151 / 149; 8-bit rows: 512 behind
+// 64000 (131 MB) 407 / 405, 1000 behind 100000 1263 / 1265, in a long run 1268 / 1294.
+constexpr int64_t kBesideBytes = 112 << 20;
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -552,9 +564,11 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
     const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 2 * kTile + s * kD;
     const int tok = row * a.group_inv >> 16;  // of the stream's
     uint32_t tile_no = 0, s_phase = 0, o_phase = 0, fin_phase = 0;
-    Cut cut = {};
+    if (row == 0 && s == 0) sm.cut = {};
     bool ok = true;
     while (__all_sync(0xffffffffu, next(ok))) {
+      // read where it lies: in registers it costs spills (8191 tokens 392 / 376 us)
+      const Segment& g = sm.seg[seg_no % kSegments];
       const int steps = g.steps_of(s), first_tok = g.dual ? s * a.run : 0;
       const bool there = tok < a.run && first_tok + tok < g.tokens;  // a row of the unit
       // keys before this row's end; rows that are not there are not masked
@@ -610,7 +624,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
       // what the segment's end takes of it; the walk to the next one hides behind the last O
       const bool dual = g.dual, whole = g.whole, both = !dual && g.steps_of(1) > 0;
       const int rows = min(a.run, g.tokens - first_tok) * a.group, token = g.token + first_tok, h = g.h, slot = g.slot();
-      cut = {g.token, g.h, g.tokens, g.pieces, 0};  // of the last segment
+      if (row == 0 && s == 0) sm.cut = {g.token, g.h, g.tokens, g.pieces, 1 << sm.plan.beside};  // of the last segment
       const bool writes = (dual || both || s == 0) && w4 * 32 < rows;
       const int c0 = both ? s * 64 : 0, c1 = both ? c0 + 64 : kD;
       const int64_t at = (int64_t)slot * a.slot_rows + (dual ? s * kTile : 0) + w4 * 32;
@@ -695,7 +709,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
       // O and the rows' maxima are read before the next segment's take their place
       if (both && !meet()) break;
     }
-    if (a.split && s == 0 && row == 0) a.cuts[blockIdx.x] = cut;
+    if (a.split && s == 0 && row == 0) a.cuts[blockIdx.x] = sm.cut;
   } else if constexpr (BITS == 8) {
     // ---- codes to bf16, all four warps each tile
     regs_fewer<96>();
@@ -792,7 +806,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prompt_join(const __grid_co
         ml[i] = make_float2(-INFINITY, 0.f);
         o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < cut.pieces) {
-          const int64_t at = (int64_t)(2 * (blockIdx.x + k) + (k == 0)) * a.slot_rows + in;
+          const int64_t at = (int64_t)(2 * (blockIdx.x + k * cut.step) + (k == 0)) * a.slot_rows + in;
           ml[i] = a.part_ml[at];
           o[i] = reinterpret_cast<const float4*>(a.part_o + at * kD)[lane];
         }
@@ -908,6 +922,7 @@ cudaError_t launch(Args& a, const Maps& maps, int64_t longest, int64_t keys, voi
   const int64_t units = prompt_units(a.tokens, a.n_seq, a.n_heads, a.group);
   const int64_t tiles = max64(1, (keys + kTile - 1) / kTile);
   a.split = tiles > 4;
+  a.beside = a.rows == kCache && !a.once && (int64_t)a.n_seq * a.n_heads * keys * (kD * BITS / 4) >= kBesideBytes;
   const int ctas = (int)max64(1, min64(kSms, a.split ? units * (tiles + 1) / 2 : units));
   static std::atomic<uint64_t> done;
   cudaError_t e = shared::allow_smem(k_prompt<BITS>, kSmem<BITS>, done);

@@ -12,6 +12,12 @@
 // one for a unit that goes on behind it, and k_prompt_join joins them in order.
 // Where units are short they are not cut: each counts one.
 //
+// Long rows of a cache, more than L2 holds, are read again by each run of a
+// sequence.  There 2, 4 or 8 runs go side by side, as one unit of the list as long as
+// the last of them: as many CTAs take the same stretch, a run each, and come by the same
+// tiles at the same time.  As many as lose 1/32 at most to runs that are missing, which
+// the lengths tell.
+//
 // Lengths are read on the device; every CTA works the cut out for itself.
 #pragma once
 
@@ -31,6 +37,8 @@ constexpr int kSoftmaxWarps = 8;
 // 58.6 / 55.6 / 55.0 / 55.9.
 constexpr int kOver = 2;
 
+constexpr int kBeside = 3;
+
 enum Rows : int32_t { kToken, kSeq, kCache };  // where keys and values lie
 
 // What the CTA that a cut unit begins in leaves for the join.
@@ -39,7 +47,7 @@ struct Cut {
   int32_t h;       // KV head
   int32_t tokens;
   int32_t pieces;  // 0: this CTA's last unit is whole
-  int32_t pad;
+  int32_t step;    // from the CTA of one piece to that of the next
 };
 
 struct Args {
@@ -54,6 +62,7 @@ struct Args {
   int32_t run;             // tokens of a stream: 128 / G
   uint32_t group_inv;      // 2^16 / group rounded up: x group_inv >> 16 is x / group for x below 256
   int32_t split;           // units may be cut
+  int32_t beside;          // runs may go side by side
   int32_t once;            // a sequence's tokens are one unit of a KV head
   int32_t slot_rows;       // rows of a slot of partial rows
   float* part_o;           // [slots][slot_rows][D]
@@ -89,6 +98,8 @@ struct Plan {
   int32_t seq, h, run;
   int32_t at, left;           // within that unit, and the stretch's length
   int32_t per;                // a stretch's length (the last ones may be shorter)
+  int32_t beside;             // 2^beside runs go side by side: this CTA takes one of each
+  int32_t total[kBeside + 1]; // what all count, by beside
 };
 
 // Runs of a sequence, keys and tiles of its run b.
@@ -133,13 +144,42 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
       top = __shfl_sync(0xffffffffu, x, 31);
     }
   }
+  if (tid <= kBeside) p.total[tid] = 0;
   __syncthreads();
+  int beside = 0;
+  if (a.beside) {
+#pragma unroll 1
+    for (int i = warp; i < N; i += nt / 32) {
+      const int t = p.start[i + 1] - p.start[i], runs = runs_of(a, t);
+      int sum[kBeside + 1] = {};
+#pragma unroll 1
+      for (int b = lane; b < runs; b += 32) {
+        const int n = count_of(a, tiles_of(a, t, p.off[i] - t, b));
+#pragma unroll
+        for (int k = 0; k <= kBeside; ++k)
+          if (b == runs - 1 || (~b & ((1 << k) - 1)) == 0) sum[k] += n;
+      }
+#pragma unroll
+      for (int k = 0; k <= kBeside; ++k) {
+        sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
+        if (lane == 0) atomicAdd(&p.total[k], sum[k] * a.n_heads);
+      }
+    }
+    __syncthreads();
+    const uint32_t per = (uint32_t)(p.total[0] + gridDim.x - 1) / gridDim.x;
+#pragma unroll 1
+    for (int k = kBeside; k > 0 && beside == 0; --k) {
+      const uint32_t groups = gridDim.x >> k;
+      if (groups > 0 && (p.total[k] + groups - 1) / groups <= per + per / 32) beside = k;
+    }
+  }
 #pragma unroll 1
   for (int i = warp; i < N; i += nt / 32) {
-    const int t = p.start[i + 1] - p.start[i], off = a.len ? p.off[i] - t : 0, runs = runs_of(a, t);
+    const int t = p.start[i + 1] - p.start[i], off = a.len ? p.off[i] - t : 0;
+    const int units = (runs_of(a, t) + (1 << beside) - 1) >> beside;
     int sum = 0;
 #pragma unroll 1
-    for (int b = lane; b < runs; b += 32) sum += count_of(a, tiles_of(a, t, off, b));
+    for (int b = lane; b < units; b += 32) sum += count_of(a, tiles_of(a, t, off, ((b + 1) << beside) - 1));
     sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) {
       p.n[i] = t;
@@ -158,7 +198,9 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
     }
     if (lane == 0) p.cum[N] = total;
     __syncwarp();
-    const int per = (uint32_t)(total + gridDim.x - 1) / gridDim.x, lo = min((int64_t)blockIdx.x * per, (int64_t)total);
+    const int groups = gridDim.x >> beside, group = blockIdx.x >> beside;
+    const int per = (uint32_t)(total + groups - 1) / groups;
+    const int lo = group < groups ? min((int64_t)group * per, (int64_t)total) : total;
     int at = 0, seq = 0, h = 0, b = 0;
     if (lo < total) {
       int x = 0, y = N - 1;  // the last sequence that begins at or before lo: empty ones end where they begin
@@ -174,8 +216,8 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
       at = lo - p.cum[seq] - h * head;
       const int t = p.n[seq], off = p.off[seq];
 #pragma unroll 1
-      for (;; b += 32) {  // 32 runs at a time
-        const int n = count_of(a, tiles_of(a, t, off, b + lane)), sum = below(n, lane);
+      for (;; b += 32) {  // 32 units at a time
+        const int n = count_of(a, tiles_of(a, t, off, ((b + lane + 1) << beside) - 1)), sum = below(n, lane);
         const uint32_t in = __ballot_sync(0xffffffffu, at < sum);
         if (in) {
           const int k = __ffs(in) - 1;
@@ -189,10 +231,11 @@ __device__ __forceinline__ void make_plan(const Args& a, Plan& p) {
     if (lane == 0) {
       p.seq = seq;
       p.h = h;
-      p.run = b;
+      p.run = (b << beside) + (blockIdx.x & ((1 << beside) - 1));
       p.at = at;
       p.left = min(per, total - lo);
       p.per = per;
+      p.beside = beside;
     }
   }
   __syncthreads();
@@ -230,7 +273,11 @@ struct Walk {
     while (left > 0) {
 #pragma unroll 1
       while (p.n[seq] == 0) ++seq;  // what is left lies in a sequence further on
-      const int t = p.n[seq], off = p.off[seq], n = tiles_of(a, t, off, run), count = count_of(a, n);
+      const int t = p.n[seq], off = p.off[seq];
+      // of the last of the runs side by side, and its own: none where that is missing
+      const int beside = p.beside, last = run | ((1 << beside) - 1);
+      const int count = count_of(a, tiles_of(a, t, off, last));
+      const int n = run * 2 * a.run < t ? tiles_of(a, t, off, run) : 0;
       const int take = min(left, count - at), done = p.left - left;
       s.seq = seq;
       s.h = h;
@@ -255,10 +302,10 @@ struct Walk {
       at += take;
       if (at == count) {
         at = 0;
-        if (s.first + 2 * a.run < t) {
-          ++run;
+        if ((last + 1) * 2 * a.run < t) {
+          run += 1 << beside;
         } else {
-          run = 0;
+          run &= (1 << beside) - 1;
           if (++h == a.n_heads) h = 0, ++seq;
         }
       }

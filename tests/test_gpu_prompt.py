@@ -134,6 +134,37 @@ def test_behind_cached_rows(pk, bits, new, past, n_max):
     run_prompt(pk, "cache", new, past, 2, 4, seed=sum(new), bits=bits, pad=2, n_max=n_max)
 
 
+# Runs of 64 tokens: eight, two and four of each sequence, mixtures of them, numbers that are no power of two, one
+# token more or less than whole runs, sequences without any.
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("new,past", [([512] * 4, [3000, 2900, 3100, 0]), ([128, 127, 65, 128], [511, 2000, 8000, 1]),
+                                      ([256, 200, 193, 256], [4000, 4500, 100, 777]), ([512, 128, 256, 384], [4096, 3072, 2048, 1024]),
+                                      ([320] * 4, [3000] * 4), ([512, 0, 1000, 30], [2000, 0, 5000, 9000]),
+                                      ([0, 0, 1025, 0], [5, 0, 6000, 0]), ([512, 512], [30000, 32000]),
+                                      ([64, 513, 64, 449], [128, 128, 128, 128])])
+def test_runs_side_by_side(pk, bits, new, past):
+    """As many rows as sequences may have make runs of a sequence go side by side, however many they do have."""
+    run_prompt(pk, "cache", new, past, 2, 4, seed=sum(new) + sum(past), bits=bits, pad=3,
+               n_max=(1 << 19) // (2 * len(new)))
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("H,G,new,past", [(1, 8, [16] * 8 + [256] * 8, [2000] * 16), (5, 3, [336, 300], [9000, 4000]),
+                                          (8, 1, [1024, 700], [3000, 5000]), (3, 7, [216], [70000])])
+def test_runs_of_other_groups_side_by_side(pk, bits, H, G, new, past):
+    run_prompt(pk, "cache", new, past, H, G, seed=G, bits=bits, n_max=(1 << 19) // (len(new) * H))
+
+
+def test_runs_side_by_side_give_equal_bits(pk):
+    got = run_prompt(pk, "cache", [512, 500, 384], [9000, 8000, 7000], 2, 4, n_max=1 << 16)
+    first = got["out"].clone()
+    for _ in range(3):
+        got["out"].zero_()
+        pk.bpkv_prompt_attend(got["a"], got["ws"], got["ws"].numel())
+        torch.cuda.synchronize()
+        assert torch.equal(got["out"], first)
+
+
 @pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("new,n_max", [([40, 3, 200, 5], None), ([40, 3, 2, 5], None), ([40, 3, 2, 5], 32768)])
 def test_more_new_tokens_than_rows(pk, bits, new, n_max):
