@@ -27,9 +27,9 @@
 // 256 rows through the load-store unit (4000, whatever way they were turned), the next S.
 // Without any softmax the products, loads and ends take 303 us of 8191 tokens' 383; without
 // the exponentials, or most of the maximum, 372 and 365.
-// Measured on a GB300, 8 x 4 heads: 8191 tokens 375 us, 1.47 PFLOP/s (394 in a long
-// run); 16383 tokens 1.36 ms, 1.62 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 617
-// us, 1.24; up to 512 tokens of four sequences behind up to 32256 rows 297 us, 1.49 (325
+// Measured on a GB300, 8 x 4 heads: 8191 tokens 362 us, 1.52 PFLOP/s (387 in a long
+// run); 16383 tokens 1.31 ms, 1.68 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 600
+// us, 1.28; up to 512 tokens of four sequences behind up to 32256 rows 290 us, 1.53 (20 more
 // where each run reads the rows when it comes to them); trees of 32 nodes of 16 sequences
 // of up to 8192 rows 53 us, 5.2 TB/s.
 //
@@ -37,8 +37,8 @@
 // into tiles of bf16: a code times its power of two is exactly a bf16 number, so
 // that products, softmax and results are those of bf16 rows of the same values.  A
 // tile of K is turned in some 1400 cycles, and there is room for three tiles of bf16
-// only, which bounds them: 1000 tokens behind 100000 rows 1.26 ms, 1.31 PFLOP/s;
-// trees of 64 nodes of 4 sequences of up to 131071 rows 224 us, 1.22 PFLOP/s.
+// only, which bounds them: 1000 tokens behind 100000 rows 1.22 ms, 1.35 PFLOP/s;
+// trees of 64 nodes of 4 sequences of up to 131071 rows 219 us, 1.26 PFLOP/s.
 #include "prompt_plan.cuh"
 #include "rows8_core.cuh"
 #include "tc.cuh"
@@ -58,7 +58,11 @@ using namespace tc;
 
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
 constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
-constexpr float kLazy = 8.f;                     // how far the maximum may pass m before O is rescaled, in powers of two
+// How far the maximum may pass m before O is rescaled, in powers of two.  Weights are
+// numbers with an exponent, and lose nothing above 1; sums of 2^30 of them times values of
+// 2^80 stay below 2^126.  With 8 / 12 / 16 / 1000, in us: 8191 tokens 371 / 367 / 364 / 364,
+// 16 packed prompts 610 / 604 / 602 / 602, 1000 behind 100000 8-bit rows 1244 / 1233 / 1228 / 1227.
+constexpr float kLazy = 16.f;
 constexpr int kQ = kTile * kD * 2;               // bytes of a stream's rows of q
 constexpr int kStage = kTile * kD * 2;           // of a K or V tile
 constexpr int kCodes = kTile * kD;               // of a tile of codes
@@ -258,13 +262,14 @@ __device__ __forceinline__ void softmax_step(uint32_t ts, uint32_t to, bool mask
     l *= f;
     if (up) m = top;
 #pragma unroll 1
-    for (int k = 0; k < kD; k += 16) {
-      uint32_t o[16];
-      tmem_ld16(to + k, o);
+    for (int k = 0; k < kD; k += 32) {  // (16 at a time: 1.5% slower over all)
+      uint32_t o[32];
+      tmem_ld32(to + k, o);
       wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
       tmem_st16(to + k, o);
+      tmem_st16(to + k + 16, o + 16);
     }
   }
   uint32_t w[32];

@@ -513,7 +513,7 @@ int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, cons
  * zeros where a token sees none.  Logits, softmax statistics and sums are
  * float32; the softmax weights enter the products as bf16, or as halves.  8-bit rows count as
  * the values they stand for.  A sequence's keys, values and rows of q must be
- * finite, logits below 2^28 and values below 2^96 in magnitude; what lies past
+ * finite, logits below 2^28 and values up to 2^80 in magnitude; what lies past
  * its rows, and other sequences, may hold anything.  Equal calls give equal bits.
  * At most BPKV_SHARED_MAX_SEQ sequences, 2^30 tokens, rows of a sequence or rows
  * of H T keys, and 2^31 tiles of 128 keys by 2 floor(128 / G) tokens and KV head

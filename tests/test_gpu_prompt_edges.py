@@ -230,6 +230,37 @@ def test_values_of_any_size(pk, bits, t):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("t,n_max", [(1, 1900), (16, 1900), (64, 1900), (64, 32768)])
+@pytest.mark.parametrize("rise", [[0, 15], [0, 15, 15, 30, 31, 62], [15, 0], [0, 5, 10, 15, 20]])
+def test_values_near_the_bound(pk, bits, t, n_max, rise):
+    """Values up to 2^80 under weights that are far above those of the first tile: logits rise by 1.02 `rise` powers of
+    two, by which the sums may be above their size before they are taken back.  All is positive, so the output's error
+    is that of its terms: a weight's rounding 2^-8, a sum of n 2^-23 n, the exponent's float32 2^-17 or less, the output
+    2^-8."""
+    g = torch.Generator(device="cuda").manual_seed(sum(rise))
+    H, G, n, cap = 2, 4, 1900, 32768 if n_max > 2048 else 2048
+    q = torch.ones((1, t, H, G, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    # rows in as many parts as there are in `rise`, the first of a tile
+    part = torch.arange(cap, device="cuda").sub(128).clamp(min=-1).div(1800 / max(1, len(rise) - 1), rounding_mode="floor")
+    part = (part + 1).clamp(0, len(rise) - 1).long()
+    k = (torch.tensor(rise, device="cuda", dtype=torch.float32)[part] / 16)[None, None, :, None].expand(1, H, cap, D)
+    v = ((torch.rand((1, H, cap, D), generator=g, device="cuda") + 1) * 2.0 ** 79).to(torch.bfloat16)
+    c, (k64, v64, *_) = make_cache(pk, bits, G, cap, [n], k.to(torch.bfloat16), v)
+    assert float(v64.abs().max()) <= 2.0 ** 80
+    c.c.n_max = n_max
+    ws = pk.tree_workspace(c, t)
+    fn = pk.bpkv_tree_attend if bits == 16 else pk.bpkv_tree_attend8
+    fn(c.c, t, torch.zeros((1, t), dtype=torch.int64, device="cuda"), q, out, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert pk.bpkv_read_status(ws) == 0
+    w = torch.softmax(k64[0, :, :n - t].double().sum(-1) / math.sqrt(D), -1)
+    want = torch.einsum("hn,hnd->hd", w, v64[0, :, :n - t].double())[None, None, :, None]
+    err = ((out.double() - want).abs() / want).max()
+    assert float(err) <= 2.0 ** -7 + n * 2.0 ** -23 + 2.0 ** -17, float(err)
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("t,n_max", [(1, 1900), (4, 1900), (16, 1900), (64, 1900), (64, 32768)])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_large_logits(pk, bits, t, n_max, sign):
