@@ -251,8 +251,8 @@ def shared_workspace(cache, prefix=None):
 
 
 def prompt_args(q, out, q_start, k=None, v=None, cache=None):
-    """bpkv_prompt_args for q [T][H][G][D] bf16 (a token's heads dense, any stride between tokens) and out of the same
-    shape, dense; q_start [N + 1] int64.  k, v: bf16 [T][H][D] (a token's heads dense, any stride between tokens), or
+    """bpkv_prompt_args for q [T][H][G][D] bf16 (a token's heads dense, tokens a multiple of 8 elements apart that is no
+    less than one's heads) and out of the same shape, dense; q_start [N + 1] int64.  k, v: bf16 [T][H][D], likewise, or
     each sequence's [H][t][D] one behind the other as [T H][D], or [N][H][t][D] for equal lengths; or cache: a Cache or
     Rows8 whose sequences end in the new tokens.  All on one device.  The struct keeps the tensors it points to alive."""
     import torch
@@ -267,6 +267,7 @@ def prompt_args(q, out, q_start, k=None, v=None, cache=None):
     device = q.device
     need(T > 0 and N > 0, "no tokens, or no sequences")
     need(_dense_from(q, 1), "a token's heads of q must be dense")
+    need(_tokens_apart(q), "q's tokens must not overlap, and lie a multiple of 8 elements apart")
     _check_arg("prompt_args", "out", out, torch.bfloat16, (T, H, G, HEAD_DIM), device)
     _check_arg("prompt_args", "q_start", q_start, torch.int64, (N + 1,), device)
     need((k is None) == (v is None) and (k is None) != (cache is None), "either k and v or cache")
@@ -281,6 +282,8 @@ def prompt_args(q, out, q_start, k=None, v=None, cache=None):
             if x.dim() == 3:
                 need(x.shape == (T, H, HEAD_DIM) and x.dtype == torch.bfloat16 and x.device == device
                      and _dense_from(x, 1), f"{name} must be bf16 [T][H][D], a token's heads dense, on {device}")
+                # a stride of 0 in the struct would say another layout
+                need(_tokens_apart(x), f"{name}'s tokens must not overlap, and lie a multiple of 8 elements apart")
                 ld[i] = x.stride(0) if T > 1 else H * HEAD_DIM
             else:
                 shape = (T * H, HEAD_DIM) if x.dim() == 2 else (N, H, T // N, HEAD_DIM)
@@ -303,6 +306,11 @@ def _dense_from(x, dim):
             return False
         n *= size
     return True
+
+
+def _tokens_apart(x):
+    """Whether the tokens (dimension 0) of x, which are dense, share nothing and start on 16-byte boundaries."""
+    return x.shape[0] == 1 or (x.stride(0) >= x[0].numel() and x.stride(0) % 8 == 0)
 
 
 def _prompt_workspace(n_new, group, device):

@@ -1,0 +1,55 @@
+"""What the Python helpers for several new tokens of a sequence make of tensors
+whose strides or types the kernels would read as something else (no GPU)."""
+import pytest
+import torch
+
+import bit_plane_kv_encode_gb300 as pk
+
+N, H, G, T, D = 2, 3, 4, 10, 128
+
+
+def bf(*shape, **kw):
+    return torch.zeros(shape, dtype=torch.bfloat16, **kw)
+
+
+def prompt(**kw):
+    d = dict(q=bf(T, H, G, D), out=bf(T, H, G, D), q_start=torch.zeros(N + 1, dtype=torch.int64), k=bf(T, H, D),
+             v=bf(T, H, D))
+    d.update(kw)
+    return pk.prompt_args(**d)
+
+
+def one_for_all(*shape):
+    """One token's heads as those of T tokens: a stride of 0, which in the struct says another layout."""
+    return bf(1, *shape).expand(T, *shape)
+
+
+def tokens(stride, *shape):
+    """T tokens of dense heads, `stride` elements apart."""
+    n = torch.Size(shape).numel()
+    dense = tuple(torch.empty(shape).stride())
+    return torch.as_strided(bf((T - 1) * stride + n), (T, *shape), (stride, *dense))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=one_for_all(H, D), v=one_for_all(H, D)), dict(k=one_for_all(H, D)), dict(v=one_for_all(H, D)),
+    dict(q=one_for_all(H, G, D)), dict(k=tokens(H * D - 8, H, D), v=tokens(H * D - 8, H, D)), dict(k=tokens(8, H, D)),
+    dict(v=tokens(H * D + 4, H, D)), dict(q=tokens(D, H, G, D)), dict(q=tokens(H * G * D + 2, H, G, D))])
+def test_tokens_that_overlap_or_lie_between_boundaries(kw):
+    with pytest.raises(ValueError):
+        prompt(**kw)
+
+
+def test_what_the_strides_read_is_there():
+    """Of a struct that is made, every element that the call may read lies in the tensor's storage."""
+    for k in (bf(T, H, D), tokens(H * D + 8, H, D), bf(T, 2 * H, D)[:, H:], bf(T * H, D), bf(N, H, T // N, D)):
+        a = prompt(k=k, v=k.clone() if k.is_contiguous() else k)
+        ld = a.ld_k or H * D
+        end = k.storage_offset() + (T - 1) * ld + H * D
+        assert end * 2 <= k.untyped_storage().nbytes() and (a.ld_k == 0) == (k.dim() != 3)
+
+
+def test_one_token_has_no_stride():
+    one = bf(1, H, D).expand(1, H, D)
+    a = prompt(q=bf(1, H, G, D), out=bf(1, H, G, D), k=one, v=one)
+    assert (a.ld_q, a.ld_k, a.ld_v) == (H * G * D, H * D, H * D)
