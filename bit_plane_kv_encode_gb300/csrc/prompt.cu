@@ -128,14 +128,18 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
   return false;
 }
 
-// The same for waits that are long and not urgent: the others keep the issue slots.
+// The same for what is not urgent: the others keep the issue slots.  tiles: of what is waited
+// for.  Two streams' tile is some 3000 cycles, of 8-bit rows 3500, and a segment may have
+// millions: with 1.2 million, 150 million rows, it is longer than kWaitCycles.  So 2^16 tiles
+// have that, 17 times what they take.  That something is stuck is known sooner, from the waits
+// of those who compute, which are for a tile.
 template <int NS>
-__device__ __forceinline__ bool doze(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-  const int64_t t0 = clock64();
+__device__ __forceinline__ bool doze(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int tiles) {
+  const int64_t end = clock64() + ((tiles >> 16) + 1) * kWaitCycles;
 #pragma unroll 1
-  for (uint32_t i = 0; i < kMbarRounds; ++i) {
+  for (uint32_t i = 0; i < 0xffffffffu; ++i) {
     if (mbar_try(bar, parity)) return true;
-    if (*abort || clock64() - t0 > kWaitCycles) break;
+    if (*abort || clock64() > end) break;
     __nanosleep(NS);
   }
   *abort = 1;
@@ -537,16 +541,17 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         const uint64_t policy = shared::evict_first_policy();
         Walk walk(sm.plan, a);
         uint32_t loads = 0;
+        int last = 0;  // tiles of the segment before
         bool ok = true;
         for (;; ++seg_no) {
           const uint32_t i = seg_no % kSegments;
           g = walk.next();
-          ok = doze<100>(smem_u32(&sm.seg_empty[i]), ((seg_no / kSegments) & 1) ^ 1, abort);
+          ok = doze<100>(smem_u32(&sm.seg_empty[i]), ((seg_no / kSegments) & 1) ^ 1, abort, 0);
           if (!ok) break;
           sm.seg[i] = g;
           mbar_arrive(smem_u32(&sm.seg_full[i]));
           if (g.tiles == 0) break;
-          if (seg_no > 0) ok = doze<100>(smem_u32(&sm.q_empty), (seg_no - 1) & 1, abort);
+          if (seg_no > 0) ok = doze<100>(smem_u32(&sm.q_empty), (seg_no - 1) & 1, abort, last);
           if (!ok) break;
           const int n = g.dual ? 2 : 1;
           mbar_expect_tx(bar, 2 * n * bytes);
@@ -556,6 +561,7 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
               tma_load_3d(smem_u32(q_smem + s * kQ + half * (kTile * 128)), &maps.q, bar, half * 64, g.h * a.group,
                           g.token + s * a.run, policy);
           ++loads;
+          last = g.tiles;
         }
         uint32_t never = 0;  // as above
         if (loads > 0) wait(bar, (loads - 1) & 1, &never);
