@@ -898,7 +898,7 @@ bool map_codes(CUtensorMap* m, const void* rows, int64_t cap, int64_t planes) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Space {
-  size_t cuts, ml, o, total;
+  size_t starts, cuts, ml, o, total;
   int slot_rows;
 };
 
@@ -907,6 +907,8 @@ Space space(int64_t tokens, int64_t group) {
   // of the tokens of a unit at most, a stream's 128 rows, or both streams'
   s.slot_rows = tokens <= kTile / group ? kTile : kRows;
   size_t off = 256;  // status word
+  s.starts = off;  // of the call's sequences, where the streaming half hands it over
+  off = up256(off + (kMaxSeq + 1) * sizeof(int64_t));
   s.cuts = off;
   off = up256(off + kSms * sizeof(Cut));
   s.ml = off;
@@ -1028,6 +1030,21 @@ int few_ctas(int bits, int64_t n, int64_t wide, int rows, bool again, int64_t ke
   return ctas;
 }
 
+// few_ctas takes a call's tokens for spread over its sequences; one may have them all, and its
+// rows, 16 at a time, are then streamed again and again by CTAs that each read all keys.  Whether
+// that would cost more than a look at the lengths on the device and a launch of both halves
+// (5 to 12 us).  Us without / with it, where one sequence has all tokens, and where each has one;
+// 8 x 4 heads, bf16 rows (8-bit rows in brackets):
+//   64 of 64 sequences of 16000: 118 / 37 and 592 / 603 (109 / 39, 385 / 398), of 100000: 659 / 92
+//   and 3618 / 3628 (601 / 103, 2295 / 2310); 16 of 16 of 16000: 111 / 24 and 149 / 156 (101 / 26,
+//   101 / 108).  Of fewer keys there is less to gain: 64 of 64 of 4000: 41, one sequence alone on
+//   the tensor cores 21 (39, 22), of 2000: 28, 19 (27, 19).
+// The groups that are then busy, of all KV heads, take turns on the SMs.
+static bool one_may_have_them(int64_t H, int64_t rows, int64_t per, int ctas, int64_t keys) {
+  const int64_t busy = H * ((rows + per - 1) / per);
+  return rows > per && keys * ((busy + kSms - 1) / kSms) > 4000 * ctas;
+}
+
 static void few_rows(FewArgs& f, const PromptRows& r, int64_t step) {
   f.len = r.len;
   f.rows[0][0] = r.k;
@@ -1060,8 +1077,15 @@ cudaError_t launch_prompt(const bpkv_prompt_args& p, void* ws, cudaStream_t st) 
     if (p.cache) few_rows(f, rows_of(*p.cache), kD * 2);
     if (p.rows8) few_rows(f, rows_of(*p.rows8), kD);
     const int64_t keys = p.cache ? p.cache->n_max : p.rows8 ? p.rows8->n_max : T;
-    const int ctas = few_ctas(p.rows8 ? 8 : 16, H * groups, prompt_units(T, p.n_seq, H, p.group), (int)(T * p.group), 2 * groups > 3 * some, keys);
-    if (ctas) return p.rows8 ? launch_few_tokens<8>(f, ctas, st) : launch_few_tokens<16>(f, ctas, st);
+    const bool again = 2 * groups > 3 * some;
+    const int ctas = few_ctas(p.rows8 ? 8 : 16, H * groups, prompt_units(T, p.n_seq, H, p.group), (int)(T * p.group), again, keys);
+    if (ctas) {
+      const bool either = f.len && !again && one_may_have_them(H, T * p.group, per, ctas, keys);
+      if (either) f.starts = reinterpret_cast<int64_t*>(static_cast<unsigned char*>(ws) + space(T, p.group).starts);
+      const cudaError_t e = p.rows8 ? launch_few_tokens<8>(f, ctas, st) : launch_few_tokens<16>(f, ctas, st);
+      if (e != cudaSuccess || !either) return e;
+      a.q_start = f.starts;
+    }
   }
   if (!map_q(&maps.q, p.q, T, H * p.group, p.ld_q, p.group, kTile / p.group)) return cudaErrorInvalidValue;
   if (p.cache) return over_cache<16>(a, maps, rows_of(*p.cache), T, ws, st);

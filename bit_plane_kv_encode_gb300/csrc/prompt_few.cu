@@ -8,6 +8,10 @@
 // the first tiles and its join cost more than such a call's work.  A tree's rows are
 // taken 16 at a time, each time over all keys, from L2 again.
 //
+// Of prompts behind long rows of a cache the host does not know whether each sequence has
+// its few rows or one has them all.  There this half looks, and leaves the call to the
+// tensor cores, which are launched behind it in any case, where rows would be read again.
+//
 // Measured on a GB300: one new token of a sequence of 4000 bf16 rows, 8 x 4 heads, 6.8 us,
 // latency; of 64000 (262 MB) 42 us, 6.3 TB/s; 64 sequences of 4000 in 8 bits (528 MB) 88 us,
 // 6.0 TB/s.  Weights enter their product as bf16 (2^-8), for 8-bit rows as halves (2^-11).
@@ -32,6 +36,48 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The tokens of sequence b + lane, and the first of them: starts as prompt_plan.cuh takes them,
+// within the tokens, none before the last.  By a warp, 32 sequences at a time; top: the end of those before.
+__device__ __forceinline__ int tokens_of(const FewArgs& a, int b, int& top, int& lo) {
+  const int lane = threadIdx.x & 31, i = min(b + lane, a.n_seq - 1);
+  lo = b + lane < a.n_seq ? (int)max64(0, min64(a.q_start[i], a.tokens)) : 0;
+  const int next = (int)max64(0, min64(a.q_start[i + 1], a.tokens));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, lo, o);
+    if (lane >= o) lo = max(lo, u);
+  }
+  lo = max(lo, top);
+  const int hi = max(lo, next);
+  top = __shfl_sync(0xffffffffu, hi, 31);
+  return b + lane < a.n_seq ? hi - lo : 0;
+}
+__device__ __forceinline__ int groups_of(const FewArgs& a, int tokens) {
+  return (tokens * a.group + a.per - 1) / a.per;
+}
+
+// Whether the sequences' groups of rows would read half as many rows again as there are (the
+// host's rule, few_ctas' `again`, but by the tokens and rows that each has).  By a warp.
+__device__ __forceinline__ bool crowded(const FewArgs& a) {
+  const int lane = threadIdx.x & 31;
+  int top = 0;
+  int64_t read = 0, rows = 0;
+#pragma unroll 1
+  for (int b = 0; b < a.n_seq; b += 32) {
+    int lo;
+    const int mine = tokens_of(a, b, top, lo);
+    if (mine > 0) {
+      const int64_t n = shared::tokens_of(a.len[b + lane], a.cap);
+      read += n * groups_of(a, mine);
+      rows += n;
+    }
+  }
+  int64_t more = 2 * read - 3 * rows;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+  return more > 0;
 }
 
 // A warp's way through the rows of one unit: every step-th tile, step the warps of all its CTAs.
@@ -65,24 +111,15 @@ struct FewWalk {
     for (int kv = 0; kv < 2; ++kv) first[kv] = row0 * a.step[kv] + (a.where == kToken ? h * (kD * 2) : 0);
   }
   // The sequence that a group of rows belongs to, and its place there; none: no tokens.
-  // Starts as prompt_plan.cuh takes them: within the tokens, none before the last.
   __device__ __forceinline__ void find(uint32_t& group) {
     const int lane = threadIdx.x & 31;
     int top = 0, before = 0;
     index = count = start = 0;
 #pragma unroll 1
     for (int b = 0; b < a.n_seq; b += 32) {
-      const int i = min(b + lane, a.n_seq - 1);
-      int lo = b + lane < a.n_seq ? (int)max64(0, min64(a.q_start[i], a.tokens)) : 0;
-      const int next = (int)max64(0, min64(a.q_start[i + 1], a.tokens));
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, lo, o);
-        if (lane >= o) lo = max(lo, u);
-      }
-      lo = max(lo, top);
-      const int hi = max(lo, next), mine = b + lane < a.n_seq ? hi - lo : 0;
-      const int groups = (mine * a.group + a.per - 1) / a.per;
+      int lo;
+      const int mine = tokens_of(a, b, top, lo);
+      const int groups = groups_of(a, mine);
       int sum = groups;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -99,7 +136,6 @@ struct FewWalk {
         return;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
-      top = __shfl_sync(0xffffffffu, hi, 31);
     }
     group = 0;
   }
@@ -149,6 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_unit(const __grid_constant_
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_enter();
+  if (a.starts) {  // this half takes the call, or the one behind it, which finds no tokens else
+    const bool theirs = crowded(a);
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= a.n_seq; i += kThreads) a.starts[i] = theirs ? a.q_start[i] : 0;
+    if (theirs) return;  // all CTAs
+  }
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const unsigned char* exps = smem + kWarps * kStages * kStage + warp * kStages * S::kExps;
   FewWalk ahead(a, S::kTok, blockIdx.x / ctas, rank * kWarps + warp, ctas * kWarps), cur = ahead;

@@ -86,6 +86,7 @@ struct FewArgs {
   int32_t n_seq, n_heads, group, t;
   int32_t where;              // Rows
   int32_t groups, per;        // a tree's query rows, per (8 or 16) at a time; groups: of a sequence, or of all
+  int64_t* starts;            // NULL, or where the tensor cores' half behind this one finds q_start (prompt_few.cu)
 };
 
 // Counts are below 2^31: the host makes sure.
