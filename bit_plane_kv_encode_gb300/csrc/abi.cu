@@ -542,6 +542,9 @@ int bpkv_rows8_accept(bpkv_rows8* c, const uint16_t* k_new, const uint16_t* v_ne
       !aligned(start, 8) || !aligned(path, 4) || !aligned(count, 4) || !aligned(status, 4))
     return BPKV_EINVAL;
   if (start == c->seq_len && c->n_max + t > c->cap_tokens) return BPKV_EINVAL;
+  // lengths are written while other CTAs still read the starts
+  const int64_t n = (int64_t)c->n_seq * sizeof(int64_t);
+  if (start != c->seq_len && overlap(start, n, c->seq_len, n)) return BPKV_EINVAL;
   if (!rows_in_range(c->n_seq, c->n_kv_heads, t)) return BPKV_EUNSUPPORTED;
   BPKV_TRY(cuda_status(launch_rows8_accept(*c, k_new, v_new, t, start, path, count, status, as_stream(stream))));
   c->n_max = min64(c->n_max + t, c->cap_tokens);

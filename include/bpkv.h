@@ -583,7 +583,7 @@ int bpkv_tree_attend8(const bpkv_rows8 *c, int32_t t, const uint64_t *tree, cons
  * nearest.  For both BPKV_DEV_OVERFLOW is set in *status (device, NULL to skip).  n_max becomes
  * min(n_max + t, cap_tokens), as for bpkv_rows8_append with start: set it to what
  * you know.  start may be seq_len itself (then n_max + t must not pass cap_tokens).
- * BPKV_EINVAL when t < 1 or t > cap_tokens.
+ * BPKV_EINVAL when t < 1 or t > cap_tokens, or when start overlaps seq_len otherwise.
  */
 int bpkv_rows8_accept(bpkv_rows8 *c, const uint16_t *k_new, const uint16_t *v_new, int32_t t, const int64_t *start,
                       const int32_t *path, const int32_t *count, int32_t *status, void *stream);

@@ -53,3 +53,16 @@ def test_one_token_has_no_stride():
     one = bf(1, H, D).expand(1, H, D)
     a = prompt(q=bf(1, H, G, D), out=bf(1, H, G, D), k=one, v=one)
     assert (a.ld_q, a.ld_k, a.ld_v) == (H * G * D, H * D, H * D)
+
+
+@pytest.mark.parametrize("shift", [-1, 1])
+def test_accept_refuses_starts_that_share_some_of_the_lengths(shift):
+    """Starts that are the lengths are read before these are set; those that lie one beside them would not be."""
+    from bit_plane_kv_encode_gb300 import build
+    build.build()
+    base, far = 1 << 40, 1 << 36  # aligned, never read
+    c = pk.bpkv_rows8(N, H, G, D, 512, 0, base, base + far, base + 2 * far, base + 3 * far, base + 4 * far)
+    with pytest.raises(pk.BpkvError) as e:
+        pk.bpkv_rows8_accept(c, base + 5 * far, base + 6 * far, 4, base + 4 * far + 8 * shift, None, base + 7 * far,
+                             stream=0)
+    assert e.value.status == -1 and c.n_max == 0
