@@ -84,7 +84,15 @@ class Cache:
 
     @property
     def n_max(self) -> int:
+        """What the host knows the sequences' lengths to be at most; every
+        append adds its tokens.  Where seq_len is set back (drafted tokens that
+        were not accepted), set it to the longest that is left: appends are
+        refused once it would pass the capacity."""
         return int(self.c.n_max)
+
+    @n_max.setter
+    def n_max(self, tokens: int):
+        _set_n_max(self.c, tokens)
 
     def append(self, k_new, v_new, stream=None):
         """Append k_new/v_new [N][H][t][D] bf16 (device) to every sequence."""
@@ -104,6 +112,12 @@ class Cache:
         if n == 0:
             raise BpkvError("bpkv_workspace_size", -1)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+
+def _set_n_max(c, tokens: int):
+    if not 0 <= tokens <= c.cap_tokens:
+        raise ValueError(f"n_max must be 0 .. {c.cap_tokens}")
+    c.n_max = int(tokens)
 
 
 def _check_arg(fn, name, x, dtype, shape, device):
@@ -150,9 +164,7 @@ class Rows8:
 
     @n_max.setter
     def n_max(self, tokens: int):
-        if not 0 <= tokens <= self.c.cap_tokens:
-            raise ValueError(f"n_max must be 0 .. {self.c.cap_tokens}")
-        self.c.n_max = int(tokens)
+        _set_n_max(self.c, tokens)
 
     def append(self, k_new, v_new, start=None, status=None, stream=None):
         """Quantise k_new/v_new [N][H][t][D] bf16 (device) behind every

@@ -66,3 +66,15 @@ def test_accept_refuses_starts_that_share_some_of_the_lengths(shift):
         pk.bpkv_rows8_accept(c, base + 5 * far, base + 6 * far, 4, base + 4 * far + 8 * shift, None, base + 7 * far,
                              stream=0)
     assert e.value.status == -1 and c.n_max == 0
+
+
+@pytest.mark.parametrize("make", [pk.Cache, pk.Rows8])
+def test_the_bound_of_the_lengths_can_be_set(make):
+    c = make(N, H, G, 512, device="cpu")
+    for n in (512, 0, 77):
+        c.n_max = n
+        assert c.n_max == c.c.n_max == n
+    for n in (-1, 513):
+        with pytest.raises(ValueError):
+            c.n_max = n
+    assert c.n_max == 77
