@@ -343,7 +343,25 @@ def prompt_workspace(args):
 def tree_workspace(cache, t: int):
     """Workspace (uint8, device) of bpkv_tree_attend / bpkv_tree_attend8 for trees of t nodes over a Cache or Rows8;
     its status word is clear."""
-    return _prompt_workspace(t, cache.c.group, cache.device)
+    return _prompt_workspace(t, cache.c.group, cache.seq_len.device)
+
+
+def tree_attend(cache, q, out, ws, tree=None, stream=None):
+    """bpkv_tree_attend over a Cache, bpkv_tree_attend8 over a Rows8: q and out [N][t][H][G][D] bf16, tree [N][t] int64
+    or uint64 (None: a chain), ws of tree_workspace.  ValueError for tensors of another type, shape or device, or with
+    other strides, which the calls themselves take at their addresses."""
+    import torch
+    c, device = cache.c, cache.seq_len.device
+    t = q.shape[1] if q.dim() == 5 else 0
+    shape = (c.n_seq, t, c.n_kv_heads, c.group, HEAD_DIM)
+    _check_arg("tree_attend", "q", q, torch.bfloat16, shape, device)
+    _check_arg("tree_attend", "out", out, torch.bfloat16, shape, device)
+    _check_arg("tree_attend", "tree", tree, torch.uint64 if tree is not None and tree.dtype is torch.uint64 else torch.int64,
+               (c.n_seq, t), device)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"tree_attend: ws must be contiguous, on {device}")
+    fn = bpkv_tree_attend8 if isinstance(cache, Rows8) else bpkv_tree_attend
+    fn(c, t, tree, q, out, ws, ws.numel() * ws.element_size(), stream)
 
 
 def cache_array(caches):
@@ -358,5 +376,5 @@ def sync_n_max(caches, arr):
         c.c.n_max = s.n_max
 
 
-__all__ = [n for n in dir() if n.startswith("bpkv_")] + ["Cache", "Rows8", "cache_array", "prompt_args", "prompt_workspace", "qkv_args", "shared_workspace", "sync_n_max", "tree_workspace", "BpkvError"]
+__all__ = [n for n in dir() if n.startswith("bpkv_")] + ["Cache", "Rows8", "cache_array", "prompt_args", "prompt_workspace", "qkv_args", "shared_workspace", "sync_n_max", "tree_attend", "tree_workspace", "BpkvError"]
 _ = ctypes

@@ -5,7 +5,7 @@ way gives its own bits, by which the tests tell the two apart.  Bounds as in
 test_gpu_prompt."""
 import pytest
 import torch
-from test_gpu_prompt import attention, causal, check, run_prompt
+from test_gpu_prompt import attention, causal, check, run_prompt, run_tree
 from test_gpu_shared import draw_rows, make_cache, pk  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +108,14 @@ def test_a_captured_call_with_other_starts(pk, bits):
     out.fill_(7.0)
     graph.replay()
     assert torch.equal(out, attend(pk, q, [60, 0, 4] + [0] * (N - 3), c)) and pk.bpkv_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("bits", BITS)
+def test_the_checked_call(pk, bits):
+    """tree_attend is the call of the cache's kind."""
+    got = run_tree(pk, bits, 3, 9, 2, 4, [700, 9, 4000])
+    out = torch.empty_like(got["out"])
+    pk.tree_attend(got["c"], got["q"], out, pk.tree_workspace(got["c"], 9), got["mask"])
+    assert torch.equal(out, got["out"])
+    with pytest.raises(ValueError):
+        pk.tree_attend(got["c"], got["q"].float(), out, got["ws"], got["mask"])

@@ -78,3 +78,45 @@ def test_the_bound_of_the_lengths_can_be_set(make):
         with pytest.raises(ValueError):
             c.n_max = n
     assert c.n_max == 77
+
+
+# ------------------------------------------------------------------ trees
+
+t = 5
+
+
+def tree_call(monkeypatch, make, **kw):
+    """What tree_attend passes on, by the name of the call."""
+    calls = []
+    for name in ("bpkv_tree_attend", "bpkv_tree_attend8"):
+        monkeypatch.setattr(pk, name, lambda *a, name=name: calls.append((name, a)))
+    d = dict(q=bf(N, t, H, G, D), out=bf(N, t, H, G, D), tree=torch.zeros((N, t), dtype=torch.int64),
+             ws=torch.zeros(1024, dtype=torch.uint8))
+    d.update(kw)
+    cache = make(N, H, G, 512, device="cpu")
+    pk.tree_attend(cache, d["q"], d["out"], d["ws"], d["tree"], stream=0)
+    (name, a), = calls
+    assert a[0] is cache.c and a[1] == t and a[2] is d["tree"] and a[3] is d["q"] and a[4] is d["out"] and a[5] is d["ws"]
+    assert a[6] == d["ws"].numel() * d["ws"].element_size() and a[7] == 0
+    return name
+
+
+@pytest.mark.parametrize("make,name", [(pk.Cache, "bpkv_tree_attend"), (pk.Rows8, "bpkv_tree_attend8")])
+def test_tree_attend_takes_what_fits(monkeypatch, make, name):
+    for tree in (torch.zeros((N, t), dtype=torch.int64), torch.zeros((N, t), dtype=torch.uint64), None):
+        assert tree_call(monkeypatch, make, tree=tree) == name
+    assert tree_call(monkeypatch, make, ws=torch.zeros(128, dtype=torch.int64)) == name
+
+
+@pytest.mark.parametrize("make", [pk.Cache, pk.Rows8])
+@pytest.mark.parametrize("kw", [
+    dict(q=bf(N, t, H, G, D).float()), dict(q=bf(N, t, G, H, D).transpose(2, 3)), dict(q=bf(N * t, H, G, D)),
+    dict(q=bf(N, 2 * t, H, G, D)[:, ::2]), dict(q=bf(N + 1, t, H, G, D)), dict(q=bf(N, t, H, G, D, device="meta")),
+    dict(out=bf(N, t, H, G, D).float()), dict(out=bf(N, t + 1, H, G, D)), dict(out=bf(N, t, H, G, 2 * D)[..., :D]),
+    dict(tree=torch.zeros((N, t), dtype=torch.int32)), dict(tree=torch.zeros((N, t, t), dtype=torch.bool)),
+    dict(tree=torch.zeros((t, N), dtype=torch.int64).T), dict(tree=torch.zeros((N, 64), dtype=torch.int64)),
+    dict(tree=torch.zeros((N, t), dtype=torch.int64, device="meta")), dict(ws=torch.zeros(1024, device="meta")),
+    dict(ws=torch.zeros(2048, dtype=torch.uint8)[::2])])
+def test_tree_attend_refuses_other_tensors(monkeypatch, make, kw):
+    with pytest.raises(ValueError):
+        tree_call(monkeypatch, make, **kw)
