@@ -253,7 +253,6 @@ struct Segment {
   bool whole;       // all of the unit's tiles
   int32_t pieces;   // of a unit that begins here and goes on, else 0
   int32_t t, off;   // of the sequence
-  __device__ int steps() const { return dual ? 2 * tiles : tiles; }
   __device__ int steps_of(int s) const { return dual ? tiles : (tiles + 1 - s) / 2; }
   __device__ int tile_of(int s, int j) const { return tile0 + (dual ? j : 2 * j + s); }
   // the segment's slot of partial rows

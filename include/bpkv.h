@@ -511,10 +511,14 @@ int bpkv_shared_attend8(const bpkv_rows8 *prefix, const int32_t *prefix_of, cons
  * q . k / sqrt(D), every query head attends over the keys that its token sees,
  *   o = sum_x softmax_x(q . k_x / sqrt(D)) v_x,
  * zeros where a token sees none.  Logits, softmax statistics and sums are
- * float32; the softmax weights enter the products as bf16, or as halves.  8-bit rows count as
- * the values they stand for.  A sequence's keys, values and rows of q must be
- * finite, logits below 2^28 and values up to 2^80 in magnitude; what lies past
- * its rows, and other sequences, may hold anything.  Equal calls give equal bits.
+ * float32; the softmax weights enter the products as bf16.  8-bit rows count as
+ * the values they stand for.  Where these are streamed (calls of few tokens; n_max
+ * has a say in it), it is a weight times its row's scale that enters, as a half:
+ * off by 2^-11 of itself, or by 2^-36 of the largest such product of the query
+ * head, of which rows with less count as zero.  A sequence's keys, values and rows
+ * of q must be finite, logits below 2^28 and values up to 2^80 in magnitude; what
+ * lies past its rows, and other sequences, may hold anything.  Equal calls give
+ * equal bits.
  * At most BPKV_SHARED_MAX_SEQ sequences, 2^30 tokens, rows of a sequence or rows
  * of H T keys, and 2^31 tiles of 128 keys by 2 floor(128 / G) tokens and KV head
  * (BPKV_EUNSUPPORTED for more, and for residency 1).
@@ -580,9 +584,9 @@ int bpkv_tree_attend8(const bpkv_rows8 *c, int32_t t, const uint64_t *tree, cons
  *   count  int32 [N] device, 0 .. t
  * A sequence whose rows would leave 0 .. cap_tokens or whose count is outside 0 .. t
  * keeps its rows and its length; a path's token outside 0 .. t - 1 is taken as the
- * nearest.  For both BPKV_DEV_OVERFLOW is set in *status (device, NULL to skip).  n_max becomes
- * min(n_max + t, cap_tokens), as for bpkv_rows8_append with start: set it to what
- * you know.  start may be seq_len itself (then n_max + t must not pass cap_tokens).
+ * nearest.  For both BPKV_DEV_OVERFLOW is set in *status (device, NULL to skip).
+ * n_max becomes min(n_max + t, cap_tokens), as for bpkv_rows8_append with start: set
+ * it to what you know.  start may be seq_len itself (then n_max + t must not pass cap_tokens).
  * BPKV_EINVAL when t < 1 or t > cap_tokens, or when start overlaps seq_len otherwise.
  */
 int bpkv_rows8_accept(bpkv_rows8 *c, const uint16_t *k_new, const uint16_t *v_new, int32_t t, const int64_t *start,
