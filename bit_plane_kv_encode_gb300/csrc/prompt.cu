@@ -55,9 +55,10 @@ cudaError_t launch_few_tokens(const FewArgs& a, int ctas, cudaStream_t st);
 namespace {
 
 using namespace tc;
+using shared::ex2;
+using shared::kLogScale;
 
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
-constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
 // How far the maximum may pass m before O is rescaled, in powers of two.  Weights are
 // numbers with an exponent, and lose nothing above 1; sums of 2^30 of them times values of
 // 2^80 stay below 2^126.  With 8 / 12 / 16 / 1000, in us: 8191 tokens 371 / 367 / 364 / 364,
@@ -162,12 +163,6 @@ __device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, volatile uin
   }
   *abort = 1;
   return false;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {

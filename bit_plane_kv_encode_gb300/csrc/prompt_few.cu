@@ -27,16 +27,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 using namespace shared::few;
+using shared::ex2;
+using shared::kLogScale;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // The tokens of sequence b + lane, and the first of them: starts as prompt_plan.cuh takes them,
 // within the tokens, none before the last.  By a warp, 32 sequences at a time; top: the end of those before.

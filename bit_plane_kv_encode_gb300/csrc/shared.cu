@@ -51,7 +51,6 @@ using namespace wide;
 
 constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
-constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
 
 // How far the maximum may pass m before O is rescaled, and where exp2's
 // results sit: bf16 P has float32's range; e5m2 pieces lie in 2^-16 .. 1.75 2^15.
@@ -124,12 +123,6 @@ struct Walk {
     return true;
   }
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 16 bytes of row r, chunk c of a 128-byte-row tile in the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }

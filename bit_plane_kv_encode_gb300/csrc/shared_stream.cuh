@@ -17,7 +17,6 @@ namespace few {
 
 constexpr int kStages = 3;
 constexpr int kStage = 8192;  // K rows then V rows
-constexpr float kLogScale = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(D)
 
 template <int BITS>
 struct Shape {
@@ -69,11 +68,6 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t*
         "%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 template <int BITS>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
