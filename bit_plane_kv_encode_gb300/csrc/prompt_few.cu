@@ -34,55 +34,16 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
 
-// The tokens of sequence b + lane, and the first of them: starts as prompt_plan.cuh takes them,
-// within the tokens, none before the last.  By a warp, 32 sequences at a time; top: the end of those before.
-__device__ __forceinline__ int tokens_of(const FewArgs& a, int b, int& top, int& lo) {
-  const int lane = threadIdx.x & 31, i = min(b + lane, a.n_seq - 1);
-  lo = b + lane < a.n_seq ? (int)max64(0, min64(a.q_start[i], a.tokens)) : 0;
-  const int next = (int)max64(0, min64(a.q_start[i + 1], a.tokens));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, lo, o);
-    if (lane >= o) lo = max(lo, u);
-  }
-  lo = max(lo, top);
-  const int hi = max(lo, next);
-  top = __shfl_sync(0xffffffffu, hi, 31);
-  return b + lane < a.n_seq ? hi - lo : 0;
-}
-__device__ __forceinline__ int groups_of(const FewArgs& a, int tokens) {
-  return (tokens * a.group + a.per - 1) / a.per;
-}
-
-// Whether the sequences' groups of rows would read half as many rows again as there are (the
-// host's rule, few_ctas' `again`, but by the tokens and rows that each has).  By a warp.
-__device__ __forceinline__ bool crowded(const FewArgs& a) {
-  const int lane = threadIdx.x & 31;
-  int top = 0;
-  int64_t read = 0, rows = 0;
-#pragma unroll 1
-  for (int b = 0; b < a.n_seq; b += 32) {
-    int lo;
-    const int mine = tokens_of(a, b, top, lo);
-    if (mine > 0) {
-      const int64_t n = shared::tokens_of(a.len[b + lane], a.cap);
-      read += n * groups_of(a, mine);
-      rows += n;
-    }
-  }
-  int64_t more = 2 * read - 3 * rows;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
-  return more > 0;
-}
-
 // A warp's way through the rows of one unit: every step-th tile, step the warps of all its CTAs.
+// EITHER: it also finds out whether the call is for the tensor cores.
+template <bool EITHER>
 struct FewWalk {
   static constexpr bool kMasked = true, kStrided = true;
   static constexpr int side = 0;
   const FewArgs& a;
   int tok, index, h, row0_q, step, tiles, t, n, count, start;
   int64_t row0, base, first[2];
+  bool theirs;
   __device__ __forceinline__ FewWalk(const FewArgs& args, int tile, uint32_t unit, int begin, int stride)
       : a(args), tok(tile), t(begin), step(stride) {
     const uint32_t head = unit / (uint32_t)a.groups;
@@ -107,15 +68,30 @@ struct FewWalk {
     for (int kv = 0; kv < 2; ++kv) first[kv] = row0 * a.step[kv] + (a.where == kToken ? h * (kD * 2) : 0);
   }
   // The sequence that a group of rows belongs to, and its place there; none: no tokens.
+  // Starts as prompt_plan.cuh takes them: within the tokens, none before the last.
+  // It is for the tensor cores where the groups would read half as many rows again as there are:
+  // the host's rule (few_ctas' `again`), but by the tokens and rows that each sequence has.
   __device__ __forceinline__ void find(uint32_t& group) {
     const int lane = threadIdx.x & 31;
     int top = 0, before = 0;
+    [[maybe_unused]] int64_t more = 0;
+    [[maybe_unused]] uint32_t found = 0xffffffffu;
     index = count = start = 0;
 #pragma unroll 1
     for (int b = 0; b < a.n_seq; b += 32) {
-      int lo;
-      const int mine = tokens_of(a, b, top, lo);
-      const int groups = groups_of(a, mine);
+      const int i = min(b + lane, a.n_seq - 1);
+      int lo = b + lane < a.n_seq ? (int)max64(0, min64(a.q_start[i], a.tokens)) : 0;
+      const int next = (int)max64(0, min64(a.q_start[i + 1], a.tokens));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, lo, o);
+        if (lane >= o) lo = max(lo, u);
+      }
+      lo = max(lo, top);
+      const int hi = max(lo, next), mine = b + lane < a.n_seq ? hi - lo : 0;
+      const int groups = (mine * a.group + a.per - 1) / a.per;
+      if constexpr (EITHER)
+        if (mine > 0) more += shared::tokens_of(a.len[i], a.cap) * (2 * groups - 3);
       int sum = groups;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -123,17 +99,27 @@ struct FewWalk {
         if (lane >= o) sum += u;
       }
       const uint32_t in = __ballot_sync(0xffffffffu, (int)group < before + sum);
-      if (in) {
+      if (in && (!EITHER || found == 0xffffffffu)) {
         const int k = __ffs(in) - 1;
         index = b + k;
         count = __shfl_sync(0xffffffffu, mine, k);
         start = __shfl_sync(0xffffffffu, lo, k);
-        group -= before + __shfl_sync(0xffffffffu, sum - groups, k);
-        return;
+        found = group - before - __shfl_sync(0xffffffffu, sum - groups, k);
+        if constexpr (!EITHER) {
+          group = found;
+          return;
+        }
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
+      top = __shfl_sync(0xffffffffu, hi, 31);
     }
     group = 0;
+    if constexpr (EITHER) {
+      if (found != 0xffffffffu) group = found;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+      theirs = more > 0;
+    }
   }
   __device__ __forceinline__ bool more() const { return t < tiles; }
   __device__ __forceinline__ bool next() {
@@ -164,7 +150,7 @@ struct FewWalk {
   }
 };
 
-template <int BITS, int NB, bool CLUSTER>
+template <int BITS, int NB, bool CLUSTER, bool EITHER>
 __global__ void __launch_bounds__(kThreads, 1) k_few_unit(const __grid_constant__ FewArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = Shape<BITS>;
@@ -181,26 +167,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_unit(const __grid_constant_
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_enter();
-  if (a.starts) {  // this half takes the call, or the one behind it, which finds no tokens else
-    const bool theirs = crowded(a);
-    if (blockIdx.x == 0)
-      for (int i = tid; i <= a.n_seq; i += kThreads) a.starts[i] = theirs ? a.q_start[i] : 0;
-    if (theirs) return;  // all CTAs
-  }
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const unsigned char* exps = smem + kWarps * kStages * kStage + warp * kStages * S::kExps;
-  FewWalk ahead(a, S::kTok, blockIdx.x / ctas, rank * kWarps + warp, ctas * kWarps), cur = ahead;
+  using Walk = FewWalk<EITHER>;
+  Walk ahead(a, S::kTok, blockIdx.x / ctas, rank * kWarps + warp, ctas * kWarps), cur = ahead;
   const uint64_t policy = shared::evict_first_policy();
+  if constexpr (EITHER) {  // this half takes the call, or the one behind it, which finds no tokens else
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= a.n_seq; i += kThreads) a.starts[i] = cur.theirs ? a.q_start[i] : 0;
+    if (cur.theirs) return;  // all CTAs
+  }
   prime<BITS>(ahead, ring, exps, policy);
   const int rows = cur.rows();
   if (rows <= 0) return;  // of no sequence: the whole cluster
-  const FewWalk unit = cur;
+  const Walk unit = cur;
   for (int i = tid; i < kWarps * kR; i += kThreads) s_ml[i / kR][i % kR] = make_float2(-INFINITY, 0.f);
   __syncthreads();
   float* rows_o = reinterpret_cast<float*>(smem + warp * kStages * kStage);  // the warp's ring, once it is read
   stream<BITS, NB>(
-      cur, ahead, ring, exps, policy, [&](const FewWalk&) { return rows; },
-      [&](const FewWalk&, const State<NB>& st, int) {
+      cur, ahead, ring, exps, policy, [&](const Walk&) { return rows; },
+      [&](const Walk&, const State<NB>& st, int) {
         cp_wait<0>();
         __syncwarp();
 #pragma unroll
@@ -271,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_unit(const __grid_constant_
   }
 }
 
-template <int BITS, int NB, bool CLUSTER>
+template <int BITS, int NB, bool CLUSTER, bool EITHER = false>
 cudaError_t go(const FewArgs& a, int ctas, cudaStream_t st) {
   constexpr int kSmem = Shape<BITS>::kRing;
   static std::atomic<uint64_t> done;
-  const auto kernel = k_few_unit<BITS, NB, CLUSTER>;
+  const auto kernel = k_few_unit<BITS, NB, CLUSTER, EITHER>;
   const cudaError_t e = shared::allow_smem(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -298,6 +284,7 @@ cudaError_t go(const FewArgs& a, int ctas, cudaStream_t st) {
 // ctas: of a unit's cluster
 template <int BITS>
 cudaError_t launch_few_tokens(const FewArgs& a, int ctas, cudaStream_t st) {
+  if (a.starts) return ctas > 1 ? go<BITS, 2, true, true>(a, ctas, st) : go<BITS, 2, false, true>(a, 1, st);
   if (a.per == 8) return ctas > 1 ? go<BITS, 1, true>(a, ctas, st) : go<BITS, 1, false>(a, 1, st);
   return ctas > 1 ? go<BITS, 2, true>(a, ctas, st) : go<BITS, 2, false>(a, 1, st);
 }
