@@ -541,7 +541,9 @@ __global__ void __launch_bounds__(Shape<BITS>::kThreads, 1) k_prompt(const __gri
         for (;; ++seg_no) {
           const uint32_t i = seg_no % kSegments;
           g = walk.next();
-          ok = doze<100>(smem_u32(&sm.seg_empty[i]), ((seg_no / kSegments) & 1) ^ 1, abort, 0);
+          const uint32_t old = smem_u32(&sm.seg_empty[i]), parity = ((seg_no / kSegments) & 1) ^ 1;
+          // that it sleeps costs 8-bit rows 1% (chunk 1241 / 1228) and gives bf16 rows as much (8191 tokens 368 / 373)
+          ok = BITS == 16 ? doze<100>(old, parity, abort, 0) : wait(old, parity, abort);
           if (!ok) break;
           sm.seg[i] = g;
           mbar_arrive(smem_u32(&sm.seg_full[i]));
@@ -1027,13 +1029,15 @@ int few_ctas(int bits, int64_t n, int64_t wide, int rows, bool again, int64_t ke
 
 // few_ctas takes a call's tokens for spread over its sequences; one may have them all, and its
 // rows, 16 at a time, are then streamed again and again by CTAs that each read all keys.  Whether
-// that would cost more than a look at the lengths on the device and a launch of both halves
-// (5 to 12 us).  Us without / with it, where one sequence has all tokens, and where each has one;
-// 8 x 4 heads, bf16 rows (8-bit rows in brackets):
-//   64 of 64 sequences of 16000: 118 / 37 and 592 / 603 (109 / 39, 385 / 398), of 100000: 659 / 92
-//   and 3618 / 3628 (601 / 103, 2295 / 2310); 16 of 16 of 16000: 111 / 24 and 149 / 156 (101 / 26,
-//   101 / 108).  Of fewer keys there is less to gain: 64 of 64 of 4000: 41, one sequence alone on
+// that would cost more than a look at the lengths on the device and a launch of both halves.  Us
+// without / with it, where one sequence has all tokens, and where each has one; 8 x 4 heads, bf16
+// rows (8-bit rows in brackets):
+//   64 of 64 sequences of 16000: 118 / 40 and 592 / 600 (109 / 41, 385 / 393), of 100000: 659 / 93
+//   and 3618 / 3600 (601 / 105, 2295 / 2285); 16 of 16 of 16000: 111 / 24 and 149 / 157 (101 / 26,
+//   101 / 106).  Of fewer keys there is less to gain: 64 of 64 of 4000: 41, one sequence alone on
 //   the tensor cores 21 (39, 22), of 2000: 28, 19 (27, 19).
+// Where n_max is far above the lengths it costs 6 us, of 64 sequences 12 (16 of one token each, of
+// 300 rows: 7.8 / 14.2; 64 25 / 37).
 // The groups that are then busy, of all KV heads, take turns on the SMs.
 static bool one_may_have_them(int64_t H, int64_t rows, int64_t per, int ctas, int64_t keys) {
   const int64_t busy = H * ((rows + per - 1) / per);
