@@ -19,17 +19,18 @@
 // of 2^kLazy, so O is seldom rescaled.  Only tiles that some row sees a part of are
 // masked, by a bit for each key.
 //
-// What bounds it: the chain of a stream, in cycles: S 700 (both its operands come from
-// shared memory, whose whole bandwidth it takes), 300 until the softmax sees it, 600 to
-// the maximum, 600 and 400 to the two halves of P, 400 to the end of O: 3000 for two
-// streams' tiles, of which the products are 2048.  And the power limit: a call of 400 us
-// runs at 2.0 GHz, calls back to back at 1.8.  Between segments 6500 cycles: the last O,
-// 256 rows through the load-store unit (4000, whatever way they were turned), the next S.
-// Without any softmax the products, loads and ends take 303 us of 8191 tokens' 383; without
-// the exponentials, or most of the maximum, 372 and 365.
-// Measured on a GB300, 8 x 4 heads: 8191 tokens 362 us, 1.52 PFLOP/s (387 in a long
-// run); 16383 tokens 1.31 ms, 1.68 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 600
-// us, 1.28; up to 512 tokens of four sequences behind up to 32256 rows 290 us, 1.53 (20 more
+// What bounds it: the chain of a stream, in cycles (timed inside the kernel when 8191 tokens
+// took 390 us): S 700 (both its operands come from shared memory, whose whole bandwidth it
+// takes), 300 until the softmax sees it, 600 to the maximum, 600 and 400 to the two halves of
+// P, 400 to the end of O: 3000 for two streams' tiles, of which the products are 2048.  And
+// the power limit: a call of 400 us runs at 2.0 GHz, calls back to back at 1.8.  Between
+// segments 6500 cycles: the last O, 256 rows through the load-store unit (4000, whatever way
+// they were turned), the next S.  Less of it, in us, 8191 tokens 369 and 16 packed prompts 602:
+// without any softmax 320 and 507, without the exponentials 343 and 566, without most of the
+// maximum 358 and 583, without the stores of O 357 and 567.
+// Measured on a GB300, 8 x 4 heads: 8191 tokens 365 us, 1.50 PFLOP/s (392 in a long
+// run); 16383 tokens 1.32 ms, 1.67 PFLOP/s; 16 packed prompts of 251 to 4001 tokens 600
+// us, 1.28; up to 512 tokens of four sequences behind up to 32256 rows 294 us, 1.51 (28 more
 // where each run reads the rows when it comes to them); trees of 32 nodes of 16 sequences
 // of up to 8192 rows 53 us, 5.2 TB/s.
 //
@@ -37,7 +38,7 @@
 // into tiles of bf16: a code times its power of two is exactly a bf16 number, so
 // that products, softmax and results are those of bf16 rows of the same values.  A
 // tile of K is turned in some 1400 cycles, and there is room for three tiles of bf16
-// only, which bounds them: 1000 tokens behind 100000 rows 1.22 ms, 1.35 PFLOP/s;
+// only, which bounds them: 1000 tokens behind 100000 rows 1.23 ms, 1.34 PFLOP/s;
 // trees of 64 nodes of 4 sequences of up to 131071 rows 219 us, 1.26 PFLOP/s.
 #include "prompt_plan.cuh"
 #include "rows8_core.cuh"
@@ -61,8 +62,8 @@ using shared::kLogScale;
 constexpr uint32_t kTmemCols = 512;              // S of both streams, then O of both
 // How far the maximum may pass m before O is rescaled, in powers of two.  Weights are
 // numbers with an exponent, and lose nothing above 1; sums of 2^30 of them times values of
-// 2^80 stay below 2^126.  With 8 / 12 / 16 / 1000, in us: 8191 tokens 371 / 367 / 364 / 364,
-// 16 packed prompts 610 / 604 / 602 / 602, 1000 behind 100000 8-bit rows 1244 / 1233 / 1228 / 1227.
+// 2^80 stay below 2^126.  With 8 / 12 / 16 / 1000, in us: 8191 tokens 372 / 370 / 367 / 367,
+// 16 packed prompts 610 / 604 / 603 / 603, 1000 behind 100000 8-bit rows 1244 / 1234 / 1229 / 1228.
 constexpr float kLazy = 16.f;
 constexpr int kQ = kTile * kD * 2;               // bytes of a stream's rows of q
 constexpr int kStage = kTile * kD * 2;           // of a K or V tile
@@ -102,10 +103,11 @@ static_assert(kSmem<16> <= 227 * 1024 && kSmem<8> <= 227 * 1024, "shared memory 
 
 // Bytes of a cache's keys and values from which runs go side by side (prompt_plan.cuh):
 // about what L2 holds.  With / without, in us, 8 x 4 heads, bf16 rows: 512 tokens behind
-// 16000 rows (66 MB) 98.7 / 97.4, 32000 (131 MB) 175 / 182, 64000 325 / 359; 128 behind
-// 8000 31.2 / 30.9, 64000 99 / 106; 256 of 4 sequences of 4000 (66 MB) 68.0 / 67.1, 8000
-// 105 / 109, 16000 181 / 197; 512 of 8 of 3000 (98 MB) 151 / 149; 8-bit rows: 512 behind
-// 64000 (131 MB) 407 / 405, 1000 behind 100000 1263 / 1265, in a long run 1268 / 1294.
+// 16000 rows (66 MB) 98 / 97, 32000 (131 MB) 175 / 186, 64000 326 / 372; 128 behind 8000
+// 30.3 / 30.3, 64000 99 / 110; 256 of 4 sequences of 4000 (66 MB) 66.7 / 68.2, 8000 105 / 110,
+// 16000 182 / 202; 512 of 8 of 3000 (98 MB) 150 / 150; 8-bit rows: 512 of 8 of 3000 (49 MB)
+// 181 / 177, behind 64000 (131 MB) 401 / 400, 1000 behind 100000 1229 / 1227, in a long run
+// 1233 / 1275.
 constexpr int64_t kBesideBytes = 112 << 20;
 
 struct Maps {
@@ -1004,18 +1006,18 @@ constexpr int64_t kFewTokens = 64;
 //
 // Streamed / tensor cores, in us, trees of t nodes of 4 heads for each of 8 KV heads, bf16
 // rows (8-bit rows in brackets).  Up to 16 rows the keys are read once either way:
-//   1 sequence, t = 1, 300 keys 5.0 / 8.9 (5.8 / 11.2), 4000 6.8 / 12.0 (7.0 / 14.5), 64000
-//   42 / 44 (39 / 50); 16 sequences of 4000 39 / 45 (22 / 54); 64 of 4000 146 / 163 (88 / 187);
-//   t = 4: 1 of 4000 10.1 / 13.0 (9.9 / 14.8), of 16000 19.1 / 17.4 (18.7 / 22.0), of 64000
-//   53 / 45 (52 / 50); 4 of 64000 151 / 154 (97 / 161); 64 of 1000 53 / 52 (47 / 77), of 4000
-//   158 / 163 (112 / 188).
+//   1 sequence, t = 1, 300 keys 5.6 / 9.3 (6.2 / 10.4), 4000 7.5 / 12.3 (7.5 / 14.0), 64000
+//   43 / 44 (40 / 48); 16 sequences of 4000 40 / 45 (23 / 52); 64 of 4000 148 / 160 (91 / 176);
+//   t = 4: 1 of 4000 10.7 / 12.6 (10.5 / 14.1), of 16000 20.7 / 17.5 (19.5 / 21.2), of 64000
+//   60 / 44 (55 / 49); 4 of 64000 152 / 153 (102 / 161); 64 of 1000 57 / 51 (51 / 69), of 4000
+//   165 / 163 (121 / 176).
 // More rows read them again, from L2, for every 16:
-//   t = 8: 1 of 1000 8.5 / 10.8 (8.5 / 13.4), of 4000 13.1 / 12.6 (12.9 / 15.2), of 16000
-//   31 / 18 (30 / 23); 4 of 1000 10.4 / 12.7 (10.4 / 15.8), of 4000 19.5 / 17.9 (19.0 / 23.6);
-//   16 of 300 15.2 / 10.4 (16.0 / 12.7); t = 16: 1 of 4000 13.2 / 13.5 (12.9 / 16.2); 4 of 1000
-//   12.2 / 13.6 (11.8 / 16.6), of 4000 28 / 20 (28 / 25).
-// Prompts over their own keys: 1 token 4.1 / 6.8, 17 5.4 / 6.9, 64 6.0 / 8.7, 32 of 1
-//   token 7.6 / 12.4; of 32 heads in groups of 1, 64 tokens 6.6 / 7.0.
+//   t = 8: 1 of 1000 9.1 / 11.0 (9.0 / 12.6), of 4000 13.9 / 12.8 (13.6 / 14.4), of 16000
+//   33 / 18 (31 / 21); 4 of 1000 11.1 / 12.9 (11.0 / 15.0), of 4000 20.9 / 18.4 (19.8 / 22.2);
+//   16 of 300 16.2 / 10.8 (17.2 / 11.7); t = 16: 1 of 4000 14.1 / 13.8 (13.6 / 15.4); 4 of 1000
+//   13.3 / 13.5 (12.9 / 15.4), of 4000 33 / 20 (31 / 22.5).
+// Prompts over their own keys: 1 token 3.9 / 7.2, 17 5.7 / 7.3, 64 6.2 / 9.3, 32 of 1
+//   token 8.0 / 13.0; of 32 heads in groups of 1, 64 tokens 7.0 / 7.5.
 int few_ctas(int bits, int64_t n, int64_t wide, int rows, bool again, int64_t keys) {
   // no wider than there are tiles for, below 600 keys not as wide: the barriers cost what it saves
   const int ctas = keys <= 128 ? 1 : n <= 12 ? (keys < 600 ? 4 : 8) : n <= 32 ? 4 : n <= 72 ? 2 : 1;

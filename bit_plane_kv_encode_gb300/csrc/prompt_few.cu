@@ -12,9 +12,9 @@
 // its few rows or one has them all.  There this half looks, and leaves the call to the
 // tensor cores, which are launched behind it in any case, where rows would be read again.
 //
-// Measured on a GB300: one new token of a sequence of 4000 bf16 rows, 8 x 4 heads, 6.8 us,
-// latency; of 64000 (262 MB) 42 us, 6.3 TB/s; 64 sequences of 4000 in 8 bits (528 MB) 88 us,
-// 6.0 TB/s.  Weights enter their product as bf16 (2^-8), for 8-bit rows as halves (2^-11).
+// Measured on a GB300: one new token of a sequence of 4000 bf16 rows, 8 x 4 heads, 7.5 us,
+// latency; of 64000 (262 MB) 43 us, 6.1 TB/s; 64 sequences of 4000 in 8 bits (528 MB) 91 us,
+// 5.8 TB/s.  Weights enter their product as bf16 (2^-8), for 8-bit rows as halves (2^-11).
 #include <cooperative_groups.h>
 
 #include "prompt_plan.cuh"

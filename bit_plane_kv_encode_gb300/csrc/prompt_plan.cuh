@@ -33,8 +33,8 @@ constexpr int kSms = 152;
 constexpr int kSoftmaxWarps = 8;
 // What a unit's start and end cost, in tiles: its rows of q, the first S and the
 // last O, that nothing of its own overlaps.  With 1 / 2 / 3 / 5, in us: 8191 tokens
-// 408 / 394 / 398 / 404, packed prompts 684 / 650 / 664 / 694, trees of 16 sequences
-// 58.6 / 55.6 / 55.0 / 55.9.
+// 391 / 367 / 369 / 374, packed prompts 655 / 603 / 616 / 643, trees of 16 sequences
+// 58.2 / 55.2 / 54.9 / 55.7.
 constexpr int kOver = 2;
 
 constexpr int kBeside = 3;
