@@ -35,3 +35,5 @@ def test_a_run_that_takes_seconds(pk):
     pk.bpkv_prompt_attend(a, ws, ws.numel())
     assert pk.bpkv_read_status(ws) == 0
     assert (out == 2).all()
+    del a, c, x
+    torch.cuda.empty_cache()
